@@ -1,0 +1,195 @@
+// Division of a paged-attention call into equal shares of key blocks.
+//
+// A unit is one tile of query rows of one sequence for one key/value head; a
+// row is a (token, query head) pair of that head's group.  A unit reads its
+// visible keys in blocks of kBlock; the blocks of all units, head by head, form
+// one line that the CTAs cut into equal stretches.  So a batch of ragged
+// lengths and one long sequence both load every SM alike.  A unit that a cut
+// crosses leaves a partial result (row maximum, sum and unnormalised output)
+// with each CTA that worked on it; the last of them to arrive joins the pieces
+// in the order of the CTAs, which does not depend on who is last.
+#pragma once
+
+#include "ops_common.cuh"
+
+namespace pw_attn {
+
+struct Params {
+  pw_attn_args a;
+  int group;          // query heads per key/value head
+  float scale_log2;   // scale * log2(e): the softmax runs in powers of two
+  uint32_t* arrived;  // one counter per CTA, all 0 between calls
+  float* part;        // 2 partial results per CTA
+  uint64_t wait_ns;
+};
+
+constexpr int kMaxCtas = 320;   // at most two CTAs on each of 160 SMs
+
+struct Sequence {
+  int q0, q_len, kv_len;
+};
+
+// Lengths of sequence b; what the call's arrays cannot hold is reported and
+// left out (a sequence without tokens, or keys past its page table).
+__device__ __forceinline__ Sequence sequence(const pw_attn_args& a, int b, bool report) {
+  Sequence s;
+  s.q0 = a.q_offsets[b];
+  s.q_len = a.q_offsets[b + 1] - s.q0;
+  s.kv_len = a.kv_lens[b];
+  if (s.q0 < 0 || s.q_len < 0 || s.q0 > a.tokens - s.q_len) {
+    if (report) pw::report_status(a.status, PW_ERR_INVALID_ARG);
+    s.q0 = s.q_len = 0;
+  }
+  const int64_t most = static_cast<int64_t>(a.pages_per_seq) * a.page_size;
+  if (s.kv_len < 0 || s.kv_len > most) {
+    if (report) pw::report_status(a.status, PW_ERR_INVALID_ARG);
+    s.kv_len = s.kv_len < 0 ? 0 : static_cast<int>(most);
+  }
+  return s;
+}
+
+// Key range [lo, hi) that the rows of a tile see, and its blocks.
+struct Range {
+  int lo, hi, b0, b1;
+};
+template <int kTile, int kBlock>
+__device__ __forceinline__ Range tile_range(const Params& p, const Sequence& s, int tile) {
+  const int rows = s.q_len * p.group;
+  const int first = tile * kTile, last = min(rows, first + kTile) - 1;
+  const int base = s.kv_len - s.q_len;
+  Range r;
+  r.hi = p.a.causal ? max(0, base + last / p.group + 1) : s.kv_len;
+  r.lo = p.a.causal && p.a.window ? max(0, base + first / p.group - p.a.window + 1) : 0;
+  if (r.lo >= r.hi) r.lo = r.hi = 0;
+  r.b0 = r.lo / kBlock;
+  r.b1 = (r.hi + kBlock - 1) / kBlock;
+  return r;
+}
+// A unit whose rows see nothing still takes one (empty) block: its zeros have
+// to be written.
+__device__ __forceinline__ int blocks_of(const Range& r) { return max(1, r.b1 - r.b0); }
+
+template <int kTile>
+__device__ __forceinline__ int tiles_of(const Params& p, const Sequence& s) {
+  return (s.q_len * p.group + kTile - 1) / kTile;
+}
+
+template <int kTile, int kBlock>
+__device__ __forceinline__ long long sequence_blocks(const Params& p, const Sequence& s) {
+  const int tiles = tiles_of<kTile>(p, s);
+  long long n = 0;
+  for (int i = 0; i < tiles; ++i) n += blocks_of(tile_range<kTile, kBlock>(p, s, i));
+  return n;
+}
+
+// Where a CTA is on the line.
+struct Cursor {
+  Sequence s;
+  Range r;
+  int head, seq, tile;
+  int block;                // next block of the unit, 0 .. blocks_of(r) - 1
+  long long pos, end;       // its position on the line, and the end of the CTA's stretch
+  __device__ __forceinline__ bool done() const { return pos >= end; }
+  // the unit's blocks on the line are [unit_begin, unit_end)
+  __device__ __forceinline__ long long unit_begin() const { return pos - block; }
+  __device__ __forceinline__ long long unit_end() const { return pos - block + blocks_of(r); }
+};
+
+// Moves to the first block of the next unit; pos is that block's already.
+template <int kTile, int kBlock>
+__device__ __forceinline__ void next_unit(const Params& p, Cursor& c) {
+  ++c.tile;
+  while (c.tile >= tiles_of<kTile>(p, c.s)) {
+    c.tile = 0;
+    if (++c.seq >= p.a.batch) {
+      c.seq = 0;
+      if (++c.head >= p.a.kv_heads) {   // only past the end of the line
+        c.end = c.pos;
+        return;
+      }
+    }
+    c.s = sequence(p.a, c.seq, false);
+  }
+  c.r = tile_range<kTile, kBlock>(p, c.s, c.tile);
+  c.block = 0;
+}
+
+// The cursor of CTA `cta` of `ctas`, found by the whole CTA (kThreads
+// threads).  Returns false when it has no stretch; `ctas` becomes the number of
+// CTAs that have one, at least a block each.
+template <int kTile, int kBlock, int kThreads>
+__device__ __forceinline__ bool find_start(const Params& p, int cta, int& ctas, Cursor& c, long long& line) {
+  __shared__ long long warp_sum[kThreads / 32];
+  __shared__ long long before, sh_rest;
+  __shared__ int sh_seq;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // blocks of one head
+  long long mine = 0;
+  for (int b = tid; b < p.a.batch; b += kThreads)
+    mine += sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, cta == 0));
+  long long sum = mine;
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) warp_sum[warp] = sum;
+  if (tid == 0) {
+    before = 0;
+    sh_seq = 0;
+    sh_rest = 0;
+  }
+  __syncthreads();
+  long long per_head = 0;
+  for (int i = 0; i < kThreads / 32; ++i) per_head += warp_sum[i];
+  line = per_head * p.a.kv_heads;
+  if (line < ctas) ctas = static_cast<int>(line);
+  if (cta >= ctas) return false;   // the same for every thread
+  c.pos = line * cta / ctas;
+  c.end = line * (cta + 1) / ctas;
+  c.head = static_cast<int>(c.pos / per_head);
+  const long long want = c.pos - c.head * per_head;
+  // the sequence that holds position `want` of the head's blocks
+  for (int b0 = 0; b0 < p.a.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    const long long n = p.a.batch <= kThreads ? mine
+                        : b < p.a.batch ? sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, false)) : 0;
+    long long incl = n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    __syncthreads();   // warp_sum and before are read above
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long base = before;
+    for (int i = 0; i < warp; ++i) base += warp_sum[i];
+    const long long lo = base + incl - n;
+    if (n > 0 && lo <= want && want < lo + n) {
+      sh_seq = b;
+      sh_rest = want - lo;
+    }
+    __syncthreads();
+    if (tid == 0)
+      for (int i = 0; i < kThreads / 32; ++i) before += warp_sum[i];
+  }
+  __syncthreads();
+  c.seq = sh_seq;
+  c.s = sequence(p.a, c.seq, false);
+  long long rest = sh_rest;
+  c.tile = 0;
+  c.r = tile_range<kTile, kBlock>(p, c.s, 0);
+  while (rest >= blocks_of(c.r)) {
+    rest -= blocks_of(c.r);
+    c.r = tile_range<kTile, kBlock>(p, c.s, ++c.tile);
+  }
+  c.block = static_cast<int>(rest);
+  return true;
+}
+
+// The CTA whose stretch holds position w of the line.
+__device__ __forceinline__ int cta_of(long long w, long long line, int ctas) {
+  // stretches start at floor(line * i / ctas): the largest i whose start is <= w
+  int i = static_cast<int>(((w + 1) * ctas - 1) / line);
+  while (i + 1 < ctas && line * (i + 1) / ctas <= w) ++i;
+  while (i > 0 && line * i / ctas > w) --i;
+  return i;
+}
+
+}  // namespace pw_attn

@@ -1,0 +1,313 @@
+// Residual addition with root-mean-square norm, and 16-bit to e4m3 conversion
+// with a scale per 128 columns of a row or per 128 x 128 block.
+//
+//   r = x + residual,  y = r * rsqrt(mean(r^2) + eps) * w
+//   s = max(max|y over the group| / 448, 2^-100),  q = e4m3(y / s)
+//
+// Both read and write every value once; memory bandwidth bounds them, and for
+// a few rows the latency of one load, one reduction and one store.
+#include "ops_common.cuh"
+
+namespace {
+
+constexpr int kVec = 8;               // values a thread holds of one chunk: 16 bytes
+constexpr int kMaxCols = 32768;       // 1024 threads x 4 chunks
+
+struct RowParams {
+  const void* x;
+  const void* res;
+  const void* w;
+  void* res_out;
+  void* y;
+  uint8_t* q;
+  float* scale;
+  int64_t x_stride, res_stride, res_out_stride, y_stride, q_stride, scale_stride;
+  int64_t rows;
+  int cols;
+  float eps;
+};
+
+// Eight values at columns c .. c+7 of a row; columns past the end are 0.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load8(const T* row, int c, int cols, float (&v)[kVec]) {
+  if (kAligned) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (c < cols) u = *reinterpret_cast<const uint4*>(row + c);
+    pw::unpack2<T>(u.x, v[0], v[1]);
+    pw::unpack2<T>(u.y, v[2], v[3]);
+    pw::unpack2<T>(u.z, v[4], v[5]);
+    pw::unpack2<T>(u.w, v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = c + i < cols ? pw::to_float(row[c + i]) : 0.0f;
+  }
+}
+template <typename T, bool kAligned>
+__device__ __forceinline__ void store8(T* row, int c, int cols, const float (&v)[kVec]) {
+  if (kAligned) {
+    if (c < cols)
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(pw::pack2<T>(v[0], v[1]), pw::pack2<T>(v[2], v[3]),
+                                                      pw::pack2<T>(v[4], v[5]), pw::pack2<T>(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (c + i < cols) row[c + i] = pw::from_float<T>(v[i]);
+  }
+}
+template <bool kAligned>
+__device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const float (&v)[kVec], float inv) {
+  const uint32_t lo = pw::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  const uint32_t hi = pw::e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  if (kAligned) {
+    if (c < cols) *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (c + i < cols) row[c + i] = static_cast<uint8_t>((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xFFu);
+  }
+}
+
+// One CTA per row.  A thread holds 8 values of each of kChunks chunks in
+// registers, so the row is read once; 16 neighbouring threads hold a group of
+// 128 columns, so a group's largest value is four shuffles away.
+template <typename T, int kChunks, bool kAligned, bool kNorm>
+__global__ void __launch_bounds__(1024) row_kernel(const RowParams p) {
+  __shared__ float sums[32];
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  float v[kChunks][kVec];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) load8<T, kAligned>(x, (c * nthr + tid) * kVec, p.cols, v[c]);
+  if (kNorm) {
+    const T* w = static_cast<const T*>(p.w);
+    if (p.res) {
+      const T* res = static_cast<const T*>(p.res) + row * p.res_stride;
+      float r[kChunks][kVec];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) load8<T, kAligned>(res, (c * nthr + tid) * kVec, p.cols, r[c]);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[c][i] += r[c][i];
+    }
+    if (p.res_out) {
+      T* res_out = static_cast<T*>(p.res_out) + row * p.res_out_stride;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) store8<T, kAligned>(res_out, (c * nthr + tid) * kVec, p.cols, v[c]);
+    }
+    // the sum of squares in 32 bits: 8 x kChunks terms a thread, then a tree
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum += v[c][i] * v[c][i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if ((tid & 31) == 0) sums[tid >> 5] = sum;
+    __syncthreads();
+    sum = (tid & 31) < (nthr >> 5) ? sums[tid & 31] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float rs = rsqrtf(sum / static_cast<float>(p.cols) + p.eps);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float wv[kVec];
+      load8<T, kAligned>(w, (c * nthr + tid) * kVec, p.cols, wv);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) v[c][i] = v[c][i] * rs * wv[i];
+    }
+    if (p.y) {
+      T* y = static_cast<T*>(p.y) + row * p.y_stride;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) store8<T, kAligned>(y, (c * nthr + tid) * kVec, p.cols, v[c]);
+    }
+  }
+  if (p.q) {
+    uint8_t* q = p.q + row * p.q_stride;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = (c * nthr + tid) * kVec;
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) top = pw::max_nan(top, fabsf(v[c][i]));
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
+      if (col < p.cols && (tid & 15) == 0) p.scale[row * p.scale_stride + col / pw::kGroup] = s;
+      store8_e4m3<kAligned>(q, col, p.cols, v[c], 1.0f / s);
+    }
+  }
+}
+
+// One CTA per 128 x 128 block: 256 threads hold 8 rows x 8 columns each.
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(256) block_kernel(const RowParams p) {
+  __shared__ float tops[8];
+  const int tid = threadIdx.x;
+  const int kb = blockIdx.x;
+  const int col = kb * pw::kGroup + (tid & 15) * kVec;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * pw::kGroup + (tid >> 4);
+  float v[8][kVec];
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = row0 + 16 * i;
+    load8<T, kAligned>(static_cast<const T*>(p.x) + (row < p.rows ? row : 0) * p.x_stride, row < p.rows ? col : p.cols,
+                       p.cols, v[i]);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) top = pw::max_nan(top, fabsf(v[i][j]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if ((tid & 31) == 0) tops[tid >> 5] = top;
+  __syncthreads();
+  top = tops[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = pw::max_nan(top, tops[i]);
+  const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
+  if (tid == 0) p.scale[blockIdx.y * p.scale_stride + kb] = s;
+  const float inv = 1.0f / s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = row0 + 16 * i;
+    if (row < p.rows) store8_e4m3<kAligned>(p.q + row * p.q_stride, col, p.cols, v[i], inv);
+  }
+}
+
+template <typename T, bool kAligned, bool kNorm>
+int launch_rows(const RowParams& p, cudaStream_t s) {
+  // threads in whole warps, each with one 8-value chunk where the row allows
+  const int units = (p.cols + kVec - 1) / kVec;
+  int chunks = 1;
+  while ((units + chunks - 1) / chunks > 1024) chunks *= 2;
+  const int threads = ((units + chunks - 1) / chunks + 31) & ~31;
+  const dim3 grid(static_cast<unsigned>(p.rows));
+  switch (chunks) {
+    case 1: row_kernel<T, 1, kAligned, kNorm><<<grid, threads, 0, s>>>(p); break;
+    case 2: row_kernel<T, 2, kAligned, kNorm><<<grid, threads, 0, s>>>(p); break;
+    default: row_kernel<T, 4, kAligned, kNorm><<<grid, threads, 0, s>>>(p); break;
+  }
+  PW_CUDA_TRY(cudaGetLastError());
+  return PW_OK;
+}
+
+template <typename T, bool kAligned>
+int launch_blocks(const RowParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.cols + pw::kGroup - 1) / pw::kGroup),
+                  static_cast<unsigned>((p.rows + pw::kGroup - 1) / pw::kGroup));
+  block_kernel<T, kAligned><<<grid, 256, 0, s>>>(p);
+  PW_CUDA_TRY(cudaGetLastError());
+  return PW_OK;
+}
+
+// 16-byte accesses of 16-bit rows need the address, the stride and the width
+// in multiples of 8 values.
+bool rows_aligned(const void* ptr, int64_t stride, int cols) {
+  return !ptr || (pw::aligned(ptr, 16) && stride % kVec == 0 && cols % kVec == 0);
+}
+bool codes_aligned(const void* ptr, int64_t stride) { return !ptr || (pw::aligned(ptr, 8) && stride % 8 == 0); }
+
+int check_matrix(const char* op, const char* name, int64_t stride, int cols) {
+  if (stride < cols)
+    return pw::set_error(PW_ERR_INVALID_ARG, "%s: row stride %lld of %s is below the %d columns", op,
+                         static_cast<long long>(stride), name, cols);
+  return PW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pw_add_rmsnorm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                   const void* d_weight, int64_t rows, int cols, float eps, int dtype, void* d_residual_out,
+                   int64_t residual_out_stride, void* d_y, int64_t y_stride, uint8_t* d_q, int64_t q_stride,
+                   float* d_scale, int64_t scale_stride, void* stream) {
+  if (!pw::is_16bit(dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: dtype %d", dtype);
+  if (rows < 0 || cols < 1) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: %lld rows of %d columns",
+                                                 static_cast<long long>(rows), cols);
+  if (cols > kMaxCols || rows > 0x7FFFFFFF)
+    return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: at most %d columns (got %d) and 2^31 - 1 rows", kMaxCols, cols);
+  if (!(eps >= 0.0f)) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: eps %g", static_cast<double>(eps));
+  if (!d_y && !d_q) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: neither a 16-bit nor an 8-bit output");
+  if (!d_q != !d_scale) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: 8-bit codes and scales come together");
+  if (int e = check_matrix("add_rmsnorm", "x", x_stride, cols)) return e;
+  if (d_residual)
+    if (int e = check_matrix("add_rmsnorm", "residual", residual_stride, cols)) return e;
+  if (d_residual_out)
+    if (int e = check_matrix("add_rmsnorm", "residual_out", residual_out_stride, cols)) return e;
+  if (d_y)
+    if (int e = check_matrix("add_rmsnorm", "y", y_stride, cols)) return e;
+  if (d_q) {
+    if (int e = check_matrix("add_rmsnorm", "q", q_stride, cols)) return e;
+    if (int e = check_matrix("add_rmsnorm", "scale", scale_stride, (cols + pw::kGroup - 1) / pw::kGroup)) return e;
+  }
+  if (rows == 0) return PW_OK;
+  if (!d_x || !d_weight) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: NULL argument");
+  if (!pw::aligned(d_x, 2) || !pw::aligned(d_weight, 2) || !pw::aligned(d_residual, 2) ||
+      !pw::aligned(d_residual_out, 2) || !pw::aligned(d_y, 2) || !pw::aligned(d_scale, 4))
+    return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: a pointer is not aligned to its values");
+  RowParams p{};
+  p.x = d_x;
+  p.res = d_residual;
+  p.w = d_weight;
+  p.res_out = d_residual_out;
+  p.y = d_y;
+  p.q = d_q;
+  p.scale = d_scale;
+  p.x_stride = x_stride;
+  p.res_stride = residual_stride;
+  p.res_out_stride = residual_out_stride;
+  p.y_stride = y_stride;
+  p.q_stride = q_stride;
+  p.scale_stride = scale_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = eps;
+  const bool al = rows_aligned(d_x, x_stride, cols) && rows_aligned(d_residual, residual_stride, cols) &&
+                  rows_aligned(d_weight, kVec, cols) && rows_aligned(d_residual_out, residual_out_stride, cols) &&
+                  rows_aligned(d_y, y_stride, cols) && codes_aligned(d_q, q_stride);
+  cudaStream_t s = pw::as_stream(stream);
+  if (dtype == PW_DTYPE_F16) return al ? launch_rows<__half, true, true>(p, s) : launch_rows<__half, false, true>(p, s);
+  return al ? launch_rows<__nv_bfloat16, true, true>(p, s) : launch_rows<__nv_bfloat16, false, true>(p, s);
+}
+
+int pw_quantize_fp8(const void* d_x, int64_t x_stride, int64_t rows, int cols, int dtype, int block_rows, uint8_t* d_q,
+                    int64_t q_stride, float* d_scale, int64_t scale_stride, void* stream) {
+  if (!pw::is_16bit(dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: dtype %d", dtype);
+  if (block_rows != 1 && block_rows != pw::kGroup)
+    return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: block_rows %d (1 or 128)", block_rows);
+  if (rows < 0 || cols < 1) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: %lld rows of %d columns",
+                                                 static_cast<long long>(rows), cols);
+  // blocks: the grid's second axis counts 128-row strips
+  if (block_rows == 1 ? (cols > kMaxCols || rows > 0x7FFFFFFF) : rows > 65535ll * pw::kGroup)
+    return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: %lld rows of %d columns are too large",
+                         static_cast<long long>(rows), cols);
+  if (int e = check_matrix("quantize_fp8", "x", x_stride, cols)) return e;
+  if (int e = check_matrix("quantize_fp8", "q", q_stride, cols)) return e;
+  if (int e = check_matrix("quantize_fp8", "scale", scale_stride, (cols + pw::kGroup - 1) / pw::kGroup)) return e;
+  if (rows == 0) return PW_OK;
+  if (!d_x || !d_q || !d_scale) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: NULL argument");
+  if (!pw::aligned(d_x, 2) || !pw::aligned(d_scale, 4))
+    return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: a pointer is not aligned to its values");
+  RowParams p{};
+  p.x = d_x;
+  p.q = d_q;
+  p.scale = d_scale;
+  p.x_stride = x_stride;
+  p.q_stride = q_stride;
+  p.scale_stride = scale_stride;
+  p.rows = rows;
+  p.cols = cols;
+  const bool al = rows_aligned(d_x, x_stride, cols) && codes_aligned(d_q, q_stride);
+  cudaStream_t s = pw::as_stream(stream);
+  if (block_rows == 1) {
+    if (dtype == PW_DTYPE_F16)
+      return al ? launch_rows<__half, true, false>(p, s) : launch_rows<__half, false, false>(p, s);
+    return al ? launch_rows<__nv_bfloat16, true, false>(p, s) : launch_rows<__nv_bfloat16, false, false>(p, s);
+  }
+  if (dtype == PW_DTYPE_F16) return al ? launch_blocks<__half, true>(p, s) : launch_blocks<__half, false>(p, s);
+  return al ? launch_blocks<__nv_bfloat16, true>(p, s) : launch_blocks<__nv_bfloat16, false>(p, s);
+}
+
+}  // extern "C"

@@ -36,6 +36,8 @@ PW_PATH_AUTO, PW_PATH_DECODE, PW_PATH_PREFILL = 0, 1, 2
 PW_KERNEL_AUTO, PW_KERNEL_TENSOR, PW_KERNEL_CUDA_CORES = 0, 1, 2
 PW_FFN_FLAG_TEST_DROP_ONE_ARRIVAL = 1
 PW_FFN_FLAG_STRIP_COMBINE = 2
+PW_DTYPE_F16, PW_DTYPE_BF16 = 0, 1
+PW_ROPE_PLAIN, PW_ROPE_LINEAR, PW_ROPE_NTK, PW_ROPE_YARN, PW_ROPE_BANDS = 0, 1, 2, 3, 4
 
 ERR_NAMES = {0: "PW_OK", -1: "PW_ERR_INVALID_ARG", -2: "PW_ERR_UNSUPPORTED", -3: "PW_ERR_NOT_RESIDENT",
              -4: "PW_ERR_CUDA", -5: "PW_ERR_TIMEOUT", -6: "PW_ERR_WORKSPACE", -7: "PW_ERR_BUSY"}
@@ -49,6 +51,8 @@ EXPORTS = (
     "pw_page_state",
     "pw_moe_apl_ffn_workspace", "pw_moe_apl_ffn", "pw_moe_apl_ffn_ex", "pw_moe_apl_ffn_noalloc",
     "pw_moe_route_apl_ffn", "pw_moe_route_apl_ffn_ex", "pw_moe_route_apl_ffn_layers",
+    "pw_add_rmsnorm", "pw_quantize_fp8", "pw_fp8_linear", "pw_rope_turns", "pw_rope_append",
+    "pw_paged_attention_workspace", "pw_paged_attention",
     "pw_unpack_indices",
     "pw_apl_linear",
 )
@@ -70,8 +74,40 @@ class pw_ffn_options(ctypes.Structure):
                 ("shared_experts", ctypes.c_int32), ("kernel", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
 
 
+class pw_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("scale", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
+
+
+class pw_rope_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "q_out", "k", "v", "k_cache", "v_cache", "turns", "positions",
+                                                "page_table", "q_offsets", "kv_lens", "status")]
+                + [(n, ctypes.c_int64) for n in (
+                    "q_stride_token", "q_stride_head", "q_out_stride_token", "q_out_stride_head", "k_stride_token",
+                    "k_stride_head", "v_stride_token", "v_stride_head", "k_cache_stride_page", "k_cache_stride_token",
+                    "k_cache_stride_head", "v_cache_stride_page", "v_cache_stride_token", "v_cache_stride_head",
+                    "page_table_stride")]
+                + [(n, ctypes.c_int32) for n in ("tokens", "batch", "heads", "kv_heads", "head_dim", "rotary_dim",
+                                                 "page_size", "num_pages", "pages_per_seq", "dtype", "interleaved")]
+                + [("factor", ctypes.c_float)])
+
+
+class pw_attn_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "out", "lse", "k_cache", "v_cache", "page_table", "q_offsets",
+                                                "kv_lens", "status")]
+                + [(n, ctypes.c_int64) for n in (
+                    "q_stride_token", "q_stride_head", "out_stride_token", "out_stride_head", "k_stride_page",
+                    "k_stride_token", "k_stride_head", "v_stride_page", "v_stride_token", "v_stride_head",
+                    "page_table_stride")]
+                + [(n, ctypes.c_int32) for n in ("tokens", "batch", "heads", "kv_heads", "head_dim", "page_size",
+                                                 "num_pages", "pages_per_seq", "max_q_len", "max_kv_len", "dtype",
+                                                 "causal", "window")]
+                + [("scale", ctypes.c_float)])
+
+
 _lib: Optional[ctypes.CDLL] = None
 P, I32, I64, U64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+F32, F64 = ctypes.c_float, ctypes.c_double
 
 
 def lib() -> ctypes.CDLL:
@@ -115,6 +151,13 @@ def lib() -> ctypes.CDLL:
                                               P, ctypes.POINTER(pw_ffn_options), P]),
             "pw_moe_route_apl_ffn_layers": (I32, [P, I32, I32, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P,
                                                   SZ, P, P, ctypes.POINTER(pw_ffn_options), P]),
+            "pw_add_rmsnorm": (I32, [P, I64, P, I64, P, I64, I32, F32, I32, P, I64, P, I64, P, I64, P, I64, P]),
+            "pw_quantize_fp8": (I32, [P, I64, I64, I32, I32, I32, P, I64, P, I64, P]),
+            "pw_fp8_linear": (I32, [P, I64, P, I64, P, I64, P, I64, I32, I32, I32, I32, P, I64, P, P]),
+            "pw_rope_turns": (I32, [I32, F64, ctypes.POINTER(pw_rope_scaling), P, ctypes.POINTER(F32)]),
+            "pw_rope_append": (I32, [ctypes.POINTER(pw_rope_args), P]),
+            "pw_paged_attention_workspace": (SZ, [I32, I32, I32, I32, I32]),
+            "pw_paged_attention": (I32, [ctypes.POINTER(pw_attn_args), P, SZ, P]),
             "pw_unpack_indices": (I32, [P, I32, I32, P, P]),
             "pw_apl_linear": (I32, [P, I32, P, I32, P, P]),
         }
@@ -376,3 +419,190 @@ def pw_apl_linear(t, block: int, x: torch.Tensor, out: torch.Tensor, stream=None
     _dev(x, torch.float16, "x")
     _dev(out, torch.float32, "out")
     _check(lib().pw_apl_linear(t, block, _ptr(x), x.shape[0], _ptr(out), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a decoder layer
+# ---------------------------------------------------------------------------
+_DTYPE = {torch.float16: PW_DTYPE_F16, torch.bfloat16: PW_DTYPE_BF16}
+
+
+def _dtype16(t: torch.Tensor, name: str) -> int:
+    d = _DTYPE.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: need fp16 or bf16, got {t.dtype}")
+    return d
+
+
+def _matrix(t: torch.Tensor, shape, dtypes, name: str) -> int:
+    """Checks a CUDA matrix whose rows are contiguous; returns its row stride."""
+    if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != tuple(shape) or (
+            t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: need a CUDA matrix {tuple(shape)} of {dtypes[0]} with contiguous rows, got "
+                         f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} on {t.device}")
+    # the stride of a single row says nothing
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+
+
+def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                   residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                   q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = r * rsqrt(mean(r^2) + eps) * weight with r = x + residual; `y` in
+    x's type and/or `q` (e4m3) with `scale` (fp32, a scale per 128 columns);
+    `residual_out` receives r."""
+    dt = _dtype16(x, "x")
+    shape, same = x.shape, (x.dtype,)
+    xs = _matrix(x, shape, same, "x")
+    if not weight.is_cuda or weight.dtype != x.dtype or tuple(weight.shape) != (shape[1],) or not weight.is_contiguous():
+        raise ValueError(f"weight: need a contiguous CUDA tensor ({shape[1]},) of {x.dtype}")
+    rs = 0 if residual is None else _matrix(residual, shape, same, "residual")
+    ros = 0 if residual_out is None else _matrix(residual_out, shape, same, "residual_out")
+    ys = 0 if y is None else _matrix(y, shape, same, "y")
+    qs = 0 if q is None else _matrix(q, shape, _CODES, "q")
+    ss = 0 if scale is None else _matrix(scale, (shape[0], -(-shape[1] // 128)), _F32, "scale")
+    _check(lib().pw_add_rmsnorm(_ptr(x), xs, _ptr(residual), rs, _ptr(weight), shape[0], shape[1], eps, dt,
+                                _ptr(residual_out), ros, _ptr(y), ys, _ptr(q), qs, _ptr(scale), ss, _stream(stream)))
+
+
+def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
+    """x (fp16 or bf16 matrix) to e4m3 codes `q` and fp32 `scale`: groups of
+    128 columns of one row (block_rows 1) or of 128 rows (block_rows 128)."""
+    dt = _dtype16(x, "x")
+    rows, cols = x.shape
+    xs, qs = _matrix(x, x.shape, (x.dtype,), "x"), _matrix(q, x.shape, _CODES, "q")
+    if block_rows < 1:
+        raise ValueError(f"block_rows: {block_rows}")
+    ss = _matrix(scale, (-(-rows // block_rows), -(-cols // 128)), _F32, "scale")
+    _check(lib().pw_quantize_fp8(_ptr(x), xs, rows, cols, dt, block_rows, _ptr(q), qs, _ptr(scale), ss,
+                                 _stream(stream)))
+
+
+def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, y: torch.Tensor,
+                  status: torch.Tensor, stream=None) -> None:
+    """y [M][N] = a [M][K] b [N][K]^T of e4m3 codes with their scales:
+    a_scale [M][ceil(K/128)], b_scale [ceil(N/128)][ceil(K/128)]."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"fp8_linear: a {tuple(a.shape)}, b {tuple(b.shape)}")
+    dt = _dtype16(y, "y")
+    (M, K), N = a.shape, b.shape[0]
+    kb = -(-K // 128)
+    lda, ldb, ldy = _matrix(a, a.shape, _CODES, "a"), _matrix(b, b.shape, _CODES, "b"), _matrix(y, (M, N), (y.dtype,), "y")
+    # a single row may have any stride: the row's own alignment is what counts
+    lda, ldb = (lda + 15) // 16 * 16 if M == 1 else lda, (ldb + 15) // 16 * 16 if N == 1 else ldb
+    sa, sb = _matrix(a_scale, (M, kb), _F32, "a_scale"), _matrix(b_scale, (-(-N // 128), kb), _F32, "b_scale")
+    _dev(status, torch.int32, "status")
+    _check(lib().pw_fp8_linear(_ptr(a), lda, _ptr(a_scale), sa, _ptr(b), ldb, _ptr(b_scale), sb, M, N, K, dt, _ptr(y),
+                               ldy, _ptr(status), _stream(stream)))
+
+
+def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_rope_scaling] = None):
+    """(int64 CPU tensor [rotary_dim/2], factor): the table of pw_rope_append."""
+    turns = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64)
+    factor = F32(0)
+    _check(lib().pw_rope_turns(rotary_dim, base, ctypes.byref(scaling) if scaling is not None else None, _ptr(turns),
+                               ctypes.byref(factor)))
+    return turns, float(factor.value)
+
+
+def _heads(t: torch.Tensor, shape, dtype, name: str):
+    """Checks a CUDA tensor whose last dimension is contiguous; returns its
+    data pointer and outer strides."""
+    st = t.stride()
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or (shape[-1] > 1 and st[-1] != 1):
+        raise ValueError(f"{name}: need a CUDA tensor {shape} of {dtype} with a contiguous last dimension, got "
+                         f"{tuple(t.shape)} of {t.dtype} with strides {st} on {t.device}")
+    return (t.data_ptr(), *st[:-1])
+
+
+def _batch(args, page_table, q_offsets, kv_lens, k_cache, status) -> None:
+    """Fills the page-table fields that the rope and attention calls share."""
+    for t, name in ((q_offsets, "q_offsets"), (kv_lens, "kv_lens"), (status, "status")):
+        _dev(t, torch.int32, name)
+    batch = kv_lens.shape[0]
+    if q_offsets.shape[0] != batch + 1:
+        raise ValueError(f"q_offsets: need {batch + 1} values, got {q_offsets.shape[0]}")
+    args.batch, args.q_offsets, args.kv_lens, args.status = batch, q_offsets.data_ptr(), kv_lens.data_ptr(), status.data_ptr()
+    if page_table is not None:
+        args.page_table_stride = _matrix(page_table, (batch, page_table.shape[1]), (torch.int32,), "page_table")
+        args.page_table, args.pages_per_seq = page_table.data_ptr(), page_table.shape[1]
+        args.num_pages, args.page_size = k_cache.shape[0], k_cache.shape[1]
+
+
+def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                   turns: torch.Tensor, k_cache: Optional[torch.Tensor], v_cache: Optional[torch.Tensor],
+                   page_table: Optional[torch.Tensor], q_offsets: torch.Tensor, kv_lens: torch.Tensor,
+                   q_out: Optional[torch.Tensor], status: torch.Tensor, interleaved: bool = False, factor: float = 1.0,
+                   positions: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotates q into q_out [T][heads][D] and k into the cache
+    [pages][page_size][kv_heads][D] (any outer strides), and appends v there.
+    The rotated part of a head is 2 * len(turns) wide."""
+    a = pw_rope_args()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("rope_append: neither q nor k")
+    if (k is None) != (v is None) or (k is None) != (k_cache is None) or (k is None) != (v_cache is None) or (
+            k is None) != (page_table is None):
+        raise ValueError("rope_append: k, v, the caches and the page table come together")
+    a.dtype, a.tokens, a.head_dim = _dtype16(x, "q"), x.shape[0], x.shape[2]
+    _dev(turns, torch.int64, "turns")
+    a.turns, a.rotary_dim = turns.data_ptr(), 2 * turns.shape[0]
+    if q is not None:
+        if q_out is None:
+            raise ValueError("rope_append: q needs q_out")
+        a.heads = q.shape[1]
+        a.q, a.q_stride_token, a.q_stride_head = _heads(q, tuple(q.shape), x.dtype, "q")
+        a.q_out, a.q_out_stride_token, a.q_out_stride_head = _heads(q_out, tuple(q.shape), x.dtype, "q_out")
+    if k is not None:
+        a.kv_heads = k.shape[1]
+        shape, cache = (a.tokens, a.kv_heads, a.head_dim), (k_cache.shape[0], k_cache.shape[1], a.kv_heads, a.head_dim)
+        a.k, a.k_stride_token, a.k_stride_head = _heads(k, shape, x.dtype, "k")
+        a.v, a.v_stride_token, a.v_stride_head = _heads(v, shape, x.dtype, "v")
+        a.k_cache, a.k_cache_stride_page, a.k_cache_stride_token, a.k_cache_stride_head = _heads(
+            k_cache, cache, x.dtype, "k_cache")
+        a.v_cache, a.v_cache_stride_page, a.v_cache_stride_token, a.v_cache_stride_head = _heads(
+            v_cache, cache, x.dtype, "v_cache")
+    _batch(a, page_table, q_offsets, kv_lens, k_cache, status)
+    if positions is not None:
+        _dev(positions, torch.int32, "positions")
+        if positions.shape[0] != a.tokens:
+            raise ValueError(f"positions: need {a.tokens} values, got {positions.shape[0]}")
+        a.positions = positions.data_ptr()
+    a.interleaved, a.factor = int(interleaved), factor
+    _check(lib().pw_rope_append(ctypes.byref(a), _stream(stream)))
+
+
+def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().pw_paged_attention_workspace(tokens, batch, heads, kv_heads, head_dim))
+
+
+def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                       q_offsets: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                       status: torch.Tensor, scale: float, causal: bool = True, window: int = 0, max_q_len: int = 0,
+                       max_kv_len: int = 0, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out [T][heads][D] = attention of the new tokens q over their sequences'
+    keys in the paged cache [pages][page_size][kv_heads][D].  `ws` must be
+    zeroed before its first use.  max_q_len / max_kv_len: bounds of the lengths
+    (0: the batch's tokens, and what the page table holds)."""
+    a = pw_attn_args()
+    a.dtype = _dtype16(q, "q")
+    a.tokens, a.heads, a.head_dim = q.shape
+    a.kv_heads = k_cache.shape[2]
+    cache = (k_cache.shape[0], k_cache.shape[1], a.kv_heads, a.head_dim)
+    a.q, a.q_stride_token, a.q_stride_head = _heads(q, tuple(q.shape), q.dtype, "q")
+    a.out, a.out_stride_token, a.out_stride_head = _heads(out, tuple(q.shape), q.dtype, "out")
+    a.k_cache, a.k_stride_page, a.k_stride_token, a.k_stride_head = _heads(k_cache, cache, q.dtype, "k_cache")
+    a.v_cache, a.v_stride_page, a.v_stride_token, a.v_stride_head = _heads(v_cache, cache, q.dtype, "v_cache")
+    _batch(a, page_table, q_offsets, kv_lens, k_cache, status)
+    if lse is not None:
+        _dev(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (a.tokens, a.heads):
+            raise ValueError(f"lse: need shape ({a.tokens}, {a.heads}), got {tuple(lse.shape)}")
+        a.lse = lse.data_ptr()
+    a.max_q_len = max_q_len or a.tokens
+    a.max_kv_len = max_kv_len or a.page_size * a.pages_per_seq
+    a.scale, a.causal, a.window = scale, int(causal), window
+    _check(lib().pw_paged_attention(ctypes.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))

@@ -424,6 +424,170 @@ int pw_moe_route_apl_ffn_layers(const void* d_desc, int layer0, int L, const uin
                                 void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The attention half of a decoder layer                                       */
+/* ------------------------------------------------------------------------ */
+/* The operators between the residual stream and the routed expert layer:
+ * norm (with an 8-bit output), 8-bit projections, rotary positions with the
+ * append to a paged key/value cache, and attention over that cache.
+ *
+ * Strides count elements; the innermost dimension is contiguous.  16-bit
+ * types are fp16 and bf16 (`dtype`); 8-bit codes are e4m3 (finite, largest
+ * magnitude 448).  Sums, statistics and scales are fp32; a 16-bit or 8-bit
+ * output is rounded once, to nearest even. */
+#define PW_DTYPE_F16 0
+#define PW_DTYPE_BF16 1
+
+/* r = x + residual;  y = r * rsqrt(mean(r^2) + eps) * weight, by rows.
+ *  d_x           [rows][cols];  d_residual the same shape, or NULL (r = x)
+ *  d_weight      [cols]
+ *  d_residual_out [rows][cols] or NULL: r, rounded (the norm itself uses the
+ *                unrounded sum); may be d_residual or d_x
+ *  d_y           [rows][cols] or NULL: y in `dtype`; may be d_x
+ *  d_q, d_scale  [rows][cols] e4m3 and fp32 [rows][ceil(cols/128)], or both
+ *                NULL: y in 8 bits (the unrounded y, not d_y), as
+ *                pw_quantize_fp8 with block_rows 1
+ * At least one of d_y and d_q.  Any alignment of the values' own size and any
+ * stride >= cols; 16-byte aligned rows of a multiple of 8 columns run on wide
+ * accesses.  cols <= 32768. */
+int pw_add_rmsnorm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                   const void* d_weight, int64_t rows, int cols, float eps, int dtype, void* d_residual_out,
+                   int64_t residual_out_stride, void* d_y, int64_t y_stride, uint8_t* d_q, int64_t q_stride,
+                   float* d_scale, int64_t scale_stride, void* stream);
+
+/* 16-bit values to e4m3 codes and fp32 scales:
+ *   scale = max(largest magnitude of the group / 448, 2^-100)
+ *   code  = e4m3(value / scale)
+ * The groups are 128 columns (the last one may be narrower) of one row
+ * (block_rows 1: activations) or of 128 rows (block_rows 128: weights).
+ * d_scale: [ceil(rows/block_rows)][ceil(cols/128)].  A group that holds NaN or
+ * an infinity comes back as NaN where it is multiplied out. */
+int pw_quantize_fp8(const void* d_x, int64_t x_stride, int64_t rows, int cols, int dtype, int block_rows, uint8_t* d_q,
+                    int64_t q_stride, float* d_scale, int64_t scale_stride, void* stream);
+
+/* y[m][n] = sum_kb a_scale[m][kb] * b_scale[n/128][kb] * sum_{k in kb} a[m][k] b[n][k]
+ * with kb the groups of 128 columns: a projection of quantised activations by
+ * a quantised weight.
+ *  d_a [M][K], d_b [N][K] e4m3; rows 16-byte aligned (address and stride)
+ *  d_a_scale fp32 [M][ceil(K/128)], d_b_scale fp32 [ceil(N/128)][ceil(K/128)]
+ *  d_y [M][N] in `dtype`
+ *  d_status as in the fused layer (PW_ERR_TIMEOUT: a wait ran out).
+ * Any M up to 2^20, N and K up to 2^24 (no multiples needed). */
+int pw_fp8_linear(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t a_scale_stride,
+                  const uint8_t* d_b, int64_t ldb, const float* d_b_scale, int64_t b_scale_stride, int M, int N,
+                  int K, int dtype, void* d_y, int64_t ldy, int32_t* d_status, void* stream);
+
+/* A batch of sequences in a paged cache, shared by the two calls below.
+ * Sequence b has kv_lens[b] keys and values in the cache; its last
+ * q_offsets[b+1] - q_offsets[b] are the call's new tokens, rows q_offsets[b]
+ * .. q_offsets[b+1]-1 of q, k, v and out.  So new token i of n sits at position
+ * kv_lens[b] - n + i.  Key j of a sequence is row j % page_size of the page
+ * page_table[b][j / page_size].  Lengths, offsets and page ids are read on the
+ * device; an offset, length or page id that the arrays cannot hold is not
+ * followed and sets d_status (PW_ERR_INVALID_ARG; PW_ERR_NOT_RESIDENT for a
+ * page id outside 0 .. num_pages-1). */
+
+/* Frequencies of rotary positions: h_turns[i] is the part of a full turn, in
+ * units of 2^-64, that pair i turns per position, for i < rotary_dim/2;
+ * *h_factor multiplies the rotated values.  Host only.
+ *   PW_ROPE_PLAIN   f_i = base^(-2i/rotary_dim) radians
+ *   PW_ROPE_LINEAR  f_i / scale
+ *   PW_ROPE_NTK     base * scale^(d/(d-2)) for base
+ *   PW_ROPE_YARN    f_i below, f_i/scale above a linear ramp of the pair index
+ *                   between the pairs that make `fast` and `slow` turns over
+ *                   original_positions; factor 0.1 ln(scale) + 1
+ *   PW_ROPE_BANDS   the same two ends, linear in the number of turns between
+ *                   `slow` and `fast`; factor 1 */
+#define PW_ROPE_PLAIN 0
+#define PW_ROPE_LINEAR 1
+#define PW_ROPE_NTK 2
+#define PW_ROPE_YARN 3
+#define PW_ROPE_BANDS 4
+typedef struct pw_rope_scaling {
+  int32_t kind;               /* PW_ROPE_* */
+  int32_t reserved;
+  double scale;               /* context extension, >= 1 */
+  double original_positions;  /* YARN, BANDS: the length trained on */
+  double fast, slow;          /* YARN, BANDS: turns over that length (32 and 1; 4 and 1) */
+} pw_rope_scaling;
+int pw_rope_turns(int rotary_dim, double base, const pw_rope_scaling* scaling, int64_t* h_turns, float* h_factor);
+
+/* Rotates queries and keys and appends keys and values to the cache.
+ *  q [tokens][heads][head_dim] -> q_out (may be q); both NULL: keys only
+ *  k, v [tokens][kv_heads][head_dim] -> k_cache, v_cache [num_pages]
+ *    [page_size][kv_heads][head_dim] in any order of the three outer
+ *    dimensions (strides); all four NULL: queries only
+ *  The first rotary_dim values of a head turn by pairs: (2i, 2i+1) when
+ *  interleaved, (i, i + rotary_dim/2) otherwise; the others are copied.
+ *  turns: DEVICE array of pw_rope_turns; positions: int32 [tokens] or NULL
+ *  (the position in the cache). */
+typedef struct pw_rope_args {
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* turns;
+  const int32_t* positions;
+  const int32_t* page_table;   /* [batch][pages_per_seq], rows page_table_stride apart */
+  const int32_t* q_offsets;    /* [batch + 1] */
+  const int32_t* kv_lens;      /* [batch] */
+  int32_t* status;
+  int64_t q_stride_token, q_stride_head, q_out_stride_token, q_out_stride_head;
+  int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+  int64_t k_cache_stride_page, k_cache_stride_token, k_cache_stride_head;
+  int64_t v_cache_stride_page, v_cache_stride_token, v_cache_stride_head;
+  int64_t page_table_stride;
+  int32_t tokens, batch, heads, kv_heads, head_dim, rotary_dim;
+  int32_t page_size, num_pages, pages_per_seq;
+  int32_t dtype;
+  int32_t interleaved;
+  float factor;
+} pw_rope_args;
+int pw_rope_append(const pw_rope_args* args, void* stream);
+
+/* out = softmax(scale * q k^T + mask) v over each sequence's keys, query head
+ * h with key/value head h / (heads/kv_heads).
+ *  q, out [tokens][heads][head_dim]; k_cache, v_cache as above; every head's
+ *    row 16-byte aligned (address and strides); head_dim 64 or 128
+ *  lse fp32 [tokens][heads] or NULL: the logarithm of the softmax's sum
+ *  causal 1: a token sees the keys up to its own position, with window > 0
+ *    the last `window` of them only (pages before them may be gone); causal 0:
+ *    all kv_lens[b] keys (a chunk that is not causal, or an encoder's states)
+ *  A row that sees no key is 0 with lse -inf.  What lies in the cache outside
+ *  the keys that the call's tokens see may be anything, NaN included.  A NaN
+ *  or infinity in a visible value may reach other rows of the same sequence
+ *  and call.
+ *  max_q_len, max_kv_len: upper bounds of the lengths; they choose the
+ *    kernel and the grid (a bound that is too low costs time only).
+ * Workspace: pw_paged_attention_workspace() bytes, 256-byte aligned, ZEROED
+ * before its first use; every call leaves it ready for the next.  Calls that
+ * overlap on the GPU need a workspace each. */
+typedef struct pw_attn_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  const int32_t* q_offsets;
+  const int32_t* kv_lens;
+  int32_t* status;
+  int64_t q_stride_token, q_stride_head, out_stride_token, out_stride_head;
+  int64_t k_stride_page, k_stride_token, k_stride_head;
+  int64_t v_stride_page, v_stride_token, v_stride_head;
+  int64_t page_table_stride;
+  int32_t tokens, batch, heads, kv_heads, head_dim;
+  int32_t page_size, num_pages, pages_per_seq;
+  int32_t max_q_len, max_kv_len;
+  int32_t dtype;
+  int32_t causal, window;
+  float scale;
+} pw_attn_args;
+size_t pw_paged_attention_workspace(int tokens, int batch, int heads, int kv_heads, int head_dim);
+int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test exports: they run the same device dequant code as the fused layer.     */
 /* ------------------------------------------------------------------------ */
 
