@@ -6,6 +6,7 @@
 // The inner sum of a 128-column group runs on the tensor cores, the outer one
 // in 32-bit registers.
 #include "ops_common.cuh"
+#include "umma.cuh"
 
 namespace {
 
@@ -18,6 +19,8 @@ struct LinearParams {
   int64_t lda, ldb, ldy, sa_stride, sb_stride;
   int M, N, K, KB;
   int32_t* status;
+  uint64_t wait_ns;
+  bool wide_y;      // rows of y take 16-byte stores
 };
 
 constexpr int kRows = 16;    // weight rows of a CTA: the m16 side of the warp MMA
@@ -101,11 +104,243 @@ int launch_stream(const LinearParams& p, cudaStream_t s) {
   return PW_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: 128 tokens x kN weight rows a tile on the tcgen05 tensor cores.
+// The MMAs of one 128-column group write a fresh accumulator in Tensor Memory;
+// eight warps (four for kN 128) read it, multiply by the group's scales and add
+// to sums in registers, while the next group's MMAs fill the other
+// accumulator.  A thread owns one token and 128 weight rows, that is one scale
+// product per group.  Persistent: one CTA per SM walks the tiles.
+// ---------------------------------------------------------------------------
+constexpr int kTileM = 128;
+constexpr int kTmaBoxBytes = 128;   // one group of columns: a swizzled row
+
+template <int kN>
+struct Tile {
+  static constexpr int kStages = kN == 256 ? 4 : 6;
+  static constexpr int kSumWarps = 4 * (kN / 128);
+  static constexpr int kThreads = 32 * (kSumWarps + 2);
+  static constexpr int kStageBytes = (kTileM + kN) * kTmaBoxBytes;
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+};
+
+template <int kN>
+struct alignas(8) TileShared {
+  uint64_t full[Tile<kN>::kStages], empty[Tile<kN>::kStages], done[2], read[2];
+  uint32_t tmem;
+  int dead;   // a wait ran out: everybody leaves
+};
+
+// Bounded wait; false once any wait of the CTA has run out.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, const LinearParams& p) {
+  const uint32_t b = pw::smem_u32(bar);
+  if (pw::mbar_try_wait_hint(b, parity, 1000)) return true;
+  const uint64_t t0 = pw::global_ns();
+  while (!pw::mbar_try_wait_hint(b, parity, 1000)) {
+    if (*reinterpret_cast<volatile int*>(dead)) return false;
+    if (pw::global_ns() - t0 > p.wait_ns) {
+      *reinterpret_cast<volatile int*>(dead) = 1;
+      pw::report_status(p.status, PW_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Tiles in strips of 16 token tiles, so that the CTAs that run at the same
+// time share both operands through L2.
+__device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int& mt, int& nt) {
+  const int per_strip = 16 * tiles_n, strip = tile / per_strip, r = tile - strip * per_strip;
+  const int height = min(16, tiles_m - strip * 16);
+  nt = r / height;
+  mt = strip * 16 + r - nt * height;
+}
+
+template <typename T, int kN>
+__global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
+    linear_tile_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_b) {
+  using C = Tile<kN>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ TileShared<kN> sh;
+  const uint32_t stages = (pw::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles_m = (p.M + kTileM - 1) / kTileM, tiles_n = (p.N + kN - 1) / kN, tiles = tiles_m * tiles_n;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      pw::mbar_init(pw::smem_u32(&sh.full[i]), 1);
+      pw::mbar_init(pw::smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      pw::mbar_init(pw::smem_u32(&sh.done[i]), 1);
+      pw::mbar_init(pw::smem_u32(&sh.read[i]), C::kSumWarps);
+    }
+    sh.dead = 0;
+    pw::mbar_init_fence();
+  }
+  if (warp == C::kSumWarps) {
+    pw::tmem_alloc(pw::smem_u32(&sh.tmem), 2 * kN);
+    pw::tmem_relinquish();
+  }
+  pw::tc_fence_before();
+  __syncthreads();
+  pw::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == C::kSumWarps) {
+    if (lane == 0) {   // copies
+      pw::prefetch_tmap(&map_a);
+      pw::prefetch_tmap(&map_b);
+      uint32_t x = 0;   // groups started
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        int mt, nt;
+        tile_at(tile, tiles_m, tiles_n, mt, nt);
+        for (int kb = 0; kb < p.KB; ++kb, ++x) {
+          const uint32_t s = x % C::kStages;
+          if (x >= C::kStages && !wait(&sh.empty[s], (x / C::kStages + 1) & 1u, &sh.dead, p)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = pw::smem_u32(&sh.full[s]), dst = stages + s * C::kStageBytes;
+          pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
+          pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, mt * kTileM, bar);
+          pw::tma_load_2d(dst + kTileM * kTmaBoxBytes, &map_b, kb * pw::kGroup, nt * kN, bar);
+        }
+      }
+      // no copy may be in flight when the CTA leaves
+      if (!ok)
+        for (uint32_t i = x > C::kStages ? x - C::kStages : 0; i < x; ++i)
+          pw::mbar_wait(pw::smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1u, p.wait_ns);
+    }
+  } else if (warp == C::kSumWarps + 1) {
+    if (lane == 0) {   // matrix instructions
+      constexpr uint32_t kIdesc = pw::idesc_f32(kTileM, kN, false, false);
+      uint32_t x = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        for (int kb = 0; kb < p.KB; ++kb, ++x) {
+          const uint32_t s = x % C::kStages, buf = x & 1u;
+          if ((x >= 2 && !wait(&sh.read[buf], ((x >> 1) + 1) & 1u, &sh.dead, p)) ||
+              !wait(&sh.full[s], (x / C::kStages) & 1u, &sh.dead, p)) {
+            ok = false;
+            break;
+          }
+          pw::tc_fence_after();
+          const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
+          const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + kTileM * kTmaBoxBytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)   // 32 columns a step: 2 units of 16 bytes
+            pw::tc_mma_f8(tmem + buf * kN, a + 2 * i, b + 2 * i, kIdesc, i);
+          pw::tc_commit(pw::smem_u32(&sh.empty[s]));
+          pw::tc_commit(pw::smem_u32(&sh.done[buf]));
+        }
+      }
+      if (!ok)   // the accumulators go back only when nothing writes them
+        for (uint32_t i = x > 2 ? x - 2 : 0; i < x; ++i)
+          pw::mbar_wait(pw::smem_u32(&sh.done[i & 1u]), (i >> 1) & 1u, p.wait_ns);
+    }
+  } else {   // sums
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    uint32_t x = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      int mt, nt;
+      tile_at(tile, tiles_m, tiles_n, mt, nt);
+      const int m = mt * kTileM + 32 * quarter + lane, n0 = nt * kN + 128 * half;
+      const bool live = m < p.M;
+      const float* sa = p.sa + static_cast<int64_t>(live ? m : 0) * p.sa_stride;
+      const float* sb = p.sb + static_cast<int64_t>(min(n0, p.N - 1) / pw::kGroup) * p.sb_stride;
+      uint64_t sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      float next = __ldg(sa) * __ldg(sb);
+      for (int kb = 0; kb < p.KB; ++kb, ++x) {
+        const uint32_t buf = x & 1u;
+        const float scale = next;
+        if (kb + 1 < p.KB) next = __ldg(sa + kb + 1) * __ldg(sb + kb + 1);
+        const uint64_t s2 = pw::pack_f32x2(__float_as_uint(scale), __float_as_uint(scale));
+        // the lanes leave together: one may see the barrier, another the failure
+        if (!__all_sync(0xFFFFFFFFu, wait(&sh.done[buf], (x >> 1) & 1u, &sh.dead, p))) {
+          ok = false;
+          break;
+        }
+        pw::tc_fence_after();
+        const uint32_t src = tmem + lanes + buf * kN + 128u * half;
+        uint32_t v[2][16];
+        pw::tmem_ld_x16(src, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          pw::tmem_ld_wait();
+          if (c < 7) pw::tmem_ld_x16(src + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sum[8 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2, sum[8 * c + i]);
+        }
+        pw::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pw::mbar_arrive(pw::smem_u32(&sh.read[buf]));
+      }
+      if (!ok || !live) continue;
+      T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pw::unpack_f32x2(sum[4 * i + j], f[2 * j], f[2 * j + 1]);
+        if (p.wide_y && n0 + 8 * i + 8 <= p.N) {
+          *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pw::pack2<T>(f[0], f[1]), pw::pack2<T>(f[2], f[3]),
+                                                            pw::pack2<T>(f[4], f[5]), pw::pack2<T>(f[6], f[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (n0 + 8 * i + j < p.N) y[8 * i + j] = pw::from_float<T>(f[j]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  pw::tc_fence_before();
+  __syncthreads();
+  pw::tc_fence_after();
+  if (warp == C::kSumWarps) pw::tmem_dealloc(tmem, 2 * kN);
+}
+
+template <typename T, int kN>
+int launch_tile(const LinearParams& p, cudaStream_t s) {
+  using C = Tile<kN>;
+  constexpr int kDevs = 64;
+  static bool attr_done[kDevs] = {};
+  int dev = 0;
+  PW_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= kDevs || !attr_done[dev]) {
+    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    if (dev < kDevs) attr_done[dev] = true;
+  }
+  const int sms = pw::sm_count();
+  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
+  CUtensorMap ma, mb;
+  const uint64_t da[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M)};
+  const uint64_t db[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N)};
+  const uint64_t sta[1] = {static_cast<uint64_t>(p.lda)}, stb[1] = {static_cast<uint64_t>(p.ldb)};
+  const uint32_t ba[2] = {kTmaBoxBytes, kTileM}, bb[2] = {kTmaBoxBytes, kN};
+  if (int e = pw::encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, da, sta, ba)) return e;
+  if (int e = pw::encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, bb)) return e;
+  const long long tiles = static_cast<long long>((p.M + kTileM - 1) / kTileM) * ((p.N + kN - 1) / kN);
+  linear_tile_kernel<T, kN><<<static_cast<unsigned>(tiles < sms ? tiles : sms), C::kThreads, C::kSmem, s>>>(p, ma, mb);
+  PW_CUDA_TRY(cudaGetLastError());
+  return PW_OK;
+}
+
 template <typename T>
 int launch(const LinearParams& p, cudaStream_t s) {
   if (p.M <= 8) return launch_stream<T, 1>(p, s);
   if (p.M <= 16) return launch_stream<T, 2>(p, s);
-  return launch_stream<T, 4>(p, s);
+  if (p.M <= 64) return launch_stream<T, 4>(p, s);
+  // wide tiles once they fill the SMs: half the weight reads per product
+  const long long wide = static_cast<long long>((p.M + kTileM - 1) / kTileM) * ((p.N + 255) / 256);
+  return wide >= pw::sm_count() ? launch_tile<T, 256>(p, s) : launch_tile<T, 128>(p, s);
 }
 
 }  // namespace
@@ -143,6 +378,8 @@ extern "C" int pw_fp8_linear(const uint8_t* d_a, int64_t lda, const float* d_a_s
   p.K = K;
   p.KB = kb;
   p.status = d_status;
+  p.wait_ns = 2000000000ull;
+  p.wide_y = pw::aligned(d_y, 16) && ldy % 8 == 0;
   cudaStream_t s = pw::as_stream(stream);
   return dtype == PW_DTYPE_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
 }

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -155,9 +156,9 @@ def lib() -> ctypes.CDLL:
             "pw_quantize_fp8": (I32, [P, I64, I64, I32, I32, I32, P, I64, P, I64, P]),
             "pw_fp8_linear": (I32, [P, I64, P, I64, P, I64, P, I64, I32, I32, I32, I32, P, I64, P, P]),
             "pw_rope_turns": (I32, [I32, F64, ctypes.POINTER(pw_rope_scaling), P, ctypes.POINTER(F32)]),
-            "pw_rope_append": (I32, [ctypes.POINTER(pw_rope_args), P]),
+            "pw_rope_append": (I32, [P, P]),
             "pw_paged_attention_workspace": (SZ, [I32, I32, I32, I32, I32]),
-            "pw_paged_attention": (I32, [ctypes.POINTER(pw_attn_args), P, SZ, P]),
+            "pw_paged_attention": (I32, [P, P, SZ, P]),
             "pw_unpack_indices": (I32, [P, I32, I32, P, P]),
             "pw_apl_linear": (I32, [P, I32, P, I32, P, P]),
         }
@@ -175,16 +176,16 @@ def _check(rc: int) -> int:
     return rc
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:   # the raw handle: a Stream object per call costs as much as a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> None:
@@ -422,9 +423,14 @@ def pw_apl_linear(t, block: int, x: torch.Tensor, out: torch.Tensor, stream=None
 
 
 # ---------------------------------------------------------------------------
-# The attention half of a decoder layer
+# The attention half of a decoder layer.  A single token's kernels run for a
+# few microseconds, so these calls keep to plain integers and tuples: pointers
+# are passed as numbers, the argument structures are packed in one go.
 # ---------------------------------------------------------------------------
 _DTYPE = {torch.float16: PW_DTYPE_F16, torch.bfloat16: PW_DTYPE_BF16}
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
 
 
 def _dtype16(t: torch.Tensor, name: str) -> int:
@@ -434,18 +440,33 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _matrix(t: torch.Tensor, shape, dtypes, name: str) -> int:
-    """Checks a CUDA matrix whose rows are contiguous; returns its row stride."""
-    if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != tuple(shape) or (
-            t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: need a CUDA matrix {tuple(shape)} of {dtypes[0]} with contiguous rows, got "
-                         f"{tuple(t.shape)} of {t.dtype} with strides {t.stride()} on {t.device}")
+def _refuse(t: torch.Tensor, shape, dtypes, name: str, rows: str):
+    raise ValueError(f"{name}: need a CUDA tensor {tuple(shape)} of {dtypes[0]} with {rows}, got {tuple(t.shape)} of "
+                     f"{t.dtype} with strides {t.stride()} on {t.device}")
+
+
+def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, dtypes, name: str):
+    """(pointer, row stride) of a CUDA matrix whose rows are contiguous; (0, 0)
+    for None."""
+    if t is None:
+        return 0, 0
+    st = t.stride()
+    if t.dtype not in dtypes or not t.is_cuda or t.shape != (rows, cols) or (st[1] != 1 and cols > 1):
+        _refuse(t, (rows, cols), dtypes, name, "contiguous rows")
     # the stride of a single row says nothing
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.data_ptr(), st[0] if rows > 1 or st[0] > cols else cols
 
 
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-_F32 = (torch.float32,)
+def _vector(t: torch.Tensor, n: int, dtypes, name: str) -> int:
+    if t.dtype not in dtypes or not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+        _refuse(t, (n,), dtypes, name, "contiguous values")
+    return t.data_ptr()
+
+
+def _status(t: torch.Tensor) -> int:
+    if t.dtype is not torch.int32 or not t.is_cuda or t.numel() < 1:
+        _refuse(t, (1,), _I32, "status", "one value")
+    return t.data_ptr()
 
 
 def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -455,17 +476,17 @@ def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: 
     x's type and/or `q` (e4m3) with `scale` (fp32, a scale per 128 columns);
     `residual_out` receives r."""
     dt = _dtype16(x, "x")
-    shape, same = x.shape, (x.dtype,)
-    xs = _matrix(x, shape, same, "x")
-    if not weight.is_cuda or weight.dtype != x.dtype or tuple(weight.shape) != (shape[1],) or not weight.is_contiguous():
-        raise ValueError(f"weight: need a contiguous CUDA tensor ({shape[1]},) of {x.dtype}")
-    rs = 0 if residual is None else _matrix(residual, shape, same, "residual")
-    ros = 0 if residual_out is None else _matrix(residual_out, shape, same, "residual_out")
-    ys = 0 if y is None else _matrix(y, shape, same, "y")
-    qs = 0 if q is None else _matrix(q, shape, _CODES, "q")
-    ss = 0 if scale is None else _matrix(scale, (shape[0], -(-shape[1] // 128)), _F32, "scale")
-    _check(lib().pw_add_rmsnorm(_ptr(x), xs, _ptr(residual), rs, _ptr(weight), shape[0], shape[1], eps, dt,
-                                _ptr(residual_out), ros, _ptr(y), ys, _ptr(q), qs, _ptr(scale), ss, _stream(stream)))
+    rows, cols = x.shape
+    same = (x.dtype,)
+    xp, xs = _matrix(x, rows, cols, same, "x")
+    wp = _vector(weight, cols, same, "weight")
+    rp, rs = _matrix(residual, rows, cols, same, "residual")
+    rop, ros = _matrix(residual_out, rows, cols, same, "residual_out")
+    yp, ys = _matrix(y, rows, cols, same, "y")
+    qp, qs = _matrix(q, rows, cols, _CODES, "q")
+    sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale")
+    _check(lib().pw_add_rmsnorm(xp, xs, rp, rs, wp, rows, cols, eps, dt, rop, ros, yp, ys, qp, qs, sp, ss,
+                                _stream(stream)))
 
 
 def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
@@ -473,30 +494,34 @@ def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block
     128 columns of one row (block_rows 1) or of 128 rows (block_rows 128)."""
     dt = _dtype16(x, "x")
     rows, cols = x.shape
-    xs, qs = _matrix(x, x.shape, (x.dtype,), "x"), _matrix(q, x.shape, _CODES, "q")
     if block_rows < 1:
         raise ValueError(f"block_rows: {block_rows}")
-    ss = _matrix(scale, (-(-rows // block_rows), -(-cols // 128)), _F32, "scale")
-    _check(lib().pw_quantize_fp8(_ptr(x), xs, rows, cols, dt, block_rows, _ptr(q), qs, _ptr(scale), ss,
-                                 _stream(stream)))
+    xp, xs = _matrix(x, rows, cols, (x.dtype,), "x")
+    qp, qs = _matrix(q, rows, cols, _CODES, "q")
+    sp, ss = _matrix(scale, -(-rows // block_rows), -(-cols // 128), _F32, "scale")
+    _check(lib().pw_quantize_fp8(xp, xs, rows, cols, dt, block_rows, qp, qs, sp, ss, _stream(stream)))
 
 
 def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, y: torch.Tensor,
                   status: torch.Tensor, stream=None) -> None:
     """y [M][N] = a [M][K] b [N][K]^T of e4m3 codes with their scales:
     a_scale [M][ceil(K/128)], b_scale [ceil(N/128)][ceil(K/128)]."""
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError(f"fp8_linear: a {tuple(a.shape)}, b {tuple(b.shape)}")
     dt = _dtype16(y, "y")
-    (M, K), N = a.shape, b.shape[0]
+    M, K = a.shape
+    N = b.shape[0]
     kb = -(-K // 128)
-    lda, ldb, ldy = _matrix(a, a.shape, _CODES, "a"), _matrix(b, b.shape, _CODES, "b"), _matrix(y, (M, N), (y.dtype,), "y")
+    ap, lda = _matrix(a, M, K, _CODES, "a")
+    bp, ldb = _matrix(b, N, K, _CODES, "b")
+    yp, ldy = _matrix(y, M, N, (y.dtype,), "y")
+    sap, sa = _matrix(a_scale, M, kb, _F32, "a_scale")
+    sbp, sb = _matrix(b_scale, -(-N // 128), kb, _F32, "b_scale")
     # a single row may have any stride: the row's own alignment is what counts
-    lda, ldb = (lda + 15) // 16 * 16 if M == 1 else lda, (ldb + 15) // 16 * 16 if N == 1 else ldb
-    sa, sb = _matrix(a_scale, (M, kb), _F32, "a_scale"), _matrix(b_scale, (-(-N // 128), kb), _F32, "b_scale")
-    _dev(status, torch.int32, "status")
-    _check(lib().pw_fp8_linear(_ptr(a), lda, _ptr(a_scale), sa, _ptr(b), ldb, _ptr(b_scale), sb, M, N, K, dt, _ptr(y),
-                               ldy, _ptr(status), _stream(stream)))
+    if M == 1:
+        lda = (lda + 15) // 16 * 16
+    if N == 1:
+        ldb = (ldb + 15) // 16 * 16
+    _check(lib().pw_fp8_linear(ap, lda, sap, sa, bp, ldb, sbp, sb, M, N, K, dt, yp, ldy, _status(status),
+                               _stream(stream)))
 
 
 def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_rope_scaling] = None):
@@ -508,28 +533,24 @@ def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_r
     return turns, float(factor.value)
 
 
-def _heads(t: torch.Tensor, shape, dtype, name: str):
-    """Checks a CUDA tensor whose last dimension is contiguous; returns its
-    data pointer and outer strides."""
+def _heads(t: torch.Tensor, shape, dtypes, name: str):
+    """(pointer, outer strides) of a CUDA tensor whose last dimension is contiguous."""
     st = t.stride()
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape or (shape[-1] > 1 and st[-1] != 1):
-        raise ValueError(f"{name}: need a CUDA tensor {shape} of {dtype} with a contiguous last dimension, got "
-                         f"{tuple(t.shape)} of {t.dtype} with strides {st} on {t.device}")
-    return (t.data_ptr(), *st[:-1])
+    if t.dtype not in dtypes or not t.is_cuda or t.shape != shape or (st[-1] != 1 and shape[-1] > 1):
+        _refuse(t, shape, dtypes, name, "a contiguous last dimension")
+    return t.data_ptr(), st
 
 
-def _batch(args, page_table, q_offsets, kv_lens, k_cache, status) -> None:
-    """Fills the page-table fields that the rope and attention calls share."""
-    for t, name in ((q_offsets, "q_offsets"), (kv_lens, "kv_lens"), (status, "status")):
-        _dev(t, torch.int32, name)
+def _sequences(q_offsets: torch.Tensor, kv_lens: torch.Tensor):
+    """(q_offsets, kv_lens, batch)"""
     batch = kv_lens.shape[0]
-    if q_offsets.shape[0] != batch + 1:
-        raise ValueError(f"q_offsets: need {batch + 1} values, got {q_offsets.shape[0]}")
-    args.batch, args.q_offsets, args.kv_lens, args.status = batch, q_offsets.data_ptr(), kv_lens.data_ptr(), status.data_ptr()
-    if page_table is not None:
-        args.page_table_stride = _matrix(page_table, (batch, page_table.shape[1]), (torch.int32,), "page_table")
-        args.page_table, args.pages_per_seq = page_table.data_ptr(), page_table.shape[1]
-        args.num_pages, args.page_size = k_cache.shape[0], k_cache.shape[1]
+    return _vector(q_offsets, batch + 1, _I32, "q_offsets"), _vector(kv_lens, batch, _I32, "kv_lens"), batch
+
+
+# the structures of pw.h, in one piece: pointers, strides, sizes, the float
+_ROPE_ARGS = struct.Struct("@12P15q11if")
+_ATTN_ARGS = struct.Struct("@9P11q13if")
+assert _ROPE_ARGS.size == ctypes.sizeof(pw_rope_args) and _ATTN_ARGS.size == ctypes.sizeof(pw_attn_args)
 
 
 def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -540,39 +561,41 @@ def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
     """Rotates q into q_out [T][heads][D] and k into the cache
     [pages][page_size][kv_heads][D] (any outer strides), and appends v there.
     The rotated part of a head is 2 * len(turns) wide."""
-    a = pw_rope_args()
     x = q if q is not None else k
     if x is None:
         raise ValueError("rope_append: neither q nor k")
-    if (k is None) != (v is None) or (k is None) != (k_cache is None) or (k is None) != (v_cache is None) or (
-            k is None) != (page_table is None):
-        raise ValueError("rope_append: k, v, the caches and the page table come together")
-    a.dtype, a.tokens, a.head_dim = _dtype16(x, "q"), x.shape[0], x.shape[2]
-    _dev(turns, torch.int64, "turns")
-    a.turns, a.rotary_dim = turns.data_ptr(), 2 * turns.shape[0]
+    dt, same = _dtype16(x, "q"), (x.dtype,)
+    T, _, D = x.shape
+    offsets, lens, batch = _sequences(q_offsets, kv_lens)
+    qp = qop = kp = vp = kcp = vcp = table = pos = 0
+    qs = qos = ks = vs = kcs = vcs = (0, 0, 0)
+    heads = kv_heads = ts = pages = page_size = width = 0
     if q is not None:
         if q_out is None:
             raise ValueError("rope_append: q needs q_out")
-        a.heads = q.shape[1]
-        a.q, a.q_stride_token, a.q_stride_head = _heads(q, tuple(q.shape), x.dtype, "q")
-        a.q_out, a.q_out_stride_token, a.q_out_stride_head = _heads(q_out, tuple(q.shape), x.dtype, "q_out")
+        heads = q.shape[1]
+        qp, qs = _heads(q, (T, heads, D), same, "q")
+        qop, qos = _heads(q_out, (T, heads, D), same, "q_out")
     if k is not None:
-        a.kv_heads = k.shape[1]
-        shape, cache = (a.tokens, a.kv_heads, a.head_dim), (k_cache.shape[0], k_cache.shape[1], a.kv_heads, a.head_dim)
-        a.k, a.k_stride_token, a.k_stride_head = _heads(k, shape, x.dtype, "k")
-        a.v, a.v_stride_token, a.v_stride_head = _heads(v, shape, x.dtype, "v")
-        a.k_cache, a.k_cache_stride_page, a.k_cache_stride_token, a.k_cache_stride_head = _heads(
-            k_cache, cache, x.dtype, "k_cache")
-        a.v_cache, a.v_cache_stride_page, a.v_cache_stride_token, a.v_cache_stride_head = _heads(
-            v_cache, cache, x.dtype, "v_cache")
-    _batch(a, page_table, q_offsets, kv_lens, k_cache, status)
+        if v is None or k_cache is None or v_cache is None or page_table is None:
+            raise ValueError("rope_append: k, v, the caches and the page table come together")
+        kv_heads, (pages, page_size) = k.shape[1], k_cache.shape[:2]
+        kp, ks = _heads(k, (T, kv_heads, D), same, "k")
+        vp, vs = _heads(v, (T, kv_heads, D), same, "v")
+        kcp, kcs = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache")
+        vcp, vcs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache")
+        width = page_table.shape[1]
+        table, ts = _matrix(page_table, batch, width, _I32, "page_table")
+    elif v is not None or k_cache is not None or v_cache is not None:
+        raise ValueError("rope_append: k, v, the caches and the page table come together")
+    half = turns.shape[0]
+    tp = _vector(turns, half, (torch.int64,), "turns")
     if positions is not None:
-        _dev(positions, torch.int32, "positions")
-        if positions.shape[0] != a.tokens:
-            raise ValueError(f"positions: need {a.tokens} values, got {positions.shape[0]}")
-        a.positions = positions.data_ptr()
-    a.interleaved, a.factor = int(interleaved), factor
-    _check(lib().pw_rope_append(ctypes.byref(a), _stream(stream)))
+        pos = _vector(positions, T, _I32, "positions")
+    args = _ROPE_ARGS.pack(qp, qop, kp, vp, kcp, vcp, tp, pos, table, offsets, lens, _status(status), qs[0], qs[1],
+                           qos[0], qos[1], ks[0], ks[1], vs[0], vs[1], kcs[0], kcs[1], kcs[2], vcs[0], vcs[1], vcs[2],
+                           ts, T, batch, heads, kv_heads, D, 2 * half, page_size, pages, width, dt, interleaved, factor)
+    _check(lib().pw_rope_append(args, _stream(stream)))
 
 
 def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -587,22 +610,24 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     keys in the paged cache [pages][page_size][kv_heads][D].  `ws` must be
     zeroed before its first use.  max_q_len / max_kv_len: bounds of the lengths
     (0: the batch's tokens, and what the page table holds)."""
-    a = pw_attn_args()
-    a.dtype = _dtype16(q, "q")
-    a.tokens, a.heads, a.head_dim = q.shape
-    a.kv_heads = k_cache.shape[2]
-    cache = (k_cache.shape[0], k_cache.shape[1], a.kv_heads, a.head_dim)
-    a.q, a.q_stride_token, a.q_stride_head = _heads(q, tuple(q.shape), q.dtype, "q")
-    a.out, a.out_stride_token, a.out_stride_head = _heads(out, tuple(q.shape), q.dtype, "out")
-    a.k_cache, a.k_stride_page, a.k_stride_token, a.k_stride_head = _heads(k_cache, cache, q.dtype, "k_cache")
-    a.v_cache, a.v_stride_page, a.v_stride_token, a.v_stride_head = _heads(v_cache, cache, q.dtype, "v_cache")
-    _batch(a, page_table, q_offsets, kv_lens, k_cache, status)
+    dt, same = _dtype16(q, "q"), (q.dtype,)
+    T, heads, D = q.shape
+    pages, page_size, kv_heads, _ = k_cache.shape
+    offsets, lens, batch = _sequences(q_offsets, kv_lens)
+    qp, qs = _heads(q, (T, heads, D), same, "q")
+    op, os_ = _heads(out, (T, heads, D), same, "out")
+    kp, ks = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache")
+    vp, vs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache")
+    width = page_table.shape[1]
+    table, ts = _matrix(page_table, batch, width, _I32, "page_table")
+    lp = 0
     if lse is not None:
-        _dev(lse, torch.float32, "lse")
-        if tuple(lse.shape) != (a.tokens, a.heads):
-            raise ValueError(f"lse: need shape ({a.tokens}, {a.heads}), got {tuple(lse.shape)}")
-        a.lse = lse.data_ptr()
-    a.max_q_len = max_q_len or a.tokens
-    a.max_kv_len = max_kv_len or a.page_size * a.pages_per_seq
-    a.scale, a.causal, a.window = scale, int(causal), window
-    _check(lib().pw_paged_attention(ctypes.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        lp, ls = _matrix(lse, T, heads, _F32, "lse")
+        if ls != heads:
+            raise ValueError("lse: need a contiguous tensor")
+    if not ws.is_cuda:
+        raise ValueError("ws: need a CUDA tensor")
+    args = _ATTN_ARGS.pack(qp, op, lp, kp, vp, table, offsets, lens, _status(status), qs[0], qs[1], os_[0], os_[1],
+                           ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts, T, batch, heads, kv_heads, D, page_size, pages,
+                           width, max_q_len or T, max_kv_len or page_size * width, dt, causal, window, scale)
+    _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _stream(stream)))
