@@ -172,12 +172,6 @@ struct Shared {
   int last;
 };
 
-// Writes a finished row: `o` unnormalised, m in powers of two.
-__device__ __forceinline__ float inverse_sum(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
-__device__ __forceinline__ float log_sum(float m, float l) {
-  return l > 0.0f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 // End of a CTA's work on a unit: the warps' states are joined, and the rows
 // are written, or left as a partial result whose last piece joins them all.
 template <typename T, int D>
@@ -249,12 +243,12 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
         const int row = g + 8 * i;
         if (row >= rows) continue;
         const int r = c.tile * kTile + row, token = c.s.q0 + r / p.group, h = c.head * p.group + r % p.group;
-        const float inv = inverse_sum(l[i]);
+        const float inv = pw_attn::inverse_sum(l[i]);
         T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
           *reinterpret_cast<uint32_t*>(out + 8 * n + 2 * t) = pw::pack2<T>(w.o[n][2 * i] * inv, w.o[n][2 * i + 1] * inv);
-        if (a.lse && t == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = log_sum(m[i], l[i]);
+        if (a.lse && t == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(m[i], l[i]);
       }
     }
     return;
@@ -310,10 +304,10 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
       o.w += f * v.w;
     }
     const int r = c.tile * kTile + row, token = c.s.q0 + r / p.group, h = c.head * p.group + r % p.group;
-    const float inv = inverse_sum(sum);
+    const float inv = pw_attn::inverse_sum(sum);
     T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head + d;
     *reinterpret_cast<uint2*>(out) = make_uint2(pw::pack2<T>(o.x * inv, o.y * inv), pw::pack2<T>(o.z * inv, o.w * inv));
-    if (a.lse && d == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = log_sum(top, sum);
+    if (a.lse && d == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(top, sum);
   }
   __syncthreads();   // sh.last
 }
@@ -394,6 +388,7 @@ int launch_stream(const Params& p, cudaStream_t s) {
 
 template <typename T>
 int launch(const Params& p, cudaStream_t s) {
+  if (pw_attn::tile_kernel_takes(p)) return pw_attn::launch_tile_kernel(p, s);
   return p.a.head_dim == 64 ? launch_stream<T, 64>(p, s) : launch_stream<T, 128>(p, s);
 }
 
@@ -408,7 +403,9 @@ extern "C" {
 
 size_t pw_paged_attention_workspace(int tokens, int batch, int heads, int kv_heads, int head_dim) {
   if (tokens < 0 || batch < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || !head_dim_ok(head_dim)) return 0;
-  return kCounterBytes + sizeof(float) * 2 * pw_attn::kMaxCtas * static_cast<size_t>(kTile) * (head_dim + 2);
+  const size_t stream = 2 * pw_attn::kMaxCtas * static_cast<size_t>(kTile) * (head_dim + 2);
+  const size_t tile = pw_attn::kMaxCtas * pw_attn::tile_part_floats(head_dim);   // one CTA an SM
+  return kCounterBytes + sizeof(float) * (stream > tile ? stream : tile);
 }
 
 int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, void* stream) {

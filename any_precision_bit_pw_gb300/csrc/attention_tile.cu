@@ -1,0 +1,572 @@
+// Attention of a chunk of new tokens over a paged cache, for many query rows
+// per key/value head: tcgen05 matrix instructions on tiles of 2 x 128 rows by
+// 128 keys (attention.cu holds the formulas and the kernel for few rows).
+//
+// The two halves of a tile take turns: while the tensor cores multiply one
+// half's weights with the values and its queries with the next keys, four
+// warps turn the other half's scores into weights.  A thread owns one row, so
+// maximum and sum need no exchange.  Scores S and outputs O live in Tensor
+// Memory; the weights P overwrite S in 16 bits and feed the second product
+// from there.
+//
+// The running maximum moves only when a row's new maximum exceeds it by 2^8:
+// until then the weights stay below 2^8 and need no common factor, so the
+// output is rescaled a few times per row instead of at every block.
+//
+// Keys and values arrive by TMA, a box per page piece, into 128-byte swizzled
+// rows.  Values outside the visible keys are zeroed in shared memory (a weight
+// of 0 does not hide a NaN).
+#include <numeric>
+
+#include "attn_schedule.cuh"
+#include "umma.cuh"
+
+namespace {
+
+using pw_attn::Cursor;
+using pw_attn::Params;
+
+constexpr int kHalf = 128;             // rows of half a tile: the lanes of Tensor Memory
+constexpr int kTile = 2 * kHalf;
+constexpr int kBlock = 128;            // keys of a block
+constexpr int kSlots = 2;              // blocks of keys, and of values, in shared memory
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
+constexpr int kThreads = 384;
+constexpr float kLazy = 8.0f;          // log2 of what a weight may grow to
+constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
+
+template <int D>
+constexpr int tile_bytes() { return (D / 64) * kHalfRow; }
+template <int D>
+constexpr int smem_bytes() { return (2 + 2 * kSlots) * tile_bytes<D>() + 1024; }
+
+struct alignas(8) Shared {
+  uint64_t q_full[2], k_full[kSlots], k_empty[kSlots], v_land[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint32_t tmem;
+  int dead;
+  int last;
+};
+
+struct Maps {
+  CUtensorMap k, v;
+  int box;   // rows of a box: a divisor of the page size and of a block
+};
+
+__device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, Shared& sh, const Params& p) {
+  return pw::wait_or_dead(bar, parity, &sh.dead, p.a.status, p.wait_ns);
+}
+__device__ __forceinline__ uint32_t bar(const uint64_t& b) { return pw::smem_u32(&b); }
+
+// Number of 128-row halves with rows.
+__device__ __forceinline__ int halves_of(const Params& p, const Cursor& c) {
+  return c.s.q_len * p.group - c.tile * kTile > kHalf ? 2 : 1;
+}
+
+// Walks the units of the CTA's stretch: f(cursor, first block, end block) with
+// block numbers of the unit.
+template <typename F>
+__device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
+  while (!c.done()) {
+    const int b0 = c.block, n = pw_attn::blocks_of(c.r);
+    const long long room = c.end - c.pos;
+    const int b1 = room < n - b0 ? b0 + static_cast<int>(room) : n;
+    if (!f(c, b0, b1)) return;
+    c.pos += b1 - b0;
+    c.block = b1;
+    if (!c.done()) pw_attn::next_unit<kTile, kBlock>(p, c);
+  }
+}
+
+// ---------------------------------------------------------------- copies (one warp)
+template <int D>
+__device__ __forceinline__ void load_role(const Params& p, const Cursor& start, const Maps& maps, Shared& sh,
+                                          uint32_t k_smem, uint32_t v_smem) {
+  const pw_attn_args& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int boxes = kBlock / maps.box;   // per 64 values
+  uint32_t x = 0;
+  bool ok = true;
+  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+    for (int b = b0; b < b1; ++b, ++x) {
+      const uint32_t slot = x % kSlots, use = x / kSlots;
+      const int key0 = (c.r.b0 + b) * kBlock;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint64_t& empty = kv ? sh.v_empty[slot] : sh.k_empty[slot];
+        const uint64_t& full = kv ? sh.v_land[slot] : sh.k_full[slot];
+        if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty, (use + 1) & 1u, sh, p))) {
+          ok = false;
+          return false;
+        }
+        // which boxes hold visible keys, and their pages
+        int total = 0;
+        for (int i0 = 0; i0 < boxes; i0 += 32) {
+          const int i = i0 + lane, key = key0 + i * maps.box;
+          bool live = i < boxes && key < c.r.hi && key + maps.box > c.r.lo;
+          if (live) {
+            const int page = a.page_table[c.seq * a.page_table_stride + key / a.page_size];
+            live = page >= 0 && page < a.num_pages;
+            if (!live && kv == 0) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+          }
+          total += __popc(__ballot_sync(0xFFFFFFFFu, live));
+        }
+        if (lane == 0) pw::mbar_arrive_expect_tx(bar(full), static_cast<uint32_t>(total * maps.box * 128 * (D / 64)));
+        __syncwarp();
+        const uint32_t dst = (kv ? v_smem : k_smem) + slot * tile_bytes<D>();
+        for (int i = lane; i < boxes; i += 32) {
+          const int key = key0 + i * maps.box;
+          if (!(key < c.r.hi && key + maps.box > c.r.lo)) continue;
+          const int index = key / a.page_size, page = a.page_table[c.seq * a.page_table_stride + index];
+          if (page < 0 || page >= a.num_pages) continue;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            pw::tma_load_4d(dst + h * kHalfRow + i * maps.box * 128, kv ? &maps.v : &maps.k, 64 * h,
+                            key - index * a.page_size, c.head, page, bar(full));
+        }
+      }
+    }
+    return true;
+  });
+  if (!ok && lane == 0)   // no copy may be in flight when the CTA leaves
+    for (uint32_t i = x > kSlots ? x - kSlots : 0; i <= x; ++i) {
+      if (i < x) pw::mbar_wait(bar(sh.v_land[i % kSlots]), (i / kSlots) & 1u, p.wait_ns);
+      // block x may have its keys under way already
+      pw::mbar_wait(bar(sh.k_full[i % kSlots]), (i / kSlots) & 1u, i < x ? p.wait_ns : p.wait_ns / 4);
+    }
+}
+
+// ---------------------------------------------------------------- values outside the visible keys (one warp)
+template <int D>
+__device__ __forceinline__ void zero_role(const Params& p, const Cursor& start, Shared& sh, unsigned char* v_smem) {
+  const int lane = threadIdx.x & 31;
+  uint32_t x = 0;
+  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+    for (int b = b0; b < b1; ++b, ++x) {
+      const uint32_t slot = x % kSlots;
+      if (!__all_sync(0xFFFFFFFFu, wait(&sh.v_land[slot], (x / kSlots) & 1u, sh, p))) return false;
+      const int key0 = (c.r.b0 + b) * kBlock;
+      if (c.r.lo > key0 || c.r.hi < key0 + kBlock) {
+        const int lo = max(0, c.r.lo - key0), hi = max(lo, min(kBlock, c.r.hi - key0));   // rows to keep
+        for (int i = lane; i < kBlock * 8; i += 32) {
+          const int row = i >> 3;
+          if (row >= lo && row < hi) continue;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<uint4*>(v_smem + slot * tile_bytes<D>() + h * kHalfRow + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        pw::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) pw::mbar_arrive(bar(sh.v_full[slot]));
+    }
+    return true;
+  });
+}
+
+// ---------------------------------------------------------------- matrix instructions (one thread)
+template <int D, bool kBf16>
+__device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, Shared& sh, uint32_t tmem,
+                                         uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+  constexpr uint32_t kScores = pw::idesc_f32(kHalf, kBlock, kBf16, false);
+  constexpr uint32_t kValues = pw::idesc_f32(kHalf, D, kBf16, true);
+  uint32_t x = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+  bool ok = true;
+  auto scores = [&](int h, uint32_t slot) {   // S_h = Q_h K^T
+    const uint64_t q = pw::sdesc_kmajor_sw128(q_smem + h * tile_bytes<D>());
+    const uint64_t k = pw::sdesc_kmajor_sw128(k_smem + slot * tile_bytes<D>());
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint64_t at = (i / 4) * (kHalfRow >> 4) + (i % 4) * 2;
+      pw::tc_mma_f16(tmem + h * kBlock, q + at, k + at, kScores, i);
+    }
+    pw::tc_commit(bar(sh.s_full[h]));
+  };
+  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+    const int halves = halves_of(p, c);
+    for (int b = b0; b < b1; ++b, ++x) {
+      const uint32_t slot = x % kSlots;
+      if (b == b0) {
+        if (!wait(&sh.k_full[slot], (x / kSlots) & 1u, sh, p)) return ok = false;
+        for (int h = 0; h < halves; ++h) {
+          if (!wait(&sh.q_full[h], n_q[h] & 1u, sh, p)) return ok = false;
+          ++n_q[h];
+          pw::tc_fence_after();
+          scores(h, slot);
+        }
+        pw::tc_commit(bar(sh.k_empty[slot]));
+      }
+      const uint32_t next = (x + 1) % kSlots;
+      if (b + 1 < b1 && !wait(&sh.k_full[next], ((x + 1) / kSlots) & 1u, sh, p)) return ok = false;
+      if (!wait(&sh.v_full[slot], (x / kSlots) & 1u, sh, p)) return ok = false;
+      for (int h = 0; h < halves; ++h) {
+        if (!wait(&sh.p_full[h], n_p[h] & 1u, sh, p)) return ok = false;
+        ++n_p[h];
+        pw::tc_fence_after();
+        const uint64_t v = pw::sdesc_nmajor_sw128(v_smem + slot * tile_bytes<D>(), kHalfRow);
+#pragma unroll
+        for (int i = 0; i < kBlock / 16; ++i)   // O_h += P_h V
+          pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues,
+                        b > b0 || i > 0);
+        pw::tc_commit(bar(sh.o_done[h]));
+        if (h + 1 == halves) pw::tc_commit(bar(sh.v_empty[slot]));
+        if (b + 1 < b1) {
+          scores(h, next);
+          if (h + 1 == halves) pw::tc_commit(bar(sh.k_empty[next]));
+        }
+      }
+    }
+    return true;
+  });
+  if (!ok)   // Tensor Memory goes back only when nothing writes it
+    for (int h = 0; h < 2; ++h)
+      if (n_p[h]) pw::mbar_wait(bar(sh.o_done[h]), (n_p[h] - 1) & 1u, p.wait_ns);
+}
+
+// ---------------------------------------------------------------- softmax (four warps a half)
+template <typename T, int D>
+__device__ __forceinline__ void write_queries(const Params& p, const Cursor& c, int h, int tid, unsigned char* q_smem) {
+  constexpr int kUnits = D / 8;   // 16-byte units of a row
+  const pw_attn_args& a = p.a;
+  const int rows = c.s.q_len * p.group;
+  const int unit = tid % kUnits;
+#pragma unroll 4
+  for (int row = tid / kUnits; row < kHalf; row += kHalf / kUnits) {
+    const int r = c.tile * kTile + h * kHalf + row;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const int token = r / p.group, head = c.head * p.group + r - token * p.group;
+      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (c.s.q0 + token) * a.q_stride_token +
+                                          head * a.q_stride_head + unit * 8);
+    }
+    *reinterpret_cast<uint4*>(q_smem + h * tile_bytes<D>() + (unit >> 3) * kHalfRow + row * 128 +
+                              (((unit & 7) ^ (row & 7)) << 4)) = v;
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void softmax_role(const Params& p, const Cursor& start, long long line, int ctas, Shared& sh,
+                                             uint32_t tmem, unsigned char* q_smem) {
+  const pw_attn_args& a = p.a;
+  const int h = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+  const uint32_t s_tmem = tmem + lanes + h * kBlock, o_tmem = tmem + lanes + 2 * kBlock + h * D;
+  const size_t part_floats = static_cast<size_t>(kTile) * (D + 2);
+  uint32_t blocks = 0;   // of this half so far
+  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+    const int rows = c.s.q_len * p.group, r = c.tile * kTile + tid + h * kHalf;
+    const bool live = r < rows;
+    float m = -INFINITY, l = 0.0f;
+    const bool active = h < halves_of(p, c);
+    if (active) {
+      write_queries<T, D>(p, c, h, tid, q_smem);
+      pw::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) pw::mbar_arrive(bar(sh.q_full[h]));
+      const int pos = c.s.kv_len - c.s.q_len + r / p.group;
+      // the row's visible keys; a row past the end takes all of them and is not written
+      const int hi = !live ? 0x7FFFFFFF : a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
+      const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
+      for (int b = b0; b < b1; ++b, ++blocks) {
+        const int key0 = (c.r.b0 + b) * kBlock;
+        __all_sync(0xFFFFFFFFu, wait(&sh.s_full[h], blocks & 1u, sh, p));
+        pw::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pw::tmem_ld_x32(s_tmem + 32 * i, s[i]);
+        pw::tmem_ld_wait();
+        if (!__all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock)) {
+          const int from = lo - key0, to = hi - key0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * i + j < from || 32 * i + j >= to) s[i][j] = 0xFF800000u;   // -inf
+        }
+        float top4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top4[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) top4[i] = fmaxf(top4[i], __uint_as_float(s[i][j]));
+        }
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        // m follows the maximum in steps of at least 2^8 (and at once from -inf)
+        const bool moves = top > m && !((top - m) * p.scale_log2 <= kLazy);
+        float keep = 1.0f;
+        if (moves) {
+          keep = pw::exp2_fast((m - top) * p.scale_log2);
+          m = top;
+          l *= keep;
+        }
+        if (b > b0 && __any_sync(0xFFFFFFFFu, moves)) {
+          // O has to be complete up to the last block before it is scaled
+          __all_sync(0xFFFFFFFFu, wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p));
+          pw::tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            pw::tmem_ld_x16(o_tmem + 16 * i, o);
+            pw::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+            pw::tmem_st_x16(o_tmem + 16 * i, o);
+          }
+          pw::tmem_st_wait();
+        }
+        const float off = m == -INFINITY ? 0.0f : -m * p.scale_log2;
+        const uint64_t scale2 = pw::pack_f32x2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+        const uint64_t off2 = pw::pack_f32x2(__float_as_uint(off), __float_as_uint(off));
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const uint32_t* src = &s[2 * i + j / 16][2 * (j % 16)];
+            float e0, e1;
+            pw::unpack_f32x2(pw::fma_f32x2(pw::pack_f32x2(src[0], src[1]), scale2, off2), e0, e1);
+            e0 = pw::exp2_fast(e0);
+            e1 = pw::exp2_fast(e1);
+            sum[j & 1] = pw::add_f32x2(sum[j & 1], pw::pack_f32x2(__float_as_uint(e0), __float_as_uint(e1)));
+            w[j] = pw::pack2<T>(e0, e1);
+          }
+          pw::tmem_st_x32(s_tmem + 32 * i, w);
+        }
+        float s0, s1;
+        pw::unpack_f32x2(pw::add_f32x2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        pw::tmem_st_wait();
+        pw::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pw::mbar_arrive(bar(sh.p_full[h]));
+      }
+      __all_sync(0xFFFFFFFFu, wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p));
+      pw::tc_fence_after();
+    }
+    const float m2 = m * p.scale_log2;   // in powers of two
+    const long long begin = c.unit_begin(), unit_end = c.unit_end();
+    const bool whole = b0 == 0 && begin + b1 == unit_end;
+    const int token = c.s.q0 + r / p.group, head = c.head * p.group + r % p.group;
+    T* out = static_cast<T*>(a.out) + token * a.out_stride_token + head * a.out_stride_head;
+    const bool dead = *reinterpret_cast<volatile int*>(&sh.dead) != 0;
+    if (whole) {
+      if (active) {
+        const float inv = pw_attn::inverse_sum(l);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t o[16];
+          pw::tmem_ld_x16(o_tmem + 16 * i, o);
+          pw::tmem_ld_wait();
+          if (live && !dead) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pw::pack2<T>(__uint_as_float(o[8 * j + 2 * k]) * inv, __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + 16 * i + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (live && !dead && a.lse) a.lse[static_cast<int64_t>(token) * a.heads + head] = pw_attn::log_sum(m2, l);
+        pw::tc_fence_before();
+      }
+      return true;
+    }
+    // a piece: [d / 4][row] of four values, so that neighbouring rows are
+    // neighbours in memory; slot 0 when it starts at the stretch's begin
+    const int cta = blockIdx.x;
+    const bool at_start = begin + b0 == line * cta / ctas;
+    float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * part_floats;
+    const int slot_row = h * kHalf + tid;
+    if (active) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t o[16];
+        pw::tmem_ld_x16(o_tmem + 16 * i, o);
+        pw::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(part + ((4 * i + j) * kTile + slot_row) * 4) =
+              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      }
+      part[kTile * D + slot_row] = m2;
+      part[kTile * D + kTile + slot_row] = l;
+      pw::tc_fence_before();
+    }
+    __threadfence();
+    pw::bar_sync(1, 32 * kSoftmaxWarps);
+    const int c0 = pw_attn::cta_of(begin, line, ctas), c1 = pw_attn::cta_of(unit_end - 1, line, ctas);
+    if (threadIdx.x == 0) {
+      const uint32_t n = atomicAdd(p.arrived + c0, 1u);
+      sh.last = n == static_cast<uint32_t>(c1 - c0);
+      if (sh.last) p.arrived[c0] = 0;
+      __threadfence();
+    }
+    pw::bar_sync(1, 32 * kSoftmaxWarps);
+    const bool last = sh.last;
+    pw::bar_sync(1, 32 * kSoftmaxWarps);   // sh.last is free again
+    if (!last || !active || !live || dead) return true;
+    const int first_slot = begin == line * c0 / ctas ? 0 : 1;
+    auto piece = [&](int i) { return p.part + (2 * static_cast<size_t>(i) + (i == c0 ? first_slot : 0)) * part_floats; };
+    float most = -INFINITY, total = 0.0f;
+    for (int i = c0; i <= c1; ++i) most = fmaxf(most, __ldcg(piece(i) + kTile * D + slot_row));
+    const float safe = most == -INFINITY ? 0.0f : most;
+    for (int i = c0; i <= c1; ++i)
+      total += pw::exp2_fast(__ldcg(piece(i) + kTile * D + slot_row) - safe) *
+               __ldcg(piece(i) + kTile * D + kTile + slot_row);
+    const float inv = pw_attn::inverse_sum(total);
+    for (int d = 0; d < D / 8; ++d) {
+      float o[8] = {};
+      for (int i = c0; i <= c1; ++i) {
+        const float f = pw::exp2_fast(__ldcg(piece(i) + kTile * D + slot_row) - safe);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i) + ((2 * d + j) * kTile + slot_row) * 4));
+          o[4 * j] += f * v.x;
+          o[4 * j + 1] += f * v.y;
+          o[4 * j + 2] += f * v.z;
+          o[4 * j + 3] += f * v.w;
+        }
+      }
+      *reinterpret_cast<uint4*>(out + 8 * d) =
+          make_uint4(pw::pack2<T>(o[0] * inv, o[1] * inv), pw::pack2<T>(o[2] * inv, o[3] * inv),
+                     pw::pack2<T>(o[4] * inv, o[5] * inv), pw::pack2<T>(o[6] * inv, o[7] * inv));
+    }
+    if (a.lse) a.lse[static_cast<int64_t>(token) * a.heads + head] = pw_attn::log_sum(most, total);
+    return true;
+  });
+}
+
+template <typename T, int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Shared sh;
+  unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Cursor c;
+  long long line;
+  int ctas = gridDim.x;
+  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, ctas, c, line)) return;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      pw::mbar_init(bar(sh.k_full[i]), 1);
+      pw::mbar_init(bar(sh.k_empty[i]), 1);
+      pw::mbar_init(bar(sh.v_land[i]), 1);
+      pw::mbar_init(bar(sh.v_full[i]), 1);
+      pw::mbar_init(bar(sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      pw::mbar_init(bar(sh.q_full[i]), 4);
+      pw::mbar_init(bar(sh.s_full[i]), 1);
+      pw::mbar_init(bar(sh.p_full[i]), 4);
+      pw::mbar_init(bar(sh.o_done[i]), 1);
+    }
+    sh.dead = 0;
+    pw::mbar_init_fence();
+  }
+  if (warp == kMmaWarp) {
+    pw::tmem_alloc(pw::smem_u32(&sh.tmem), 512);
+    pw::tmem_relinquish();
+  }
+  pw::tc_fence_before();
+  __syncthreads();
+  pw::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  unsigned char* q_smem = smem;
+  unsigned char* k_smem = smem + 2 * tile_bytes<D>();
+  unsigned char* v_smem = k_smem + kSlots * tile_bytes<D>();
+  // Registers move from the third warpgroup to the softmax warps: 256 threads
+  // x 208 and 128 x 88 are the launch's 384 x 168.
+  if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
+  if (warp < kSoftmaxWarps) {
+    softmax_role<T, D>(p, c, line, ctas, sh, tmem, q_smem);
+  } else if (warp == kLoadWarp) {
+    load_role<D>(p, c, maps, sh, pw::smem_u32(k_smem), pw::smem_u32(v_smem));
+  } else if (warp == kMmaWarp) {
+    if (lane == 0)
+      mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(q_smem), pw::smem_u32(k_smem), pw::smem_u32(v_smem));
+  } else if (warp == kZeroWarp) {
+    zero_role<D>(p, c, sh, v_smem);
+  }
+  __syncwarp();
+  pw::tc_fence_before();
+  __syncthreads();
+  pw::tc_fence_after();
+  if (warp == kMmaWarp) pw::tmem_dealloc(tmem, 512);
+}
+
+int encode_cache(CUtensorMap* m, const pw_attn_args& a, const void* base, int64_t page, int64_t token, int64_t head,
+                 int box, bool bf16) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(a.head_dim), static_cast<uint64_t>(a.page_size),
+                            static_cast<uint64_t>(a.kv_heads), static_cast<uint64_t>(a.num_pages)};
+  // the stride of a dimension of one is never used, but the map wants a valid one
+  const uint64_t strides[3] = {a.page_size > 1 ? 2ull * token : 256, a.kv_heads > 1 ? 2ull * head : 256,
+                               a.num_pages > 1 ? 2ull * page : 256};
+  const uint32_t bx[4] = {64, static_cast<uint32_t>(box), 1, 1};
+  return pw::encode_tensor_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
+                               strides, bx);
+}
+
+template <typename T, int D, bool kBf16>
+int launch(const Params& p, cudaStream_t s) {
+  constexpr int kDevs = 64;
+  static bool attr_done[kDevs] = {};
+  int dev = 0;
+  PW_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev >= kDevs || !attr_done[dev]) {
+    PW_CUDA_TRY(cudaFuncSetAttribute(attn_tile_kernel<T, D, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     smem_bytes<D>()));
+    if (dev < kDevs) attr_done[dev] = true;
+  }
+  const int sms = pw::sm_count();
+  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
+  const pw_attn_args& a = p.a;
+  Maps maps;
+  maps.box = std::gcd(a.page_size, kBlock);
+  if (int e = encode_cache(&maps.k, a, a.k_cache, a.k_stride_page, a.k_stride_token, a.k_stride_head, maps.box, kBf16))
+    return e;
+  if (int e = encode_cache(&maps.v, a, a.v_cache, a.v_stride_page, a.v_stride_token, a.v_stride_head, maps.box, kBf16))
+    return e;
+  const long long tiles = (static_cast<long long>(a.tokens) * p.group + kTile - 1) / kTile + a.batch;
+  const long long blocks = tiles * a.kv_heads * ((a.max_kv_len + kBlock - 1) / kBlock + 1);
+  long long ctas = sms < pw_attn::kMaxCtas / 2 ? sms : pw_attn::kMaxCtas / 2;
+  if (blocks < ctas) ctas = blocks < 1 ? 1 : blocks;
+  attn_tile_kernel<T, D, kBf16><<<static_cast<unsigned>(ctas), kThreads, smem_bytes<D>(), s>>>(p, maps);
+  PW_CUDA_TRY(cudaGetLastError());
+  return PW_OK;
+}
+
+}  // namespace
+
+namespace pw_attn {
+
+size_t tile_part_floats(int head_dim) { return static_cast<size_t>(kTile) * (head_dim + 2); }
+
+bool tile_kernel_takes(const Params& p) {
+  const pw_attn_args& a = p.a;
+  // More rows per key/value head than two 16-row tiles; a positive scale (the
+  // running maximum is kept on unscaled scores); boxes of whole 8-row swizzle
+  // groups; strides that a tensor map can hold.
+  if (static_cast<long long>(a.max_q_len) * p.group <= 32 || !(a.scale > 0.0f)) return false;
+  if (std::gcd(a.page_size, kBlock) < 8) return false;
+  const int64_t most = 1ll << 38;
+  for (int64_t st : {a.k_stride_page, a.k_stride_token, a.k_stride_head, a.v_stride_page, a.v_stride_token, a.v_stride_head})
+    if (st < 1 || st > most) return false;
+  return true;
+}
+
+int launch_tile_kernel(const Params& p, cudaStream_t s) {
+  if (p.a.dtype == PW_DTYPE_F16)
+    return p.a.head_dim == 64 ? launch<__half, 64, false>(p, s) : launch<__half, 128, false>(p, s);
+  return p.a.head_dim == 64 ? launch<__nv_bfloat16, 64, true>(p, s) : launch<__nv_bfloat16, 128, true>(p, s);
+}
+
+}  // namespace pw_attn

@@ -25,6 +25,18 @@ struct Params {
 
 constexpr int kMaxCtas = 320;   // at most two CTAs on each of 160 SMs
 
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
+// Logarithm of the softmax's sum l * 2^m.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l > 0.0f || l != l ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The tcgen05 kernel (attention_tile.cu): whether it can take the call, the
+// floats of one partial result, and the launch.
+bool tile_kernel_takes(const Params& p);
+size_t tile_part_floats(int head_dim);
+int launch_tile_kernel(const Params& p, cudaStream_t s);
+
 struct Sequence {
   int q0, q_len, kv_len;
 };

@@ -131,20 +131,8 @@ struct alignas(8) TileShared {
   int dead;   // a wait ran out: everybody leaves
 };
 
-// Bounded wait; false once any wait of the CTA has run out.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, const LinearParams& p) {
-  const uint32_t b = pw::smem_u32(bar);
-  if (pw::mbar_try_wait_hint(b, parity, 1000)) return true;
-  const uint64_t t0 = pw::global_ns();
-  while (!pw::mbar_try_wait_hint(b, parity, 1000)) {
-    if (*reinterpret_cast<volatile int*>(dead)) return false;
-    if (pw::global_ns() - t0 > p.wait_ns) {
-      *reinterpret_cast<volatile int*>(dead) = 1;
-      pw::report_status(p.status, PW_ERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
+__device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, int* dead, const LinearParams& p) {
+  return pw::wait_or_dead(bar, parity, dead, p.status, p.wait_ns);
 }
 
 // Tiles in strips of 16 token tiles, so that the CTAs that run at the same

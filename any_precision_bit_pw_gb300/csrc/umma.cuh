@@ -12,6 +12,26 @@
 
 namespace pw {
 
+// ---------------------------------------------------------------- bounded waits
+// Waits for phase `parity`, at most `limit_ns`.  A wait that runs out reports
+// PW_ERR_TIMEOUT and sets the CTA's `dead` word, which ends every other wait of
+// the CTA: the caller stops issuing work, lets its own finish and returns.
+__device__ __forceinline__ bool wait_or_dead(const uint64_t* bar, uint32_t parity, int* dead, int32_t* status,
+                                             uint64_t limit_ns) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait_hint(b, parity, 1000)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait_hint(b, parity, 1000)) {
+    if (*reinterpret_cast<volatile int*>(dead)) return false;
+    if (global_ns() - t0 > limit_ns) {
+      *reinterpret_cast<volatile int*>(dead) = 1;
+      if (status) atomicCAS(status, 0, PW_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- matrix instructions
 // D[tmem] (+)= A[smem] x B[smem]^T, e4m3 operands (K = 32 a step), fp32 accumulate.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -43,6 +63,19 @@ constexpr uint32_t idesc_f32(int M, int N, bool bf16, bool b_mn_major) {
          | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Shared-memory descriptor of an N-major operand (rows of K, 64 values of N to
+// a 128-byte swizzled row): 8-row groups of K are 1024 bytes apart, the next 64
+// values of N `n_stride` bytes.  A step of 16 K advances the address by 2048.
+__device__ __forceinline__ uint64_t sdesc_nmajor_sw128(uint32_t smem_addr, uint32_t n_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(n_stride >> 4) << 16;           // leading byte offset
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;              // stride byte offset
+  d |= static_cast<uint64_t>(1u) << 46;                      // descriptor version
+  d |= static_cast<uint64_t>(2u) << 61;                      // 128-byte swizzle
+  return d;
+}
+
 // ---------------------------------------------------------------- tiled copies (TMA)
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -71,6 +104,10 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&v)[32]) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ---------------------------------------------------------------- packed fp32
