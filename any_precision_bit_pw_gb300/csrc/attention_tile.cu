@@ -14,7 +14,7 @@
 // output is rescaled a few times per row instead of at every block.
 //
 // Keys and values arrive by TMA, a box per page piece, into 128-byte swizzled
-// rows.  Values outside the visible keys are zeroed in shared memory (a weight
+// rows.  Values outside the visible keys are zeros in shared memory (a weight
 // of 0 does not hide a NaN).
 #include <numeric>
 
@@ -29,9 +29,9 @@ using pw_attn::Params;
 constexpr int kHalf = 128;             // rows of half a tile: the lanes of Tensor Memory
 constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;            // keys of a block
-constexpr int kSlots = 2;              // blocks of keys, and of values, in shared memory
+constexpr int kSlots = 5;              // ring of key and value blocks, in turn
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kZeroWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;
 constexpr float kLazy = 8.0f;          // log2 of what a weight may grow to
 constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
@@ -39,10 +39,10 @@ constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
 template <int D>
 constexpr int tile_bytes() { return (D / 64) * kHalfRow; }
 template <int D>
-constexpr int smem_bytes() { return (2 + 2 * kSlots) * tile_bytes<D>() + 1024; }
+constexpr int smem_bytes() { return (2 + kSlots) * tile_bytes<D>() + 1024; }
 
 struct alignas(8) Shared {
-  uint64_t q_full[2], k_full[kSlots], k_empty[kSlots], v_land[kSlots], v_full[kSlots], v_empty[kSlots];
+  uint64_t q_full[2], full[kSlots], empty[kSlots];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint32_t tmem;
   int dead;
@@ -55,23 +55,23 @@ struct Maps {
 };
 
 __device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, Shared& sh, const Params& p) {
-  return pw::wait_or_dead(bar, parity, &sh.dead, p.a.status, p.wait_ns);
+  return pw::warp_wait_or_dead(bar, parity, &sh.dead, p.a.status, p.wait_ns);
 }
 __device__ __forceinline__ uint32_t bar(const uint64_t& b) { return pw::smem_u32(&b); }
 
 // Number of 128-row halves with rows.
 __device__ __forceinline__ int halves_of(const Params& p, const Cursor& c) {
-  return c.s.q_len * p.group - c.tile * kTile > kHalf ? 2 : 1;
+  return pw::uniform(c.s.q_len * p.group - c.tile * kTile > kHalf ? 2 : 1);
 }
 
 // Walks the units of the CTA's stretch: f(cursor, first block, end block) with
 // block numbers of the unit.
 template <typename F>
 __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
-  while (!c.done()) {
-    const int b0 = c.block, n = pw_attn::blocks_of(c.r);
+  while (pw::uniform(!c.done())) {
+    const int b0 = pw::uniform(c.block), n = pw_attn::blocks_of(c.r);
     const long long room = c.end - c.pos;
-    const int b1 = room < n - b0 ? b0 + static_cast<int>(room) : n;
+    const int b1 = pw::uniform(room < n - b0 ? b0 + static_cast<int>(room) : n);
     if (!f(c, b0, b1)) return;
     c.pos += b1 - b0;
     c.block = b1;
@@ -80,141 +80,148 @@ __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
 }
 
 // ---------------------------------------------------------------- copies (one warp)
+// Item 2x of the ring is the keys of the CTA's block x, item 2x + 1 its values.
+//
+// Rows of values outside the visible keys have to be zero.  They occur in a
+// unit's first and last block only: there the boxes that hold such rows are
+// copied row by row, with zeros for the others.
+template <int D>
+__device__ __forceinline__ void copy_rows(const Params& p, const Cursor& c, int key0, int first, int rows, int page,
+                                          unsigned char* dst) {
+  const pw_attn_args& a = p.a;
+  constexpr int kUnits = D / 8;
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < rows * kUnits; i += 32) {
+    const int row = first + i / kUnits, unit = i % kUnits, key = key0 + row;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (page >= 0 && key >= c.r.lo && key < c.r.hi)
+      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_cache) + page * a.v_stride_page +
+                                          (key % a.page_size) * a.v_stride_token + c.head * a.v_stride_head + unit * 8);
+    *reinterpret_cast<uint4*>(dst + (unit >> 3) * kHalfRow + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) = v;
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, const Maps& maps, Shared& sh,
-                                          uint32_t k_smem, uint32_t v_smem) {
+                                          unsigned char* ring) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31;
-  const int boxes = kBlock / maps.box;   // per 64 values
-  uint32_t x = 0;
-  bool ok = true;
+  const int box = maps.box, boxes = kBlock / box;   // at most 16 boxes of 64 values
+  uint32_t y = 0;                                   // items started
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
-    for (int b = b0; b < b1; ++b, ++x) {
-      const uint32_t slot = x % kSlots, use = x / kSlots;
-      const int key0 = (c.r.b0 + b) * kBlock;
+    const int32_t* table = a.page_table + c.seq * a.page_table_stride;
+    // this lane's box of block b: its page (-1: nothing to load) and row there
+    auto find = [&](int b, int& page, int& in_page) {
+      const int key = (c.r.b0 + b) * kBlock + lane * box;
+      page = -1;
+      if (lane < boxes && key < c.r.hi && key + box > c.r.lo) {
+        const int index = key / a.page_size;
+        in_page = key - index * a.page_size;
+        page = table[index];
+      }
+    };
+    int page, in_page = 0, next_page = -1, next_in_page = 0;
+    find(b0, next_page, next_in_page);
+    for (int b = b0; b < b1; ++b) {
+      page = next_page;
+      in_page = next_in_page;
+      next_page = -1;
+      if (b + 1 < b1) find(b + 1, next_page, next_in_page);   // its latency passes during this block's waits
+      const int key0 = (c.r.b0 + b) * kBlock, key = key0 + lane * box;
+      const bool wanted = lane < boxes && key < c.r.hi && key + box > c.r.lo;
+      const bool live = wanted && page >= 0 && page < a.num_pages;
+      if (wanted && !live) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+      const bool inside = live && key >= c.r.lo && key + box <= c.r.hi;   // every row is visible
+      const uint32_t live_mask = __ballot_sync(0xFFFFFFFFu, live), inside_mask = __ballot_sync(0xFFFFFFFFu, inside);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint64_t& empty = kv ? sh.v_empty[slot] : sh.k_empty[slot];
-        const uint64_t& full = kv ? sh.v_land[slot] : sh.k_full[slot];
-        if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(&empty, (use + 1) & 1u, sh, p))) {
-          ok = false;
-          return false;
+      for (int kv = 0; kv < 2; ++kv, ++y) {
+        const uint32_t slot = y % kSlots, use = y / kSlots;
+        if (use > 0 && !wait(&sh.empty[slot], (use + 1) & 1u, sh, p)) return false;
+        const uint32_t full = bar(sh.full[slot]), mask = kv ? inside_mask : live_mask;
+        unsigned char* dst = ring + slot * tile_bytes<D>();
+        if (kv && mask != (boxes == 32 ? 0xFFFFFFFFu : (1u << boxes) - 1u)) {
+          for (int i = 0; i < boxes; ++i)
+            if (!(mask >> i & 1u))
+              copy_rows<D>(p, c, key0, i * box, box, __shfl_sync(0xFFFFFFFFu, live ? page : -1, i), dst);
+          pw::fence_proxy_async_smem();
+          __syncwarp();
         }
-        // which boxes hold visible keys, and their pages
-        int total = 0;
-        for (int i0 = 0; i0 < boxes; i0 += 32) {
-          const int i = i0 + lane, key = key0 + i * maps.box;
-          bool live = i < boxes && key < c.r.hi && key + maps.box > c.r.lo;
-          if (live) {
-            const int page = a.page_table[c.seq * a.page_table_stride + key / a.page_size];
-            live = page >= 0 && page < a.num_pages;
-            if (!live && kv == 0) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
-          }
-          total += __popc(__ballot_sync(0xFFFFFFFFu, live));
-        }
-        if (lane == 0) pw::mbar_arrive_expect_tx(bar(full), static_cast<uint32_t>(total * maps.box * 128 * (D / 64)));
+        if (lane == 0)
+          pw::mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * static_cast<uint32_t>(box * 2 * D));
         __syncwarp();
-        const uint32_t dst = (kv ? v_smem : k_smem) + slot * tile_bytes<D>();
-        for (int i = lane; i < boxes; i += 32) {
-          const int key = key0 + i * maps.box;
-          if (!(key < c.r.hi && key + maps.box > c.r.lo)) continue;
-          const int index = key / a.page_size, page = a.page_table[c.seq * a.page_table_stride + index];
-          if (page < 0 || page >= a.num_pages) continue;
+        if (mask >> lane & 1u) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            pw::tma_load_4d(dst + h * kHalfRow + i * maps.box * 128, kv ? &maps.v : &maps.k, 64 * h,
-                            key - index * a.page_size, c.head, page, bar(full));
+            pw::tma_load_4d(pw::smem_u32(dst) + h * kHalfRow + lane * box * 128, kv ? &maps.v : &maps.k, 64 * h, in_page,
+                            c.head, page, full);
         }
       }
     }
     return true;
   });
-  if (!ok && lane == 0)   // no copy may be in flight when the CTA leaves
-    for (uint32_t i = x > kSlots ? x - kSlots : 0; i <= x; ++i) {
-      if (i < x) pw::mbar_wait(bar(sh.v_land[i % kSlots]), (i / kSlots) & 1u, p.wait_ns);
-      // block x may have its keys under way already
-      pw::mbar_wait(bar(sh.k_full[i % kSlots]), (i / kSlots) & 1u, i < x ? p.wait_ns : p.wait_ns / 4);
-    }
+  __syncwarp();
+  // No copy may be in flight when the CTA leaves: in a call that went well the
+  // matrix instructions have waited for every one of them.
+  if (*reinterpret_cast<volatile int*>(&sh.dead))
+    for (uint32_t i = y > kSlots ? y - kSlots : 0; i < y; ++i)
+      pw::mbar_wait(bar(sh.full[i % kSlots]), (i / kSlots) & 1u, p.wait_ns);
 }
 
-// ---------------------------------------------------------------- values outside the visible keys (one warp)
-template <int D>
-__device__ __forceinline__ void zero_role(const Params& p, const Cursor& start, Shared& sh, unsigned char* v_smem) {
-  const int lane = threadIdx.x & 31;
-  uint32_t x = 0;
-  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
-    for (int b = b0; b < b1; ++b, ++x) {
-      const uint32_t slot = x % kSlots;
-      if (!__all_sync(0xFFFFFFFFu, wait(&sh.v_land[slot], (x / kSlots) & 1u, sh, p))) return false;
-      const int key0 = (c.r.b0 + b) * kBlock;
-      if (c.r.lo > key0 || c.r.hi < key0 + kBlock) {
-        const int lo = max(0, c.r.lo - key0), hi = max(lo, min(kBlock, c.r.hi - key0));   // rows to keep
-        for (int i = lane; i < kBlock * 8; i += 32) {
-          const int row = i >> 3;
-          if (row >= lo && row < hi) continue;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            *reinterpret_cast<uint4*>(v_smem + slot * tile_bytes<D>() + h * kHalfRow + i * 16) = make_uint4(0, 0, 0, 0);
-        }
-        pw::fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (lane == 0) pw::mbar_arrive(bar(sh.v_full[slot]));
-    }
-    return true;
-  });
-}
-
-// ---------------------------------------------------------------- matrix instructions (one thread)
+// ---------------------------------------------------------------- matrix instructions (one warp)
 template <int D, bool kBf16>
 __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, Shared& sh, uint32_t tmem,
-                                         uint32_t q_smem, uint32_t k_smem, uint32_t v_smem) {
+                                         uint32_t q_smem, uint32_t ring) {
   constexpr uint32_t kScores = pw::idesc_f32(kHalf, kBlock, kBf16, false);
   constexpr uint32_t kValues = pw::idesc_f32(kHalf, D, kBf16, true);
-  uint32_t x = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+  uint32_t y = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};   // y: item of the block's keys
   bool ok = true;
-  auto scores = [&](int h, uint32_t slot) {   // S_h = Q_h K^T
+  auto scores = [&](int h, uint32_t item, bool free_after) {   // S_h = Q_h K^T
+    const uint32_t slot = item % kSlots;
     const uint64_t q = pw::sdesc_kmajor_sw128(q_smem + h * tile_bytes<D>());
-    const uint64_t k = pw::sdesc_kmajor_sw128(k_smem + slot * tile_bytes<D>());
+    const uint64_t k = pw::sdesc_kmajor_sw128(ring + slot * tile_bytes<D>());
+    if (pw::elect_one()) {
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint64_t at = (i / 4) * (kHalfRow >> 4) + (i % 4) * 2;
-      pw::tc_mma_f16(tmem + h * kBlock, q + at, k + at, kScores, i);
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t at = (i / 4) * (kHalfRow >> 4) + (i % 4) * 2;
+        pw::tc_mma_f16(tmem + h * kBlock, q + at, k + at, kScores, i);
+      }
+      pw::tc_commit(bar(sh.s_full[h]));
+      if (free_after) pw::tc_commit(bar(sh.empty[slot]));
     }
-    pw::tc_commit(bar(sh.s_full[h]));
+    __syncwarp();
   };
+  auto values = [&](int h, uint32_t item, bool first, bool free_after) {   // O_h (+)= P_h V
+    const uint32_t slot = item % kSlots;
+    const uint64_t v = pw::sdesc_nmajor_sw128(ring + slot * tile_bytes<D>(), kHalfRow);
+    if (pw::elect_one()) {
+#pragma unroll
+      for (int i = 0; i < kBlock / 16; ++i)
+        pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues, !first || i > 0);
+      pw::tc_commit(bar(sh.o_done[h]));
+      if (free_after) pw::tc_commit(bar(sh.empty[slot]));
+    }
+    __syncwarp();
+  };
+  auto ready = [&](uint32_t item) { return ok = wait(&sh.full[item % kSlots], (item / kSlots) & 1u, sh, p); };
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
     const int halves = halves_of(p, c);
-    for (int b = b0; b < b1; ++b, ++x) {
-      const uint32_t slot = x % kSlots;
+    for (int b = b0; b < b1; ++b, y += 2) {
       if (b == b0) {
-        if (!wait(&sh.k_full[slot], (x / kSlots) & 1u, sh, p)) return ok = false;
+        if (!ready(y)) return false;
         for (int h = 0; h < halves; ++h) {
-          if (!wait(&sh.q_full[h], n_q[h] & 1u, sh, p)) return ok = false;
+          if (!(ok = wait(&sh.q_full[h], n_q[h] & 1u, sh, p))) return false;
           ++n_q[h];
           pw::tc_fence_after();
-          scores(h, slot);
+          scores(h, y, h + 1 == halves);
         }
-        pw::tc_commit(bar(sh.k_empty[slot]));
       }
-      const uint32_t next = (x + 1) % kSlots;
-      if (b + 1 < b1 && !wait(&sh.k_full[next], ((x + 1) / kSlots) & 1u, sh, p)) return ok = false;
-      if (!wait(&sh.v_full[slot], (x / kSlots) & 1u, sh, p)) return ok = false;
+      if (!ready(y + 1) || (b + 1 < b1 && !ready(y + 2))) return false;
       for (int h = 0; h < halves; ++h) {
-        if (!wait(&sh.p_full[h], n_p[h] & 1u, sh, p)) return ok = false;
+        if (!(ok = wait(&sh.p_full[h], n_p[h] & 1u, sh, p))) return false;
         ++n_p[h];
         pw::tc_fence_after();
-        const uint64_t v = pw::sdesc_nmajor_sw128(v_smem + slot * tile_bytes<D>(), kHalfRow);
-#pragma unroll
-        for (int i = 0; i < kBlock / 16; ++i)   // O_h += P_h V
-          pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues,
-                        b > b0 || i > 0);
-        pw::tc_commit(bar(sh.o_done[h]));
-        if (h + 1 == halves) pw::tc_commit(bar(sh.v_empty[slot]));
-        if (b + 1 < b1) {
-          scores(h, next);
-          if (h + 1 == halves) pw::tc_commit(bar(sh.k_empty[next]));
-        }
+        values(h, y + 1, b == b0, h + 1 == halves);
+        if (b + 1 < b1) scores(h, y + 2, h + 1 == halves);
       }
     }
     return true;
@@ -270,7 +277,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
       for (int b = b0; b < b1; ++b, ++blocks) {
         const int key0 = (c.r.b0 + b) * kBlock;
-        __all_sync(0xFFFFFFFFu, wait(&sh.s_full[h], blocks & 1u, sh, p));
+        wait(&sh.s_full[h], blocks & 1u, sh, p);
         pw::tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -302,7 +309,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         }
         if (b > b0 && __any_sync(0xFFFFFFFFu, moves)) {
           // O has to be complete up to the last block before it is scaled
-          __all_sync(0xFFFFFFFFu, wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p));
+          wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p);
           pw::tc_fence_after();
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -342,7 +349,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         __syncwarp();
         if (lane == 0) pw::mbar_arrive(bar(sh.p_full[h]));
       }
-      __all_sync(0xFFFFFFFFu, wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p));
+      wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p);
       pw::tc_fence_after();
     }
     const float m2 = m * p.scale_log2;   // in powers of two
@@ -446,18 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ Shared sh;
   unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5));
   Cursor c;
   long long line;
   int ctas = gridDim.x;
   if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, ctas, c, line)) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      pw::mbar_init(bar(sh.k_full[i]), 1);
-      pw::mbar_init(bar(sh.k_empty[i]), 1);
-      pw::mbar_init(bar(sh.v_land[i]), 1);
-      pw::mbar_init(bar(sh.v_full[i]), 1);
-      pw::mbar_init(bar(sh.v_empty[i]), 1);
+      pw::mbar_init(bar(sh.full[i]), 1);
+      pw::mbar_init(bar(sh.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       pw::mbar_init(bar(sh.q_full[i]), 4);
@@ -475,26 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   pw::tc_fence_before();
   __syncthreads();
   pw::tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  unsigned char* q_smem = smem;
-  unsigned char* k_smem = smem + 2 * tile_bytes<D>();
-  unsigned char* v_smem = k_smem + kSlots * tile_bytes<D>();
+  const uint32_t tmem = pw::uniform(sh.tmem);
+  unsigned char* ring = smem + 2 * tile_bytes<D>();
   // Registers move from the third warpgroup to the softmax warps: 256 threads
-  // x 208 and 128 x 88 are the launch's 384 x 168.
+  // x 192 and 128 x 120 are the launch's 384 x 168.
   if (warp < kSoftmaxWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  }
-  if (warp < kSoftmaxWarps) {
-    softmax_role<T, D>(p, c, line, ctas, sh, tmem, q_smem);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    softmax_role<T, D>(p, c, line, ctas, sh, tmem, smem);
   } else if (warp == kLoadWarp) {
-    load_role<D>(p, c, maps, sh, pw::smem_u32(k_smem), pw::smem_u32(v_smem));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    load_role<D>(p, c, maps, sh, ring);
   } else if (warp == kMmaWarp) {
-    if (lane == 0)
-      mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(q_smem), pw::smem_u32(k_smem), pw::smem_u32(v_smem));
-  } else if (warp == kZeroWarp) {
-    zero_role<D>(p, c, sh, v_smem);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(ring));
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");   // a warpgroup gives and takes as a whole
   }
   __syncwarp();
   pw::tc_fence_before();

@@ -119,7 +119,7 @@ template <int kN>
 struct Tile {
   static constexpr int kStages = kN == 256 ? 4 : 6;
   static constexpr int kSumWarps = 4 * (kN / 128);
-  static constexpr int kThreads = 32 * (kSumWarps + 2);
+  static constexpr int kThreads = kN == 256 ? 384 : 192;   // whole warpgroups where registers are moved
   static constexpr int kStageBytes = (kTileM + kN) * kTmaBoxBytes;
   static constexpr int kSmem = kStages * kStageBytes + 1024;
 };
@@ -132,7 +132,7 @@ struct alignas(8) TileShared {
 };
 
 __device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, int* dead, const LinearParams& p) {
-  return pw::wait_or_dead(bar, parity, dead, p.status, p.wait_ns);
+  return pw::warp_wait_or_dead(bar, parity, dead, p.status, p.wait_ns);
 }
 
 // Tiles in strips of 16 token tiles, so that the CTAs that run at the same
@@ -144,6 +144,13 @@ __device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int&
   mt = strip * 16 + r - nt * height;
 }
 
+// Wide tiles: registers move to the sums.  256 threads x 208 and 128 x 88 are
+// the launch's 384 x 168.
+template <int kN>
+__device__ __forceinline__ void give_registers() {
+  if constexpr (kN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+}
+
 template <typename T, int kN>
 __global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_a,
@@ -152,7 +159,7 @@ __global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ TileShared<kN> sh;
   const uint32_t stages = (pw::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int tiles_m = (p.M + kTileM - 1) / kTileM, tiles_n = (p.N + kN - 1) / kN, tiles = tiles_m * tiles_n;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -173,62 +180,67 @@ __global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
   pw::tc_fence_before();
   __syncthreads();
   pw::tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = pw::uniform(sh.tmem);
 
   if (warp == C::kSumWarps) {
-    if (lane == 0) {   // copies
+    give_registers<kN>();
+    // copies
+    if (pw::elect_one()) {
       pw::prefetch_tmap(&map_a);
       pw::prefetch_tmap(&map_b);
-      uint32_t x = 0;   // groups started
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        int mt, nt;
-        tile_at(tile, tiles_m, tiles_n, mt, nt);
-        for (int kb = 0; kb < p.KB; ++kb, ++x) {
-          const uint32_t s = x % C::kStages;
-          if (x >= C::kStages && !wait(&sh.empty[s], (x / C::kStages + 1) & 1u, &sh.dead, p)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = pw::smem_u32(&sh.full[s]), dst = stages + s * C::kStageBytes;
+    }
+    uint32_t x = 0;   // groups started
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      int mt, nt;
+      tile_at(tile, tiles_m, tiles_n, mt, nt);
+      for (int kb = 0; kb < p.KB; ++kb, ++x) {
+        const uint32_t s = x % C::kStages;
+        if (x >= C::kStages && !(ok = wait(&sh.empty[s], (x / C::kStages + 1) & 1u, &sh.dead, p))) break;
+        const uint32_t bar = pw::smem_u32(&sh.full[s]), dst = stages + s * C::kStageBytes;
+        if (pw::elect_one()) {
           pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
           pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, mt * kTileM, bar);
           pw::tma_load_2d(dst + kTileM * kTmaBoxBytes, &map_b, kb * pw::kGroup, nt * kN, bar);
         }
+        __syncwarp();
       }
-      // no copy may be in flight when the CTA leaves
-      if (!ok)
-        for (uint32_t i = x > C::kStages ? x - C::kStages : 0; i < x; ++i)
-          pw::mbar_wait(pw::smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1u, p.wait_ns);
     }
+    // no copy may be in flight when the CTA leaves
+    if (!ok)
+      for (uint32_t i = x > C::kStages ? x - C::kStages : 0; i < x; ++i)
+        pw::mbar_wait(pw::smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1u, p.wait_ns);
   } else if (warp == C::kSumWarps + 1) {
-    if (lane == 0) {   // matrix instructions
-      constexpr uint32_t kIdesc = pw::idesc_f32(kTileM, kN, false, false);
-      uint32_t x = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        for (int kb = 0; kb < p.KB; ++kb, ++x) {
-          const uint32_t s = x % C::kStages, buf = x & 1u;
-          if ((x >= 2 && !wait(&sh.read[buf], ((x >> 1) + 1) & 1u, &sh.dead, p)) ||
-              !wait(&sh.full[s], (x / C::kStages) & 1u, &sh.dead, p)) {
-            ok = false;
-            break;
-          }
-          pw::tc_fence_after();
-          const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
-          const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + kTileM * kTmaBoxBytes);
+    give_registers<kN>();
+    // matrix instructions
+    constexpr uint32_t kIdesc = pw::idesc_f32(kTileM, kN, false, false);
+    uint32_t x = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      for (int kb = 0; kb < p.KB; ++kb, ++x) {
+        const uint32_t s = x % C::kStages, buf = x & 1u;
+        if (x >= 2) ok = wait(&sh.read[buf], ((x >> 1) + 1) & 1u, &sh.dead, p);
+        if (!ok || !(ok = wait(&sh.full[s], (x / C::kStages) & 1u, &sh.dead, p))) break;
+        pw::tc_fence_after();
+        const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
+        const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + kTileM * kTmaBoxBytes);
+        if (pw::elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)   // 32 columns a step: 2 units of 16 bytes
             pw::tc_mma_f8(tmem + buf * kN, a + 2 * i, b + 2 * i, kIdesc, i);
           pw::tc_commit(pw::smem_u32(&sh.empty[s]));
           pw::tc_commit(pw::smem_u32(&sh.done[buf]));
         }
+        __syncwarp();
       }
-      if (!ok)   // the accumulators go back only when nothing writes them
-        for (uint32_t i = x > 2 ? x - 2 : 0; i < x; ++i)
-          pw::mbar_wait(pw::smem_u32(&sh.done[i & 1u]), (i >> 1) & 1u, p.wait_ns);
     }
+    if (!ok)   // the accumulators go back only when nothing writes them
+      for (uint32_t i = x > 2 ? x - 2 : 0; i < x; ++i)
+        pw::mbar_wait(pw::smem_u32(&sh.done[i & 1u]), (i >> 1) & 1u, p.wait_ns);
+  } else if (warp > C::kSumWarps) {
+    give_registers<kN>();   // a warpgroup gives and takes as a whole
   } else {   // sums
+    if constexpr (kN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     uint32_t x = 0;
@@ -249,11 +261,7 @@ __global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
         const float scale = next;
         if (kb + 1 < p.KB) next = __ldg(sa + kb + 1) * __ldg(sb + kb + 1);
         const uint64_t s2 = pw::pack_f32x2(__float_as_uint(scale), __float_as_uint(scale));
-        // the lanes leave together: one may see the barrier, another the failure
-        if (!__all_sync(0xFFFFFFFFu, wait(&sh.done[buf], (x >> 1) & 1u, &sh.dead, p))) {
-          ok = false;
-          break;
-        }
+        if (!(ok = wait(&sh.done[buf], (x >> 1) & 1u, &sh.dead, p))) break;
         pw::tc_fence_after();
         const uint32_t src = tmem + lanes + buf * kN + 128u * half;
         uint32_t v[2][16];
