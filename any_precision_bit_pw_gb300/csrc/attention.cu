@@ -447,7 +447,6 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.arrived = static_cast<uint32_t*>(d_ws);
   p.part = reinterpret_cast<float*>(static_cast<char*>(d_ws) + kCounterBytes);
-  p.wait_ns = 2000000000ull;
   cudaStream_t s = pw::as_stream(stream);
   return a.dtype == PW_DTYPE_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
 }

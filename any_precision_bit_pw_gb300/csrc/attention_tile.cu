@@ -31,8 +31,9 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;            // keys of a block
 constexpr int kSlots = 5;              // ring of key and value blocks, in turn
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kKeyWarp = 8, kValueWarp = 9, kMmaWarp = 10;
 constexpr int kThreads = 384;
+constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr float kLazy = 8.0f;          // log2 of what a weight may grow to
 constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
 
@@ -43,7 +44,7 @@ constexpr int smem_bytes() { return (2 + kSlots) * tile_bytes<D>() + 1024; }
 
 struct alignas(8) Shared {
   uint64_t q_full[2], full[kSlots], empty[kSlots];
-  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t drained, s_full[2], p_full[2][2], o_done[2];   // p_full: weights of the first and the last 64 keys
   uint32_t tmem;
   int dead;
   int last;
@@ -55,7 +56,7 @@ struct Maps {
 };
 
 __device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, Shared& sh, const Params& p) {
-  return pw::warp_wait_or_dead(bar, parity, &sh.dead, p.a.status, p.wait_ns);
+  return pw::warp_wait(bar, parity, &sh.dead, p.a.status);
 }
 __device__ __forceinline__ uint32_t bar(const uint64_t& b) { return pw::smem_u32(&b); }
 
@@ -79,7 +80,7 @@ __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
   }
 }
 
-// ---------------------------------------------------------------- copies (one warp)
+// ---------------------------------------------------------------- copies (a warp for keys, a warp for values)
 // Item 2x of the ring is the keys of the CTA's block x, item 2x + 1 its values.
 //
 // Rows of values outside the visible keys have to be zero.  They occur in a
@@ -101,61 +102,64 @@ __device__ __forceinline__ void copy_rows(const Params& p, const Cursor& c, int 
   }
 }
 
-template <int D>
+template <int D, bool kValues>
 __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, const Maps& maps, Shared& sh,
                                           unsigned char* ring) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31;
   const int box = maps.box, boxes = kBlock / box;   // at most 16 boxes of 64 values
-  uint32_t y = 0;                                   // items started
+  const uint32_t every = (1u << boxes) - 1u;
+  const int step_pages = kBlock / a.page_size, step_rows = kBlock % a.page_size;
+  uint32_t y = kValues ? 1 : 0;                     // the warp's next item
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
     const int32_t* table = a.page_table + c.seq * a.page_table_stride;
-    // this lane's box of block b: its page (-1: nothing to load) and row there
-    auto find = [&](int b, int& page, int& in_page) {
-      const int key = (c.r.b0 + b) * kBlock + lane * box;
-      page = -1;
-      if (lane < boxes && key < c.r.hi && key + box > c.r.lo) {
-        const int index = key / a.page_size;
-        in_page = key - index * a.page_size;
-        page = table[index];
+    // this lane's box: its first key, and where that is in the page table
+    int key0 = (c.r.b0 + b0) * kBlock, key = key0 + lane * box;
+    int index = key / a.page_size, in_page = key - index * a.page_size;
+    auto wanted = [&]() { return lane < boxes && key < c.r.hi && key + box > c.r.lo; };
+    int page = wanted() ? table[index] : -1;
+    for (int b = b0; b < b1; ++b, y += 2) {
+      const bool want = wanted();
+      const int this_page = page, row = in_page;
+      bool take = want && this_page >= 0 && this_page < a.num_pages;
+      if (want && !take && !kValues) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+      const uint32_t live = __ballot_sync(0xFFFFFFFFu, take);
+      if (kValues) take = take && key >= c.r.lo && key + box <= c.r.hi;   // every row is visible
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
+      // the next block's page: its latency passes during this block's waits
+      key += kBlock;
+      index += step_pages;
+      in_page += step_rows;
+      if (in_page >= a.page_size) {
+        in_page -= a.page_size;
+        ++index;
       }
-    };
-    int page, in_page = 0, next_page = -1, next_in_page = 0;
-    find(b0, next_page, next_in_page);
-    for (int b = b0; b < b1; ++b) {
-      page = next_page;
-      in_page = next_in_page;
-      next_page = -1;
-      if (b + 1 < b1) find(b + 1, next_page, next_in_page);   // its latency passes during this block's waits
-      const int key0 = (c.r.b0 + b) * kBlock, key = key0 + lane * box;
-      const bool wanted = lane < boxes && key < c.r.hi && key + box > c.r.lo;
-      const bool live = wanted && page >= 0 && page < a.num_pages;
-      if (wanted && !live) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
-      const bool inside = live && key >= c.r.lo && key + box <= c.r.hi;   // every row is visible
-      const uint32_t live_mask = __ballot_sync(0xFFFFFFFFu, live), inside_mask = __ballot_sync(0xFFFFFFFFu, inside);
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++y) {
-        const uint32_t slot = y % kSlots, use = y / kSlots;
-        if (use > 0 && !wait(&sh.empty[slot], (use + 1) & 1u, sh, p)) return false;
-        const uint32_t full = bar(sh.full[slot]), mask = kv ? inside_mask : live_mask;
-        unsigned char* dst = ring + slot * tile_bytes<D>();
-        if (kv && mask != (boxes == 32 ? 0xFFFFFFFFu : (1u << boxes) - 1u)) {
-          for (int i = 0; i < boxes; ++i)
-            if (!(mask >> i & 1u))
-              copy_rows<D>(p, c, key0, i * box, box, __shfl_sync(0xFFFFFFFFu, live ? page : -1, i), dst);
-          pw::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0)
-          pw::mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * static_cast<uint32_t>(box * 2 * D));
+      page = b + 1 < b1 && wanted() ? table[index] : -1;
+      const uint32_t slot = y % kSlots, use = y / kSlots;
+      if (use > 0 && !wait(&sh.empty[slot], (use + 1) & 1u, sh, p)) return false;
+      const uint32_t full = bar(sh.full[slot]);
+      unsigned char* dst = ring + slot * tile_bytes<D>();
+      if (kValues && mask != every) {
+        for (int i = 0; i < boxes; ++i)
+          if (!(mask >> i & 1u))
+            copy_rows<D>(p, c, key0, i * box, box, __shfl_sync(0xFFFFFFFFu, live >> lane & 1u ? this_page : -1, i), dst);
+        pw::fence_proxy_async_smem();
         __syncwarp();
-        if (mask >> lane & 1u) {
+      }
+      if (pw::elect_one())
+        pw::mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(mask)) * static_cast<uint32_t>(box * 2 * D));
+      __syncwarp();
+      for (int i = 0; i < boxes; ++i) {
+        const int pg = __shfl_sync(0xFFFFFFFFu, this_page, i), at = __shfl_sync(0xFFFFFFFFu, row, i);
+        if ((mask >> i & 1u) && pw::elect_one()) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            pw::tma_load_4d(pw::smem_u32(dst) + h * kHalfRow + lane * box * 128, kv ? &maps.v : &maps.k, 64 * h, in_page,
-                            c.head, page, full);
+            pw::tma_load_4d(pw::smem_u32(dst) + h * kHalfRow + i * box * 128, kValues ? &maps.v : &maps.k, 64 * h, at,
+                            c.head, pg, full);
         }
+        __syncwarp();
       }
+      key0 += kBlock;
     }
     return true;
   });
@@ -163,8 +167,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
   // No copy may be in flight when the CTA leaves: in a call that went well the
   // matrix instructions have waited for every one of them.
   if (*reinterpret_cast<volatile int*>(&sh.dead))
-    for (uint32_t i = y > kSlots ? y - kSlots : 0; i < y; ++i)
-      pw::mbar_wait(bar(sh.full[i % kSlots]), (i / kSlots) & 1u, p.wait_ns);
+    for (uint32_t i = y > 2 * kSlots ? y - 2 * kSlots : (kValues ? 1 : 0); i < y; i += 2)
+      pw::mbar_wait(bar(sh.full[i % kSlots]), (i / kSlots) & 1u, kDrainNs);
 }
 
 // ---------------------------------------------------------------- matrix instructions (one warp)
@@ -190,15 +194,21 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
     }
     __syncwarp();
   };
-  auto values = [&](int h, uint32_t item, bool first, bool free_after) {   // O_h (+)= P_h V
+  // O_h (+)= P_h V, the first or the last 64 keys
+  auto values = [&](int h, int part, uint32_t item, bool first, bool free_after) {
     const uint32_t slot = item % kSlots;
     const uint64_t v = pw::sdesc_nmajor_sw128(ring + slot * tile_bytes<D>(), kHalfRow);
     if (pw::elect_one()) {
 #pragma unroll
-      for (int i = 0; i < kBlock / 16; ++i)
-        pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues, !first || i > 0);
-      pw::tc_commit(bar(sh.o_done[h]));
-      if (free_after) pw::tc_commit(bar(sh.empty[slot]));
+      for (int j = 0; j < kBlock / 32; ++j) {
+        const int i = part * (kBlock / 32) + j;
+        pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues,
+                      !first || part > 0 || j > 0);
+      }
+      if (part) {
+        pw::tc_commit(bar(sh.o_done[h]));
+        if (free_after) pw::tc_commit(bar(sh.empty[slot]));
+      }
     }
     __syncwarp();
   };
@@ -207,7 +217,7 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
     const int halves = halves_of(p, c);
     for (int b = b0; b < b1; ++b, y += 2) {
       if (b == b0) {
-        if (!ready(y)) return false;
+        if (!ready(y) || !ready(y + 1)) return false;
         for (int h = 0; h < halves; ++h) {
           if (!(ok = wait(&sh.q_full[h], n_q[h] & 1u, sh, p))) return false;
           ++n_q[h];
@@ -215,20 +225,29 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
           scores(h, y, h + 1 == halves);
         }
       }
-      if (!ready(y + 1) || (b + 1 < b1 && !ready(y + 2))) return false;
       for (int h = 0; h < halves; ++h) {
-        if (!(ok = wait(&sh.p_full[h], n_p[h] & 1u, sh, p))) return false;
+        for (int part = 0; part < 2; ++part) {
+          if (!(ok = wait(&sh.p_full[h][part], n_p[h] & 1u, sh, p))) return false;
+          pw::tc_fence_after();
+          values(h, part, y + 1, b == b0, h + 1 == halves);
+        }
         ++n_p[h];
-        pw::tc_fence_after();
-        values(h, y + 1, b == b0, h + 1 == halves);
-        if (b + 1 < b1) scores(h, y + 2, h + 1 == halves);
+        if (b + 1 < b1) {
+          // one wait between any two groups of instructions: the queue of the
+          // tensor cores covers it
+          if (h == 0 && !ready(y + 2)) return false;
+          if (h + 1 == halves && !ready(y + 3)) return false;
+          scores(h, y + 2, h + 1 == halves);
+        }
       }
     }
     return true;
   });
-  if (!ok)   // Tensor Memory goes back only when nothing writes it
-    for (int h = 0; h < 2; ++h)
-      if (n_p[h]) pw::mbar_wait(bar(sh.o_done[h]), (n_p[h] - 1) & 1u, p.wait_ns);
+  if (!ok) {   // Tensor Memory goes back only when nothing writes it
+    if (pw::elect_one()) pw::tc_commit(bar(sh.drained));
+    __syncwarp();
+    pw::mbar_wait(bar(sh.drained), 0, kDrainNs);
+  }
 }
 
 // ---------------------------------------------------------------- softmax (four warps a half)
@@ -294,9 +313,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         float top4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          top4[i] = __uint_as_float(s[i][0]);
+          top4[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-          for (int j = 1; j < 32; ++j) top4[i] = fmaxf(top4[i], __uint_as_float(s[i][j]));
+          for (int j = 2; j < 32; j += 2)
+            top4[i] = pw::max3(top4[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
         }
         const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
         // m follows the maximum in steps of at least 2^8 (and at once from -inf)
@@ -340,14 +360,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
             w[j] = pw::pack2<T>(e0, e1);
           }
           pw::tmem_st_x32(s_tmem + 32 * i, w);
+          pw::tmem_st_wait();
+          pw::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) pw::mbar_arrive(bar(sh.p_full[h][i]));
         }
         float s0, s1;
         pw::unpack_f32x2(pw::add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
-        pw::tmem_st_wait();
-        pw::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) pw::mbar_arrive(bar(sh.p_full[h]));
       }
       wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p);
       pw::tc_fence_after();
@@ -466,9 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       pw::mbar_init(bar(sh.q_full[i]), 4);
       pw::mbar_init(bar(sh.s_full[i]), 1);
-      pw::mbar_init(bar(sh.p_full[i]), 4);
+      pw::mbar_init(bar(sh.p_full[i][0]), 4);
+      pw::mbar_init(bar(sh.p_full[i][1]), 4);
       pw::mbar_init(bar(sh.o_done[i]), 1);
     }
+    pw::mbar_init(bar(sh.drained), 1);
     sh.dead = 0;
     pw::mbar_init_fence();
   }
@@ -486,9 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftmaxWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_role<T, D>(p, c, line, ctas, sh, tmem, smem);
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kKeyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    load_role<D>(p, c, maps, sh, ring);
+    load_role<D, false>(p, c, maps, sh, ring);
+  } else if (warp == kValueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    load_role<D, true>(p, c, maps, sh, ring);
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(ring));

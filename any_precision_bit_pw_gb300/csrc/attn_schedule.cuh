@@ -20,7 +20,6 @@ struct Params {
   float scale_log2;   // scale * log2(e): the softmax runs in powers of two
   uint32_t* arrived;  // one counter per CTA, all 0 between calls
   float* part;        // 2 partial results per CTA
-  uint64_t wait_ns;
 };
 
 constexpr int kMaxCtas = 320;   // at most two CTAs on each of 160 SMs

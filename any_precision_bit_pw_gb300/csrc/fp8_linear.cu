@@ -18,9 +18,10 @@ struct LinearParams {
   void* y;
   int64_t lda, ldb, ldy, sa_stride, sb_stride;
   int M, N, K, KB;
+  int splits;       // CTAs of a cluster that share a tile's groups
   int32_t* status;
-  uint64_t wait_ns;
-  bool wide_y;      // rows of y take 16-byte stores
+  bool wide_y;      // rows of y start at 16-byte addresses
+  bool wide_scales; // scales through tensor maps
 };
 
 constexpr int kRows = 16;    // weight rows of a CTA: the m16 side of the warp MMA
@@ -105,62 +106,81 @@ int launch_stream(const LinearParams& p, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 128 tokens x kN weight rows a tile on the tcgen05 tensor cores.
-// The MMAs of one 128-column group write a fresh accumulator in Tensor Memory;
-// eight warps (four for kN 128) read it, multiply by the group's scales and add
-// to sums in registers, while the next group's MMAs fill the other
-// accumulator.  A thread owns one token and 128 weight rows, that is one scale
-// product per group.  Persistent: one CTA per SM walks the tiles.
+// More tokens: tiles on the tcgen05 tensor cores.  The MMAs of one 128-column
+// group write a fresh accumulator in Tensor Memory; eight warps read it,
+// multiply by the group's scales and add to sums in registers, while the next
+// group's MMAs fill the other accumulator.  Tokens are the lanes of Tensor
+// Memory, so a thread owns one token and has one scale product per group.
+//
+//  kPair: 256 tokens x 256 weight rows by a pair of CTAs, persistent.  Each
+//    CTA holds half of both operands, so a group costs its shared memory 32 KB
+//    in and 32 KB out for 512 cycles of matrix work: at 128 bytes a cycle both
+//    are busy to the end.  (One CTA with 128 x 256 moves 96 KB for the same
+//    work and stays at two thirds: 360 us instead of PAIR_US for 8192^2 x 6144.)
+//  otherwise: 128 x 128 by one CTA, for fewer tokens; with few tiles the groups
+//    are split among the CTAs of a cluster, which add their sums through
+//    distributed shared memory, in the order of their ranks.
 // ---------------------------------------------------------------------------
-constexpr int kTileM = 128;
-constexpr int kTmaBoxBytes = 128;   // one group of columns: a swizzled row
+constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr int kBoxBytes = 128;      // one group of columns: a swizzled row
+constexpr int kSumWarps = 8;
+constexpr int kCopyWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
 
-template <int kN>
+constexpr int kOutBytes = 32 * 64 * 2;     // 32 rows x 64 columns of 16-bit results on their way out, of one warp
+constexpr int kScaleSlots = 4;
+constexpr int kTokenScaleBytes = 128 * 16;             // the token scales of four groups
+constexpr int kScaleBytes = kTokenScaleBytes + 128;    // and the weight scales of the tile's 128-row blocks
+
+template <bool kPair>
 struct Tile {
-  static constexpr int kStages = kN == 256 ? 4 : 6;
-  static constexpr int kSumWarps = 4 * (kN / 128);
-  static constexpr int kThreads = kN == 256 ? 384 : 192;   // whole warpgroups where registers are moved
-  static constexpr int kStageBytes = (kTileM + kN) * kTmaBoxBytes;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kM = kPair ? 256 : 128;        // tokens
+  static constexpr int kN = kPair ? 256 : 128;        // weight rows
+  static constexpr int kCols = kN / 2;                // of one warpgroup
+  static constexpr int kStages = 5;
+  static constexpr int kThreads = kPair ? 384 : 320;  // whole warpgroups where registers are moved
+  static constexpr int kStageBytes = 2 * 128 * kBoxBytes;   // a CTA's 128 rows of each operand
+  static constexpr int kSmem = kStages * kStageBytes + kSumWarps * kOutBytes + kScaleSlots * kScaleBytes + 1024;
 };
+constexpr int kPartRow = 132;       // floats of a row of sums in shared memory: 16-byte lanes on distinct banks
 
-template <int kN>
 struct alignas(8) TileShared {
-  uint64_t full[Tile<kN>::kStages], empty[Tile<kN>::kStages], done[2], read[2];
+  uint64_t full[5], empty[5], done[2], read[2], scales[kScaleSlots], drained;
   uint32_t tmem;
   int dead;   // a wait ran out: everybody leaves
 };
 
-__device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, int* dead, const LinearParams& p) {
-  return pw::warp_wait_or_dead(bar, parity, dead, p.status, p.wait_ns);
+__device__ __forceinline__ bool wait(const uint64_t& bar, uint32_t parity, TileShared& sh, const LinearParams& p) {
+  return pw::warp_wait(&bar, parity, &sh.dead, p.status);
 }
 
-// Tiles in strips of 16 token tiles, so that the CTAs that run at the same
-// time share both operands through L2.
+// Tiles in strips of 2048 tokens, so that the CTAs that run at the same time
+// share both operands through L2.
+template <bool kPair>
 __device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int& mt, int& nt) {
-  const int per_strip = 16 * tiles_n, strip = tile / per_strip, r = tile - strip * per_strip;
-  const int height = min(16, tiles_m - strip * 16);
+  constexpr int kStrip = 2048 / Tile<kPair>::kM;
+  const int per_strip = kStrip * tiles_n, strip = tile / per_strip, r = tile - strip * per_strip;
+  const int height = min(kStrip, tiles_m - strip * kStrip);
   nt = r / height;
-  mt = strip * 16 + r - nt * height;
+  mt = strip * kStrip + r - nt * height;
 }
 
-// Wide tiles: registers move to the sums.  256 threads x 208 and 128 x 88 are
-// the launch's 384 x 168.
-template <int kN>
-__device__ __forceinline__ void give_registers() {
-  if constexpr (kN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-}
-
-template <typename T, int kN>
-__global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
+template <typename T, bool kPair>
+__global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_b) {
-  using C = Tile<kN>;
+                       const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_y,
+                       const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb) {
+  using C = Tile<kPair>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ TileShared<kN> sh;
-  const uint32_t stages = (pw::smem_u32(smem_raw) + 1023u) & ~1023u;
+  __shared__ TileShared sh;
+  unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t stages = pw::smem_u32(smem);
   const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-  const int tiles_m = (p.M + kTileM - 1) / kTileM, tiles_n = (p.N + kN - 1) / kN, tiles = tiles_m * tiles_n;
+  const int tiles_m = (p.M + C::kM - 1) / C::kM, tiles_n = (p.N + C::kN - 1) / C::kN, tiles = tiles_m * tiles_n;
+  // the CTA's place: rank in its pair, or its share of the groups
+  const int rank = kPair || p.splits > 1 ? static_cast<int>(pw::cluster_rank()) : 0;
+  const int group_size = kPair ? 2 : p.splits;
+  const int first_tile = blockIdx.x / group_size, tile_step = gridDim.x / group_size;
+  const int kb0 = kPair ? 0 : p.KB * rank / p.splits, kb1 = kPair ? p.KB : p.KB * (rank + 1) / p.splits;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       pw::mbar_init(pw::smem_u32(&sh.full[i]), 1);
@@ -168,175 +188,363 @@ __global__ void __launch_bounds__(Tile<kN>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       pw::mbar_init(pw::smem_u32(&sh.done[i]), 1);
-      pw::mbar_init(pw::smem_u32(&sh.read[i]), C::kSumWarps);
+      pw::mbar_init(pw::smem_u32(&sh.read[i]), kSumWarps * (kPair ? 2 : 1));
     }
+    for (int i = 0; i < kScaleSlots; ++i) pw::mbar_init(pw::smem_u32(&sh.scales[i]), 1);
+    pw::mbar_init(pw::smem_u32(&sh.drained), 1);
     sh.dead = 0;
     pw::mbar_init_fence();
   }
-  if (warp == C::kSumWarps) {
-    pw::tmem_alloc(pw::smem_u32(&sh.tmem), 2 * kN);
-    pw::tmem_relinquish();
+  if (warp == kCopyWarp) {
+    if constexpr (kPair) {
+      pw::tmem_alloc_pair(pw::smem_u32(&sh.tmem), 2 * C::kN);
+    } else {
+      pw::tmem_alloc(pw::smem_u32(&sh.tmem), 2 * C::kN);
+      pw::tmem_relinquish();
+    }
   }
   pw::tc_fence_before();
   __syncthreads();
+  if (group_size > 1) pw::cluster_sync();   // the other CTAs' barriers are set up
   pw::tc_fence_after();
   const uint32_t tmem = pw::uniform(sh.tmem);
+  const uint32_t scale_smem = stages + C::kStages * C::kStageBytes + kSumWarps * kOutBytes;
 
-  if (warp == C::kSumWarps) {
-    give_registers<kN>();
-    // copies
+  if (warp == kCopyWarp) {
+    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (pw::elect_one()) {
       pw::prefetch_tmap(&map_a);
       pw::prefetch_tmap(&map_b);
+      pw::prefetch_tmap(&map_y);
+      pw::prefetch_tmap(&map_sa);
+      pw::prefetch_tmap(&map_sb);
     }
-    uint32_t x = 0;   // groups started
+    uint32_t x = 0, fours = 0;   // groups, and fours of groups, started
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       int mt, nt;
-      tile_at(tile, tiles_m, tiles_n, mt, nt);
-      for (int kb = 0; kb < p.KB; ++kb, ++x) {
+      tile_at<kPair>(tile, tiles_m, tiles_n, mt, nt);
+      const int row_a = mt * C::kM + (kPair ? 128 * rank : 0), row_b = nt * C::kN + (kPair ? 128 * rank : 0);
+      for (int kb = kb0; kb < kb1; ++kb, ++x) {
         const uint32_t s = x % C::kStages;
-        if (x >= C::kStages && !(ok = wait(&sh.empty[s], (x / C::kStages + 1) & 1u, &sh.dead, p))) break;
+        if (x >= C::kStages && !(ok = wait(sh.empty[s], (x / C::kStages + 1) & 1u, sh, p))) break;
         const uint32_t bar = pw::smem_u32(&sh.full[s]), dst = stages + s * C::kStageBytes;
+        if (p.wide_scales && (kb == kb0 || (kb & 3) == 0)) {
+          // The slot is free: the MMAs of group x - 5 are done, they were issued
+          // after every warp had read the accumulator of group x - 7, and the
+          // slot's last user is at least seven groups back (three fours of a
+          // tile of two groups or more).
+          const uint32_t slot = fours++ % kScaleSlots, sbar = pw::smem_u32(&sh.scales[slot]);
+          if (pw::elect_one()) {
+            const uint32_t dst = scale_smem + slot * kScaleBytes;
+            pw::mbar_arrive_expect_tx(sbar, kTokenScaleBytes + 16 * (C::kN / 128));
+            pw::tma_load_2d(dst, &map_sa, kb & ~3, row_a, sbar);
+            pw::tma_load_2d(dst + kTokenScaleBytes, &map_sb, kb & ~3, nt * (C::kN / 128), sbar);
+          }
+          __syncwarp();
+        }
         if (pw::elect_one()) {
-          pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
-          pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, mt * kTileM, bar);
-          pw::tma_load_2d(dst + kTileM * kTmaBoxBytes, &map_b, kb * pw::kGroup, nt * kN, bar);
+          if constexpr (kPair) {
+            // both CTAs' copies complete on the first one's barrier
+            if (rank == 0) pw::mbar_arrive_expect_tx(bar, 2 * C::kStageBytes);
+            const uint32_t lead = pw::map_shared(bar, 0);
+            pw::tma_load_2d_pair(dst, &map_a, kb * pw::kGroup, row_a, lead);
+            pw::tma_load_2d_pair(dst + 128 * kBoxBytes, &map_b, kb * pw::kGroup, row_b, lead);
+          } else {
+            pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
+            pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, row_a, bar);
+            pw::tma_load_2d(dst + 128 * kBoxBytes, &map_b, kb * pw::kGroup, row_b, bar);
+          }
         }
         __syncwarp();
       }
     }
-    // no copy may be in flight when the CTA leaves
-    if (!ok)
+    // No copy may be in flight when the CTA leaves.  A pair's second CTA leaves
+    // after the first (cluster barrier below), which sees both CTAs' copies.
+    if (!ok && (!kPair || rank == 0))
       for (uint32_t i = x > C::kStages ? x - C::kStages : 0; i < x; ++i)
-        pw::mbar_wait(pw::smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1u, p.wait_ns);
-  } else if (warp == C::kSumWarps + 1) {
-    give_registers<kN>();
-    // matrix instructions
-    constexpr uint32_t kIdesc = pw::idesc_f32(kTileM, kN, false, false);
-    uint32_t x = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      for (int kb = 0; kb < p.KB; ++kb, ++x) {
-        const uint32_t s = x % C::kStages, buf = x & 1u;
-        if (x >= 2) ok = wait(&sh.read[buf], ((x >> 1) + 1) & 1u, &sh.dead, p);
-        if (!ok || !(ok = wait(&sh.full[s], (x / C::kStages) & 1u, &sh.dead, p))) break;
-        pw::tc_fence_after();
-        const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
-        const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + kTileM * kTmaBoxBytes);
-        if (pw::elect_one()) {
+        pw::mbar_wait(pw::smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1u, kDrainNs);
+    if (!ok)
+      for (uint32_t i = fours > kScaleSlots ? fours - kScaleSlots : 0; i < fours; ++i)
+        pw::mbar_wait(pw::smem_u32(&sh.scales[i % kScaleSlots]), (i / kScaleSlots) & 1u, kDrainNs);
+  } else if (warp == kMmaWarp) {
+    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (!kPair || rank == 0) {
+      constexpr uint32_t kIdesc = pw::idesc_f32(C::kM, C::kN, false, false);
+      uint32_t x = 0;
+      bool ok = true;
+      for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++x) {
+          const uint32_t s = x % C::kStages, buf = x & 1u;
+          if (x >= 2) ok = wait(sh.read[buf], ((x >> 1) + 1) & 1u, sh, p);
+          if (!ok || !(ok = wait(sh.full[s], (x / C::kStages) & 1u, sh, p))) break;
+          pw::tc_fence_after();
+          const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
+          const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + 128 * kBoxBytes);
+          if (pw::elect_one()) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)   // 32 columns a step: 2 units of 16 bytes
-            pw::tc_mma_f8(tmem + buf * kN, a + 2 * i, b + 2 * i, kIdesc, i);
-          pw::tc_commit(pw::smem_u32(&sh.empty[s]));
-          pw::tc_commit(pw::smem_u32(&sh.done[buf]));
+            for (int i = 0; i < 4; ++i) {   // 32 columns a step: 2 units of 16 bytes
+              if constexpr (kPair)
+                pw::tc_mma_f8_pair(tmem + buf * C::kN, a + 2 * i, b + 2 * i, kIdesc, i);
+              else
+                pw::tc_mma_f8(tmem + buf * C::kN, a + 2 * i, b + 2 * i, kIdesc, i);
+            }
+            if constexpr (kPair) {
+              pw::tc_commit_pair(pw::smem_u32(&sh.empty[s]));
+              pw::tc_commit_pair(pw::smem_u32(&sh.done[buf]));
+            } else {
+              pw::tc_commit(pw::smem_u32(&sh.empty[s]));
+              pw::tc_commit(pw::smem_u32(&sh.done[buf]));
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {   // the accumulators go back only when nothing writes them
+        if (pw::elect_one()) {
+          if constexpr (kPair)
+            pw::tc_commit_pair(pw::smem_u32(&sh.drained));
+          else
+            pw::tc_commit(pw::smem_u32(&sh.drained));
         }
         __syncwarp();
+        pw::mbar_wait(pw::smem_u32(&sh.drained), 0, kDrainNs);
       }
     }
-    if (!ok)   // the accumulators go back only when nothing writes them
-      for (uint32_t i = x > 2 ? x - 2 : 0; i < x; ++i)
-        pw::mbar_wait(pw::smem_u32(&sh.done[i & 1u]), (i >> 1) & 1u, p.wait_ns);
-  } else if (warp > C::kSumWarps) {
-    give_registers<kN>();   // a warpgroup gives and takes as a whole
-  } else {   // sums
-    if constexpr (kN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int quarter = warp & 3, half = warp >> 2;
+  } else if (warp > kMmaWarp) {
+    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");   // a warpgroup gives as a whole
+  } else {
+    // sums; registers: 256 threads x 208 and 128 x 88 are the pair kernel's 384 x 168
+    if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    uint32_t x = 0;
+    const uint32_t read0 = kPair ? pw::map_shared(pw::smem_u32(&sh.read[0]), 0) : pw::smem_u32(&sh.read[0]);
+    unsigned char* out = smem + C::kStages * C::kStageBytes + warp * kOutBytes;
+    uint32_t x = 0, fours = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       int mt, nt;
-      tile_at(tile, tiles_m, tiles_n, mt, nt);
-      const int m = mt * kTileM + 32 * quarter + lane, n0 = nt * kN + 128 * half;
-      const bool live = m < p.M;
-      const float* sa = p.sa + static_cast<int64_t>(live ? m : 0) * p.sa_stride;
+      tile_at<kPair>(tile, tiles_m, tiles_n, mt, nt);
+      const int m0 = mt * C::kM + (kPair ? 128 * rank : 0) + 32 * quarter, m = m0 + lane;
+      const int n0 = nt * C::kN + C::kCols * side;
+      const float* sa = p.sa + static_cast<int64_t>(m < p.M ? m : 0) * p.sa_stride;
       const float* sb = p.sb + static_cast<int64_t>(min(n0, p.N - 1) / pw::kGroup) * p.sb_stride;
-      uint64_t sum[64];
+      uint64_t sum[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0;
-      float next = __ldg(sa) * __ldg(sb);
-      for (int kb = 0; kb < p.KB; ++kb, ++x) {
+      for (int i = 0; i < C::kCols / 2; ++i) sum[i] = 0;
+      // Scales, four groups at a time, through shared memory where their layout
+      // allows: a load from here would queue behind the ring's copies, 160 KB
+      // of them, and hold up the sums for 450 cycles at every fourth group.
+      for (int four = kb0 & ~3; ok && four < kb1; four += 4) {
+        float a_now[4], b_now[4];
+        if (p.wide_scales) {
+          const uint32_t slot = fours % kScaleSlots;
+          if (!(ok = wait(sh.scales[slot], (fours / kScaleSlots) & 1u, sh, p))) break;
+          ++fours;
+          const unsigned char* src = smem + (scale_smem - stages) + slot * kScaleBytes;
+          const float4 f = *reinterpret_cast<const float4*>(src + (32 * quarter + lane) * 16);
+          const float4 g = *reinterpret_cast<const float4*>(src + kTokenScaleBytes + (kPair ? 16 * side : 0));
+          a_now[0] = f.x, a_now[1] = f.y, a_now[2] = f.z, a_now[3] = f.w;
+          b_now[0] = g.x, b_now[1] = g.y, b_now[2] = g.z, b_now[3] = g.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a_now[i] = four + i < kb1 ? __ldg(sa + four + i) : 0.0f;
+            b_now[i] = four + i < kb1 ? __ldg(sb + four + i) : 0.0f;
+          }
+        }
+#pragma unroll 1
+        for (int kb = max(four, kb0); kb < min(four + 4, kb1); ++kb, ++x) {
         const uint32_t buf = x & 1u;
-        const float scale = next;
-        if (kb + 1 < p.KB) next = __ldg(sa + kb + 1) * __ldg(sb + kb + 1);
-        const uint64_t s2 = pw::pack_f32x2(__float_as_uint(scale), __float_as_uint(scale));
-        if (!(ok = wait(&sh.done[buf], (x >> 1) & 1u, &sh.dead, p))) break;
+        const int at = kb & 3;
+        const float sc = (at & 2 ? (at & 1 ? a_now[3] : a_now[2]) : (at & 1 ? a_now[1] : a_now[0])) *
+                         (at & 2 ? (at & 1 ? b_now[3] : b_now[2]) : (at & 1 ? b_now[1] : b_now[0]));
+        const uint64_t scale = pw::pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
+        if (!(ok = wait(sh.done[buf], (x >> 1) & 1u, sh, p))) break;
         pw::tc_fence_after();
-        const uint32_t src = tmem + lanes + buf * kN + 128u * half;
+        const uint32_t src = tmem + lanes + buf * C::kN + C::kCols * side;
         uint32_t v[2][16];
         pw::tmem_ld_x16(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < C::kCols / 16; ++c) {
           pw::tmem_ld_wait();
-          if (c < 7) pw::tmem_ld_x16(src + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < C::kCols / 16) pw::tmem_ld_x16(src + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            sum[8 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), s2, sum[8 * c + i]);
+            sum[8 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), scale, sum[8 * c + i]);
         }
         pw::tc_fence_before();
         __syncwarp();
-        if (lane == 0) pw::mbar_arrive(pw::smem_u32(&sh.read[buf]));
+        if (lane == 0) {
+          if constexpr (kPair)
+            pw::mbar_arrive_cluster(read0 + 8 * buf);
+          else
+            pw::mbar_arrive(read0 + 8 * buf);
+        }
       }
-      if (!ok || !live) continue;
-      T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
+      }
+      if (!ok) break;
+      if (!kPair && p.splits > 1) {
+        // rows of sums for the cluster; the copies' memory is free (every MMA
+        // of the CTA has completed)
+        float* part = reinterpret_cast<float*>(smem) + (32 * quarter + lane) * kPartRow + C::kCols * side;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float f[8];
+        for (int i = 0; i < C::kCols / 4; ++i) {
+          float4 f;
+          pw::unpack_f32x2(sum[2 * i], f.x, f.y);
+          pw::unpack_f32x2(sum[2 * i + 1], f.z, f.w);
+          *reinterpret_cast<float4*>(part + 4 * i) = f;
+        }
+        break;   // one tile per cluster
+      }
+      if (p.wide_y) {
+        // 16-bit rows through shared memory, 32 rows x 64 columns at a time
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pw::unpack_f32x2(sum[4 * i + j], f[2 * j], f[2 * j + 1]);
-        if (p.wide_y && n0 + 8 * i + 8 <= p.N) {
-          *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pw::pack2<T>(f[0], f[1]), pw::pack2<T>(f[2], f[3]),
-                                                            pw::pack2<T>(f[4], f[5]), pw::pack2<T>(f[6], f[7]));
-        } else {
+        for (int box = 0; box < C::kCols / 64; ++box) {
+          pw::bulk_wait_read();   // the box before has left
+          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (n0 + 8 * i + j < p.N) y[8 * i + j] = pw::from_float<T>(f[j]);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float lo, hi;
+              pw::unpack_f32x2(sum[32 * box + 4 * i + j], lo, hi);
+              w[j] = pw::pack2<T>(lo, hi);
+            }
+            *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          pw::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 < p.M && n0 + 64 * box < p.N) {
+            pw::tma_store_2d(&map_y, n0 + 64 * box, m0, pw::smem_u32(out));
+            pw::bulk_commit();
+          }
+        }
+      } else if (m < p.M) {
+        T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
+#pragma unroll
+        for (int i = 0; i < C::kCols / 2; ++i) {
+          float lo, hi;
+          pw::unpack_f32x2(sum[i], lo, hi);
+          if (n0 + 2 * i < p.N) y[2 * i] = pw::from_float<T>(lo);
+          if (n0 + 2 * i + 1 < p.N) y[2 * i + 1] = pw::from_float<T>(hi);
         }
       }
     }
+    if (lane == 0) pw::bulk_wait();
   }
   __syncwarp();
   pw::tc_fence_before();
   __syncthreads();
+  if (group_size > 1) pw::cluster_sync();   // sums are in place; nobody still signals or feeds a CTA that leaves
   pw::tc_fence_after();
-  if (warp == C::kSumWarps) pw::tmem_dealloc(tmem, 2 * kN);
+  if (warp == kCopyWarp) {
+    if constexpr (kPair)
+      pw::tmem_dealloc_pair(tmem, 2 * C::kN);
+    else
+      pw::tmem_dealloc(tmem, 2 * C::kN);
+  }
+  if constexpr (!kPair) {
+    if (p.splits > 1) {
+      // each CTA of the cluster finishes its share of the tile's rows
+      int mt, nt;
+      tile_at<kPair>(first_tile, tiles_m, tiles_n, mt, nt);
+      const int rows = min(128, p.M - mt * 128), col = 4 * lane, n = nt * 128 + col;
+      for (int row = rank + p.splits * warp; row < rows; row += p.splits * (C::kThreads / 32)) {
+        const uint32_t at = stages + 4u * static_cast<uint32_t>(row * kPartRow + col);
+        float4 v = pw::ld_cluster_f4(pw::map_shared(at, 0));
+        for (int i = 1; i < p.splits; ++i) {
+          const float4 w = pw::ld_cluster_f4(pw::map_shared(at, i));
+          v.x += w.x;
+          v.y += w.y;
+          v.z += w.z;
+          v.w += w.w;
+        }
+        if (sh.dead) continue;
+        T* y = static_cast<T*>(p.y) + static_cast<int64_t>(mt * 128 + row) * p.ldy + n;
+        if (p.wide_y && n + 4 <= p.N) {
+          *reinterpret_cast<uint2*>(y) = make_uint2(pw::pack2<T>(v.x, v.y), pw::pack2<T>(v.z, v.w));
+        } else {
+          const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) y[i] = pw::from_float<T>(f[i]);
+        }
+      }
+      pw::cluster_sync();   // the sums have been read
+    }
+  }
 }
 
-template <typename T, int kN>
-int launch_tile(const LinearParams& p, cudaStream_t s) {
-  using C = Tile<kN>;
+template <typename T, bool kPair>
+int launch_tile(LinearParams p, int sms, cudaStream_t s) {
+  using C = Tile<kPair>;
   constexpr int kDevs = 64;
   static bool attr_done[kDevs] = {};
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= kDevs || !attr_done[dev]) {
-    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
     if (dev < kDevs) attr_done[dev] = true;
   }
-  const int sms = pw::sm_count();
-  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, my, msa, msb;
   const uint64_t da[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M)};
   const uint64_t db[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N)};
+  const uint64_t dy[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)};
   const uint64_t sta[1] = {static_cast<uint64_t>(p.lda)}, stb[1] = {static_cast<uint64_t>(p.ldb)};
-  const uint32_t ba[2] = {kTmaBoxBytes, kTileM}, bb[2] = {kTmaBoxBytes, kN};
-  if (int e = pw::encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, da, sta, ba)) return e;
-  if (int e = pw::encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, bb)) return e;
-  const long long tiles = static_cast<long long>((p.M + kTileM - 1) / kTileM) * ((p.N + kN - 1) / kN);
-  linear_tile_kernel<T, kN><<<static_cast<unsigned>(tiles < sms ? tiles : sms), C::kThreads, C::kSmem, s>>>(p, ma, mb);
-  PW_CUDA_TRY(cudaGetLastError());
+  const uint64_t sty[1] = {2 * static_cast<uint64_t>(p.ldy)};
+  const uint32_t box[2] = {kBoxBytes, 128}, boxy[2] = {64, 32};
+  if (int e = pw::encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, da, sta, box)) return e;
+  if (int e = pw::encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, box)) return e;
+  my = msa = msb = ma;
+  if (p.wide_scales) {
+    const uint64_t dsa[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>(p.M)};
+    const uint64_t dsb[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>((p.N + pw::kGroup - 1) / pw::kGroup)};
+    const uint64_t stsa[1] = {4 * static_cast<uint64_t>(p.sa_stride)}, stsb[1] = {4 * static_cast<uint64_t>(p.sb_stride)};
+    const uint32_t boxa[2] = {4, 128}, boxb[2] = {4, C::kN / 128};
+    if (int e = pw::encode_tensor_map(&msa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.sa, dsa, stsa, boxa, false)) return e;
+    if (int e = pw::encode_tensor_map(&msb, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.sb, dsb, stsb, boxb, false)) return e;
+  }
+  if (p.wide_y)
+    if (int e = pw::encode_tensor_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, p.y, dy, sty, boxy)) return e;
+  const long long tiles = static_cast<long long>((p.M + C::kM - 1) / C::kM) * ((p.N + C::kN - 1) / C::kN);
+  int cluster = 1;
+  long long ctas;
+  if (kPair) {
+    cluster = 2;
+    ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
+  } else {
+    // few tiles: up to 8 CTAs share one's groups, as long as all run at once
+    // and each has two groups
+    p.splits = 1;
+    while (p.splits < 8 && tiles * (p.splits + 1) <= sms && p.KB >= 2 * (p.splits + 1)) ++p.splits;
+    cluster = p.splits;
+    ctas = p.splits > 1 ? tiles * p.splits : (tiles < sms ? tiles : sms);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_tile_kernel<T, kPair>, p, ma, mb, my, msa, msb));
   return PW_OK;
 }
 
 template <typename T>
 int launch(const LinearParams& p, cudaStream_t s) {
+  const int sms = pw::sm_count();
+  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   if (p.M <= 8) return launch_stream<T, 1>(p, s);
   if (p.M <= 16) return launch_stream<T, 2>(p, s);
-  if (p.M <= 64) return launch_stream<T, 4>(p, s);
-  // wide tiles once they fill the SMs: half the weight reads per product
-  const long long wide = static_cast<long long>((p.M + kTileM - 1) / kTileM) * ((p.N + 255) / 256);
-  return wide >= pw::sm_count() ? launch_tile<T, 256>(p, s) : launch_tile<T, 128>(p, s);
+  const long long pairs = static_cast<long long>((p.M + 255) / 256) * ((p.N + 255) / 256);
+  return pairs >= sms / 2 ? launch_tile<T, true>(p, sms, s) : launch_tile<T, false>(p, sms, s);
 }
 
 }  // namespace
@@ -374,8 +582,10 @@ extern "C" int pw_fp8_linear(const uint8_t* d_a, int64_t lda, const float* d_a_s
   p.K = K;
   p.KB = kb;
   p.status = d_status;
-  p.wait_ns = 2000000000ull;
   p.wide_y = pw::aligned(d_y, 16) && ldy % 8 == 0;
+  // with one group a tile the slots of the scales would be reused too early
+  p.wide_scales = kb >= 2 && pw::aligned(d_a_scale, 16) && pw::aligned(d_b_scale, 16) && a_scale_stride % 4 == 0 &&
+                  b_scale_stride % 4 == 0;
   cudaStream_t s = pw::as_stream(stream);
   return dtype == PW_DTYPE_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
 }

@@ -31,29 +31,24 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // ---------------------------------------------------------------- bounded waits
-// Waits for phase `parity`, at most `limit_ns`.  A wait that runs out reports
+// A whole warp waits for phase `parity`.  Each try sleeps up to 1 us; after
+// kWaitTries of them (80 ms at the least, seconds in practice; the waits here
+// are for the CTA's own work and take microseconds) the wait reports
 // PW_ERR_TIMEOUT and sets the CTA's `dead` word, which ends every other wait of
-// the CTA: the caller stops issuing work, lets its own finish and returns.
-__device__ __forceinline__ bool wait_or_dead(const uint64_t* bar, uint32_t parity, int* dead, int32_t* status,
-                                             uint64_t limit_ns) {
+// the CTA: the caller stops issuing work, lets its own finish and returns.  The
+// lanes leave together.  Kept this short because every role holds copies of it
+// in the instruction cache.
+constexpr int kWaitTries = 1 << 22;
+__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, int* dead, int32_t* status) {
   const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait_hint(b, parity, 1000)) return true;
-  const uint64_t t0 = global_ns();
-  while (!mbar_try_wait_hint(b, parity, 1000)) {
-    if (*reinterpret_cast<volatile int*>(dead)) return false;
-    if (global_ns() - t0 > limit_ns) {
-      *reinterpret_cast<volatile int*>(dead) = 1;
-      if (status) atomicCAS(status, 0, PW_ERR_TIMEOUT);
+  int tries = 0;
+  while (!__all_sync(0xFFFFFFFFu, mbar_try_wait_hint(b, parity, 1000))) {
+    if (__any_sync(0xFFFFFFFFu, ++tries > kWaitTries || *reinterpret_cast<volatile int*>(dead))) {
+      if (atomicExch(dead, 1) == 0) atomicCAS(status, 0, PW_ERR_TIMEOUT);
       return false;
     }
   }
   return true;
-}
-// The same for a whole warp: its lanes leave together (one may see the
-// barrier, another the failure).
-__device__ __forceinline__ bool warp_wait_or_dead(const uint64_t* bar, uint32_t parity, int* dead, int32_t* status,
-                                                  uint64_t limit_ns) {
-  return __all_sync(0xFFFFFFFFu, wait_or_dead(bar, parity, dead, status, limit_ns));
 }
 
 // ---------------------------------------------------------------- matrix instructions
@@ -76,6 +71,64 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// The same by a pair of CTAs: 256 rows of A (128 in each CTA's shared memory),
+// N rows of B (half in each), and each CTA's Tensor Memory gets its 128 rows.
+// One thread of the pair's first CTA issues it.
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs of the pair once the
+// thread's matrix instructions have completed.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Arrives on a barrier of any CTA of the cluster.  Orders nothing but this
+// thread's tcgen05 work (with the fence before it): a release at cluster scope
+// costs over 1000 cycles and has no memory to publish here.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
 }
 
 // Instruction descriptor: D fp32, A K-major, shape M x N.  kind::f8f6f4 with
@@ -108,6 +161,25 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
+// A copy into this CTA's shared memory that completes on a barrier of the
+// pair's first CTA (a shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int c0, int c1, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's stores have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
