@@ -40,67 +40,60 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K, bool v
 }
 
 // Few tokens: the weights stream from memory into registers.  A CTA owns 16
-// weight rows and 8 * kTiles tokens; its warps take every eighth group of 128
-// columns.  A lane loads 16 contiguous bytes of a row and feeds them to two
-// MMAs as if they were the four columns each of those wants: the same
-// reordering of k on both operands leaves the sum as it is.
-template <typename T, int kTiles>
+// weight rows and 8 tokens; its warps take every eighth group of 128 columns.
+// A lane loads 16 contiguous bytes of a row and feeds them to two MMAs as if
+// they were the four columns each of those wants: the same reordering of k on
+// both operands leaves the sum as it is.  Memory bounds it; 32 warps an SM keep
+// enough loads in flight (two or four groups a warp at once came out slower).
+// 1 x 6144 x 4096: 7.8 us, 3.2 TB/s of weights with the launch included.
+template <typename T>
 __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid_constant__ LinearParams p) {
-  __shared__ float red[kWarps][kRows][8 * kTiles + 1];
+  __shared__ float red[kWarps][kRows][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kRows, m0 = blockIdx.y * 8 * kTiles;
+  const int n0 = blockIdx.x * kRows;
   const uint8_t* b_lo = p.b + static_cast<int64_t>(n0 + g) * p.ldb;
   const uint8_t* b_hi = b_lo + 8 * p.ldb;
-  const bool v_lo = n0 + g < p.N, v_hi = n0 + g + 8 < p.N;
+  const uint8_t* a = p.a + static_cast<int64_t>(g) * p.lda;
+  const bool v_lo = n0 + g < p.N, v_hi = n0 + g + 8 < p.N, v_a = g < p.M;
   const float* sb = p.sb + (n0 / pw::kGroup) * p.sb_stride;
-  float sum[kTiles][4] = {};
+  const int c = 2 * t;   // the lane's two tokens of the result
+  const float* sa0 = p.sa + static_cast<int64_t>(c < p.M ? c : 0) * p.sa_stride;
+  const float* sa1 = p.sa + static_cast<int64_t>(c + 1 < p.M ? c + 1 : 0) * p.sa_stride;
+  float sum[4] = {};
   for (int kb = warp; kb < p.KB; kb += kWarps) {
     const int k = kb * pw::kGroup + 16 * t;
     const uint4 w0 = load16(b_lo, k, p.K, v_lo), w1 = load16(b_hi, k, p.K, v_hi);
     const uint4 w2 = load16(b_lo, k + 64, p.K, v_lo), w3 = load16(b_hi, k + 64, p.K, v_hi);
-    const float s = sb[kb];
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      const int m = m0 + 8 * j + g;
-      const uint8_t* a = p.a + static_cast<int64_t>(m) * p.lda;
-      const uint4 x0 = load16(a, k, p.K, m < p.M), x1 = load16(a, k + 64, p.K, m < p.M);
-      float acc[4] = {};
-      pw::mma_16832_e4m3(acc, w0.x, w1.x, w0.y, w1.y, x0.x, x0.y);
-      pw::mma_16832_e4m3(acc, w0.z, w1.z, w0.w, w1.w, x0.z, x0.w);
-      pw::mma_16832_e4m3(acc, w2.x, w3.x, w2.y, w3.y, x1.x, x1.y);
-      pw::mma_16832_e4m3(acc, w2.z, w3.z, w2.w, w3.w, x1.z, x1.w);
-      const int c = m0 + 8 * j + 2 * t;   // the lane's two tokens of the result
-      const float s0 = c < p.M ? s * p.sa[c * p.sa_stride + kb] : 0.0f;
-      const float s1 = c + 1 < p.M ? s * p.sa[(c + 1) * p.sa_stride + kb] : 0.0f;
-      sum[j][0] += s0 * acc[0];
-      sum[j][1] += s1 * acc[1];
-      sum[j][2] += s0 * acc[2];
-      sum[j][3] += s1 * acc[3];
-    }
+    const uint4 x0 = load16(a, k, p.K, v_a), x1 = load16(a, k + 64, p.K, v_a);
+    const float s = __ldg(sb + kb), s0 = s * __ldg(sa0 + kb), s1 = s * __ldg(sa1 + kb);
+    float acc[4] = {};
+    pw::mma_16832_e4m3(acc, w0.x, w1.x, w0.y, w1.y, x0.x, x0.y);
+    pw::mma_16832_e4m3(acc, w0.z, w1.z, w0.w, w1.w, x0.z, x0.w);
+    pw::mma_16832_e4m3(acc, w2.x, w3.x, w2.y, w3.y, x1.x, x1.y);
+    pw::mma_16832_e4m3(acc, w2.z, w3.z, w2.w, w3.w, x1.z, x1.w);
+    sum[0] += s0 * acc[0];
+    sum[1] += s1 * acc[1];
+    sum[2] += s0 * acc[2];
+    sum[3] += s1 * acc[3];
   }
-#pragma unroll
-  for (int j = 0; j < kTiles; ++j) {
-    red[warp][g][8 * j + 2 * t] = sum[j][0];
-    red[warp][g][8 * j + 2 * t + 1] = sum[j][1];
-    red[warp][g + 8][8 * j + 2 * t] = sum[j][2];
-    red[warp][g + 8][8 * j + 2 * t + 1] = sum[j][3];
-  }
+  red[warp][g][2 * t] = sum[0];
+  red[warp][g][2 * t + 1] = sum[1];
+  red[warp][g + 8][2 * t] = sum[2];
+  red[warp][g + 8][2 * t + 1] = sum[3];
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * 8 * kTiles; i += 32 * kWarps) {
-    const int row = i % kRows, col = i / kRows;
+  if (threadIdx.x < kRows * 8) {
+    const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][row][col];
-    if (n0 + row < p.N && m0 + col < p.M)
-      static_cast<T*>(p.y)[static_cast<int64_t>(m0 + col) * p.ldy + n0 + row] = pw::from_float<T>(v);
+    for (int i = 0; i < kWarps; ++i) v += red[i][row][col];
+    if (n0 + row < p.N && col < p.M)
+      static_cast<T*>(p.y)[static_cast<int64_t>(col) * p.ldy + n0 + row] = pw::from_float<T>(v);
   }
 }
 
-template <typename T, int kTiles>
+template <typename T>
 int launch_stream(const LinearParams& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.N + kRows - 1) / kRows),
-                  static_cast<unsigned>((p.M + 8 * kTiles - 1) / (8 * kTiles)));
-  linear_stream_kernel<T, kTiles><<<grid, 32 * kWarps, 0, s>>>(p);
+  linear_stream_kernel<T><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), 32 * kWarps, 0, s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -115,8 +108,8 @@ int launch_stream(const LinearParams& p, cudaStream_t s) {
 //  kPair: 256 tokens x 256 weight rows by a pair of CTAs, persistent.  Each
 //    CTA holds half of both operands, so a group costs its shared memory 32 KB
 //    in and 32 KB out for 512 cycles of matrix work: at 128 bytes a cycle both
-//    are busy to the end.  (One CTA with 128 x 256 moves 96 KB for the same
-//    work and stays at two thirds: 360 us instead of PAIR_US for 8192^2 x 6144.)
+//    are busy to the end.  (128 x 128 by one CTA move twice that for the same
+//    work: 406 us instead of 310 for 8192 x 8192 x 6144.)
 //  otherwise: 128 x 128 by one CTA, for fewer tokens; with few tiles the groups
 //    are split among the CTAs of a cluster, which add their sums through
 //    distributed shared memory, in the order of their ranks.
@@ -127,24 +120,30 @@ constexpr int kSumWarps = 8;
 constexpr int kCopyWarp = kSumWarps, kMmaWarp = kSumWarps + 1;
 
 constexpr int kOutBytes = 32 * 64 * 2;     // 32 rows x 64 columns of 16-bit results on their way out, of one warp
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 8;
 constexpr int kTokenScaleBytes = 128 * 16;             // the token scales of four groups
 constexpr int kScaleBytes = kTokenScaleBytes + 128;    // and the weight scales of the tile's 128-row blocks
 
-template <bool kPair>
+template <int kTokens, int kWide>
 struct Tile {
-  static constexpr int kM = kPair ? 256 : 128;        // tokens
-  static constexpr int kN = kPair ? 256 : 128;        // weight rows
-  static constexpr int kCols = kN / 2;                // of one warpgroup
-  static constexpr int kStages = 5;
-  static constexpr int kThreads = kPair ? 384 : 320;  // whole warpgroups where registers are moved
-  static constexpr int kStageBytes = 2 * 128 * kBoxBytes;   // a CTA's 128 rows of each operand
+  static constexpr bool kPair = kTokens == 256;
+  static constexpr int kM = kTokens;                  // tokens
+  static constexpr int kN = kWide;                    // weight rows
+  static constexpr int kRowsA = kPair ? 128 : kM;     // of both, in one CTA's shared memory
+  static constexpr int kRowsB = kPair ? kN / 2 : kN;
+  static constexpr int kCols = kN / 2;                // of one warpgroup's sums
+  static constexpr int kQuarters = kRowsA / 32;       // warps of a warpgroup with tokens
+  static constexpr int kStages = kRowsA == 128 ? 5 : 7;
+  static constexpr int kAccs = 512 / kN;              // accumulators in Tensor Memory
+  static constexpr bool kMove = kN == 256;            // registers move to the sums
+  static constexpr int kThreads = kMove ? 384 : 320;  // whole warpgroups for that
+  static constexpr int kStageBytes = (kRowsA + kRowsB) * kBoxBytes;
   static constexpr int kSmem = kStages * kStageBytes + kSumWarps * kOutBytes + kScaleSlots * kScaleBytes + 1024;
 };
 constexpr int kPartRow = 132;       // floats of a row of sums in shared memory: 16-byte lanes on distinct banks
 
 struct alignas(8) TileShared {
-  uint64_t full[5], empty[5], done[2], read[2], scales[kScaleSlots], drained;
+  uint64_t full[7], empty[7], done[4], read[4], scales[kScaleSlots], drained;
   uint32_t tmem;
   int dead;   // a wait ran out: everybody leaves
 };
@@ -155,21 +154,22 @@ __device__ __forceinline__ bool wait(const uint64_t& bar, uint32_t parity, TileS
 
 // Tiles in strips of 2048 tokens, so that the CTAs that run at the same time
 // share both operands through L2.
-template <bool kPair>
+template <int kM>
 __device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int& mt, int& nt) {
-  constexpr int kStrip = 2048 / Tile<kPair>::kM;
+  constexpr int kStrip = 2048 / kM;
   const int per_strip = kStrip * tiles_n, strip = tile / per_strip, r = tile - strip * per_strip;
   const int height = min(kStrip, tiles_m - strip * kStrip);
   nt = r / height;
   mt = strip * kStrip + r - nt * height;
 }
 
-template <typename T, bool kPair>
-__global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
+template <typename T, int kTokens, int kWide>
+__global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ LinearParams p, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_y,
                        const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb) {
-  using C = Tile<kPair>;
+  using C = Tile<kTokens, kWide>;
+  constexpr bool kPair = C::kPair;
   extern __shared__ unsigned char smem_raw[];
   __shared__ TileShared sh;
   unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -186,9 +186,9 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
       pw::mbar_init(pw::smem_u32(&sh.full[i]), 1);
       pw::mbar_init(pw::smem_u32(&sh.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kAccs; ++i) {
       pw::mbar_init(pw::smem_u32(&sh.done[i]), 1);
-      pw::mbar_init(pw::smem_u32(&sh.read[i]), kSumWarps * (kPair ? 2 : 1));
+      pw::mbar_init(pw::smem_u32(&sh.read[i]), 2 * C::kQuarters * (kPair ? 2 : 1));
     }
     for (int i = 0; i < kScaleSlots; ++i) pw::mbar_init(pw::smem_u32(&sh.scales[i]), 1);
     pw::mbar_init(pw::smem_u32(&sh.drained), 1);
@@ -197,9 +197,9 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
   }
   if (warp == kCopyWarp) {
     if constexpr (kPair) {
-      pw::tmem_alloc_pair(pw::smem_u32(&sh.tmem), 2 * C::kN);
+      pw::tmem_alloc_pair(pw::smem_u32(&sh.tmem), 512);
     } else {
-      pw::tmem_alloc(pw::smem_u32(&sh.tmem), 2 * C::kN);
+      pw::tmem_alloc(pw::smem_u32(&sh.tmem), 512);
       pw::tmem_relinquish();
     }
   }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
   const uint32_t scale_smem = stages + C::kStages * C::kStageBytes + kSumWarps * kOutBytes;
 
   if (warp == kCopyWarp) {
-    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (C::kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (pw::elect_one()) {
       pw::prefetch_tmap(&map_a);
       pw::prefetch_tmap(&map_b);
@@ -219,28 +219,32 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
       pw::prefetch_tmap(&map_sa);
       pw::prefetch_tmap(&map_sb);
     }
+    pw::Ring<C::kStages> stage;
+    pw::Ring<kScaleSlots> slot;
     uint32_t x = 0, fours = 0;   // groups, and fours of groups, started
     bool ok = true;
     for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       int mt, nt;
-      tile_at<kPair>(tile, tiles_m, tiles_n, mt, nt);
-      const int row_a = mt * C::kM + (kPair ? 128 * rank : 0), row_b = nt * C::kN + (kPair ? 128 * rank : 0);
+      tile_at<C::kM>(tile, tiles_m, tiles_n, mt, nt);
+      const int row_a = mt * C::kM + (kPair ? 128 * rank : 0), row_b = nt * C::kN + (kPair ? C::kRowsB * rank : 0);
       for (int kb = kb0; kb < kb1; ++kb, ++x) {
-        const uint32_t s = x % C::kStages;
-        if (x >= C::kStages && !(ok = wait(sh.empty[s], (x / C::kStages + 1) & 1u, sh, p))) break;
-        const uint32_t bar = pw::smem_u32(&sh.full[s]), dst = stages + s * C::kStageBytes;
+        if (x >= C::kStages && !(ok = wait(sh.empty[stage.at], stage.parity ^ 1u, sh, p))) break;
+        const uint32_t bar = pw::smem_u32(&sh.full[stage.at]), dst = stages + stage.at * C::kStageBytes;
+        stage.next();
         if (p.wide_scales && (kb == kb0 || (kb & 3) == 0)) {
-          // The slot is free: the MMAs of group x - 5 are done, they were issued
-          // after every warp had read the accumulator of group x - 7, and the
-          // slot's last user is at least seven groups back (three fours of a
+          // The slot is free: the MMAs of group x - kStages are done, they were issued
+          // after every warp had read the accumulator of group x - kStages -
+          // kAccs (at most 11 back), and the slot's last user is at least 14 back (seven fours of a
           // tile of two groups or more).
-          const uint32_t slot = fours++ % kScaleSlots, sbar = pw::smem_u32(&sh.scales[slot]);
+          const uint32_t sbar = pw::smem_u32(&sh.scales[slot.at]);
           if (pw::elect_one()) {
-            const uint32_t dst = scale_smem + slot * kScaleBytes;
-            pw::mbar_arrive_expect_tx(sbar, kTokenScaleBytes + 16 * (C::kN / 128));
+            const uint32_t dst = scale_smem + slot.at * kScaleBytes;
+            pw::mbar_arrive_expect_tx(sbar, 16 * (C::kRowsA + C::kN / 128));
             pw::tma_load_2d(dst, &map_sa, kb & ~3, row_a, sbar);
             pw::tma_load_2d(dst + kTokenScaleBytes, &map_sb, kb & ~3, nt * (C::kN / 128), sbar);
           }
+          ++fours;
+          slot.next();
           __syncwarp();
         }
         if (pw::elect_one()) {
@@ -249,11 +253,11 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
             if (rank == 0) pw::mbar_arrive_expect_tx(bar, 2 * C::kStageBytes);
             const uint32_t lead = pw::map_shared(bar, 0);
             pw::tma_load_2d_pair(dst, &map_a, kb * pw::kGroup, row_a, lead);
-            pw::tma_load_2d_pair(dst + 128 * kBoxBytes, &map_b, kb * pw::kGroup, row_b, lead);
+            pw::tma_load_2d_pair(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, lead);
           } else {
             pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
             pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, row_a, bar);
-            pw::tma_load_2d(dst + 128 * kBoxBytes, &map_b, kb * pw::kGroup, row_b, bar);
+            pw::tma_load_2d(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, bar);
           }
         }
         __syncwarp();
@@ -268,19 +272,24 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
       for (uint32_t i = fours > kScaleSlots ? fours - kScaleSlots : 0; i < fours; ++i)
         pw::mbar_wait(pw::smem_u32(&sh.scales[i % kScaleSlots]), (i / kScaleSlots) & 1u, kDrainNs);
   } else if (warp == kMmaWarp) {
-    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (C::kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (!kPair || rank == 0) {
-      constexpr uint32_t kIdesc = pw::idesc_f32(C::kM, C::kN, false, false);
-      uint32_t x = 0;
+      // (fewer tokens than the 128 lanes: the rows after them are those of the
+      // weights, in lanes that nobody reads)
+      constexpr uint32_t kIdesc = pw::idesc_f32(kPair ? 256 : 128, C::kN, false, false);
+      pw::Ring<C::kStages> stage;
+      pw::Ring<C::kAccs> acc;
       bool ok = true;
       for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++x) {
-          const uint32_t s = x % C::kStages, buf = x & 1u;
-          if (x >= 2) ok = wait(sh.read[buf], ((x >> 1) + 1) & 1u, sh, p);
-          if (!ok || !(ok = wait(sh.full[s], (x / C::kStages) & 1u, sh, p))) break;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          // (an accumulator's first use waits for the phase before the first: passed)
+          if (!(ok = pw::warp_wait2(&sh.full[stage.at], stage.parity, &sh.read[acc.at], acc.parity ^ 1u, &sh.dead,
+                                    p.status)))
+            break;
           pw::tc_fence_after();
+          const uint32_t s = stage.at, buf = acc.at;
           const uint64_t a = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes);
-          const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + 128 * kBoxBytes);
+          const uint64_t b = pw::sdesc_kmajor_sw128(stages + s * C::kStageBytes + C::kRowsA * kBoxBytes);
           if (pw::elect_one()) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {   // 32 columns a step: 2 units of 16 bytes
@@ -297,6 +306,8 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
               pw::tc_commit(pw::smem_u32(&sh.done[buf]));
             }
           }
+          stage.next();
+          acc.next();
           __syncwarp();
         }
       }
@@ -311,20 +322,21 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
         pw::mbar_wait(pw::smem_u32(&sh.drained), 0, kDrainNs);
       }
     }
-  } else if (warp > kMmaWarp) {
-    if constexpr (kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");   // a warpgroup gives as a whole
+  } else if (warp > kMmaWarp || (warp & 3) >= C::kQuarters) {
+    if constexpr (C::kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");   // a warpgroup gives as a whole
   } else {
     // sums; registers: 256 threads x 208 and 128 x 88 are the pair kernel's 384 x 168
-    if constexpr (kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (C::kMove) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int quarter = warp & 3, side = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t read0 = kPair ? pw::map_shared(pw::smem_u32(&sh.read[0]), 0) : pw::smem_u32(&sh.read[0]);
     unsigned char* out = smem + C::kStages * C::kStageBytes + warp * kOutBytes;
-    uint32_t x = 0, fours = 0;
+    pw::Ring<C::kAccs> acc;
+    pw::Ring<kScaleSlots> slot;
     bool ok = true;
     for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       int mt, nt;
-      tile_at<kPair>(tile, tiles_m, tiles_n, mt, nt);
+      tile_at<C::kM>(tile, tiles_m, tiles_n, mt, nt);
       const int m0 = mt * C::kM + (kPair ? 128 * rank : 0) + 32 * quarter, m = m0 + lane;
       const int n0 = nt * C::kN + C::kCols * side;
       const float* sa = p.sa + static_cast<int64_t>(m < p.M ? m : 0) * p.sa_stride;
@@ -335,43 +347,34 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
       // Scales, four groups at a time, through shared memory where their layout
       // allows: a load from here would queue behind the ring's copies, 160 KB
       // of them, and hold up the sums for 450 cycles at every fourth group.
-      for (int four = kb0 & ~3; ok && four < kb1; four += 4) {
-        float a_now[4], b_now[4];
+      const unsigned char* scales = smem + (scale_smem - stages);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t buf = acc.at;
+        float sc;
         if (p.wide_scales) {
-          const uint32_t slot = fours % kScaleSlots;
-          if (!(ok = wait(sh.scales[slot], (fours / kScaleSlots) & 1u, sh, p))) break;
-          ++fours;
-          const unsigned char* src = smem + (scale_smem - stages) + slot * kScaleBytes;
-          const float4 f = *reinterpret_cast<const float4*>(src + (32 * quarter + lane) * 16);
-          const float4 g = *reinterpret_cast<const float4*>(src + kTokenScaleBytes + (kPair ? 16 * side : 0));
-          a_now[0] = f.x, a_now[1] = f.y, a_now[2] = f.z, a_now[3] = f.w;
-          b_now[0] = g.x, b_now[1] = g.y, b_now[2] = g.z, b_now[3] = g.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a_now[i] = four + i < kb1 ? __ldg(sa + four + i) : 0.0f;
-            b_now[i] = four + i < kb1 ? __ldg(sb + four + i) : 0.0f;
+          if (kb == kb0 || (kb & 3) == 0) {
+            if (!(ok = wait(sh.scales[slot.at], slot.parity, sh, p))) break;
+            scales = smem + (scale_smem - stages) + slot.at * kScaleBytes;
+            slot.next();
           }
+          sc = *reinterpret_cast<const float*>(scales + (32 * quarter + lane) * 16 + 4 * (kb & 3)) *
+               *reinterpret_cast<const float*>(scales + kTokenScaleBytes + (C::kN == 256 ? 16 * side : 0) + 4 * (kb & 3));
+        } else {
+          sc = __ldg(sa + kb) * __ldg(sb + kb);
         }
-#pragma unroll 1
-        for (int kb = max(four, kb0); kb < min(four + 4, kb1); ++kb, ++x) {
-        const uint32_t buf = x & 1u;
-        const int at = kb & 3;
-        const float sc = (at & 2 ? (at & 1 ? a_now[3] : a_now[2]) : (at & 1 ? a_now[1] : a_now[0])) *
-                         (at & 2 ? (at & 1 ? b_now[3] : b_now[2]) : (at & 1 ? b_now[1] : b_now[0]));
         const uint64_t scale = pw::pack_f32x2(__float_as_uint(sc), __float_as_uint(sc));
-        if (!(ok = wait(sh.done[buf], (x >> 1) & 1u, sh, p))) break;
+        if (!(ok = wait(sh.done[buf], acc.parity, sh, p))) break;
         pw::tc_fence_after();
         const uint32_t src = tmem + lanes + buf * C::kN + C::kCols * side;
         uint32_t v[2][16];
-        pw::tmem_ld_x16(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < C::kCols / 16; ++c) {
+        for (int c = 0; c < C::kCols / 32; ++c) {
+          pw::tmem_ld_x16(src + 32 * c, v[0]);
+          pw::tmem_ld_x16(src + 32 * c + 16, v[1]);
           pw::tmem_ld_wait();
-          if (c + 1 < C::kCols / 16) pw::tmem_ld_x16(src + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            sum[8 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[c & 1][2 * i], v[c & 1][2 * i + 1]), scale, sum[8 * c + i]);
+          for (int i = 0; i < 16; ++i)
+            sum[16 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[i / 8][2 * (i % 8)], v[i / 8][2 * (i % 8) + 1]), scale, sum[16 * c + i]);
         }
         pw::tc_fence_before();
         __syncwarp();
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
           else
             pw::mbar_arrive(read0 + 8 * buf);
         }
-      }
+        acc.next();
       }
       if (!ok) break;
       if (!kPair && p.splits > 1) {
@@ -441,16 +444,16 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
   pw::tc_fence_after();
   if (warp == kCopyWarp) {
     if constexpr (kPair)
-      pw::tmem_dealloc_pair(tmem, 2 * C::kN);
+      pw::tmem_dealloc_pair(tmem, 512);
     else
-      pw::tmem_dealloc(tmem, 2 * C::kN);
+      pw::tmem_dealloc(tmem, 512);
   }
   if constexpr (!kPair) {
     if (p.splits > 1) {
       // each CTA of the cluster finishes its share of the tile's rows
       int mt, nt;
-      tile_at<kPair>(first_tile, tiles_m, tiles_n, mt, nt);
-      const int rows = min(128, p.M - mt * 128), col = 4 * lane, n = nt * 128 + col;
+      tile_at<C::kM>(first_tile, tiles_m, tiles_n, mt, nt);
+      const int rows = min(C::kM, p.M - mt * C::kM), col = 4 * lane, n = nt * 128 + col;
       for (int row = rank + p.splits * warp; row < rows; row += p.splits * (C::kThreads / 32)) {
         const uint32_t at = stages + 4u * static_cast<uint32_t>(row * kPartRow + col);
         float4 v = pw::ld_cluster_f4(pw::map_shared(at, 0));
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
           v.w += w.w;
         }
         if (sh.dead) continue;
-        T* y = static_cast<T*>(p.y) + static_cast<int64_t>(mt * 128 + row) * p.ldy + n;
+        T* y = static_cast<T*>(p.y) + static_cast<int64_t>(mt * C::kM + row) * p.ldy + n;
         if (p.wide_y && n + 4 <= p.N) {
           *reinterpret_cast<uint2*>(y) = make_uint2(pw::pack2<T>(v.x, v.y), pw::pack2<T>(v.z, v.w));
         } else {
@@ -477,15 +480,41 @@ __global__ void __launch_bounds__(Tile<kPair>::kThreads, 1)
   }
 }
 
-template <typename T, bool kPair>
+// How many clusters of n CTAs the device runs at once (asked once per device).
+template <typename T, int kTokens, int kWide>
+int clusters_at_once(int dev, int n, int& fit) {
+  using C = Tile<kTokens, kWide>;
+  constexpr int kDevs = 64;
+  static int known[kDevs][8] = {};
+  if (dev < kDevs && known[dev][n]) {
+    fit = known[dev][n] - 1;
+    return PW_OK;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(n));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(n);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  PW_CUDA_TRY(cudaOccupancyMaxActiveClusters(&fit, linear_tile_kernel<T, kTokens, kWide>, &cfg));
+  if (dev < kDevs) known[dev][n] = fit + 1;
+  return PW_OK;
+}
+
+template <typename T, int kTokens, int kWide>
 int launch_tile(LinearParams p, int sms, cudaStream_t s) {
-  using C = Tile<kPair>;
+  using C = Tile<kTokens, kWide>;
+  constexpr bool kPair = C::kPair;
   constexpr int kDevs = 64;
   static bool attr_done[kDevs] = {};
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= kDevs || !attr_done[dev]) {
-    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kTokens, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
     if (dev < kDevs) attr_done[dev] = true;
   }
   CUtensorMap ma, mb, my, msa, msb;
@@ -494,15 +523,15 @@ int launch_tile(LinearParams p, int sms, cudaStream_t s) {
   const uint64_t dy[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)};
   const uint64_t sta[1] = {static_cast<uint64_t>(p.lda)}, stb[1] = {static_cast<uint64_t>(p.ldb)};
   const uint64_t sty[1] = {2 * static_cast<uint64_t>(p.ldy)};
-  const uint32_t box[2] = {kBoxBytes, 128}, boxy[2] = {64, 32};
+  const uint32_t box[2] = {kBoxBytes, C::kRowsA}, boxw[2] = {kBoxBytes, C::kRowsB}, boxy[2] = {64, 32};
   if (int e = pw::encode_tensor_map(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, da, sta, box)) return e;
-  if (int e = pw::encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, box)) return e;
+  if (int e = pw::encode_tensor_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, boxw)) return e;
   my = msa = msb = ma;
   if (p.wide_scales) {
     const uint64_t dsa[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>(p.M)};
     const uint64_t dsb[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>((p.N + pw::kGroup - 1) / pw::kGroup)};
     const uint64_t stsa[1] = {4 * static_cast<uint64_t>(p.sa_stride)}, stsb[1] = {4 * static_cast<uint64_t>(p.sb_stride)};
-    const uint32_t boxa[2] = {4, 128}, boxb[2] = {4, C::kN / 128};
+    const uint32_t boxa[2] = {4, C::kRowsA}, boxb[2] = {4, C::kN / 128};
     if (int e = pw::encode_tensor_map(&msa, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.sa, dsa, stsa, boxa, false)) return e;
     if (int e = pw::encode_tensor_map(&msb, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p.sb, dsb, stsb, boxb, false)) return e;
   }
@@ -515,10 +544,16 @@ int launch_tile(LinearParams p, int sms, cudaStream_t s) {
     cluster = 2;
     ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   } else {
-    // few tiles: up to 8 CTAs share one's groups, as long as all run at once
-    // and each has two groups
+    // Few tiles: 2 or 4 CTAs share one's groups, as long as all clusters run at
+    // once (4 do not fit everywhere) and each CTA has two groups.  A step less
+    // of the loop takes 0.2 us, a cluster's addition about 1: 32 x 4096 x 4096
+    // takes 14.2, 10.3 and 9.2 us with 1, 2 and 4.
     p.splits = 1;
-    while (p.splits < 8 && tiles * (p.splits + 1) <= sms && p.KB >= 2 * (p.splits + 1)) ++p.splits;
+    for (int n = 2; n <= 4; n *= 2) {
+      int fit = 0;
+      if (int e = clusters_at_once<T, kTokens, kWide>(dev, n, fit)) return e;
+      if (tiles <= fit && p.KB >= 2 * n) p.splits = n;
+    }
     cluster = p.splits;
     ctas = p.splits > 1 ? tiles * p.splits : (tiles < sms ? tiles : sms);
   }
@@ -533,7 +568,7 @@ int launch_tile(LinearParams p, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_tile_kernel<T, kPair>, p, ma, mb, my, msa, msb));
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_tile_kernel<T, kTokens, kWide>, p, ma, mb, my, msa, msb));
   return PW_OK;
 }
 
@@ -541,10 +576,18 @@ template <typename T>
 int launch(const LinearParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
-  if (p.M <= 8) return launch_stream<T, 1>(p, s);
-  if (p.M <= 16) return launch_stream<T, 2>(p, s);
+  // Up to 8 tokens, the weights stream through the warps' registers (8 x 6144 x
+  // 4096: 8.2 us, 11 by tiles); with 16 the tiles are ahead (10.9, 11.9 us).
+  if (p.M <= 8) return launch_stream<T>(p, s);
+  if (p.M <= 64) return launch_tile<T, 64, 128>(p, sms, s);
+  // Above, whichever needs less time in whole rounds over the SMs: a round of
+  // pairs takes 1.5 times one of single CTAs (14.0 and 9.7 us at K = 4096) and
+  // does twice the work.  1024 x 6144 x 4096: 33 and 35 us; 509 x 4096 x 4096:
+  // 18 and 14.2 us.
   const long long pairs = static_cast<long long>((p.M + 255) / 256) * ((p.N + 255) / 256);
-  return pairs >= sms / 2 ? launch_tile<T, true>(p, sms, s) : launch_tile<T, false>(p, sms, s);
+  const long long singles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
+  const long long pair_rounds = (pairs + sms / 2 - 1) / (sms / 2), single_rounds = (singles + sms - 1) / sms;
+  return 3 * pair_rounds <= 2 * single_rounds ? launch_tile<T, 256, 256>(p, sms, s) : launch_tile<T, 128, 128>(p, sms, s);
 }
 
 }  // namespace

@@ -51,6 +51,26 @@ __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, 
   return true;
 }
 
+// Two barriers in one step, for a role whose waits are on its critical path.
+__device__ __forceinline__ bool warp_wait2(const uint64_t* bar1, uint32_t parity1, const uint64_t* bar2, uint32_t parity2,
+                                           int* dead, int32_t* status) {
+  const bool one = mbar_try_wait(smem_u32(bar1), parity1), two = mbar_try_wait(smem_u32(bar2), parity2);
+  if (__all_sync(0xFFFFFFFFu, one && two)) return true;
+  return warp_wait(bar1, parity1, dead, status) && warp_wait(bar2, parity2, dead, status);
+}
+
+// A position in a ring of kSize barriers and the parity of its current use.
+template <uint32_t kSize>
+struct Ring {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kSize) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 // ---------------------------------------------------------------- matrix instructions
 // D[tmem] (+)= A[smem] x B[smem]^T, e4m3 operands (K = 32 a step), fp32 accumulate.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
