@@ -110,7 +110,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
   const int box = maps.box, boxes = kBlock / box;   // at most 16 boxes of 64 values
   const uint32_t every = (1u << boxes) - 1u;
   const int step_pages = kBlock / a.page_size, step_rows = kBlock % a.page_size;
-  uint32_t y = kValues ? 1 : 0;                     // the warp's next item
+  uint32_t y = kValues ? 1 : 0, slot = y, use = 0;  // the warp's next item, its slot and how often that was used
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
     const int32_t* table = a.page_table + c.seq * a.page_table_stride;
     // this lane's box: its first key, and where that is in the page table
@@ -135,10 +135,14 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
         ++index;
       }
       page = b + 1 < b1 && wanted() ? table[index] : -1;
-      const uint32_t slot = y % kSlots, use = y / kSlots;
       if (use > 0 && !wait(&sh.empty[slot], (use + 1) & 1u, sh, p)) return false;
       const uint32_t full = bar(sh.full[slot]);
       unsigned char* dst = ring + slot * tile_bytes<D>();
+      slot += 2;
+      if (slot >= kSlots) {
+        slot -= kSlots;
+        ++use;
+      }
       if (kValues && mask != every) {
         for (int i = 0; i < boxes; ++i)
           if (!(mask >> i & 1u))
@@ -177,10 +181,12 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
                                          uint32_t q_smem, uint32_t ring) {
   constexpr uint32_t kScores = pw::idesc_f32(kHalf, kBlock, kBf16, false);
   constexpr uint32_t kValues = pw::idesc_f32(kHalf, D, kBf16, true);
-  uint32_t y = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};   // y: item of the block's keys
+  // Items of the ring: a block's keys, its values, the next block's keys, ...
+  pw::Ring<kSlots> keys, vals;
+  vals.next();
+  uint32_t q_parity[2] = {0, 0}, p_parity[2] = {0, 0};
   bool ok = true;
-  auto scores = [&](int h, uint32_t item, bool free_after) {   // S_h = Q_h K^T
-    const uint32_t slot = item % kSlots;
+  auto scores = [&](int h, uint32_t slot, bool free_after) {   // S_h = Q_h K^T
     const uint64_t q = pw::sdesc_kmajor_sw128(q_smem + h * tile_bytes<D>());
     const uint64_t k = pw::sdesc_kmajor_sw128(ring + slot * tile_bytes<D>());
     if (pw::elect_one()) {
@@ -195,8 +201,7 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
     __syncwarp();
   };
   // O_h (+)= P_h V, the first or the last 64 keys
-  auto values = [&](int h, int part, uint32_t item, bool first, bool free_after) {
-    const uint32_t slot = item % kSlots;
+  auto values = [&](int h, int part, uint32_t slot, bool first, bool free_after) {
     const uint64_t v = pw::sdesc_nmajor_sw128(ring + slot * tile_bytes<D>(), kHalfRow);
     if (pw::elect_one()) {
 #pragma unroll
@@ -212,33 +217,39 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
     }
     __syncwarp();
   };
-  auto ready = [&](uint32_t item) { return ok = wait(&sh.full[item % kSlots], (item / kSlots) & 1u, sh, p); };
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
     const int halves = halves_of(p, c);
-    for (int b = b0; b < b1; ++b, y += 2) {
-      if (b == b0) {
-        if (!ready(y) || !ready(y + 1)) return false;
-        for (int h = 0; h < halves; ++h) {
-          if (!(ok = wait(&sh.q_full[h], n_q[h] & 1u, sh, p))) return false;
-          ++n_q[h];
-          pw::tc_fence_after();
-          scores(h, y, h + 1 == halves);
-        }
-      }
+    for (int h = 0; h < halves; ++h) {
+      ok = pw::warp_wait2(&sh.full[keys.at], keys.parity, &sh.q_full[h], q_parity[h], &sh.dead, p.a.status);
+      if (!ok) return false;
+      q_parity[h] ^= 1u;
+      pw::tc_fence_after();
+      scores(h, keys.at, h + 1 == halves);
+    }
+    keys.next();
+    keys.next();
+    for (int b = b0; b < b1; ++b) {
+      const bool more = b + 1 < b1;
+      // one wait between any two groups of instructions: the queue of the
+      // tensor cores covers it
       for (int h = 0; h < halves; ++h) {
-        for (int part = 0; part < 2; ++part) {
-          if (!(ok = wait(&sh.p_full[h][part], n_p[h] & 1u, sh, p))) return false;
-          pw::tc_fence_after();
-          values(h, part, y + 1, b == b0, h + 1 == halves);
-        }
-        ++n_p[h];
-        if (b + 1 < b1) {
-          // one wait between any two groups of instructions: the queue of the
-          // tensor cores covers it
-          if (h == 0 && !ready(y + 2)) return false;
-          if (h + 1 == halves && !ready(y + 3)) return false;
-          scores(h, y + 2, h + 1 == halves);
-        }
+        ok = pw::warp_wait2(&sh.p_full[h][0], p_parity[h], &sh.full[vals.at], vals.parity, &sh.dead, p.a.status);
+        if (!ok) return false;
+        pw::tc_fence_after();
+        values(h, 0, vals.at, b == b0, false);
+        const uint64_t* next = more ? &sh.full[keys.at] : &sh.p_full[h][1];
+        ok = pw::warp_wait2(&sh.p_full[h][1], p_parity[h], next, more ? keys.parity : p_parity[h], &sh.dead, p.a.status);
+        if (!ok) return false;
+        pw::tc_fence_after();
+        values(h, 1, vals.at, b == b0, h + 1 == halves);
+        p_parity[h] ^= 1u;
+        if (more) scores(h, keys.at, h + 1 == halves);
+      }
+      vals.next();
+      vals.next();
+      if (more) {
+        keys.next();
+        keys.next();
       }
     }
     return true;
