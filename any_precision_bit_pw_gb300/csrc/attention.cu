@@ -78,7 +78,7 @@ __device__ __forceinline__ void start_unit(const Params& p, const Cursor& c, Row
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = c.tile * kTile + g + 8 * i;
-    const int token = r / p.group, h = r - token * p.group;
+    const int token = pw_attn::token_of(p, r), h = r - token * p.group;
     q[i] = r < rows ? static_cast<const T*>(a.q) + (c.s.q0 + token) * a.q_stride_token +
                           (c.head * p.group + h) * a.q_stride_head
                     : nullptr;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void compute_chunk(const Params& p, const Cursor& c, 
   for (int i = 0; i < 2; ++i) {
     // the row's visible keys are [lo, hi)
     const int r = c.tile * kTile + g + 8 * i;
-    const int pos = base + r / p.group;
+    const int pos = base + pw_attn::token_of(p, r);
     int hi = a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
     if (r >= rows) hi = 0;
     const int lo = a.causal && a.window ? pos - a.window + 1 : 0;
@@ -242,7 +242,8 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
       for (int i = 0; i < 2; ++i) {
         const int row = g + 8 * i;
         if (row >= rows) continue;
-        const int r = c.tile * kTile + row, token = c.s.q0 + r / p.group, h = c.head * p.group + r % p.group;
+        const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
+    const int h = c.head * p.group + r - t0 * p.group;
         const float inv = pw_attn::inverse_sum(l[i]);
         T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head;
 #pragma unroll
@@ -303,7 +304,8 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
       o.z += f * v.z;
       o.w += f * v.w;
     }
-    const int r = c.tile * kTile + row, token = c.s.q0 + r / p.group, h = c.head * p.group + r % p.group;
+    const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
+    const int h = c.head * p.group + r - t0 * p.group;
     const float inv = pw_attn::inverse_sum(sum);
     T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head + d;
     *reinterpret_cast<uint2*>(out) = make_uint2(pw::pack2<T>(o.x * inv, o.y * inv), pw::pack2<T>(o.z * inv, o.w * inv));
@@ -444,6 +446,9 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
   Params p{};
   p.a = a;
   p.group = a.heads / a.kv_heads;
+  // n * group_inv / 2^32 is exact while n times the excess of group_inv stays below 2^32 / group
+  p.group_inv = static_cast<uint32_t>(((1ull << 32) + p.group - 1) / p.group);
+  p.group_max = p.group > 1 ? static_cast<int>(((1ull << 31) - 1) / p.group) : -1;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.arrived = static_cast<uint32_t*>(d_ws);
   p.part = reinterpret_cast<float*>(static_cast<char*>(d_ws) + kCounterBytes);

@@ -83,19 +83,20 @@ __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
 // ---------------------------------------------------------------- copies (a warp for keys, a warp for values)
 // Item 2x of the ring is the keys of the CTA's block x, item 2x + 1 its values.
 //
-// Rows of values outside the visible keys have to be zero.  They occur in a
-// unit's first and last block only: there the boxes that hold such rows are
-// copied row by row, with zeros for the others.
+// Rows of values that no token of the call sees have to be zero: past the
+// sequence's end, and before every window.  They occur in the blocks at those
+// two places only: there the boxes that hold such rows are copied row by row,
+// with zeros for the others.
 template <int D>
 __device__ __forceinline__ void copy_rows(const Params& p, const Cursor& c, int key0, int first, int rows, int page,
-                                          unsigned char* dst) {
+                                          int begin, unsigned char* dst) {
   const pw_attn_args& a = p.a;
   constexpr int kUnits = D / 8;
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < rows * kUnits; i += 32) {
     const int row = first + i / kUnits, unit = i % kUnits, key = key0 + row;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (page >= 0 && key >= c.r.lo && key < c.r.hi)
+    if (page >= 0 && key >= begin && key < c.s.kv_len)
       v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_cache) + page * a.v_stride_page +
                                           (key % a.page_size) * a.v_stride_token + c.head * a.v_stride_head + unit * 8);
     *reinterpret_cast<uint4*>(dst + (unit >> 3) * kHalfRow + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) = v;
@@ -116,7 +117,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
     // this lane's box: its first key, and where that is in the page table
     int key0 = (c.r.b0 + b0) * kBlock, key = key0 + lane * box;
     int index = key / a.page_size, in_page = key - index * a.page_size;
-    auto wanted = [&]() { return lane < boxes && key < c.r.hi && key + box > c.r.lo; };
+    const int begin = pw_attn::first_key(a, c.s), end = c.s.kv_len;
+    auto wanted = [&]() { return lane < boxes && key < end && key + box > begin; };
     int page = wanted() ? table[index] : -1;
     for (int b = b0; b < b1; ++b, y += 2) {
       const bool want = wanted();
@@ -124,7 +126,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
       bool take = want && this_page >= 0 && this_page < a.num_pages;
       if (want && !take && !kValues) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, take);
-      if (kValues) take = take && key >= c.r.lo && key + box <= c.r.hi;   // every row is visible
+      if (kValues) take = take && key >= begin && key + box <= end;   // every row is visible to some token
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
       // the next block's page: its latency passes during this block's waits
       key += kBlock;
@@ -146,7 +148,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
       if (kValues && mask != every) {
         for (int i = 0; i < boxes; ++i)
           if (!(mask >> i & 1u))
-            copy_rows<D>(p, c, key0, i * box, box, __shfl_sync(0xFFFFFFFFu, live >> lane & 1u ? this_page : -1, i), dst);
+            copy_rows<D>(p, c, key0, i * box, box, __shfl_sync(0xFFFFFFFFu, live >> lane & 1u ? this_page : -1, i), begin, dst);
         pw::fence_proxy_async_smem();
         __syncwarp();
       }
@@ -264,21 +266,33 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
 // ---------------------------------------------------------------- softmax (four warps a half)
 template <typename T, int D>
 __device__ __forceinline__ void write_queries(const Params& p, const Cursor& c, int h, int tid, unsigned char* q_smem) {
-  constexpr int kUnits = D / 8;   // 16-byte units of a row
+  constexpr int kUnits = D / 8;             // 16-byte units of a row
+  constexpr int kStep = kHalf / kUnits;     // rows at once
   const pw_attn_args& a = p.a;
-  const int rows = c.s.q_len * p.group;
-  const int unit = tid % kUnits;
-#pragma unroll 4
-  for (int row = tid / kUnits; row < kHalf; row += kHalf / kUnits) {
-    const int r = c.tile * kTile + h * kHalf + row;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int token = r / p.group, head = c.head * p.group + r - token * p.group;
-      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (c.s.q0 + token) * a.q_stride_token +
-                                          head * a.q_stride_head + unit * 8);
+  const int rows = c.s.q_len * p.group, unit = tid % kUnits, first = tid / kUnits;
+  const int r0 = c.tile * kTile + h * kHalf + first;
+  int token = pw_attn::token_of(p, r0), head = r0 - token * p.group;
+  const int token_step = kStep / p.group, head_step = kStep % p.group;
+  const T* base = static_cast<const T*>(a.q) + c.s.q0 * a.q_stride_token + c.head * p.group * a.q_stride_head + unit * 8;
+  // all loads at once: each queues behind the copies of keys and values
+  uint4 v[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + i * kStep < rows)
+      v[i] = __ldg(reinterpret_cast<const uint4*>(base + token * a.q_stride_token + head * a.q_stride_head));
+    token += token_step;
+    head += head_step;
+    if (head >= p.group) {
+      head -= p.group;
+      ++token;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int row = first + i * kStep;
     *reinterpret_cast<uint4*>(q_smem + h * tile_bytes<D>() + (unit >> 3) * kHalfRow + row * 128 +
-                              (((unit & 7) ^ (row & 7)) << 4)) = v;
+                              (((unit & 7) ^ (row & 7)) << 4)) = v[i];
   }
 }
 
@@ -301,7 +315,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       pw::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) pw::mbar_arrive(bar(sh.q_full[h]));
-      const int pos = c.s.kv_len - c.s.q_len + r / p.group;
+      const int pos = c.s.kv_len - c.s.q_len + pw_attn::token_of(p, r);
       // the row's visible keys; a row past the end takes all of them and is not written
       const int hi = !live ? 0x7FFFFFFF : a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
       const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
@@ -309,27 +323,38 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         const int key0 = (c.r.b0 + b) * kBlock;
         wait(&sh.s_full[h], blocks & 1u, sh, p);
         pw::tc_fence_after();
-        uint32_t s[4][32];
+        const bool all = __all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock);   // no mask in this block
+        // 64 scores at a time, twice: once for the maximum, once for the
+        // weights.  Loading them again costs 70 cycles; keeping all 128 costs
+        // spills, and a loop of twice the instructions that keeps the other
+        // roles' out of the instruction cache.
+        uint32_t s[2][32];
+        auto load = [&](int i) {
+          pw::tmem_ld_x32(s_tmem + 64 * i, s[0]);
+          pw::tmem_ld_x32(s_tmem + 64 * i + 32, s[1]);
+          pw::tmem_ld_wait();
+          if (!all) {
+            const int from = lo - key0 - 64 * i, to = hi - key0 - 64 * i;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pw::tmem_ld_x32(s_tmem + 32 * i, s[i]);
-        pw::tmem_ld_wait();
-        if (!__all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock)) {
-          const int from = lo - key0, to = hi - key0;
+            for (int j = 0; j < 64; ++j)
+              if (j < from || j >= to) s[j >> 5][j & 31] = 0xFF800000u;   // -inf
+          }
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          load(i);
+          float most[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[j >> 1][16 * (j & 1)]), __uint_as_float(s[j >> 1][16 * (j & 1) + 1]));
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * i + j < from || 32 * i + j >= to) s[i][j] = 0xFF800000u;   // -inf
+          for (int k = 2; k < 16; k += 2)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              most[j] = pw::max3(most[j], __uint_as_float(s[j >> 1][16 * (j & 1) + k]),
+                                 __uint_as_float(s[j >> 1][16 * (j & 1) + k + 1]));
+          top = pw::max3(top, pw::max3(most[0], most[1], most[2]), most[3]);
         }
-        float top4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          top4[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
-#pragma unroll
-          for (int j = 2; j < 32; j += 2)
-            top4[i] = pw::max3(top4[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
-        }
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
         // m follows the maximum in steps of at least 2^8 (and at once from -inf)
         const bool moves = top > m && !((top - m) * p.scale_log2 <= kLazy);
         float keep = 1.0f;
@@ -357,12 +382,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         const uint64_t scale2 = pw::pack_f32x2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
         const uint64_t off2 = pw::pack_f32x2(__float_as_uint(off), __float_as_uint(off));
         uint64_t sum[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
+          load(i);
           uint32_t w[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const uint32_t* src = &s[2 * i + j / 16][2 * (j % 16)];
+            const uint32_t* src = &s[j >> 4][2 * (j & 15)];
             float e0, e1;
             pw::unpack_f32x2(pw::fma_f32x2(pw::pack_f32x2(src[0], src[1]), scale2, off2), e0, e1);
             e0 = pw::exp2_fast(e0);
@@ -386,7 +412,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
     const float m2 = m * p.scale_log2;   // in powers of two
     const long long begin = c.unit_begin(), unit_end = c.unit_end();
     const bool whole = b0 == 0 && begin + b1 == unit_end;
-    const int token = c.s.q0 + r / p.group, head = c.head * p.group + r % p.group;
+    const int t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0, head = c.head * p.group + r - t0 * p.group;
     T* out = static_cast<T*>(a.out) + token * a.out_stride_token + head * a.out_stride_head;
     const bool dead = *reinterpret_cast<volatile int*>(&sh.dead) != 0;
     if (whole) {
@@ -456,22 +482,29 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       total += pw::exp2_fast(__ldcg(piece(i) + kTile * D + slot_row) - safe) *
                __ldcg(piece(i) + kTile * D + kTile + slot_row);
     const float inv = pw_attn::inverse_sum(total);
-    for (int d = 0; d < D / 8; ++d) {
-      float o[8] = {};
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+      float o[32] = {};
       for (int i = c0; i <= c1; ++i) {
-        const float f = pw::exp2_fast(__ldcg(piece(i) + kTile * D + slot_row) - safe);
+        const float* src = piece(i);
+        const float f = pw::exp2_fast(__ldcg(src + kTile * D + slot_row) - safe);
+        float4 v[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i) + ((2 * d + j) * kTile + slot_row) * 4));
-          o[4 * j] += f * v.x;
-          o[4 * j + 1] += f * v.y;
-          o[4 * j + 2] += f * v.z;
-          o[4 * j + 3] += f * v.w;
+        for (int j = 0; j < 8; ++j)
+          v[j] = __ldcg(reinterpret_cast<const float4*>(src + ((d0 / 4 + j) * kTile + slot_row) * 4));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[4 * j] += f * v[j].x;
+          o[4 * j + 1] += f * v[j].y;
+          o[4 * j + 2] += f * v[j].z;
+          o[4 * j + 3] += f * v[j].w;
         }
       }
-      *reinterpret_cast<uint4*>(out + 8 * d) =
-          make_uint4(pw::pack2<T>(o[0] * inv, o[1] * inv), pw::pack2<T>(o[2] * inv, o[3] * inv),
-                     pw::pack2<T>(o[4] * inv, o[5] * inv), pw::pack2<T>(o[6] * inv, o[7] * inv));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(out + d0 + 8 * j) =
+            make_uint4(pw::pack2<T>(o[8 * j] * inv, o[8 * j + 1] * inv), pw::pack2<T>(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                       pw::pack2<T>(o[8 * j + 4] * inv, o[8 * j + 5] * inv), pw::pack2<T>(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
     }
     if (a.lse) a.lse[static_cast<int64_t>(token) * a.heads + head] = pw_attn::log_sum(most, total);
     return true;
@@ -517,19 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Registers move from the third warpgroup to the softmax warps: 256 threads
   // x 192 and 128 x 120 are the launch's 384 x 168.
   if (warp < kSoftmaxWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     softmax_role<T, D>(p, c, line, ctas, sh, tmem, smem);
   } else if (warp == kKeyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     load_role<D, false>(p, c, maps, sh, ring);
   } else if (warp == kValueWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     load_role<D, true>(p, c, maps, sh, ring);
   } else if (warp == kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(ring));
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");   // a warpgroup gives and takes as a whole
   }
   __syncwarp();
   pw::tc_fence_before();

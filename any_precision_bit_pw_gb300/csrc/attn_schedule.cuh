@@ -17,6 +17,8 @@ namespace pw_attn {
 struct Params {
   pw_attn_args a;
   int group;          // query heads per key/value head
+  uint32_t group_inv; // ceil(2^32 / group): rows up to group_max divide by a product
+  int group_max;
   float scale_log2;   // scale * log2(e): the softmax runs in powers of two
   uint32_t* arrived;  // one counter per CTA, all 0 between calls
   float* part;        // 2 partial results per CTA
@@ -36,9 +38,18 @@ bool tile_kernel_takes(const Params& p);
 size_t tile_part_floats(int head_dim);
 int launch_tile_kernel(const Params& p, cudaStream_t s);
 
+// Row number to token.
+__device__ __forceinline__ int token_of(const Params& p, int row) {
+  return row <= p.group_max ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.group_inv)) : row / p.group;
+}
+
 struct Sequence {
   int q0, q_len, kv_len;
 };
+// First key that any of the call's tokens sees: the pages before it may be gone.
+__device__ __forceinline__ int first_key(const pw_attn_args& a, const Sequence& s) {
+  return a.causal && a.window ? max(0, s.kv_len - s.q_len - a.window + 1) : 0;
+}
 
 // Lengths of sequence b; what the call's arrays cannot hold is reported and
 // left out (a sequence without tokens, or keys past its page table).
@@ -69,8 +80,8 @@ __device__ __forceinline__ Range tile_range(const Params& p, const Sequence& s, 
   const int first = tile * kTile, last = min(rows, first + kTile) - 1;
   const int base = s.kv_len - s.q_len;
   Range r;
-  r.hi = p.a.causal ? max(0, base + last / p.group + 1) : s.kv_len;
-  r.lo = p.a.causal && p.a.window ? max(0, base + first / p.group - p.a.window + 1) : 0;
+  r.hi = p.a.causal ? max(0, base + token_of(p, last) + 1) : s.kv_len;
+  r.lo = p.a.causal && p.a.window ? max(0, base + token_of(p, first) - p.a.window + 1) : 0;
   if (r.lo >= r.hi) r.lo = r.hi = 0;
   r.b0 = r.lo / kBlock;
   r.b1 = (r.hi + kBlock - 1) / kBlock;
