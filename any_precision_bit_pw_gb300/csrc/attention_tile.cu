@@ -29,7 +29,7 @@ using pw_attn::Params;
 constexpr int kHalf = 128;             // rows of half a tile: the lanes of Tensor Memory
 constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;            // keys of a block
-constexpr int kSlots = 5;              // ring of key and value blocks, in turn
+constexpr int kKeySlots = 2, kValueSlots = 3;   // rings of key and value blocks in shared memory
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKeyWarp = 8, kValueWarp = 9, kMmaWarp = 10;
 constexpr int kThreads = 384;
@@ -40,10 +40,10 @@ constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
 template <int D>
 constexpr int tile_bytes() { return (D / 64) * kHalfRow; }
 template <int D>
-constexpr int smem_bytes() { return (2 + kSlots) * tile_bytes<D>() + 1024; }
+constexpr int smem_bytes() { return (2 + kKeySlots + kValueSlots) * tile_bytes<D>() + 1024; }
 
 struct alignas(8) Shared {
-  uint64_t q_full[2], full[kSlots], empty[kSlots];
+  uint64_t q_full[2], k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots];
   uint64_t drained, s_full[2], p_full[2][2], o_done[2];   // p_full: weights of the first and the last 64 keys
   uint32_t tmem;
   int dead;
@@ -55,8 +55,8 @@ struct Maps {
   int box;   // rows of a box: a divisor of the page size and of a block
 };
 
-__device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, Shared& sh, const Params& p) {
-  return pw::warp_wait(bar, parity, &sh.dead, p.a.status);
+__device__ __forceinline__ bool wait(const uint64_t& bar, uint32_t parity, Shared& sh, const Params& p) {
+  return pw::warp_wait(&bar, parity, &sh.dead, p.a.status);
 }
 __device__ __forceinline__ uint32_t bar(const uint64_t& b) { return pw::smem_u32(&b); }
 
@@ -81,8 +81,6 @@ __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
 }
 
 // ---------------------------------------------------------------- copies (a warp for keys, a warp for values)
-// Item 2x of the ring is the keys of the CTA's block x, item 2x + 1 its values.
-//
 // Rows of values that no token of the call sees have to be zero: past the
 // sequence's end, and before every window.  They occur in the blocks at those
 // two places only: there the boxes that hold such rows are copied row by row,
@@ -111,7 +109,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
   const int box = maps.box, boxes = kBlock / box;   // at most 16 boxes of 64 values
   const uint32_t every = (1u << boxes) - 1u;
   const int step_pages = kBlock / a.page_size, step_rows = kBlock % a.page_size;
-  uint32_t y = kValues ? 1 : 0, slot = y, use = 0;  // the warp's next item, its slot and how often that was used
+  uint64_t* const fulls = kValues ? sh.v_full : sh.k_full;
+  uint64_t* const empties = kValues ? sh.v_empty : sh.k_empty;
+  constexpr uint32_t kSlots = kValues ? kValueSlots : kKeySlots;
+  pw::Ring<kSlots> slot;
+  uint32_t x = 0;                                   // blocks started
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
     const int32_t* table = a.page_table + c.seq * a.page_table_stride;
     // this lane's box: its first key, and where that is in the page table
@@ -120,7 +122,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
     const int begin = pw_attn::first_key(a, c.s), end = c.s.kv_len;
     auto wanted = [&]() { return lane < boxes && key < end && key + box > begin; };
     int page = wanted() ? table[index] : -1;
-    for (int b = b0; b < b1; ++b, y += 2) {
+    for (int b = b0; b < b1; ++b, ++x) {
       const bool want = wanted();
       const int this_page = page, row = in_page;
       bool take = want && this_page >= 0 && this_page < a.num_pages;
@@ -137,14 +139,10 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
         ++index;
       }
       page = b + 1 < b1 && wanted() ? table[index] : -1;
-      if (use > 0 && !wait(&sh.empty[slot], (use + 1) & 1u, sh, p)) return false;
-      const uint32_t full = bar(sh.full[slot]);
-      unsigned char* dst = ring + slot * tile_bytes<D>();
-      slot += 2;
-      if (slot >= kSlots) {
-        slot -= kSlots;
-        ++use;
-      }
+      if (x >= kSlots && !wait(empties[slot.at], slot.parity ^ 1u, sh, p)) return false;
+      const uint32_t full = bar(fulls[slot.at]);
+      unsigned char* dst = ring + slot.at * tile_bytes<D>();
+      slot.next();
       if (kValues && mask != every) {
         for (int i = 0; i < boxes; ++i)
           if (!(mask >> i & 1u))
@@ -173,24 +171,30 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
   // No copy may be in flight when the CTA leaves: in a call that went well the
   // matrix instructions have waited for every one of them.
   if (*reinterpret_cast<volatile int*>(&sh.dead))
-    for (uint32_t i = y > 2 * kSlots ? y - 2 * kSlots : (kValues ? 1 : 0); i < y; i += 2)
-      pw::mbar_wait(bar(sh.full[i % kSlots]), (i / kSlots) & 1u, kDrainNs);
+    for (uint32_t i = x > kSlots ? x - kSlots : 0; i < x; ++i)
+      pw::mbar_wait(bar(fulls[i % kSlots]), (i / kSlots) & 1u, kDrainNs);
 }
 
 // ---------------------------------------------------------------- matrix instructions (one warp)
+// The tensor cores queue a few instructions only, so what this warp does
+// between two groups of them is time in which they run dry: addresses and
+// descriptors are made beforehand, the halves are written out.  (One issuing
+// warp a half instead lets the halves' products alternate, and both finish
+// late: 1330 us against 1257 on 7.2k tokens over 16k keys.)
 template <int D, bool kBf16>
 __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, Shared& sh, uint32_t tmem,
-                                         uint32_t q_smem, uint32_t ring) {
+                                         uint32_t q_smem, uint32_t k_ring, uint32_t v_ring) {
   constexpr uint32_t kScores = pw::idesc_f32(kHalf, kBlock, kBf16, false);
   constexpr uint32_t kValues = pw::idesc_f32(kHalf, D, kBf16, true);
-  // Items of the ring: a block's keys, its values, the next block's keys, ...
-  pw::Ring<kSlots> keys, vals;
-  vals.next();
-  uint32_t q_parity[2] = {0, 0}, p_parity[2] = {0, 0};
+  constexpr uint32_t kStep = tile_bytes<D>() >> 4;
+  const uint64_t q_desc = pw::sdesc_kmajor_sw128(q_smem), k_desc = pw::sdesc_kmajor_sw128(k_ring);
+  const uint64_t v_desc = pw::sdesc_nmajor_sw128(v_ring, kHalfRow);
+  pw::Ring<kKeySlots> keys;
+  pw::Ring<kValueSlots> vals;
+  uint32_t q_parity = 0, p_parity = 0;   // a bit a half
   bool ok = true;
-  auto scores = [&](int h, uint32_t slot, bool free_after) {   // S_h = Q_h K^T
-    const uint64_t q = pw::sdesc_kmajor_sw128(q_smem + h * tile_bytes<D>());
-    const uint64_t k = pw::sdesc_kmajor_sw128(ring + slot * tile_bytes<D>());
+  auto scores = [&](int h, bool free_after) {   // S_h = Q_h K^T
+    const uint64_t q = q_desc + h * kStep, k = k_desc + keys.at * kStep;
     if (pw::elect_one()) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -198,13 +202,13 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
         pw::tc_mma_f16(tmem + h * kBlock, q + at, k + at, kScores, i);
       }
       pw::tc_commit(bar(sh.s_full[h]));
-      if (free_after) pw::tc_commit(bar(sh.empty[slot]));
+      if (free_after) pw::tc_commit(bar(sh.k_empty[keys.at]));
     }
     __syncwarp();
   };
   // O_h (+)= P_h V, the first or the last 64 keys
-  auto values = [&](int h, int part, uint32_t slot, bool first, bool free_after) {
-    const uint64_t v = pw::sdesc_nmajor_sw128(ring + slot * tile_bytes<D>(), kHalfRow);
+  auto values = [&](int h, int part, bool first, bool free_after) {
+    const uint64_t v = v_desc + vals.at * kStep;
     if (pw::elect_one()) {
 #pragma unroll
       for (int j = 0; j < kBlock / 32; ++j) {
@@ -214,45 +218,43 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
       }
       if (part) {
         pw::tc_commit(bar(sh.o_done[h]));
-        if (free_after) pw::tc_commit(bar(sh.empty[slot]));
+        if (free_after) pw::tc_commit(bar(sh.v_empty[vals.at]));
       }
     }
     __syncwarp();
   };
+  auto both = [&](const uint64_t& b1, uint32_t parity1, const uint64_t& b2, uint32_t parity2) {
+    ok = pw::warp_wait2(&b1, parity1, &b2, parity2, &sh.dead, p.a.status);
+    pw::tc_fence_after();
+    return ok;
+  };
   for_units(p, start, [&](const Cursor& c, int b0, int b1) {
-    const int halves = halves_of(p, c);
-    for (int h = 0; h < halves; ++h) {
-      ok = pw::warp_wait2(&sh.full[keys.at], keys.parity, &sh.q_full[h], q_parity[h], &sh.dead, p.a.status);
-      if (!ok) return false;
-      q_parity[h] ^= 1u;
-      pw::tc_fence_after();
-      scores(h, keys.at, h + 1 == halves);
+    const bool two = halves_of(p, c) == 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !two) break;
+      if (!both(sh.k_full[keys.at], keys.parity, sh.q_full[h], (q_parity >> h) & 1u)) return false;
+      q_parity ^= 1u << h;
+      scores(h, h == 1 || !two);
     }
-    keys.next();
     keys.next();
     for (int b = b0; b < b1; ++b) {
       const bool more = b + 1 < b1;
-      // one wait between any two groups of instructions: the queue of the
-      // tensor cores covers it
-      for (int h = 0; h < halves; ++h) {
-        ok = pw::warp_wait2(&sh.p_full[h][0], p_parity[h], &sh.full[vals.at], vals.parity, &sh.dead, p.a.status);
-        if (!ok) return false;
-        pw::tc_fence_after();
-        values(h, 0, vals.at, b == b0, false);
-        const uint64_t* next = more ? &sh.full[keys.at] : &sh.p_full[h][1];
-        ok = pw::warp_wait2(&sh.p_full[h][1], p_parity[h], next, more ? keys.parity : p_parity[h], &sh.dead, p.a.status);
-        if (!ok) return false;
-        pw::tc_fence_after();
-        values(h, 1, vals.at, b == b0, h + 1 == halves);
-        p_parity[h] ^= 1u;
-        if (more) scores(h, keys.at, h + 1 == halves);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !two) break;
+        const bool last = h == 1 || !two;
+        const uint32_t parity = (p_parity >> h) & 1u;
+        if (!both(sh.p_full[h][0], parity, sh.v_full[vals.at], vals.parity)) return false;
+        values(h, 0, b == b0, false);
+        if (!both(sh.p_full[h][1], parity, more ? sh.k_full[keys.at] : sh.p_full[h][1], more ? keys.parity : parity))
+          return false;
+        values(h, 1, b == b0, last);
+        p_parity ^= 1u << h;
+        if (more) scores(h, last);
       }
       vals.next();
-      vals.next();
-      if (more) {
-        keys.next();
-        keys.next();
-      }
+      if (more) keys.next();
     }
     return true;
   });
@@ -321,7 +323,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
       for (int b = b0; b < b1; ++b, ++blocks) {
         const int key0 = (c.r.b0 + b) * kBlock;
-        wait(&sh.s_full[h], blocks & 1u, sh, p);
+        wait(sh.s_full[h], blocks & 1u, sh, p);
         pw::tc_fence_after();
         const bool all = __all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock);   // no mask in this block
         // 64 scores at a time, twice: once for the maximum, once for the
@@ -365,7 +367,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         }
         if (b > b0 && __any_sync(0xFFFFFFFFu, moves)) {
           // O has to be complete up to the last block before it is scaled
-          wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p);
+          wait(sh.o_done[h], (blocks - 1) & 1u, sh, p);
           pw::tc_fence_after();
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -406,7 +408,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         pw::unpack_f32x2(pw::add_f32x2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
-      wait(&sh.o_done[h], (blocks - 1) & 1u, sh, p);
+      wait(sh.o_done[h], (blocks - 1) & 1u, sh, p);
       pw::tc_fence_after();
     }
     const float m2 = m * p.scale_log2;   // in powers of two
@@ -523,9 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int ctas = gridDim.x;
   if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, ctas, c, line)) return;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      pw::mbar_init(bar(sh.full[i]), 1);
-      pw::mbar_init(bar(sh.empty[i]), 1);
+    for (int i = 0; i < kKeySlots; ++i) {
+      pw::mbar_init(bar(sh.k_full[i]), 1);
+      pw::mbar_init(bar(sh.k_empty[i]), 1);
+    }
+    for (int i = 0; i < kValueSlots; ++i) {
+      pw::mbar_init(bar(sh.v_full[i]), 1);
+      pw::mbar_init(bar(sh.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       pw::mbar_init(bar(sh.q_full[i]), 4);
@@ -546,17 +552,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   pw::tc_fence_after();
   const uint32_t tmem = pw::uniform(sh.tmem);
-  unsigned char* ring = smem + 2 * tile_bytes<D>();
+  unsigned char* k_ring = smem + 2 * tile_bytes<D>();
+  unsigned char* v_ring = k_ring + kKeySlots * tile_bytes<D>();
   // Registers move from the third warpgroup to the softmax warps: 256 threads
   // x 192 and 128 x 120 are the launch's 384 x 168.
   if (warp < kSoftmaxWarps) {
     softmax_role<T, D>(p, c, line, ctas, sh, tmem, smem);
   } else if (warp == kKeyWarp) {
-    load_role<D, false>(p, c, maps, sh, ring);
+    load_role<D, false>(p, c, maps, sh, k_ring);
   } else if (warp == kValueWarp) {
-    load_role<D, true>(p, c, maps, sh, ring);
+    load_role<D, true>(p, c, maps, sh, v_ring);
   } else if (warp == kMmaWarp) {
-    mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(ring));
+    mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(k_ring), pw::smem_u32(v_ring));
   } else {
   }
   __syncwarp();
