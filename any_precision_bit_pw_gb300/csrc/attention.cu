@@ -25,7 +25,7 @@ constexpr int kStages = 3;           // chunks in flight per warp
 template <int D>
 constexpr int stage_bytes() { return 2 * kChunk * D * 2; }   // keys, then values
 template <int D>
-constexpr int smem_bytes() { return kWarps * kStages * stage_bytes<D>() + 2 * kTile * D * 4; }
+constexpr int smem_bytes() { return kWarps * kStages * stage_bytes<D>() + kWarps * 8 * D * 4; }
 template <int D>
 constexpr size_t part_floats() { return static_cast<size_t>(kTile) * (D + 2); }
 
@@ -176,7 +176,7 @@ struct Shared {
 // are written, or left as a partial result whose last piece joins them all.
 template <typename T, int D>
 __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, long long begin, long long seg_begin,
-                                            long long seg_end, long long line, int ctas, Rows<T, D>& w, Shared& sh,
+                                            long long seg_end, const pw_attn::Cut& cut, Rows<T, D>& w, Shared& sh,
                                             float* buf) {
   const pw_attn_args& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -193,90 +193,74 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
     }
   }
   __syncthreads();
-  float m[2], l[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.0f;
+    float top = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) m[i] = fmaxf(m[i], sh.m[x][g + 8 * i]);
-    const float safe = m[i] == -INFINITY ? 0.0f : m[i];
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) l[i] += sh.l[x][g + 8 * i] * pw::exp2_fast(sh.m[x][g + 8 * i] - safe);
-    const float mine = pw::exp2_fast(w.m[i] - safe);
+    for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sh.m[x][g + 8 * i]);
+    const float mine = pw::exp2_fast(w.m[i] - (top == -INFINITY ? 0.0f : top));
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) {
       w.o[n][2 * i] *= mine;
       w.o[n][2 * i + 1] *= mine;
     }
   }
-  // the warps' outputs: 2 and 3 to 0 and 1, then 1 to 0
-#pragma unroll
-  for (int half = kWarps / 2; half; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-      float* dst = buf + (warp - half) * kTile * D;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<float2*>(dst + (g + 8 * i) * D + 8 * n + 2 * t) = make_float2(w.o[n][2 * i], w.o[n][2 * i + 1]);
-    }
-    __syncthreads();
-    if (warp < half) {
-      const float* src = buf + warp * kTile * D;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 v = *reinterpret_cast<const float2*>(src + (g + 8 * i) * D + 8 * n + 2 * t);
-          w.o[n][2 * i] += v.x;
-          w.o[n][2 * i + 1] += v.y;
-        }
-    }
-    __syncthreads();
-  }
+  // The warps' outputs are added through shared memory, eight rows at a time:
+  // a thread owns four columns of a row.
   const bool whole = seg_begin == begin && seg_end == unit_end;
-  if (whole) {
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = g + 8 * i;
-        if (row >= rows) continue;
-        const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
-    const int h = c.head * p.group + r - t0 * p.group;
-        const float inv = pw_attn::inverse_sum(l[i]);
-        T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<uint32_t*>(out + 8 * n + 2 * t) = pw::pack2<T>(w.o[n][2 * i] * inv, w.o[n][2 * i + 1] * inv);
-        if (a.lse && t == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(m[i], l[i]);
-      }
-    }
-    return;
-  }
-  // a piece: slot 0 of the CTA when it continues a unit or starts exactly at
-  // its stretch's begin, slot 1 otherwise
   const int cta = blockIdx.x;
   constexpr size_t kFloats = part_floats<D>();
-  const bool at_start = seg_begin == line * cta / ctas;
-  if (warp == 0) {
-    float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * kFloats;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = g + 8 * i;
-      if (row >= rows) continue;
+  constexpr int kRowItems = D / 4;
+  // a piece: slot 0 of the CTA when it continues a unit or starts exactly at
+  // its stretch's begin, slot 1 otherwise
+  const bool at_start = seg_begin == cut.begin(cta);
+  float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * kFloats;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    const int i = r0 >> 3, live = min(8, rows - r0);
+    if (g < live) {
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float2*>(part + row * D + 8 * n + 2 * t) = make_float2(w.o[n][2 * i], w.o[n][2 * i + 1]);
-      if (t == 0) {
-        part[kTile * D + row] = m[i];
-        part[kTile * D + kTile + row] = l[i];
+        *reinterpret_cast<float2*>(buf + (warp * 8 + g) * D + 8 * n + 2 * t) =
+            i ? make_float2(w.o[n][2], w.o[n][3]) : make_float2(w.o[n][0], w.o[n][1]);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < live * kRowItems; e += kThreads) {
+      const int row = e / kRowItems, d = (e % kRowItems) * 4;
+      float4 o = *reinterpret_cast<const float4*>(buf + row * D + d);
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) {
+        const float4 v = *reinterpret_cast<const float4*>(buf + (x * 8 + row) * D + d);
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) top = fmaxf(top, sh.m[x][r0 + row]);
+      const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) sum += sh.l[x][r0 + row] * pw::exp2_fast(sh.m[x][r0 + row] - safe);
+      if (whole) {
+        const int r = c.tile * kTile + r0 + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
+        const int h = c.head * p.group + r - t0 * p.group;
+        const float inv = pw_attn::inverse_sum(sum);
+        T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head + d;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pw::pack2<T>(o.x * inv, o.y * inv), pw::pack2<T>(o.z * inv, o.w * inv));
+        if (a.lse && d == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(top, sum);
+      } else {
+        *reinterpret_cast<float4*>(part + (r0 + row) * D + d) = o;
+        if (d == 0) {
+          part[kTile * D + r0 + row] = top;
+          part[kTile * D + kTile + r0 + row] = sum;
+        }
       }
     }
-    __threadfence();
+    if (!whole) __threadfence();
+    __syncthreads();
   }
-  __syncthreads();
-  const int c0 = pw_attn::cta_of(begin, line, ctas), c1 = pw_attn::cta_of(unit_end - 1, line, ctas);
+  if (whole) return;
+  const int c0 = cut.cta_of(begin), c1 = cut.cta_of(unit_end - 1);
   if (threadIdx.x == 0) {
     const uint32_t n = atomicAdd(p.arrived + c0, 1u);
     sh.last = n == static_cast<uint32_t>(c1 - c0);
@@ -285,24 +269,46 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
   }
   __syncthreads();
   if (!sh.last) return;
-  const int first_slot = begin == line * c0 / ctas ? 0 : 1;
-  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
-    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+  // The last piece joins all.  Maxima and sums come into shared memory with one
+  // round trip (where they fit), then a thread adds the outputs of four columns
+  // of a row, eight loads under way together.
+  const int first_slot = begin == cut.begin(c0) ? 0 : 1, pieces = c1 - c0 + 1;
+  auto piece = [&](int x) { return p.part + (2 * static_cast<size_t>(c0 + x) + (x == 0 ? first_slot : 0)) * kFloats; };
+  float2* ml = reinterpret_cast<float2*>(buf);
+  const bool fits = pieces * rows * 8 <= kWarps * 8 * D * 4;
+  auto state = [&](int x, int row) {
+    const float* src = piece(x) + kTile * D + row;
+    return make_float2(__ldcg(src), __ldcg(src + kTile));
+  };
+  if (fits) {
+    for (int e = threadIdx.x; e < pieces * rows; e += kThreads) ml[e] = state(e / rows, e % rows);
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int e = threadIdx.x; e < rows * kRowItems; e += kThreads) {
+    const int row = e / kRowItems, d = (e % kRowItems) * 4;
     float top = -INFINITY;
-    for (int x = c0; x <= c1; ++x)
-      top = fmaxf(top, __ldcg(p.part + (2 * static_cast<size_t>(x) + (x == c0 ? first_slot : 0)) * kFloats + kTile * D + row));
+    for (int x = 0; x < pieces; ++x) top = fmaxf(top, fits ? ml[x * rows + row].x : state(x, row).x);
     const float safe = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
-    for (int x = c0; x <= c1; ++x) {
-      const float* part = p.part + (2 * static_cast<size_t>(x) + (x == c0 ? first_slot : 0)) * kFloats;
-      const float f = pw::exp2_fast(__ldcg(part + kTile * D + row) - safe);
-      sum += f * __ldcg(part + kTile * D + kTile + row);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + row * D + d));
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+#pragma unroll 1
+    for (int x = 0; x < pieces; x += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = x + j < pieces ? __ldcg(reinterpret_cast<const float4*>(piece(x + j) + row * D + d)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (x + j >= pieces) break;
+        const float2 t = fits ? ml[(x + j) * rows + row] : state(x + j, row);
+        const float f = pw::exp2_fast(t.x - safe);
+        sum += f * t.y;
+        o.x += f * v[j].x;
+        o.y += f * v[j].y;
+        o.z += f * v[j].z;
+        o.w += f * v[j].w;
+      }
     }
     const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
     const int h = c.head * p.group + r - t0 * p.group;
@@ -322,9 +328,8 @@ __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_cons
   const uint32_t ring = pw::smem_u32(smem) + static_cast<uint32_t>(warp * kStages * stage_bytes<D>());
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * stage_bytes<D>());
   Cursor c;
-  long long line;
-  int ctas = gridDim.x;
-  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, ctas, c, line)) return;
+  pw_attn::Cut cut;
+  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, gridDim.x, c, cut)) return;
   Cursor ahead = c;   // the copies run kStages - 1 blocks ahead of the arithmetic
   int fill = 0;
   auto load_next = [&]() {
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_cons
     ++c.block;
     const bool unit_done = c.block >= pw_attn::blocks_of(c.r);
     if (unit_done || c.done()) {
-      finish_unit<T, D>(p, c, begin, seg_begin, c.pos, line, ctas, w, sh, buf);
+      finish_unit<T, D>(p, c, begin, seg_begin, c.pos, cut, w, sh, buf);
       if (!c.done()) {
         pw_attn::next_unit<kTile, kBlock>(p, c);
         start_unit<T, D>(p, c, w);

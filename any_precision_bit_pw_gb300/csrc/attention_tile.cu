@@ -299,7 +299,7 @@ __device__ __forceinline__ void write_queries(const Params& p, const Cursor& c, 
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void softmax_role(const Params& p, const Cursor& start, long long line, int ctas, Shared& sh,
+__device__ __forceinline__ void softmax_role(const Params& p, const Cursor& start, const pw_attn::Cut& cut, Shared& sh,
                                              uint32_t tmem, unsigned char* q_smem) {
   const pw_attn_args& a = p.a;
   const int h = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
@@ -444,7 +444,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
     // a piece: [d / 4][row] of four values, so that neighbouring rows are
     // neighbours in memory; slot 0 when it starts at the stretch's begin
     const int cta = blockIdx.x;
-    const bool at_start = begin + b0 == line * cta / ctas;
+    const bool at_start = begin + b0 == cut.begin(cta);
     float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * part_floats;
     const int slot_row = h * kHalf + tid;
     if (active) {
@@ -464,7 +464,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
     }
     __threadfence();
     pw::bar_sync(1, 32 * kSoftmaxWarps);
-    const int c0 = pw_attn::cta_of(begin, line, ctas), c1 = pw_attn::cta_of(unit_end - 1, line, ctas);
+    const int c0 = cut.cta_of(begin), c1 = cut.cta_of(unit_end - 1);
     if (threadIdx.x == 0) {
       const uint32_t n = atomicAdd(p.arrived + c0, 1u);
       sh.last = n == static_cast<uint32_t>(c1 - c0);
@@ -475,7 +475,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
     const bool last = sh.last;
     pw::bar_sync(1, 32 * kSoftmaxWarps);   // sh.last is free again
     if (!last || !active || !live || dead) return true;
-    const int first_slot = begin == line * c0 / ctas ? 0 : 1;
+    const int first_slot = begin == cut.begin(c0) ? 0 : 1;
     auto piece = [&](int i) { return p.part + (2 * static_cast<size_t>(i) + (i == c0 ? first_slot : 0)) * part_floats; };
     float most = -INFINITY, total = 0.0f;
     for (int i = c0; i <= c1; ++i) most = fmaxf(most, __ldcg(piece(i) + kTile * D + slot_row));
@@ -521,9 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5));
   Cursor c;
-  long long line;
-  int ctas = gridDim.x;
-  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, ctas, c, line)) return;
+  pw_attn::Cut cut;
+  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, gridDim.x, c, cut)) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKeySlots; ++i) {
       pw::mbar_init(bar(sh.k_full[i]), 1);
@@ -557,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Registers move from the third warpgroup to the softmax warps: 256 threads
   // x 192 and 128 x 120 are the launch's 384 x 168.
   if (warp < kSoftmaxWarps) {
-    softmax_role<T, D>(p, c, line, ctas, sh, tmem, smem);
+    softmax_role<T, D>(p, c, cut, sh, tmem, smem);
   } else if (warp == kKeyWarp) {
     load_role<D, false>(p, c, maps, sh, k_ring);
   } else if (warp == kValueWarp) {

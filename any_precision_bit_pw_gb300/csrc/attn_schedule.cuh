@@ -136,60 +136,89 @@ __device__ __forceinline__ void next_unit(const Params& p, Cursor& c) {
   c.block = 0;
 }
 
+// 64-bit quotient; short operands, the usual case, take a short division.
+__device__ __forceinline__ long long quotient(long long n, long long d) {
+  return (n | d) >> 31 ? n / d : static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+}
+
+// The line's cut: the first `extra` CTAs take q + 1 blocks, the others q.
+struct Cut {
+  long long q;
+  int extra;
+  __device__ __forceinline__ long long begin(int cta) const { return q * cta + min(cta, extra); }
+  __device__ __forceinline__ int cta_of(long long w) const {
+    const long long big = (q + 1) * extra;
+    return static_cast<int>(w < big ? quotient(w, q + 1) : extra + quotient(w - big, q));
+  }
+};
+
 // The cursor of CTA `cta` of `ctas`, found by the whole CTA (kThreads
-// threads).  Returns false when it has no stretch; `ctas` becomes the number of
-// CTAs that have one, at least a block each.
+// threads).  Returns false when it has no stretch: there are never more
+// stretches than blocks.
 template <int kTile, int kBlock, int kThreads>
-__device__ __forceinline__ bool find_start(const Params& p, int cta, int& ctas, Cursor& c, long long& line) {
-  __shared__ long long warp_sum[kThreads / 32];
-  __shared__ long long before, sh_rest;
+__device__ __forceinline__ bool find_start(const Params& p, int cta, int ctas, Cursor& c, Cut& cut) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ long long warp_sum[2][kWarps];
+  __shared__ long long sh_rest;
   __shared__ int sh_seq;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // blocks of one head
+  // blocks of one head, and (batch <= kThreads) the prefix of this thread's sequence
   long long mine = 0;
   for (int b = tid; b < p.a.batch; b += kThreads)
     mine += sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, cta == 0));
-  long long sum = mine;
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) warp_sum[warp] = sum;
-  if (tid == 0) {
-    before = 0;
-    sh_seq = 0;
-    sh_rest = 0;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
   }
+  if (lane == 31) warp_sum[0][warp] = incl;
   __syncthreads();
-  long long per_head = 0;
-  for (int i = 0; i < kThreads / 32; ++i) per_head += warp_sum[i];
-  line = per_head * p.a.kv_heads;
+  long long per_head = 0, base = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i == warp) base = per_head;
+    per_head += warp_sum[0][i];
+  }
+  const long long line = per_head * p.a.kv_heads;
   if (line < ctas) ctas = static_cast<int>(line);
   if (cta >= ctas) return false;   // the same for every thread
-  c.pos = line * cta / ctas;
-  c.end = line * (cta + 1) / ctas;
-  c.head = static_cast<int>(c.pos / per_head);
+  cut.q = quotient(line, ctas);
+  cut.extra = static_cast<int>(line - cut.q * ctas);
+  c.pos = cut.begin(cta);
+  c.end = cut.begin(cta + 1);
+  c.head = static_cast<int>(quotient(c.pos, per_head));
   const long long want = c.pos - c.head * per_head;
   // the sequence that holds position `want` of the head's blocks
-  for (int b0 = 0; b0 < p.a.batch; b0 += kThreads) {
-    const int b = b0 + tid;
-    const long long n = p.a.batch <= kThreads ? mine
-                        : b < p.a.batch ? sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, false)) : 0;
-    long long incl = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    __syncthreads();   // warp_sum and before are read above
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    long long base = before;
-    for (int i = 0; i < warp; ++i) base += warp_sum[i];
-    const long long lo = base + incl - n;
-    if (n > 0 && lo <= want && want < lo + n) {
-      sh_seq = b;
+  if (p.a.batch <= kThreads) {
+    const long long lo = base + incl - mine;
+    if (mine > 0 && lo <= want && want < lo + mine) {
+      sh_seq = tid;
       sh_rest = want - lo;
     }
-    __syncthreads();
-    if (tid == 0)
-      for (int i = 0; i < kThreads / 32; ++i) before += warp_sum[i];
+  } else {
+    long long before = 0;
+    for (int b0 = 0, turn = 1; b0 < p.a.batch; b0 += kThreads, turn ^= 1) {
+      const int b = b0 + tid;
+      const long long n = b < p.a.batch ? sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, false)) : 0;
+      incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (lane == 31) warp_sum[turn][warp] = incl;
+      __syncthreads();   // two buffers in turn: the one written next was last read before this
+      long long lo = before + incl - n;
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) lo += warp_sum[turn][i];
+        before += warp_sum[turn][i];
+      }
+      if (n > 0 && lo <= want && want < lo + n) {
+        sh_seq = b;
+        sh_rest = want - lo;
+      }
+    }
   }
   __syncthreads();
   c.seq = sh_seq;
@@ -203,15 +232,6 @@ __device__ __forceinline__ bool find_start(const Params& p, int cta, int& ctas, 
   }
   c.block = static_cast<int>(rest);
   return true;
-}
-
-// The CTA whose stretch holds position w of the line.
-__device__ __forceinline__ int cta_of(long long w, long long line, int ctas) {
-  // stretches start at floor(line * i / ctas): the largest i whose start is <= w
-  int i = static_cast<int>(((w + 1) * ctas - 1) / line);
-  while (i + 1 < ctas && line * (i + 1) / ctas <= w) ++i;
-  while (i > 0 && line * i / ctas > w) --i;
-  return i;
 }
 
 }  // namespace pw_attn
