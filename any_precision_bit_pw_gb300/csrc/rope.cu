@@ -9,151 +9,201 @@
 // lose a digit with every factor of ten in p).
 //
 // Reads q, k and v once and writes as much: bound by memory bandwidth for
-// prompts, by the chain offsets -> length -> page -> store for single tokens.
+// prompts (7.3k tokens of 48 + 8 + 8 heads: 51 us, 4.7 TB/s; five CTAs an SM
+// with two units a thread under way, four with four units took 77 us), by the
+// chain offsets -> page -> store for single tokens (128 tokens: 3.7 us).
 #include "ops_common.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 2;    // units of a thread under way together
+constexpr int kPerCta = 2;
+constexpr int kMost = 8;     // tokens of a CTA
 
+// Units of work: a rotated head is pair units, then units of kVec values that
+// are copied; a value head is copied units.  A pair unit is one vector where
+// pairs are neighbours, else two vectors rotary_dim/2 apart (or two neighbours,
+// where an access is one value).
 struct RopeParams {
   pw_rope_args a;
-  int group_q, group_k;   // work units of one query head, and of one key head
-  int groups_v;           // and of one value head
+  int pair_units;      // of one query or key head
+  int head_units;      // pair units and copied ones
+  int value_units;     // of one value head
+  int units_q, units_k, units;   // of a token: queries, keys, all
+  uint32_t head_inv, value_inv, token_inv;   // ceil(2^32 / units): numbers below 2^16 divide by a product
+  int per_cta;         // tokens of a CTA
 };
 
-template <typename T, int kVec>
+template <int kVec>
 struct Vec;
-template <typename T>
-struct Vec<T, 8> {
+template <>
+struct Vec<8> {
   using type = uint4;
 };
-template <typename T>
-struct Vec<T, 4> {
+template <>
+struct Vec<4> {
   using type = uint2;
 };
-template <typename T>
-struct Vec<T, 1> {
+template <>
+struct Vec<1> {
   using type = uint16_t;
 };
 
 template <typename T, int kVec>
 union Values {
-  typename Vec<T, kVec>::type raw;
+  typename Vec<kVec>::type raw;
   T v[kVec];
   __device__ Values() {}
 };
 
-// Unit u of a rotated head: pair units first (two vectors of kVec values that
-// hold kVec pairs), then units of kVec values that are copied.
-template <typename T, int kVec>
-__device__ __forceinline__ void rotate_unit(const T* src, T* dst, int u, int rotary, bool interleaved, float factor,
-                                            const float2* cs) {
-  using V = typename Vec<T, kVec>::type;
-  const int pair_units = rotary / 2 / kVec;
-  if (u >= pair_units) {
-    const int at = rotary + (u - pair_units) * kVec;
-    *reinterpret_cast<V*>(dst + at) = *reinterpret_cast<const V*>(src + at);
-    return;
-  }
-  const int first = interleaved ? 2 * u * kVec : u * kVec;
-  const int second = interleaved ? first + kVec : rotary / 2 + u * kVec;
-  Values<T, kVec> x, y;
-  x.raw = *reinterpret_cast<const V*>(src + first);
-  y.raw = *reinterpret_cast<const V*>(src + second);
-  if (interleaved && kVec > 1) {
-#pragma unroll
-    for (int i = 0; i + 1 < kVec; i += 2) {
-      const float2 c0 = cs[u * kVec + i / 2], c1 = cs[u * kVec + (kVec + i) / 2];
-      const float a0 = pw::to_float(x.v[i]), b0 = pw::to_float(x.v[i + 1]);
-      const float a1 = pw::to_float(y.v[i]), b1 = pw::to_float(y.v[i + 1]);
-      x.v[i] = pw::from_float<T>(a0 * c0.x - b0 * c0.y);
-      x.v[i + 1] = pw::from_float<T>(a0 * c0.y + b0 * c0.x);
-      y.v[i] = pw::from_float<T>(a1 * c1.x - b1 * c1.y);
-      y.v[i + 1] = pw::from_float<T>(a1 * c1.y + b1 * c1.x);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float2 c = cs[u * kVec + i];
-      const float a = pw::to_float(x.v[i]), b = pw::to_float(y.v[i]);
-      x.v[i] = pw::from_float<T>(a * c.x - b * c.y);
-      y.v[i] = pw::from_float<T>(a * c.y + b * c.x);
-    }
-  }
-  *reinterpret_cast<V*>(dst + first) = x.raw;
-  *reinterpret_cast<V*>(dst + second) = y.raw;
+__device__ __forceinline__ int quotient(int n, int d, uint32_t inv) {
+  return inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), inv)) : n / d;
 }
 
-// One CTA per token.
+constexpr int kCopied = -1, kNear = -2;   // Unit::second of a copied unit, and of one whose pairs are neighbours
+
+// One unit: what it is, and its values.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  using V = typename Vec<T, kVec>::type;
-  extern __shared__ float2 cs[];
-  __shared__ int below;
+struct Unit {
+  Values<T, kVec> x, y;
+  int token;         // of the CTA's; -1: no unit
+  int head;          // of its kind
+  int first, second; // offsets of the vectors in the head, or kNear, kCopied
+};
+
+// Unit number w of the CTA's tokens, which start at t0 (a token's are those of
+// its queries, then keys, then values): loads it.  kind 0, 1, 2: query, key, value.
+template <typename T, int kVec>
+__device__ __forceinline__ void load_unit(const RopeParams& p, int t0, int w, int total, Unit<T, kVec>& u, int& kind) {
+  using V = typename Vec<kVec>::type;
   const pw_rope_args& a = p.a;
-  const int tid = threadIdx.x;
-  const int t = blockIdx.x;
-  // the token's sequence: how many sequences end at or before it
-  if (tid == 0) below = 0;
-  __syncthreads();
-  int n = 0;
-  for (int b = tid; b < a.batch; b += kThreads) n += a.q_offsets[b + 1] <= t;
-  if (n) atomicAdd(&below, n);
-  __syncthreads();
-  const int seq = below;
-  if (seq >= a.batch || a.q_offsets[seq] > t || a.q_offsets[seq] < 0) {
-    if (tid == 0) pw::report_status(a.status, PW_ERR_INVALID_ARG);
-    return;
+  u.token = -1;
+  if (w >= total) return;
+  u.token = quotient(w, p.units, p.token_inv);
+  w -= u.token * p.units;
+  const int64_t t = t0 + u.token;
+  const T* src;
+  if (w < p.units_q + p.units_k) {
+    kind = w < p.units_q ? 0 : 1;
+    if (kind) w -= p.units_q;
+    u.head = quotient(w, p.head_units, p.head_inv);
+    const int at = w - u.head * p.head_units;
+    src = kind ? static_cast<const T*>(a.k) + t * a.k_stride_token + u.head * a.k_stride_head
+               : static_cast<const T*>(a.q) + t * a.q_stride_token + u.head * a.q_stride_head;
+    if (at < p.pair_units) {
+      const bool near = a.interleaved && kVec > 1;
+      u.first = a.interleaved && kVec == 1 ? 2 * at : at * kVec;
+      u.second = near ? kNear : a.interleaved ? u.first + 1 : a.rotary_dim / 2 + u.first;
+      if (!near) u.y.raw = *reinterpret_cast<const V*>(src + u.second);
+    } else {
+      u.first = a.rotary_dim + (at - p.pair_units) * kVec;
+      u.second = kCopied;
+    }
+  } else {
+    kind = 2;
+    w -= p.units_q + p.units_k;
+    u.head = quotient(w, p.value_units, p.value_inv);
+    src = static_cast<const T*>(a.v) + t * a.v_stride_token + u.head * a.v_stride_head;
+    u.first = (w - u.head * p.value_units) * kVec;
+    u.second = kCopied;
   }
-  const int slot = a.kv_lens[seq] - (a.q_offsets[seq + 1] - t);
-  const int pos = a.positions ? a.positions[t] : slot;
-  const int half = a.rotary_dim / 2;
-  for (int i = tid; i < half; i += kThreads) {
-    const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(a.turns[i]) * static_cast<uint64_t>(static_cast<int64_t>(pos)));
-    float s, c;
-    sincospif(static_cast<float>(turn) * 0x1p-63f, &s, &c);   // in half turns, -1 .. 1
+  u.x.raw = *reinterpret_cast<const V*>(src + u.first);
+}
+
+template <typename T, int kVec>
+__device__ __forceinline__ void finish_unit(Unit<T, kVec>& u, T* dst, bool interleaved, const float2* cs) {
+  using V = typename Vec<kVec>::type;
+  if (kVec > 1 && u.second == kNear) {
+#pragma unroll
+    for (int i = 0; i + 1 < kVec; i += 2) {
+      const float2 c = cs[u.first / 2 + i / 2];
+      const float a = pw::to_float(u.x.v[i]), b = pw::to_float(u.x.v[i + 1]);
+      u.x.v[i] = pw::from_float<T>(a * c.x - b * c.y);
+      u.x.v[i + 1] = pw::from_float<T>(a * c.y + b * c.x);
+    }
+  } else if (u.second >= 0) {
+    const float2* c = cs + (interleaved ? u.first / 2 : u.first);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float a = pw::to_float(u.x.v[i]), b = pw::to_float(u.y.v[i]);
+      u.x.v[i] = pw::from_float<T>(a * c[i].x - b * c[i].y);
+      u.y.v[i] = pw::from_float<T>(a * c[i].y + b * c[i].x);
+    }
+    *reinterpret_cast<V*>(dst + u.second) = u.y.raw;
+  }
+  *reinterpret_cast<V*>(dst + u.first) = u.x.raw;
+}
+
+// A CTA takes p.per_cta tokens.  Their first values are loaded at once: they
+// depend on nothing, and the way to their place (sequence, length, page) takes
+// two trips to memory.
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ float2 cs[];
+  __shared__ int found[kMost], slots[kMost];
+  __shared__ int64_t k_at[kMost], v_at[kMost];   // offsets in the caches; -1: no place
+  const pw_rope_args& a = p.a;
+  const int tid = threadIdx.x, half = a.rotary_dim / 2;
+  const int t0 = blockIdx.x * p.per_cta, tokens = min(p.per_cta, a.tokens - t0), total = tokens * p.units;
+  if (tid < kMost) found[tid] = -1;
+  Unit<T, kVec> u[kAhead];
+  int kind[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load_unit<T, kVec>(p, t0, tid + i * kThreads, total, u[i], kind[i]);
+  __syncthreads();
+  // the tokens' sequences
+  for (int b = tid; b < a.batch; b += kThreads) {
+    const int lo = a.q_offsets[b], hi = a.q_offsets[b + 1], len = a.kv_lens[b];
+    for (int t = max(lo, t0); t < min(hi, t0 + tokens); ++t) {
+      found[t - t0] = b;
+      slots[t - t0] = len - (hi - t);
+    }
+  }
+  __syncthreads();
+  // their places in the cache
+  if (tid < tokens) {
+    const int seq = found[tid], slot = slots[tid];
+    int64_t k_off = -1, v_off = -1;
+    if (seq < 0) {
+      pw::report_status(a.status, PW_ERR_INVALID_ARG);
+    } else if (a.k) {
+      const int index = slot >= 0 ? slot / a.page_size : -1, in_page = slot - index * a.page_size;
+      const int page = index >= 0 && index < a.pages_per_seq ? a.page_table[seq * a.page_table_stride + index] : -1;
+      if (page < 0 || page >= a.num_pages) {
+        pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+      } else {
+        k_off = page * a.k_cache_stride_page + in_page * a.k_cache_stride_token;
+        v_off = page * a.v_cache_stride_page + in_page * a.v_cache_stride_token;
+      }
+    }
+    k_at[tid] = k_off;
+    v_at[tid] = v_off;
+  }
+  for (int i = tid; i < tokens * half; i += kThreads) {
+    const int token = i / half, pair = i - token * half;
+    const int64_t pos = a.positions ? a.positions[t0 + token] : slots[token];
+    const uint64_t turn = static_cast<uint64_t>(a.turns[pair]) * static_cast<uint64_t>(pos);
+    float s, c;   // in half turns, -1 .. 1
+    sincospif(static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
     cs[i] = make_float2(c * a.factor, s * a.factor);
   }
-  // the slot in the cache
-  const T* k_src = nullptr;
-  const T* v_src = nullptr;
-  T* k_dst = nullptr;
-  T* v_dst = nullptr;
-  int kv_heads = 0;
-  if (a.k) {
-    const int index = slot >= 0 ? slot / a.page_size : -1;
-    const int page = index >= 0 && index < a.pages_per_seq ? a.page_table[seq * a.page_table_stride + index] : -1;
-    if (page < 0 || page >= a.num_pages) {
-      if (tid == 0) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
-    } else {
-      const int64_t in_page = slot - index * a.page_size;
-      kv_heads = a.kv_heads;
-      k_src = static_cast<const T*>(a.k) + t * a.k_stride_token;
-      v_src = static_cast<const T*>(a.v) + t * a.v_stride_token;
-      k_dst = static_cast<T*>(a.k_cache) + page * a.k_cache_stride_page + in_page * a.k_cache_stride_token;
-      v_dst = static_cast<T*>(a.v_cache) + page * a.v_cache_stride_page + in_page * a.v_cache_stride_token;
-    }
-  }
   __syncthreads();
-  const int units_q = (a.q ? a.heads : 0) * p.group_q;
-  const int units_k = kv_heads * p.group_k;
-  const int units = units_q + units_k + kv_heads * p.groups_v;
-  for (int w = tid; w < units; w += kThreads) {
-    if (w < units_q) {
-      const int h = w / p.group_q;
-      rotate_unit<T, kVec>(static_cast<const T*>(a.q) + t * a.q_stride_token + h * a.q_stride_head,
-                           static_cast<T*>(a.q_out) + t * a.q_out_stride_token + h * a.q_out_stride_head,
-                           w - h * p.group_q, a.rotary_dim, a.interleaved, a.factor, cs);
-    } else if (w < units_q + units_k) {
-      const int h = (w - units_q) / p.group_k;
-      rotate_unit<T, kVec>(k_src + h * a.k_stride_head, k_dst + h * a.k_cache_stride_head,
-                           w - units_q - h * p.group_k, a.rotary_dim, a.interleaved, a.factor, cs);
-    } else {
-      const int r = w - units_q - units_k, h = r / p.groups_v, at = (r - h * p.groups_v) * kVec;
-      *reinterpret_cast<V*>(v_dst + h * a.v_cache_stride_head + at) =
-          *reinterpret_cast<const V*>(v_src + h * a.v_stride_head + at);
+  for (int w0 = 0;;) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int token = u[i].token;
+      if (token < 0 || found[token] < 0 || (kind[i] && k_at[token] < 0)) continue;
+      T* dst = kind[i] == 0   ? static_cast<T*>(a.q_out) + static_cast<int64_t>(t0 + token) * a.q_out_stride_token +
+                                  u[i].head * a.q_out_stride_head
+               : kind[i] == 1 ? static_cast<T*>(a.k_cache) + k_at[token] + u[i].head * a.k_cache_stride_head
+                              : static_cast<T*>(a.v_cache) + v_at[token] + u[i].head * a.v_cache_stride_head;
+      finish_unit<T, kVec>(u[i], dst, a.interleaved, cs + token * half);
     }
+    w0 += kAhead * kThreads;
+    if (w0 >= total) break;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_unit<T, kVec>(p, t0, w0 + tid + i * kThreads, total, u[i], kind[i]);
   }
 }
 
@@ -185,9 +235,24 @@ template <typename T, int kVec>
 int launch(const pw_rope_args& a, cudaStream_t s) {
   RopeParams p{};
   p.a = a;
-  p.group_q = p.group_k = a.rotary_dim / 2 / kVec + (a.head_dim - a.rotary_dim) / kVec;
-  p.groups_v = a.head_dim / kVec;
-  rope_kernel<T, kVec><<<static_cast<unsigned>(a.tokens), kThreads, sizeof(float2) * (a.rotary_dim / 2 + 1), s>>>(p);
+  p.pair_units = a.interleaved && kVec > 1 ? a.rotary_dim / kVec : a.rotary_dim / 2 / kVec;
+  p.head_units = p.pair_units + (a.head_dim - a.rotary_dim) / kVec;
+  p.value_units = a.head_dim / kVec;
+  p.units_q = a.q ? a.heads * p.head_units : 0;
+  p.units_k = a.k ? a.kv_heads * p.head_units : 0;
+  p.units = p.units_q + p.units_k + (a.k ? a.kv_heads * p.value_units : 0);
+  if (p.units == 0) return PW_OK;   // no heads
+  // one token a CTA while they do not fill the SMs, then kPerCta: the search for
+  // the place is shared (59 us with one, 56 with two)
+  const int sms = pw::sm_count();
+  p.per_cta = a.tokens > 8 * sms ? kPerCta : 1;
+  const bool few = static_cast<int64_t>(p.units) * p.per_cta < (1 << 16);
+  auto inverse = [&](int d) { return few && d > 1 ? static_cast<uint32_t>(((1ull << 32) + d - 1) / d) : 0u; };
+  p.head_inv = inverse(p.head_units);
+  p.value_inv = inverse(p.value_units);
+  p.token_inv = inverse(p.units);
+  rope_kernel<T, kVec><<<static_cast<unsigned>((a.tokens + p.per_cta - 1) / p.per_cta), kThreads,
+                         sizeof(float2) * (p.per_cta * (a.rotary_dim / 2) + 1), s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
