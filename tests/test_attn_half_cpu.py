@@ -212,3 +212,27 @@ def test_binding_checks():
         pw.pw_quantize_fp8(x.float(), x, x)
     with pytest.raises(ValueError):
         pw.pw_rope_append(None, None, None, x, None, None, None, x, x, None, x)
+
+
+def test_paged_cache_hands_out_pages():
+    from any_precision_bit_pw_gb300.decoder import PagedCache
+    c = PagedCache(6, 4, 1, 8, device="cpu")
+    b = c.batch([5, 9], [7, 0])
+    assert (b.tokens, b.max_q_len, b.max_kv_len) == (7, 7, 7)
+    assert b.q_offsets.tolist() == [0, 7, 7] and b.kv_lens.tolist() == [7, 0]
+    assert b.page_table.tolist() == [c.pages[5], [-1, -1]] and len(set(c.pages[5])) == 2
+    before = list(c.pages[5])
+    b = c.batch([9, 5], [1, 1], width=3)                 # sequence 5 still has room in its second page
+    assert c.pages[5] == before and b.kv_lens.tolist() == [1, 8] and b.page_table.shape == (2, 3)
+    assert len(c.free_pages) == 3 and b.page_table[0, 1:].tolist() == [-1, -1]
+    for bad in (dict(seqs=[5, 5], new_tokens=[1, 1]), dict(seqs=[5], new_tokens=[-1]), dict(seqs=[5], new_tokens=[4], width=2)):
+        with pytest.raises((ValueError, RuntimeError)):
+            c.batch(**bad)
+    with pytest.raises(RuntimeError):
+        c.batch([5], [40])
+    free = len(c.free_pages)
+    held = len(c.pages[5])
+    c.release(5)
+    assert len(c.free_pages) == free + held and 5 not in c.lens
+    c.release(5)                                         # nothing left to return
+    assert len(c.free_pages) == free + held
