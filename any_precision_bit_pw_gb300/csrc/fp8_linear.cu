@@ -181,21 +181,74 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
   const int group_size = kPair ? 2 : p.splits;
   const int first_tile = blockIdx.x / group_size, tile_step = gridDim.x / group_size;
   const int kb0 = kPair ? 0 : p.KB * rank / p.splits, kb1 = kPair ? p.KB : p.KB * (rank + 1) / p.splits;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      pw::mbar_init(pw::smem_u32(&sh.full[i]), 1);
-      pw::mbar_init(pw::smem_u32(&sh.empty[i]), 1);
+  const uint32_t scale_smem = stages + C::kStages * C::kStageBytes + kSumWarps * kOutBytes;
+  // Copies of one group (the copy warp).
+  pw::Ring<C::kStages> stage;
+  pw::Ring<kScaleSlots> slot;
+  uint32_t x = 0, fours = 0;   // groups, and fours of groups, started
+  auto start_group = [&](int kb, int mt, int nt) {
+    const int row_a = mt * C::kM + (kPair ? 128 * rank : 0), row_b = nt * C::kN + (kPair ? C::kRowsB * rank : 0);
+    const uint32_t bar = pw::smem_u32(&sh.full[stage.at]), dst = stages + stage.at * C::kStageBytes;
+    if (p.wide_scales && (kb == kb0 || (kb & 3) == 0)) {
+      // The slot is free: the MMAs of group x - kStages are done, they were
+      // issued after every warp had read the accumulator of group x - kStages -
+      // kAccs (at most 11 back), and the slot's last user is at least 14 back
+      // (seven fours of a tile of two groups or more).
+      const uint32_t sbar = pw::smem_u32(&sh.scales[slot.at]), sdst = scale_smem + slot.at * kScaleBytes;
+      if (pw::elect_one()) {
+        pw::mbar_arrive_expect_tx(sbar, 16 * (C::kRowsA + C::kN / 128));
+        pw::tma_load_2d(sdst, &map_sa, kb & ~3, row_a, sbar);
+        pw::tma_load_2d(sdst + kTokenScaleBytes, &map_sb, kb & ~3, nt * (C::kN / 128), sbar);
+      }
+      ++fours;
+      slot.next();
+      __syncwarp();
     }
-    for (int i = 0; i < C::kAccs; ++i) {
-      pw::mbar_init(pw::smem_u32(&sh.done[i]), 1);
-      pw::mbar_init(pw::smem_u32(&sh.read[i]), 2 * C::kQuarters * (kPair ? 2 : 1));
+    if (pw::elect_one()) {
+      if constexpr (kPair) {
+        // both CTAs' copies complete on the first one's barrier
+        if (rank == 0) pw::mbar_arrive_expect_tx(bar, 2 * C::kStageBytes);
+        const uint32_t lead = pw::map_shared(bar, 0);
+        pw::tma_load_2d_pair(dst, &map_a, kb * pw::kGroup, row_a, lead);
+        pw::tma_load_2d_pair(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, lead);
+      } else {
+        pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
+        pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, row_a, bar);
+        pw::tma_load_2d(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, bar);
+      }
     }
-    for (int i = 0; i < kScaleSlots; ++i) pw::mbar_init(pw::smem_u32(&sh.scales[i]), 1);
-    pw::mbar_init(pw::smem_u32(&sh.drained), 1);
-    sh.dead = 0;
-    pw::mbar_init_fence();
-  }
+    stage.next();
+    ++x;
+    __syncwarp();
+  };
+  int kb_early = kb0;   // groups of the first tile that are under way before the set-up is done
   if (warp == kCopyWarp) {
+    if (pw::elect_one()) {
+      pw::prefetch_tmap(&map_a);
+      pw::prefetch_tmap(&map_b);
+      for (int i = 0; i < C::kStages; ++i) {
+        pw::mbar_init(pw::smem_u32(&sh.full[i]), 1);
+        pw::mbar_init(pw::smem_u32(&sh.empty[i]), 1);
+      }
+      for (int i = 0; i < C::kAccs; ++i) {
+        pw::mbar_init(pw::smem_u32(&sh.done[i]), 1);
+        pw::mbar_init(pw::smem_u32(&sh.read[i]), 2 * C::kQuarters * (kPair ? 2 : 1));
+      }
+      for (int i = 0; i < kScaleSlots; ++i) pw::mbar_init(pw::smem_u32(&sh.scales[i]), 1);
+      pw::mbar_init(pw::smem_u32(&sh.drained), 1);
+      sh.dead = 0;
+      pw::mbar_init_fence();
+    }
+    __syncwarp();
+    // A single CTA's copies need its own barriers only: they start here, while
+    // the others set up Tensor Memory.
+    if constexpr (!kPair) {
+      int mt, nt;
+      tile_at<C::kM>(first_tile, tiles_m, tiles_n, mt, nt);
+      for (; kb_early < kb1 && x < C::kStages; ++kb_early) start_group(kb_early, mt, nt);
+    }
+  }
+  if (warp == kMmaWarp) {
     if constexpr (kPair) {
       pw::tmem_alloc_pair(pw::smem_u32(&sh.tmem), 512);
     } else {
@@ -205,62 +258,19 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
   }
   pw::tc_fence_before();
   __syncthreads();
-  if (group_size > 1) pw::cluster_sync();   // the other CTAs' barriers are set up
+  if constexpr (kPair) pw::cluster_sync();   // the other CTA's barriers are set up
   pw::tc_fence_after();
   const uint32_t tmem = pw::uniform(sh.tmem);
-  const uint32_t scale_smem = stages + C::kStages * C::kStageBytes + kSumWarps * kOutBytes;
 
   if (warp == kCopyWarp) {
     if constexpr (C::kMove) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (pw::elect_one()) {
-      pw::prefetch_tmap(&map_a);
-      pw::prefetch_tmap(&map_b);
-      pw::prefetch_tmap(&map_y);
-      pw::prefetch_tmap(&map_sa);
-      pw::prefetch_tmap(&map_sb);
-    }
-    pw::Ring<C::kStages> stage;
-    pw::Ring<kScaleSlots> slot;
-    uint32_t x = 0, fours = 0;   // groups, and fours of groups, started
     bool ok = true;
     for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
       int mt, nt;
       tile_at<C::kM>(tile, tiles_m, tiles_n, mt, nt);
-      const int row_a = mt * C::kM + (kPair ? 128 * rank : 0), row_b = nt * C::kN + (kPair ? C::kRowsB * rank : 0);
-      for (int kb = kb0; kb < kb1; ++kb, ++x) {
+      for (int kb = tile == first_tile ? kb_early : kb0; kb < kb1; ++kb) {
         if (x >= C::kStages && !(ok = wait(sh.empty[stage.at], stage.parity ^ 1u, sh, p))) break;
-        const uint32_t bar = pw::smem_u32(&sh.full[stage.at]), dst = stages + stage.at * C::kStageBytes;
-        stage.next();
-        if (p.wide_scales && (kb == kb0 || (kb & 3) == 0)) {
-          // The slot is free: the MMAs of group x - kStages are done, they were issued
-          // after every warp had read the accumulator of group x - kStages -
-          // kAccs (at most 11 back), and the slot's last user is at least 14 back (seven fours of a
-          // tile of two groups or more).
-          const uint32_t sbar = pw::smem_u32(&sh.scales[slot.at]);
-          if (pw::elect_one()) {
-            const uint32_t dst = scale_smem + slot.at * kScaleBytes;
-            pw::mbar_arrive_expect_tx(sbar, 16 * (C::kRowsA + C::kN / 128));
-            pw::tma_load_2d(dst, &map_sa, kb & ~3, row_a, sbar);
-            pw::tma_load_2d(dst + kTokenScaleBytes, &map_sb, kb & ~3, nt * (C::kN / 128), sbar);
-          }
-          ++fours;
-          slot.next();
-          __syncwarp();
-        }
-        if (pw::elect_one()) {
-          if constexpr (kPair) {
-            // both CTAs' copies complete on the first one's barrier
-            if (rank == 0) pw::mbar_arrive_expect_tx(bar, 2 * C::kStageBytes);
-            const uint32_t lead = pw::map_shared(bar, 0);
-            pw::tma_load_2d_pair(dst, &map_a, kb * pw::kGroup, row_a, lead);
-            pw::tma_load_2d_pair(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, lead);
-          } else {
-            pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
-            pw::tma_load_2d(dst, &map_a, kb * pw::kGroup, row_a, bar);
-            pw::tma_load_2d(dst + C::kRowsA * kBoxBytes, &map_b, kb * pw::kGroup, row_b, bar);
-          }
-        }
-        __syncwarp();
+        start_group(kb, mt, nt);
       }
     }
     // No copy may be in flight when the CTA leaves.  A pair's second CTA leaves
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
   __syncthreads();
   if (group_size > 1) pw::cluster_sync();   // sums are in place; nobody still signals or feeds a CTA that leaves
   pw::tc_fence_after();
-  if (warp == kCopyWarp) {
+  if (warp == kMmaWarp) {
     if constexpr (kPair)
       pw::tmem_dealloc_pair(tmem, 512);
     else
@@ -456,13 +466,18 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
       const int rows = min(C::kM, p.M - mt * C::kM), col = 4 * lane, n = nt * 128 + col;
       for (int row = rank + p.splits * warp; row < rows; row += p.splits * (C::kThreads / 32)) {
         const uint32_t at = stages + 4u * static_cast<uint32_t>(row * kPartRow + col);
-        float4 v = pw::ld_cluster_f4(pw::map_shared(at, 0));
-        for (int i = 1; i < p.splits; ++i) {
-          const float4 w = pw::ld_cluster_f4(pw::map_shared(at, i));
-          v.x += w.x;
-          v.y += w.y;
-          v.z += w.z;
-          v.w += w.w;
+        float4 part[4];   // all loads, then the sum in the order of the ranks
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < p.splits) part[i] = pw::ld_cluster_f4(pw::map_shared(at, i));
+        float4 v = part[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+          if (i >= p.splits) break;
+          v.x += part[i].x;
+          v.y += part[i].y;
+          v.z += part[i].z;
+          v.w += part[i].w;
         }
         if (sh.dead) continue;
         T* y = static_cast<T*>(p.y) + static_cast<int64_t>(mt * C::kM + row) * p.ldy + n;
