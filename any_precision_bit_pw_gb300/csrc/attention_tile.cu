@@ -9,9 +9,10 @@
 // Memory; the weights P overwrite S in 16 bits and feed the second product
 // from there.
 //
-// The running maximum moves only when a row's new maximum exceeds it by 2^8:
-// until then the weights stay below 2^8 and need no common factor, so the
-// output is rescaled a few times per row instead of at every block.
+// The running maximum moves only when a row's new maximum exceeds it by 2^8
+// (by 2^15 inside a block): until then the weights stay in the 16-bit range and
+// need no common factor, so the output is rescaled a few times per row instead
+// of at every block.
 //
 // Keys and values arrive by TMA, a box per page piece, into 128-byte swizzled
 // rows.  Values outside the visible keys are zeros in shared memory (a weight
@@ -34,7 +35,8 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kKeyWarp = 8, kValueWarp = 9, kMmaWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint64_t kDrainNs = 1000000000ull;
-constexpr float kLazy = 8.0f;          // log2 of what a weight may grow to
+constexpr float kLazy = 8.0f;          // log2 of what a weight may grow to, from block to block
+constexpr float kLazyInside = 15.0f;   // and inside a block
 constexpr int kHalfRow = kBlock * 128; // bytes of 64 values of 128 rows
 
 template <int D>
@@ -44,7 +46,7 @@ constexpr int smem_bytes() { return (2 + kKeySlots + kValueSlots) * tile_bytes<D
 
 struct alignas(8) Shared {
   uint64_t q_full[2], k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots];
-  uint64_t drained, s_full[2], p_full[2][2], o_done[2];   // p_full: weights of the first and the last 64 keys
+  uint64_t drained, s_full[2], p_full[2][2], o_half[2], o_done[2];   // p_full: weights of the first and the last 64 keys
   uint32_t tmem;
   int dead;
   int last;
@@ -216,8 +218,8 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
         pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues,
                       !first || part > 0 || j > 0);
       }
+      pw::tc_commit(bar(part ? sh.o_done[h] : sh.o_half[h]));
       if (part) {
-        pw::tc_commit(bar(sh.o_done[h]));
         if (free_after) pw::tc_commit(bar(sh.v_empty[vals.at]));
       }
     }
@@ -318,6 +320,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       __syncwarp();
       if (lane == 0) pw::mbar_arrive(bar(sh.q_full[h]));
       const int pos = c.s.kv_len - c.s.q_len + pw_attn::token_of(p, r);
+      const uint64_t scale2 = pw::pack_f32x2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
       // the row's visible keys; a row past the end takes all of them and is not written
       const int hi = !live ? 0x7FFFFFFF : a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
       const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
@@ -326,12 +329,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
         wait(sh.s_full[h], blocks & 1u, sh, p);
         pw::tc_fence_after();
         const bool all = __all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock);   // no mask in this block
-        // 64 scores at a time, twice: once for the maximum, once for the
-        // weights.  Loading them again costs 70 cycles; keeping all 128 costs
-        // spills, and a loop of twice the instructions that keeps the other
-        // roles' out of the instruction cache.
-        uint32_t s[2][32];
-        auto load = [&](int i) {
+        // 64 scores at a time: their maximum, then their weights, so that the
+        // second product can start on the first 64 keys (with the maximum of all
+        // 128 first it starts 350 cycles later, and the period is longer by as
+        // much).
+        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          uint32_t s[2][32];
           pw::tmem_ld_x32(s_tmem + 64 * i, s[0]);
           pw::tmem_ld_x32(s_tmem + 64 * i + 32, s[1]);
           pw::tmem_ld_wait();
@@ -341,52 +346,55 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
             for (int j = 0; j < 64; ++j)
               if (j < from || j >= to) s[j >> 5][j & 31] = 0xFF800000u;   // -inf
           }
-        };
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          load(i);
           float most[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) most[j] = fmaxf(__uint_as_float(s[j >> 1][16 * (j & 1)]), __uint_as_float(s[j >> 1][16 * (j & 1) + 1]));
+          for (int j = 0; j < 4; ++j)
+            most[j] = fmaxf(__uint_as_float(s[j >> 1][16 * (j & 1)]), __uint_as_float(s[j >> 1][16 * (j & 1) + 1]));
 #pragma unroll
           for (int k = 2; k < 16; k += 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               most[j] = pw::max3(most[j], __uint_as_float(s[j >> 1][16 * (j & 1) + k]),
                                  __uint_as_float(s[j >> 1][16 * (j & 1) + k + 1]));
-          top = pw::max3(top, pw::max3(most[0], most[1], most[2]), most[3]);
-        }
-        // m follows the maximum in steps of at least 2^8 (and at once from -inf)
-        const bool moves = top > m && !((top - m) * p.scale_log2 <= kLazy);
-        float keep = 1.0f;
-        if (moves) {
-          keep = pw::exp2_fast((m - top) * p.scale_log2);
-          m = top;
-          l *= keep;
-        }
-        if (b > b0 && __any_sync(0xFFFFFFFFu, moves)) {
-          // O has to be complete up to the last block before it is scaled
-          wait(sh.o_done[h], (blocks - 1) & 1u, sh, p);
-          pw::tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t o[16];
-            pw::tmem_ld_x16(o_tmem + 16 * i, o);
-            pw::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-            pw::tmem_st_x16(o_tmem + 16 * i, o);
-          }
-          pw::tmem_st_wait();
-        }
-        const float off = m == -INFINITY ? 0.0f : -m * p.scale_log2;
-        const uint64_t scale2 = pw::pack_f32x2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
-        const uint64_t off2 = pw::pack_f32x2(__float_as_uint(off), __float_as_uint(off));
-        uint64_t sum[2] = {0, 0};
+          const float top = fmaxf(pw::max3(most[0], most[1], most[2]), most[3]);
+          // m follows the maximum in steps of at least 2^8 (and at once from
+          // -inf); between a block's two parts only where the weights would
+          // leave the 16-bit range otherwise.
+          const bool moves = top > m && !((top - m) * p.scale_log2 <= (i ? kLazyInside : kLazy));
+          if (__any_sync(0xFFFFFFFFu, moves)) {
+            const bool scales = moves && m != -INFINITY;   // else there is nothing to scale
+            float keep = 1.0f;
+            if (moves) {
+              keep = pw::exp2_fast((m - top) * p.scale_log2);
+              m = top;
+              l *= keep;
+            }
+            if (__any_sync(0xFFFFFFFFu, scales)) {
+              if (!scales) keep = 1.0f;
+              // the sum so far of this block's first part
+              if (i) {
+                float s0, s1;
+                pw::unpack_f32x2(pw::add_f32x2(sum[0], sum[1]), s0, s1);
+                l += (s0 + s1) * keep;
+                sum[0] = sum[1] = 0;
+              }
+              // O has to be complete up to here before it is scaled
+              wait(i ? sh.o_half[h] : sh.o_done[h], (i ? blocks : blocks - 1) & 1u, sh, p);
+              pw::tc_fence_after();
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          load(i);
+              for (int j = 0; j < D / 16; ++j) {
+                uint32_t o[16];
+                pw::tmem_ld_x16(o_tmem + 16 * j, o);
+                pw::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                pw::tmem_st_x16(o_tmem + 16 * j, o);
+              }
+              pw::tmem_st_wait();
+            }
+          }
+          const float off = m == -INFINITY ? 0.0f : -m * p.scale_log2;
+          const uint64_t off2 = pw::pack_f32x2(__float_as_uint(off), __float_as_uint(off));
           uint32_t w[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -537,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pw::mbar_init(bar(sh.s_full[i]), 1);
       pw::mbar_init(bar(sh.p_full[i][0]), 4);
       pw::mbar_init(bar(sh.p_full[i][1]), 4);
+      pw::mbar_init(bar(sh.o_half[i]), 1);
       pw::mbar_init(bar(sh.o_done[i]), 1);
     }
     pw::mbar_init(bar(sh.drained), 1);
