@@ -607,43 +607,49 @@ int launch(const LinearParams& p, cudaStream_t s) {
 
 }  // namespace
 
-extern "C" int pw_fp8_linear(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t a_scale_stride,
-                             const uint8_t* d_b, int64_t ldb, const float* d_b_scale, int64_t b_scale_stride, int M,
-                             int N, int K, int dtype, void* d_y, int64_t ldy, int32_t* d_status, void* stream) {
-  if (!pw::is_16bit(dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "fp8_linear: dtype %d", dtype);
-  if (M < 0 || N < 1 || K < 1) return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: bad sizes M=%d N=%d K=%d", M, N, K);
-  if (M > (1 << 20) || N > (1 << 24) || K > (1 << 24))
-    return pw::set_error(PW_ERR_UNSUPPORTED, "fp8_linear: M=%d (at most 2^20), N=%d, K=%d (at most 2^24)", M, N, K);
-  const int kb = (K + pw::kGroup - 1) / pw::kGroup;
-  if (lda < K || ldb < K || ldy < N || a_scale_stride < kb || b_scale_stride < kb)
+extern "C" int pw_fp8_linear(const pw_linear_args* args, void* stream) {
+  if (!args) return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: NULL argument");
+  const pw_linear_args& a = *args;
+  if (!pw::is_16bit(a.dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "fp8_linear: dtype %d", a.dtype);
+  if (a.m < 0 || a.n < 1 || a.k < 1)
+    return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: bad sizes m=%d n=%d k=%d", a.m, a.n, a.k);
+  if (a.m > (1 << 20) || a.n > (1 << 24) || a.k > (1 << 24))
+    return pw::set_error(PW_ERR_UNSUPPORTED, "fp8_linear: m=%d (at most 2^20), n=%d, k=%d (at most 2^24)", a.m, a.n, a.k);
+  const int kb = (a.k + pw::kGroup - 1) / pw::kGroup;
+  if (a.lda < a.k || a.ldb < a.k || a.ldy < a.n || a.a_scale_stride < kb || a.b_scale_stride < kb)
     return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: a row stride is below its columns");
-  if (M == 0) return PW_OK;
-  if (!d_a || !d_a_scale || !d_b || !d_b_scale || !d_y || !d_status)
+  if (a.m == 0) return PW_OK;
+  if (!a.a || !a.a_scale || !a.b || !a.b_scale || !a.y || !a.status)
     return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: NULL argument");
-  if (!pw::aligned(d_a, 16) || !pw::aligned(d_b, 16) || lda % 16 || ldb % 16)
+  if (!pw::aligned(a.a, 16) || !pw::aligned(a.b, 16) || a.lda % 16 || a.ldb % 16)
     return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: the rows of a and b must be 16-byte aligned");
-  if (!pw::aligned(d_a_scale, 4) || !pw::aligned(d_b_scale, 4) || !pw::aligned(d_y, 2))
+  // what a tensor map can hold
+  if (a.lda >= (1ll << 39) || a.ldb >= (1ll << 39) || a.ldy >= (1ll << 38) || a.a_scale_stride >= (1ll << 37) ||
+      a.b_scale_stride >= (1ll << 37))
+    return pw::set_error(PW_ERR_UNSUPPORTED, "fp8_linear: a row stride is too large");
+  if (!pw::aligned(a.a_scale, 4) || !pw::aligned(a.b_scale, 4) || !pw::aligned(a.y, 2) || !pw::aligned(a.status, 4))
     return pw::set_error(PW_ERR_INVALID_ARG, "fp8_linear: a pointer is not aligned to its values");
   LinearParams p{};
-  p.a = d_a;
-  p.b = d_b;
-  p.sa = d_a_scale;
-  p.sb = d_b_scale;
-  p.y = d_y;
-  p.lda = lda;
-  p.ldb = ldb;
-  p.ldy = ldy;
-  p.sa_stride = a_scale_stride;
-  p.sb_stride = b_scale_stride;
-  p.M = M;
-  p.N = N;
-  p.K = K;
+  p.a = a.a;
+  p.b = a.b;
+  p.sa = a.a_scale;
+  p.sb = a.b_scale;
+  p.y = a.y;
+  p.lda = a.lda;
+  p.ldb = a.ldb;
+  p.ldy = a.ldy;
+  p.sa_stride = a.a_scale_stride;
+  p.sb_stride = a.b_scale_stride;
+  p.M = a.m;
+  p.N = a.n;
+  p.K = a.k;
   p.KB = kb;
-  p.status = d_status;
-  p.wide_y = pw::aligned(d_y, 16) && ldy % 8 == 0;
+  p.splits = 1;
+  p.status = a.status;
+  p.wide_y = pw::aligned(a.y, 16) && a.ldy % 8 == 0;
   // with one group a tile the slots of the scales would be reused too early
-  p.wide_scales = kb >= 2 && pw::aligned(d_a_scale, 16) && pw::aligned(d_b_scale, 16) && a_scale_stride % 4 == 0 &&
-                  b_scale_stride % 4 == 0;
+  p.wide_scales = kb >= 2 && pw::aligned(a.a_scale, 16) && pw::aligned(a.b_scale, 16) && a.a_scale_stride % 4 == 0 &&
+                  a.b_scale_stride % 4 == 0;
   cudaStream_t s = pw::as_stream(stream);
-  return dtype == PW_DTYPE_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
+  return a.dtype == PW_DTYPE_F16 ? launch<__half>(p, s) : launch<__nv_bfloat16>(p, s);
 }

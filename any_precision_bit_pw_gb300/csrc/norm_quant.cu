@@ -271,94 +271,95 @@ int check_matrix(const char* op, const char* name, int64_t stride, int cols) {
 
 extern "C" {
 
-int pw_add_rmsnorm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
-                   const void* d_weight, int64_t rows, int cols, float eps, int dtype, void* d_residual_out,
-                   int64_t residual_out_stride, void* d_y, int64_t y_stride, uint8_t* d_q, int64_t q_stride,
-                   float* d_scale, int64_t scale_stride, void* stream) {
-  if (!pw::is_16bit(dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: dtype %d", dtype);
-  if (rows < 0 || cols < 1) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: %lld rows of %d columns",
-                                                 static_cast<long long>(rows), cols);
-  if (cols > kMaxCols || rows > 0x7FFFFFFF)
-    return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: at most %d columns (got %d) and 2^31 - 1 rows", kMaxCols, cols);
-  if (!(eps >= 0.0f)) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: eps %g", static_cast<double>(eps));
-  if (!d_y && !d_q) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: neither a 16-bit nor an 8-bit output");
-  if (!d_q != !d_scale) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: 8-bit codes and scales come together");
-  if (int e = check_matrix("add_rmsnorm", "x", x_stride, cols)) return e;
-  if (d_residual)
-    if (int e = check_matrix("add_rmsnorm", "residual", residual_stride, cols)) return e;
-  if (d_residual_out)
-    if (int e = check_matrix("add_rmsnorm", "residual_out", residual_out_stride, cols)) return e;
-  if (d_y)
-    if (int e = check_matrix("add_rmsnorm", "y", y_stride, cols)) return e;
-  if (d_q) {
-    if (int e = check_matrix("add_rmsnorm", "q", q_stride, cols)) return e;
-    if (int e = check_matrix("add_rmsnorm", "scale", scale_stride, (cols + pw::kGroup - 1) / pw::kGroup)) return e;
+int pw_add_rmsnorm(const pw_norm_args* args, void* stream) {
+  if (!args) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: NULL argument");
+  const pw_norm_args& a = *args;
+  if (!pw::is_16bit(a.dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: dtype %d", a.dtype);
+  if (a.rows < 0 || a.cols < 1)
+    return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: %lld rows of %d columns", static_cast<long long>(a.rows), a.cols);
+  if (a.cols > kMaxCols || a.rows > 0x7FFFFFFF)
+    return pw::set_error(PW_ERR_UNSUPPORTED, "add_rmsnorm: at most %d columns (got %d) and 2^31 - 1 rows", kMaxCols, a.cols);
+  if (!(a.eps >= 0.0f)) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: eps %g", static_cast<double>(a.eps));
+  if (!a.y && !a.q) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: neither a 16-bit nor an 8-bit output");
+  if (!a.q != !a.scale) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: 8-bit codes and scales come together");
+  if (int e = check_matrix("add_rmsnorm", "x", a.x_stride, a.cols)) return e;
+  if (a.residual)
+    if (int e = check_matrix("add_rmsnorm", "residual", a.residual_stride, a.cols)) return e;
+  if (a.residual_out)
+    if (int e = check_matrix("add_rmsnorm", "residual_out", a.residual_out_stride, a.cols)) return e;
+  if (a.y)
+    if (int e = check_matrix("add_rmsnorm", "y", a.y_stride, a.cols)) return e;
+  if (a.q) {
+    if (int e = check_matrix("add_rmsnorm", "q", a.q_stride, a.cols)) return e;
+    if (int e = check_matrix("add_rmsnorm", "scale", a.scale_stride, (a.cols + pw::kGroup - 1) / pw::kGroup)) return e;
   }
-  if (rows == 0) return PW_OK;
-  if (!d_x || !d_weight) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: NULL argument");
-  if (!pw::aligned(d_x, 2) || !pw::aligned(d_weight, 2) || !pw::aligned(d_residual, 2) ||
-      !pw::aligned(d_residual_out, 2) || !pw::aligned(d_y, 2) || !pw::aligned(d_scale, 4))
+  if (a.rows == 0) return PW_OK;
+  if (!a.x || !a.weight) return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: NULL argument");
+  if (!pw::aligned(a.x, 2) || !pw::aligned(a.weight, 2) || !pw::aligned(a.residual, 2) ||
+      !pw::aligned(a.residual_out, 2) || !pw::aligned(a.y, 2) || !pw::aligned(a.scale, 4))
     return pw::set_error(PW_ERR_INVALID_ARG, "add_rmsnorm: a pointer is not aligned to its values");
   RowParams p{};
-  p.x = d_x;
-  p.res = d_residual;
-  p.w = d_weight;
-  p.res_out = d_residual_out;
-  p.y = d_y;
-  p.q = d_q;
-  p.scale = d_scale;
-  p.x_stride = x_stride;
-  p.res_stride = residual_stride;
-  p.res_out_stride = residual_out_stride;
-  p.y_stride = y_stride;
-  p.q_stride = q_stride;
-  p.scale_stride = scale_stride;
-  p.rows = rows;
-  p.cols = cols;
-  p.eps = eps;
-  const bool al = rows_aligned(d_x, x_stride, cols) && rows_aligned(d_residual, residual_stride, cols) &&
-                  rows_aligned(d_weight, kVec, cols) && rows_aligned(d_residual_out, residual_out_stride, cols) &&
-                  rows_aligned(d_y, y_stride, cols) && codes_aligned(d_q, q_stride);
+  p.x = a.x;
+  p.res = a.residual;
+  p.w = a.weight;
+  p.res_out = a.residual_out;
+  p.y = a.y;
+  p.q = a.q;
+  p.scale = a.scale;
+  p.x_stride = a.x_stride;
+  p.res_stride = a.residual_stride;
+  p.res_out_stride = a.residual_out_stride;
+  p.y_stride = a.y_stride;
+  p.q_stride = a.q_stride;
+  p.scale_stride = a.scale_stride;
+  p.rows = a.rows;
+  p.cols = a.cols;
+  p.eps = a.eps;
+  const bool al = rows_aligned(a.x, a.x_stride, a.cols) && rows_aligned(a.residual, a.residual_stride, a.cols) &&
+                  rows_aligned(a.weight, kVec, a.cols) && rows_aligned(a.residual_out, a.residual_out_stride, a.cols) &&
+                  rows_aligned(a.y, a.y_stride, a.cols) && codes_aligned(a.q, a.q_stride);
   cudaStream_t s = pw::as_stream(stream);
-  if (dtype == PW_DTYPE_F16) return al ? launch_rows<__half, true, true>(p, s) : launch_rows<__half, false, true>(p, s);
+  if (a.dtype == PW_DTYPE_F16) return al ? launch_rows<__half, true, true>(p, s) : launch_rows<__half, false, true>(p, s);
   return al ? launch_rows<__nv_bfloat16, true, true>(p, s) : launch_rows<__nv_bfloat16, false, true>(p, s);
 }
 
-int pw_quantize_fp8(const void* d_x, int64_t x_stride, int64_t rows, int cols, int dtype, int block_rows, uint8_t* d_q,
-                    int64_t q_stride, float* d_scale, int64_t scale_stride, void* stream) {
-  if (!pw::is_16bit(dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: dtype %d", dtype);
-  if (block_rows != 1 && block_rows != pw::kGroup)
-    return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: block_rows %d (1 or 128)", block_rows);
-  if (rows < 0 || cols < 1) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: %lld rows of %d columns",
-                                                 static_cast<long long>(rows), cols);
+int pw_quantize_fp8(const pw_quant_args* args, void* stream) {
+  if (!args) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: NULL argument");
+  const pw_quant_args& a = *args;
+  if (!pw::is_16bit(a.dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: dtype %d", a.dtype);
+  if (a.block_rows != 1 && a.block_rows != pw::kGroup)
+    return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: block_rows %d (1 or 128)", a.block_rows);
+  if (a.rows < 0 || a.cols < 1)
+    return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: %lld rows of %d columns", static_cast<long long>(a.rows), a.cols);
   // blocks: the grid's second axis counts 128-row strips
-  if (block_rows == 1 ? (cols > kMaxCols || rows > 0x7FFFFFFF) : rows > 65535ll * pw::kGroup)
+  if (a.block_rows == 1 ? (a.cols > kMaxCols || a.rows > 0x7FFFFFFF)
+                        : (a.rows > 65535ll * pw::kGroup || a.cols > 0x7FFFFFFF - pw::kGroup))
     return pw::set_error(PW_ERR_UNSUPPORTED, "quantize_fp8: %lld rows of %d columns are too large",
-                         static_cast<long long>(rows), cols);
-  if (int e = check_matrix("quantize_fp8", "x", x_stride, cols)) return e;
-  if (int e = check_matrix("quantize_fp8", "q", q_stride, cols)) return e;
-  if (int e = check_matrix("quantize_fp8", "scale", scale_stride, (cols + pw::kGroup - 1) / pw::kGroup)) return e;
-  if (rows == 0) return PW_OK;
-  if (!d_x || !d_q || !d_scale) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: NULL argument");
-  if (!pw::aligned(d_x, 2) || !pw::aligned(d_scale, 4))
+                         static_cast<long long>(a.rows), a.cols);
+  if (int e = check_matrix("quantize_fp8", "x", a.x_stride, a.cols)) return e;
+  if (int e = check_matrix("quantize_fp8", "q", a.q_stride, a.cols)) return e;
+  if (int e = check_matrix("quantize_fp8", "scale", a.scale_stride, (a.cols + pw::kGroup - 1) / pw::kGroup)) return e;
+  if (a.rows == 0) return PW_OK;
+  if (!a.x || !a.q || !a.scale) return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: NULL argument");
+  if (!pw::aligned(a.x, 2) || !pw::aligned(a.scale, 4))
     return pw::set_error(PW_ERR_INVALID_ARG, "quantize_fp8: a pointer is not aligned to its values");
   RowParams p{};
-  p.x = d_x;
-  p.q = d_q;
-  p.scale = d_scale;
-  p.x_stride = x_stride;
-  p.q_stride = q_stride;
-  p.scale_stride = scale_stride;
-  p.rows = rows;
-  p.cols = cols;
-  const bool al = rows_aligned(d_x, x_stride, cols) && codes_aligned(d_q, q_stride);
+  p.x = a.x;
+  p.q = a.q;
+  p.scale = a.scale;
+  p.x_stride = a.x_stride;
+  p.q_stride = a.q_stride;
+  p.scale_stride = a.scale_stride;
+  p.rows = a.rows;
+  p.cols = a.cols;
+  const bool al = rows_aligned(a.x, a.x_stride, a.cols) && codes_aligned(a.q, a.q_stride);
   cudaStream_t s = pw::as_stream(stream);
-  if (block_rows == 1) {
-    if (dtype == PW_DTYPE_F16)
+  if (a.block_rows == 1) {
+    if (a.dtype == PW_DTYPE_F16)
       return al ? launch_rows<__half, true, false>(p, s) : launch_rows<__half, false, false>(p, s);
     return al ? launch_rows<__nv_bfloat16, true, false>(p, s) : launch_rows<__nv_bfloat16, false, false>(p, s);
   }
-  if (dtype == PW_DTYPE_F16) return al ? launch_blocks<__half, true>(p, s) : launch_blocks<__half, false>(p, s);
+  if (a.dtype == PW_DTYPE_F16) return al ? launch_blocks<__half, true>(p, s) : launch_blocks<__half, false>(p, s);
   return al ? launch_blocks<__nv_bfloat16, true>(p, s) : launch_blocks<__nv_bfloat16, false>(p, s);
 }
 

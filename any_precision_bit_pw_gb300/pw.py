@@ -80,6 +80,26 @@ class pw_rope_scaling(ctypes.Structure):
                 ("original_positions", ctypes.c_double), ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
 
 
+class pw_norm_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "residual_out", "y", "q", "scale")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "residual_out_stride", "y_stride",
+                                                 "q_stride", "scale_stride", "rows")]
+                + [("cols", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                   ("reserved", ctypes.c_int32)])
+
+
+class pw_quant_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "q", "scale")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "q_stride", "scale_stride", "rows")]
+                + [(n, ctypes.c_int32) for n in ("cols", "dtype", "block_rows", "reserved")])
+
+
+class pw_linear_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "a_scale", "b", "b_scale", "y", "status")]
+                + [(n, ctypes.c_int64) for n in ("lda", "a_scale_stride", "ldb", "b_scale_stride", "ldy")]
+                + [(n, ctypes.c_int32) for n in ("m", "n", "k", "dtype")])
+
+
 class pw_rope_args(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "q_out", "k", "v", "k_cache", "v_cache", "turns", "positions",
                                                 "page_table", "q_offsets", "kv_lens", "status")]
@@ -152,9 +172,9 @@ def lib() -> ctypes.CDLL:
                                               P, ctypes.POINTER(pw_ffn_options), P]),
             "pw_moe_route_apl_ffn_layers": (I32, [P, I32, I32, P, P, I32, I32, I32, I32, I32, P, P, P, P, P, P, P,
                                                   SZ, P, P, ctypes.POINTER(pw_ffn_options), P]),
-            "pw_add_rmsnorm": (I32, [P, I64, P, I64, P, I64, I32, F32, I32, P, I64, P, I64, P, I64, P, I64, P]),
-            "pw_quantize_fp8": (I32, [P, I64, I64, I32, I32, I32, P, I64, P, I64, P]),
-            "pw_fp8_linear": (I32, [P, I64, P, I64, P, I64, P, I64, I32, I32, I32, I32, P, I64, P, P]),
+            "pw_add_rmsnorm": (I32, [P, P]),
+            "pw_quantize_fp8": (I32, [P, P]),
+            "pw_fp8_linear": (I32, [P, P]),
             "pw_rope_turns": (I32, [I32, F64, ctypes.POINTER(pw_rope_scaling), P, ctypes.POINTER(F32)]),
             "pw_rope_append": (I32, [P, P]),
             "pw_paged_attention_workspace": (SZ, [I32, I32, I32, I32, I32]),
@@ -469,6 +489,17 @@ def _status(t: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+# the structures of pw.h, packed in one go: pointers, strides, sizes
+_NORM_ARGS = struct.Struct("@7P7q2ifi")
+_QUANT_ARGS = struct.Struct("@3P4q4i")
+_LINEAR_ARGS = struct.Struct("@6P5q4i")
+_ROPE_ARGS = struct.Struct("@12P15q11if")
+_ATTN_ARGS = struct.Struct("@9P11q13if")
+for _packed, _struct in ((_NORM_ARGS, pw_norm_args), (_QUANT_ARGS, pw_quant_args), (_LINEAR_ARGS, pw_linear_args),
+                         (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args)):
+    assert _packed.size == ctypes.sizeof(_struct)
+
+
 def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
                    residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                    q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -485,8 +516,8 @@ def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: 
     yp, ys = _matrix(y, rows, cols, same, "y")
     qp, qs = _matrix(q, rows, cols, _CODES, "q")
     sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale")
-    _check(lib().pw_add_rmsnorm(xp, xs, rp, rs, wp, rows, cols, eps, dt, rop, ros, yp, ys, qp, qs, sp, ss,
-                                _stream(stream)))
+    args = _NORM_ARGS.pack(xp, rp, wp, rop, yp, qp, sp, xs, rs, ros, ys, qs, ss, rows, cols, dt, eps, 0)
+    _check(lib().pw_add_rmsnorm(args, _stream(stream)))
 
 
 def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
@@ -499,7 +530,8 @@ def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block
     xp, xs = _matrix(x, rows, cols, (x.dtype,), "x")
     qp, qs = _matrix(q, rows, cols, _CODES, "q")
     sp, ss = _matrix(scale, -(-rows // block_rows), -(-cols // 128), _F32, "scale")
-    _check(lib().pw_quantize_fp8(xp, xs, rows, cols, dt, block_rows, qp, qs, sp, ss, _stream(stream)))
+    args = _QUANT_ARGS.pack(xp, qp, sp, xs, qs, ss, rows, cols, dt, block_rows, 0)
+    _check(lib().pw_quantize_fp8(args, _stream(stream)))
 
 
 def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, y: torch.Tensor,
@@ -520,8 +552,8 @@ def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
         lda = (lda + 15) // 16 * 16
     if N == 1:
         ldb = (ldb + 15) // 16 * 16
-    _check(lib().pw_fp8_linear(ap, lda, sap, sa, bp, ldb, sbp, sb, M, N, K, dt, yp, ldy, _status(status),
-                               _stream(stream)))
+    args = _LINEAR_ARGS.pack(ap, sap, bp, sbp, yp, _status(status), lda, sa, ldb, sb, ldy, M, N, K, dt)
+    _check(lib().pw_fp8_linear(args, _stream(stream)))
 
 
 def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_rope_scaling] = None):
@@ -545,12 +577,6 @@ def _sequences(q_offsets: torch.Tensor, kv_lens: torch.Tensor):
     """(q_offsets, kv_lens, batch)"""
     batch = kv_lens.shape[0]
     return _vector(q_offsets, batch + 1, _I32, "q_offsets"), _vector(kv_lens, batch, _I32, "kv_lens"), batch
-
-
-# the structures of pw.h, in one piece: pointers, strides, sizes, the float
-_ROPE_ARGS = struct.Struct("@12P15q11if")
-_ATTN_ARGS = struct.Struct("@9P11q13if")
-assert _ROPE_ARGS.size == ctypes.sizeof(pw_rope_args) and _ATTN_ARGS.size == ctypes.sizeof(pw_attn_args)
 
 
 def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],

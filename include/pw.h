@@ -438,43 +438,76 @@ int pw_moe_route_apl_ffn_layers(const void* d_desc, int layer0, int L, const uin
 #define PW_DTYPE_BF16 1
 
 /* r = x + residual;  y = r * rsqrt(mean(r^2) + eps) * weight, by rows.
- *  d_x           [rows][cols];  d_residual the same shape, or NULL (r = x)
- *  d_weight      [cols]
- *  d_residual_out [rows][cols] or NULL: r, rounded (the norm itself uses the
- *                unrounded sum); may be d_residual or d_x
- *  d_y           [rows][cols] or NULL: y in `dtype`; may be d_x
- *  d_q, d_scale  [rows][cols] e4m3 and fp32 [rows][ceil(cols/128)], or both
- *                NULL: y in 8 bits (the unrounded y, not d_y), as
- *                pw_quantize_fp8 with block_rows 1
- * At least one of d_y and d_q.  Any alignment of the values' own size and any
+ *  x             [rows][cols];  residual the same shape, or NULL (r = x)
+ *  weight        [cols]
+ *  residual_out  [rows][cols] or NULL: r, rounded (the norm itself uses the
+ *                unrounded sum); may be residual or x
+ *  y             [rows][cols] or NULL: y in `dtype`; may be x
+ *  q, scale      [rows][cols] e4m3 and fp32 [rows][ceil(cols/128)], or both
+ *                NULL: y in 8 bits (the unrounded y), as pw_quantize_fp8 with
+ *                block_rows 1
+ * At least one of y and q.  Any alignment of the values' own size and any
  * stride >= cols; 16-byte aligned rows of a multiple of 8 columns run on wide
  * accesses.  cols <= 32768. */
-int pw_add_rmsnorm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
-                   const void* d_weight, int64_t rows, int cols, float eps, int dtype, void* d_residual_out,
-                   int64_t residual_out_stride, void* d_y, int64_t y_stride, uint8_t* d_q, int64_t q_stride,
-                   float* d_scale, int64_t scale_stride, void* stream);
+typedef struct pw_norm_args {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* residual_out;
+  void* y;
+  uint8_t* q;
+  float* scale;
+  int64_t x_stride, residual_stride, residual_out_stride, y_stride, q_stride, scale_stride;
+  int64_t rows;
+  int32_t cols;
+  int32_t dtype;
+  float eps;
+  int32_t reserved;
+} pw_norm_args;
+int pw_add_rmsnorm(const pw_norm_args* args, void* stream);
 
-/* 16-bit values to e4m3 codes and fp32 scales:
+/* 16-bit values x [rows][cols] to e4m3 codes q and fp32 scales:
  *   scale = max(largest magnitude of the group / 448, 2^-100)
  *   code  = e4m3(value / scale)
  * The groups are 128 columns (the last one may be narrower) of one row
- * (block_rows 1: activations) or of 128 rows (block_rows 128: weights).
- * d_scale: [ceil(rows/block_rows)][ceil(cols/128)].  A group that holds NaN or
- * an infinity comes back as NaN where it is multiplied out. */
-int pw_quantize_fp8(const void* d_x, int64_t x_stride, int64_t rows, int cols, int dtype, int block_rows, uint8_t* d_q,
-                    int64_t q_stride, float* d_scale, int64_t scale_stride, void* stream);
+ * (block_rows 1: activations, cols <= 32768) or of 128 rows (block_rows 128:
+ * weights).  scale: [ceil(rows/block_rows)][ceil(cols/128)].  A group that
+ * holds NaN or an infinity comes back as NaN where it is multiplied out. */
+typedef struct pw_quant_args {
+  const void* x;
+  uint8_t* q;
+  float* scale;
+  int64_t x_stride, q_stride, scale_stride;
+  int64_t rows;
+  int32_t cols;
+  int32_t dtype;
+  int32_t block_rows;
+  int32_t reserved;
+} pw_quant_args;
+int pw_quantize_fp8(const pw_quant_args* args, void* stream);
 
 /* y[m][n] = sum_kb a_scale[m][kb] * b_scale[n/128][kb] * sum_{k in kb} a[m][k] b[n][k]
  * with kb the groups of 128 columns: a projection of quantised activations by
  * a quantised weight.
- *  d_a [M][K], d_b [N][K] e4m3; rows 16-byte aligned (address and stride)
- *  d_a_scale fp32 [M][ceil(K/128)], d_b_scale fp32 [ceil(N/128)][ceil(K/128)]
- *  d_y [M][N] in `dtype`
- *  d_status as in the fused layer (PW_ERR_TIMEOUT: a wait ran out).
- * Any M up to 2^20, N and K up to 2^24 (no multiples needed). */
-int pw_fp8_linear(const uint8_t* d_a, int64_t lda, const float* d_a_scale, int64_t a_scale_stride,
-                  const uint8_t* d_b, int64_t ldb, const float* d_b_scale, int64_t b_scale_stride, int M, int N,
-                  int K, int dtype, void* d_y, int64_t ldy, int32_t* d_status, void* stream);
+ *  a [m][k], b [n][k] e4m3; rows 16-byte aligned (address and stride)
+ *  a_scale fp32 [m][ceil(k/128)], b_scale fp32 [ceil(n/128)][ceil(k/128)]
+ *  y [m][n] in `dtype`
+ *  status as in the fused layer (PW_ERR_TIMEOUT: a wait ran out).
+ * m up to 2^20, n and k up to 2^24, no multiples needed.  Scales whose rows
+ * start at 16-byte addresses (ceil(k/128) a multiple of 4, or padded strides)
+ * and a y whose rows do take the wide paths. */
+typedef struct pw_linear_args {
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* b;
+  const float* b_scale;
+  void* y;
+  int32_t* status;
+  int64_t lda, a_scale_stride, ldb, b_scale_stride, ldy;
+  int32_t m, n, k;
+  int32_t dtype;
+} pw_linear_args;
+int pw_fp8_linear(const pw_linear_args* args, void* stream);
 
 /* A batch of sequences in a paged cache, shared by the two calls below.
  * Sequence b has kv_lens[b] keys and values in the cache; its last

@@ -92,56 +92,66 @@ def test_rope_turns_refusals(L, d, base, sc):
         pw.pw_rope_turns(d, base, s)
 
 
+def _call(f, struct, defaults, kw):
+    a = struct()
+    for k, v in {**defaults, **kw}.items():
+        setattr(a, k, v)
+    return f(ctypes.byref(a), None)
+
+
 def _norm(L, **kw):
-    a = dict(x=FAKE, xs=64, res=FAKE, rs=64, w=FAKE, rows=4, cols=64, eps=1e-5, dtype=0, ro=FAKE, ros=64, y=FAKE, ys=64,
-             q=FAKE, qs=64, sc=FAKE, ss=1)
-    a.update(kw)
-    return L.pw_add_rmsnorm(a["x"], a["xs"], a["res"], a["rs"], a["w"], a["rows"], a["cols"], a["eps"], a["dtype"], a["ro"],
-                            a["ros"], a["y"], a["ys"], a["q"], a["qs"], a["sc"], a["ss"], None)
+    return _call(L.pw_add_rmsnorm, pw.pw_norm_args, dict(
+        x=FAKE, x_stride=64, residual=FAKE, residual_stride=64, weight=FAKE, rows=4, cols=64, eps=1e-5, dtype=0,
+        residual_out=FAKE, residual_out_stride=64, y=FAKE, y_stride=64, q=FAKE, q_stride=64, scale=FAKE, scale_stride=1), kw)
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=2), -2), (dict(rows=-1), -1), (dict(cols=0), -1), (dict(cols=32769, xs=40000), -2),
-    (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(y=None, q=None, sc=None), -1), (dict(q=None), -1), (dict(sc=None), -1),
-    (dict(xs=63), -1), (dict(rs=63), -1), (dict(ros=1), -1), (dict(ys=63), -1), (dict(qs=63), -1), (dict(ss=0), -1),
-    (dict(x=None), -1), (dict(w=None), -1), (dict(x=FAKE + 1), -1), (dict(sc=FAKE + 2), -1)])
+    (dict(dtype=2), -2), (dict(rows=-1), -1), (dict(cols=0), -1), (dict(cols=32769, x_stride=40000), -2),
+    (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(y=None, q=None, scale=None), -1), (dict(q=None), -1),
+    (dict(scale=None), -1), (dict(x_stride=63), -1), (dict(residual_stride=63), -1), (dict(residual_out_stride=1), -1),
+    (dict(y_stride=63), -1), (dict(q_stride=63), -1), (dict(scale_stride=0), -1), (dict(x=None), -1), (dict(weight=None), -1),
+    (dict(x=FAKE + 1), -1), (dict(scale=FAKE + 2), -1)])
 def test_norm_refusals(L, kw, code):
     assert _norm(L, **kw) == code and "add_rmsnorm" in pw.pw_last_error()
+    assert L.pw_add_rmsnorm(None, None) == -1
 
 
-def test_empty_calls_touch_nothing(L):
-    assert _norm(L, rows=0, x=None, w=None) == 0
-    assert L.pw_quantize_fp8(None, 64, 0, 64, 0, 1, None, 64, None, 1, None) == 0
-    assert L.pw_fp8_linear(None, 64, None, 1, None, 64, None, 1, 0, 8, 64, 0, None, 8, None, None) == 0
+def _quant(L, **kw):
+    return _call(L.pw_quantize_fp8, pw.pw_quant_args, dict(
+        x=FAKE, x_stride=64, rows=4, cols=64, dtype=0, block_rows=1, q=FAKE, q_stride=64, scale=FAKE, scale_stride=1), kw)
 
 
-@pytest.mark.parametrize("args,code", [
-    ((FAKE, 64, 4, 64, 3, 1, FAKE, 64, FAKE, 1), -2), ((FAKE, 64, 4, 64, 0, 64, FAKE, 64, FAKE, 1), -2),
-    ((FAKE, 64, -4, 64, 0, 1, FAKE, 64, FAKE, 1), -1), ((FAKE, 64, 4, 0, 0, 1, FAKE, 64, FAKE, 1), -1),
-    ((FAKE, 63, 4, 64, 0, 1, FAKE, 64, FAKE, 1), -1), ((FAKE, 64, 4, 64, 0, 1, FAKE, 63, FAKE, 1), -1),
-    ((FAKE, 129, 4, 129, 0, 1, FAKE, 129, FAKE, 1), -1), ((None, 64, 4, 64, 0, 1, FAKE, 64, FAKE, 1), -1),
-    ((FAKE, 64, 4, 64, 0, 1, None, 64, FAKE, 1), -1), ((FAKE, 64, 4, 64, 0, 1, FAKE, 64, None, 1), -1),
-    ((FAKE, 1 << 16, 4, 1 << 16, 0, 1, FAKE, 1 << 16, FAKE, 1 << 9), -2),
-    ((FAKE, 64, 1 << 23, 64, 0, 128, FAKE, 64, FAKE, 1), -2)])
-def test_quantize_refusals(L, args, code):
-    assert L.pw_quantize_fp8(*args, None) == code and "quantize_fp8" in pw.pw_last_error()
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=3), -2), (dict(block_rows=64), -2), (dict(rows=-4), -1), (dict(cols=0), -1), (dict(x_stride=63), -1),
+    (dict(q_stride=63), -1), (dict(cols=129, x_stride=129, q_stride=129), -1), (dict(x=None), -1), (dict(q=None), -1),
+    (dict(scale=None), -1), (dict(cols=1 << 16, x_stride=1 << 16, q_stride=1 << 16, scale_stride=1 << 9), -2),
+    (dict(rows=1 << 23, block_rows=128), -2), (dict(x=FAKE + 1), -1), (dict(scale=FAKE + 1), -1)])
+def test_quantize_refusals(L, kw, code):
+    assert _quant(L, **kw) == code and "quantize_fp8" in pw.pw_last_error()
+    assert L.pw_quantize_fp8(None, None) == -1
 
 
 def _linear(L, **kw):
-    a = dict(a=FAKE, lda=256, sa=FAKE, ss=2, b=FAKE, ldb=256, sb=FAKE, bs=2, M=4, N=128, K=256, dtype=0, y=FAKE, ldy=128,
-             st=FAKE)
-    a.update(kw)
-    return L.pw_fp8_linear(a["a"], a["lda"], a["sa"], a["ss"], a["b"], a["ldb"], a["sb"], a["bs"], a["M"], a["N"], a["K"],
-                           a["dtype"], a["y"], a["ldy"], a["st"], None)
+    return _call(L.pw_fp8_linear, pw.pw_linear_args, dict(
+        a=FAKE, lda=256, a_scale=FAKE, a_scale_stride=2, b=FAKE, ldb=256, b_scale=FAKE, b_scale_stride=2, m=4, n=128, k=256,
+        dtype=0, y=FAKE, ldy=128, status=FAKE), kw)
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=2), -2), (dict(M=-1), -1), (dict(N=0), -1), (dict(K=0), -1), (dict(M=(1 << 20) + 1), -2),
-    (dict(lda=240), -1), (dict(ldb=240), -1), (dict(ldy=127), -1), (dict(ss=1), -1), (dict(bs=1), -1),
-    (dict(a=None), -1), (dict(sa=None), -1), (dict(b=None), -1), (dict(sb=None), -1), (dict(y=None), -1), (dict(st=None), -1),
-    (dict(a=FAKE + 8), -1), (dict(b=FAKE + 4), -1), (dict(lda=264), -1), (dict(ldb=257), -1), (dict(sa=FAKE + 1), -1)])
+    (dict(dtype=2), -2), (dict(m=-1), -1), (dict(n=0), -1), (dict(k=0), -1), (dict(m=(1 << 20) + 1), -2),
+    (dict(lda=240), -1), (dict(ldb=240), -1), (dict(ldy=127), -1), (dict(a_scale_stride=1), -1), (dict(b_scale_stride=1), -1),
+    (dict(a=None), -1), (dict(a_scale=None), -1), (dict(b=None), -1), (dict(b_scale=None), -1), (dict(y=None), -1),
+    (dict(status=None), -1), (dict(a=FAKE + 8), -1), (dict(b=FAKE + 4), -1), (dict(lda=264), -1), (dict(ldb=257), -1),
+    (dict(a_scale=FAKE + 1), -1), (dict(status=FAKE + 2), -1), (dict(ldb=1 << 39), -2)])
 def test_linear_refusals(L, kw, code):
     assert _linear(L, **kw) == code and "fp8_linear" in pw.pw_last_error()
+    assert L.pw_fp8_linear(None, None) == -1
+
+
+def test_empty_calls_touch_nothing(L):
+    assert _norm(L, rows=0, x=None, weight=None) == 0
+    assert _quant(L, rows=0, x=None, q=None, scale=None) == 0
+    assert _linear(L, m=0, a=None, b=None, y=None, status=None) == 0
 
 
 def _rope_args(**kw):
