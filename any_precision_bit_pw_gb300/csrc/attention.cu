@@ -208,13 +208,12 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
   // The warps' outputs are added through shared memory, eight rows at a time:
   // a thread owns four columns of a row.
   const bool whole = seg_begin == begin && seg_end == unit_end;
-  const int cta = blockIdx.x;
   constexpr size_t kFloats = part_floats<D>();
   constexpr int kRowItems = D / 4;
   // a piece: slot 0 of the CTA when it continues a unit or starts exactly at
   // its stretch's begin, slot 1 otherwise
-  const bool at_start = seg_begin == cut.begin(cta);
-  float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * kFloats;
+  const bool at_start = seg_begin == cut.most * blockIdx.x;
+  float* part = p.part + (2 * static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) + (at_start ? 0 : 1)) * kFloats;
   for (int r0 = 0; r0 < rows; r0 += 8) {
     const int i = r0 >> 3, live = min(8, rows - r0);
     if (g < live) {
@@ -256,68 +255,20 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
         }
       }
     }
-    if (!whole) __threadfence();
     __syncthreads();
   }
   if (whole) return;
-  const int c0 = cut.cta_of(begin), c1 = cut.cta_of(unit_end - 1);
-  if (threadIdx.x == 0) {
-    const uint32_t n = atomicAdd(p.arrived + c0, 1u);
-    sh.last = n == static_cast<uint32_t>(c1 - c0);
-    if (sh.last) p.arrived[c0] = 0;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!sh.last) return;
-  // The last piece joins all.  Maxima and sums come into shared memory with one
-  // round trip (where they fit), then a thread adds the outputs of four columns
-  // of a row, eight loads under way together.
-  const int first_slot = begin == cut.begin(c0) ? 0 : 1, pieces = c1 - c0 + 1;
-  auto piece = [&](int x) { return p.part + (2 * static_cast<size_t>(c0 + x) + (x == 0 ? first_slot : 0)) * kFloats; };
-  float2* ml = reinterpret_cast<float2*>(buf);
-  const bool fits = pieces * rows * 8 <= kWarps * 8 * D * 4;
-  auto state = [&](int x, int row) {
-    const float* src = piece(x) + kTile * D + row;
-    return make_float2(__ldcg(src), __ldcg(src + kTile));
-  };
-  if (fits) {
-    for (int e = threadIdx.x; e < pieces * rows; e += kThreads) ml[e] = state(e / rows, e % rows);
-    __syncthreads();
-  }
-#pragma unroll 1
-  for (int e = threadIdx.x; e < rows * kRowItems; e += kThreads) {
-    const int row = e / kRowItems, d = (e % kRowItems) * 4;
-    float top = -INFINITY;
-    for (int x = 0; x < pieces; ++x) top = fmaxf(top, fits ? ml[x * rows + row].x : state(x, row).x);
-    const float safe = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int x = 0; x < pieces; x += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = x + j < pieces ? __ldcg(reinterpret_cast<const float4*>(piece(x + j) + row * D + d)) : make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (x + j >= pieces) break;
-        const float2 t = fits ? ml[(x + j) * rows + row] : state(x + j, row);
-        const float f = pw::exp2_fast(t.x - safe);
-        sum += f * t.y;
-        o.x += f * v[j].x;
-        o.y += f * v[j].y;
-        o.z += f * v[j].z;
-        o.w += f * v[j].w;
-      }
-    }
-    const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
-    const int h = c.head * p.group + r - t0 * p.group;
-    const float inv = pw_attn::inverse_sum(sum);
-    T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head + d;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pw::pack2<T>(o.x * inv, o.y * inv), pw::pack2<T>(o.z * inv, o.w * inv));
-    if (a.lse && d == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(top, sum);
-  }
-  __syncthreads();   // sh.last
+  static_assert(pw_attn::state_entries(pw_attn::kMaxCtas, kTile) * sizeof(float2) <= kWarps * 8 * D * 4, "state");
+  pw_attn::join<kTile, D, true, kThreads, 1, 8>(
+      p, cut, begin, unit_end, rows, reinterpret_cast<float2*>(buf), sh.last, [] { __syncthreads(); },
+      [&](int row, int d, const float4* o, float top, float sum) {
+        const int r = c.tile * kTile + row, t0 = pw_attn::token_of(p, r), token = c.s.q0 + t0;
+        const int h = c.head * p.group + r - t0 * p.group;
+        const float inv = pw_attn::inverse_sum(sum);
+        T* out = static_cast<T*>(a.out) + token * a.out_stride_token + h * a.out_stride_head + d;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pw::pack2<T>(o->x * inv, o->y * inv), pw::pack2<T>(o->z * inv, o->w * inv));
+        if (a.lse && d == 0) a.lse[static_cast<int64_t>(token) * a.heads + h] = pw_attn::log_sum(top, sum);
+      });
 }
 
 template <typename T, int D>
@@ -329,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_cons
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * stage_bytes<D>());
   Cursor c;
   pw_attn::Cut cut;
-  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, gridDim.x, c, cut)) return;
+  if (!pw_attn::find_start<kTile, kBlock, kThreads, 1>(p, c, cut)) return;
   Cursor ahead = c;   // the copies run kStages - 1 blocks ahead of the arithmetic
   int fill = 0;
   auto load_next = [&]() {
@@ -385,10 +336,9 @@ int launch_stream(const Params& p, cudaStream_t s) {
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   // two CTAs an SM, but no more than there are blocks to share out
   const long long tiles = (static_cast<long long>(p.a.tokens) * p.group + kTile - 1) / kTile + p.a.batch;
-  const long long blocks = tiles * p.a.kv_heads * ((p.a.max_kv_len + kBlock - 1) / kBlock + 1);
-  long long ctas = 2ll * sms < pw_attn::kMaxCtas ? 2ll * sms : pw_attn::kMaxCtas;
-  if (blocks < ctas) ctas = blocks < 1 ? 1 : blocks;
-  attn_stream_kernel<T, D><<<static_cast<unsigned>(ctas), kThreads, smem_bytes<D>(), s>>>(p);
+  const long long blocks = tiles * ((p.a.max_kv_len + kBlock - 1) / kBlock + 1);
+  const dim3 grid = pw_attn::grid_of(2ll * sms < pw_attn::kMaxCtas ? 2ll * sms : pw_attn::kMaxCtas, blocks, p.a.kv_heads);
+  attn_stream_kernel<T, D><<<grid, kThreads, smem_bytes<D>(), s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -399,8 +349,8 @@ int launch(const Params& p, cudaStream_t s) {
   return p.a.head_dim == 64 ? launch_stream<T, 64>(p, s) : launch_stream<T, 128>(p, s);
 }
 
-constexpr size_t kCounterBytes = 2048;   // kMaxCtas counters, rounded up
-static_assert(kCounterBytes >= 4 * pw_attn::kMaxCtas, "counters");
+constexpr size_t kCounterBytes = 4096;   // the counters, rounded up
+static_assert(kCounterBytes >= 2 * 4 * pw_attn::kMaxCtas, "counters");
 
 bool head_dim_ok(int d) { return d == 64 || d == 128; }
 

@@ -31,6 +31,9 @@ constexpr int kHalf = 128;             // rows of half a tile: the lanes of Tens
 constexpr int kTile = 2 * kHalf;
 constexpr int kBlock = 128;            // keys of a block
 constexpr int kKeySlots = 2, kValueSlots = 3;   // rings of key and value blocks in shared memory
+// A piece of a tile costs its join as much as a block of keys costs the matrix
+// units: no CTA takes fewer blocks (64 tokens over 1000 keys: 23 us, 29 with 1).
+constexpr int kLeast = 3;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kKeyWarp = 8, kValueWarp = 9, kMmaWarp = 10;
 constexpr int kThreads = 384;
@@ -451,9 +454,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
     }
     // a piece: [d / 4][row] of four values, so that neighbouring rows are
     // neighbours in memory; slot 0 when it starts at the stretch's begin
-    const int cta = blockIdx.x;
-    const bool at_start = begin + b0 == cut.begin(cta);
-    float* part = p.part + (2 * static_cast<size_t>(cta) + (at_start ? 0 : 1)) * part_floats;
+    const bool at_start = begin + b0 == cut.most * blockIdx.x;
+    float* part = p.part + (2 * static_cast<size_t>(blockIdx.y * gridDim.x + blockIdx.x) + (at_start ? 0 : 1)) * part_floats;
     const int slot_row = h * kHalf + tid;
     if (active) {
 #pragma unroll
@@ -470,53 +472,25 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       part[kTile * D + kTile + slot_row] = l;
       pw::tc_fence_before();
     }
-    __threadfence();
-    pw::bar_sync(1, 32 * kSoftmaxWarps);
-    const int c0 = cut.cta_of(begin), c1 = cut.cta_of(unit_end - 1);
-    if (threadIdx.x == 0) {
-      const uint32_t n = atomicAdd(p.arrived + c0, 1u);
-      sh.last = n == static_cast<uint32_t>(c1 - c0);
-      if (sh.last) p.arrived[c0] = 0;
-      __threadfence();
-    }
-    pw::bar_sync(1, 32 * kSoftmaxWarps);
-    const bool last = sh.last;
-    pw::bar_sync(1, 32 * kSoftmaxWarps);   // sh.last is free again
-    if (!last || !active || !live || dead) return true;
-    const int first_slot = begin == cut.begin(c0) ? 0 : 1;
-    auto piece = [&](int i) { return p.part + (2 * static_cast<size_t>(i) + (i == c0 ? first_slot : 0)) * part_floats; };
-    float most = -INFINITY, total = 0.0f;
-    for (int i = c0; i <= c1; ++i) most = fmaxf(most, __ldcg(piece(i) + kTile * D + slot_row));
-    const float safe = most == -INFINITY ? 0.0f : most;
-    for (int i = c0; i <= c1; ++i)
-      total += pw::exp2_fast(__ldcg(piece(i) + kTile * D + slot_row) - safe) *
-               __ldcg(piece(i) + kTile * D + kTile + slot_row);
-    const float inv = pw_attn::inverse_sum(total);
-#pragma unroll 1
-    for (int d0 = 0; d0 < D; d0 += 32) {
-      float o[32] = {};
-      for (int i = c0; i <= c1; ++i) {
-        const float* src = piece(i);
-        const float f = pw::exp2_fast(__ldcg(src + kTile * D + slot_row) - safe);
-        float4 v[8];
+    // All eight warps add the pieces, whichever half has rows; the queries' part
+    // of shared memory, read to the end by now, holds the joined state.
+    static_assert(pw_attn::state_entries(pw_attn::kMaxCtas / 2, kTile) * sizeof(float2) <= 2 * tile_bytes<D>(), "state");
+    pw_attn::join<kTile, D, false, 32 * kSoftmaxWarps, 8, 2>(
+        p, cut, begin, unit_end, min(kTile, c.s.q_len * p.group - c.tile * kTile), reinterpret_cast<float2*>(q_smem), sh.last,
+        [] { pw::bar_sync(1, 32 * kSoftmaxWarps); },
+        [&](int row, int d, const float4* o, float top, float total) {
+          if (*reinterpret_cast<volatile int*>(&sh.dead)) return;
+          const int jr = c.tile * kTile + row, jt = pw_attn::token_of(p, jr), to = c.s.q0 + jt;
+          const int hd = c.head * p.group + jr - jt * p.group;
+          const float inv = pw_attn::inverse_sum(total);
+          T* dst = static_cast<T*>(a.out) + to * a.out_stride_token + hd * a.out_stride_head + d;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = __ldcg(reinterpret_cast<const float4*>(src + ((d0 / 4 + j) * kTile + slot_row) * 4));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[4 * j] += f * v[j].x;
-          o[4 * j + 1] += f * v[j].y;
-          o[4 * j + 2] += f * v[j].z;
-          o[4 * j + 3] += f * v[j].w;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(out + d0 + 8 * j) =
-            make_uint4(pw::pack2<T>(o[8 * j] * inv, o[8 * j + 1] * inv), pw::pack2<T>(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                       pw::pack2<T>(o[8 * j + 4] * inv, o[8 * j + 5] * inv), pw::pack2<T>(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-    }
-    if (a.lse) a.lse[static_cast<int64_t>(token) * a.heads + head] = pw_attn::log_sum(most, total);
+          for (int k = 0; k < 8; k += 2)
+            *reinterpret_cast<uint4*>(dst + 4 * k) =
+                make_uint4(pw::pack2<T>(o[k].x * inv, o[k].y * inv), pw::pack2<T>(o[k].z * inv, o[k].w * inv),
+                           pw::pack2<T>(o[k + 1].x * inv, o[k + 1].y * inv), pw::pack2<T>(o[k + 1].z * inv, o[k + 1].w * inv));
+          if (a.lse && d == 0) a.lse[static_cast<int64_t>(to) * a.heads + hd] = pw_attn::log_sum(top, total);
+        });
     return true;
   });
 }
@@ -530,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5));
   Cursor c;
   pw_attn::Cut cut;
-  if (!pw_attn::find_start<kTile, kBlock, kThreads>(p, blockIdx.x, gridDim.x, c, cut)) return;
+  if (!pw_attn::find_start<kTile, kBlock, kThreads, kLeast>(p, c, cut)) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKeySlots; ++i) {
       pw::mbar_init(bar(sh.k_full[i]), 1);
@@ -562,8 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = pw::uniform(sh.tmem);
   unsigned char* k_ring = smem + 2 * tile_bytes<D>();
   unsigned char* v_ring = k_ring + kKeySlots * tile_bytes<D>();
-  // Registers move from the third warpgroup to the softmax warps: 256 threads
-  // x 192 and 128 x 120 are the launch's 384 x 168.
   if (warp < kSoftmaxWarps) {
     softmax_role<T, D>(p, c, cut, sh, tmem, smem);
   } else if (warp == kKeyWarp) {
@@ -572,7 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_role<D, true>(p, c, maps, sh, v_ring);
   } else if (warp == kMmaWarp) {
     mma_role<D, kBf16>(p, c, sh, tmem, pw::smem_u32(smem), pw::smem_u32(k_ring), pw::smem_u32(v_ring));
-  } else {
   }
   __syncwarp();
   pw::tc_fence_before();
@@ -614,10 +585,9 @@ int launch(const Params& p, cudaStream_t s) {
   if (int e = encode_cache(&maps.v, a, a.v_cache, a.v_stride_page, a.v_stride_token, a.v_stride_head, maps.box, kBf16))
     return e;
   const long long tiles = (static_cast<long long>(a.tokens) * p.group + kTile - 1) / kTile + a.batch;
-  const long long blocks = tiles * a.kv_heads * ((a.max_kv_len + kBlock - 1) / kBlock + 1);
-  long long ctas = sms < pw_attn::kMaxCtas / 2 ? sms : pw_attn::kMaxCtas / 2;
-  if (blocks < ctas) ctas = blocks < 1 ? 1 : blocks;
-  attn_tile_kernel<T, D, kBf16><<<static_cast<unsigned>(ctas), kThreads, smem_bytes<D>(), s>>>(p, maps);
+  const long long blocks = tiles * ((a.max_kv_len + kBlock - 1) / kBlock + 1);
+  const dim3 grid = pw_attn::grid_of(sms < pw_attn::kMaxCtas / 2 ? sms : pw_attn::kMaxCtas / 2, blocks, a.kv_heads);
+  attn_tile_kernel<T, D, kBf16><<<grid, kThreads, smem_bytes<D>(), s>>>(p, maps);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -630,10 +600,12 @@ size_t tile_part_floats(int head_dim) { return static_cast<size_t>(kTile) * (hea
 
 bool tile_kernel_takes(const Params& p) {
   const pw_attn_args& a = p.a;
-  // More rows per key/value head than two 16-row tiles; a positive scale (the
-  // running maximum is kept on unscaled scores); boxes of whole 8-row swizzle
-  // groups; strides that a tensor map can hold.
-  if (static_cast<long long>(a.max_q_len) * p.group <= 32 || !(a.scale > 0.0f)) return false;
+  // More rows per key/value head than one 16-row tile: the other kernel would
+  // read the keys once per 16 rows (64 sequences of 4096 keys, 4 query heads to
+  // a key head: 8 tokens 185 us here, 333 there; 4 tokens 184 and 177).  A
+  // positive scale (the running maximum is kept on unscaled scores); boxes of
+  // whole 8-row swizzle groups; strides that a tensor map can hold.
+  if (static_cast<long long>(a.max_q_len) * p.group <= 16 || !(a.scale > 0.0f)) return false;
   if (std::gcd(a.page_size, kBlock) < 8) return false;
   const int64_t most = 1ll << 38;
   for (int64_t st : {a.k_stride_page, a.k_stride_token, a.k_stride_head, a.v_stride_page, a.v_stride_token, a.v_stride_head})

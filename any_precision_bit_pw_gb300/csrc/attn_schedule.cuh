@@ -7,7 +7,14 @@
 // lengths and one long sequence both load every SM alike.  A unit that a cut
 // crosses leaves a partial result (row maximum, sum and unnormalised output)
 // with each CTA that worked on it; the last of them to arrive joins the pieces
-// in the order of the CTAs, which does not depend on who is last.
+// in the order of the CTAs, which does not depend on who is last.  Many pieces
+// of many rows are joined in groups first, each by its last CTA.
+//
+// The grid is (CTAs, kv_heads) with each head's part of the line cut by itself,
+// where the CTAs divide evenly among the heads and the longest stretch is no
+// longer for it: fewer CTAs then have two units to finish (24 sequences of 17 to
+// 65536 keys, one token each: 152 us, 164 cut as one line).  Otherwise it is
+// (CTAs, 1).
 #pragma once
 
 #include "ops_common.cuh"
@@ -20,7 +27,7 @@ struct Params {
   uint32_t group_inv; // ceil(2^32 / group): rows up to group_max divide by a product
   int group_max;
   float scale_log2;   // scale * log2(e): the softmax runs in powers of two
-  uint32_t* arrived;  // one counter per CTA, all 0 between calls
+  uint32_t* arrived;  // two counters per CTA, all 0 between calls
   float* part;        // 2 partial results per CTA
 };
 
@@ -141,22 +148,24 @@ __device__ __forceinline__ long long quotient(long long n, long long d) {
   return (n | d) >> 31 ? n / d : static_cast<long long>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
 }
 
-// The line's cut: the first `extra` CTAs take q + 1 blocks, the others q.
+// The cut of a line, or of one head's part of it: every CTA takes `most`
+// consecutive blocks, the last one what is left.
 struct Cut {
-  long long q;
-  int extra;
-  __device__ __forceinline__ long long begin(int cta) const { return q * cta + min(cta, extra); }
-  __device__ __forceinline__ int cta_of(long long w) const {
-    const long long big = (q + 1) * extra;
-    return static_cast<int>(w < big ? quotient(w, q + 1) : extra + quotient(w - big, q));
-  }
+  long long most;
+  __device__ __forceinline__ int cta_of(long long w) const { return static_cast<int>(quotient(w, most)); }
 };
 
-// The cursor of CTA `cta` of `ctas`, found by the whole CTA (kThreads
-// threads).  Returns false when it has no stretch: there are never more
-// stretches than blocks.
-template <int kTile, int kBlock, int kThreads>
-__device__ __forceinline__ bool find_start(const Params& p, int cta, int ctas, Cursor& c, Cut& cut) {
+// Grid of at most `ctas` CTAs, for at most `blocks` blocks per head.
+inline dim3 grid_of(long long ctas, long long blocks, int kv_heads) {
+  const bool by_head = ctas % kv_heads == 0;
+  const long long n = by_head ? ctas / kv_heads : ctas, most = by_head ? blocks : blocks * kv_heads;
+  return dim3(static_cast<unsigned>(n < most ? n : most < 1 ? 1 : most), by_head ? static_cast<unsigned>(kv_heads) : 1u);
+}
+
+// The cursor of this CTA, found by all its kThreads threads.  Returns false
+// when it has no stretch.
+template <int kTile, int kBlock, int kThreads, int kLeast>
+__device__ __forceinline__ bool find_start(const Params& p, Cursor& c, Cut& cut) {
   constexpr int kWarps = kThreads / 32;
   __shared__ long long warp_sum[2][kWarps];
   __shared__ long long sh_rest;
@@ -165,7 +174,7 @@ __device__ __forceinline__ bool find_start(const Params& p, int cta, int ctas, C
   // blocks of one head, and (batch <= kThreads) the prefix of this thread's sequence
   long long mine = 0;
   for (int b = tid; b < p.a.batch; b += kThreads)
-    mine += sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, cta == 0));
+    mine += sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, blockIdx.x + blockIdx.y == 0));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -180,15 +189,14 @@ __device__ __forceinline__ bool find_start(const Params& p, int cta, int ctas, C
     if (i == warp) base = per_head;
     per_head += warp_sum[0][i];
   }
-  const long long line = per_head * p.a.kv_heads;
-  if (line < ctas) ctas = static_cast<int>(line);
-  if (cta >= ctas) return false;   // the same for every thread
-  cut.q = quotient(line, ctas);
-  cut.extra = static_cast<int>(line - cut.q * ctas);
-  c.pos = cut.begin(cta);
-  c.end = cut.begin(cta + 1);
-  c.head = static_cast<int>(quotient(c.pos, per_head));
-  const long long want = c.pos - c.head * per_head;
+  const bool by_head = gridDim.y > 1;
+  const long long span = by_head ? per_head : per_head * p.a.kv_heads;
+  cut.most = max(static_cast<long long>(kLeast), quotient(span + gridDim.x - 1, gridDim.x));
+  c.pos = cut.most * blockIdx.x;
+  if (c.pos >= span) return false;   // the same for every thread
+  c.end = min(span, c.pos + cut.most);
+  c.head = by_head ? static_cast<int>(blockIdx.y) : static_cast<int>(quotient(c.pos, per_head));
+  const long long want = by_head ? c.pos : c.pos - c.head * per_head;
   // the sequence that holds position `want` of the head's blocks
   if (p.a.batch <= kThreads) {
     const long long lo = base + incl - mine;
@@ -232,6 +240,161 @@ __device__ __forceinline__ bool find_start(const Params& p, int cta, int ctas, C
   }
   c.block = static_cast<int>(rest);
   return true;
+}
+
+// ---------------------------------------------------------------- joining the pieces of a unit
+// A piece is kTile x D outputs, kTile maxima (in powers of two) and kTile sums;
+// kColumnsInside: the outputs lie [row][D], otherwise [D / 4][row][4].
+template <int kTile, int D, bool kColumnsInside>
+__device__ __forceinline__ int piece_at(int row, int d) {
+  return kColumnsInside ? row * D + d : (d * kTile / 4 + row) * 4;
+}
+
+// Whether this CTA is the last of `n` that come here; all its threads get the
+// answer, and what the others wrote before they came is visible to them.
+template <typename Sync>
+__device__ __forceinline__ bool last_of(uint32_t* counter, int n, int& flag, Sync sync) {
+  __threadfence();
+  sync();
+  if (threadIdx.x == 0) {
+    const bool last = atomicAdd(counter, 1u) == static_cast<uint32_t>(n - 1);
+    if (last) *counter = 0;
+    flag = last;
+    __threadfence();
+  }
+  sync();
+  const bool last = flag;
+  sync();
+  return last;
+}
+
+// Adds `count` pieces in order; f(row, d, o, m, l) gets kColumns x 4 columns
+// of every row at a time.  Maxima and sums come into shared memory in one round trip; then a
+// thread has the loads of kColumns x 4 columns of kAtOnce pieces under way
+// together.
+template <int kTile, int D, bool kColumnsInside, int kThreads, int kColumns, int kAtOnce, typename Piece, typename Sync,
+          typename F>
+__device__ __forceinline__ void combine(int count, int rows, float2* state, Piece piece, Sync sync, F f) {
+  const int tid = threadIdx.x;
+  const int bits = rows > 1 ? 32 - __clz(rows - 1) : 0, mask = (1 << bits) - 1;   // rows, rounded up to a power of two
+  const int step = kThreads >> bits;
+  if ((tid & mask) < rows)
+    for (int x0 = tid >> bits; x0 < count; x0 += 4 * step) {
+      float2 t[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = x0 + j * step;
+        const float* src = piece(x < count ? x : x0) + kTile * D + (tid & mask);
+        t[j] = make_float2(__ldcg(src), __ldcg(src + kTile));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (x0 + j * step < count) state[(x0 + j * step) * rows + (tid & mask)] = t[j];
+    }
+  sync();
+  constexpr int kItems = D / (4 * kColumns);   // of a row
+  const int items = kColumnsInside ? rows * kItems : kItems << bits;
+  float top = -INFINITY, safe = 0.0f, sum = 0.0f;
+#pragma unroll 1
+  for (int e = tid; e < items; e += kThreads) {
+    const int row = kColumnsInside ? e / kItems : e & mask;
+    const int d = 4 * kColumns * (kColumnsInside ? e % kItems : e >> bits);
+    if (row >= rows) continue;
+    if (kColumnsInside || e == tid) {   // otherwise a thread keeps its row
+      top = -INFINITY;
+      sum = 0.0f;
+      for (int x = 0; x < count; ++x) top = fmaxf(top, state[x * rows + row].x);
+      safe = top == -INFINITY ? 0.0f : top;
+      if (!kColumnsInside)
+        for (int x = 0; x < count; ++x) sum += pw::exp2_fast(state[x * rows + row].x - safe) * state[x * rows + row].y;
+    }
+    float4 o[kColumns];
+#pragma unroll
+    for (int k = 0; k < kColumns; ++k) o[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int x = 0; x < count; x += kAtOnce) {
+      float4 v[kAtOnce][kColumns];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k)
+          v[j][k] = x + j < count ? __ldcg(reinterpret_cast<const float4*>(
+                                        piece(x + j) + piece_at<kTile, D, kColumnsInside>(row, d + 4 * k)))
+                                  : make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (x + j >= count) break;
+        const float2 t = state[(x + j) * rows + row];
+        const float w = pw::exp2_fast(t.x - safe);
+        if (kColumnsInside) sum += w * t.y;
+#pragma unroll
+        for (int k = 0; k < kColumns; ++k) {
+          o[k].x += w * v[j][k].x;
+          o[k].y += w * v[j][k].y;
+          o[k].z += w * v[j][k].z;
+          o[k].w += w * v[j][k].w;
+        }
+      }
+    }
+    f(row, d, o, top, sum);
+  }
+  sync();   // the state is free again
+}
+
+// Number of pieces that are joined at a time.  Few, or of few rows: all, in one
+// step; else about the square root of their number, so that both steps are
+// alike.  A CTA adds 130 KB in about 1 us, as long as a second step takes to
+// begin (64 tokens over 8192 keys, 16 pieces of 256 rows a head: 42 us in two
+// steps, 54 in one; one token, 32 pieces of 4 rows: 16.8 and 18.8 in one and two).
+constexpr int kPiecesAtOnce = 6, kRowsAtOnce = 256;
+__device__ __forceinline__ int group_of(int pieces, int rows) {
+  if (pieces <= kPiecesAtOnce || pieces * rows <= kRowsAtOnce) return pieces;
+  int n = 3;
+  while (n * n < pieces) ++n;
+  return n;
+}
+// Entries of the shared state for tiles of `rows` rows on at most `ctas` CTAs.
+constexpr int state_entries(int ctas, int rows) {
+  int n = 4;
+  while (n * n < ctas) ++n;
+  return n * rows > kRowsAtOnce ? n * rows : kRowsAtOnce;
+}
+
+// This CTA has written its piece of the unit whose blocks are [begin, end).
+// The last CTA of each group adds its pieces into the group's first, the last
+// of those adds the groups; f as above.  (A CTA is the first of at most one cut
+// unit, and of at most one group of two and more: the counters need no other
+// index.)
+template <int kTile, int D, bool kColumnsInside, int kThreads, int kColumns, int kAtOnce, typename Sync, typename F>
+__device__ __forceinline__ void join(const Params& p, const Cut& cut, long long begin, long long end, int rows, float2* state,
+                                     int& flag, Sync sync, F f) {
+  constexpr size_t kFloats = static_cast<size_t>(kTile) * (D + 2);
+  const int c0 = cut.cta_of(begin), n = cut.cta_of(end - 1) - c0 + 1;
+  const int first = static_cast<int>(blockIdx.y * gridDim.x) + c0, first_slot = begin == cut.most * c0 ? 0 : 1;
+  auto piece = [&](int x) { return p.part + (2 * static_cast<size_t>(first + x) + (x == 0 ? first_slot : 0)) * kFloats; };
+  const int size = group_of(n, rows), groups = (n + size - 1) / size;
+  const int lead = (static_cast<int>(blockIdx.x) - c0) / size * size, members = min(size, n - lead);
+  if (members > 1 && !last_of(p.arrived + first + lead, members, flag, sync)) return;
+  if (groups > 1) {
+    if (members > 1) {
+      float* sum = piece(lead);
+      combine<kTile, D, kColumnsInside, kThreads, kColumns, kAtOnce>(
+          members, rows, state, [&](int x) { return piece(lead + x); }, sync,
+          [&](int row, int d, const float4* o, float m, float l) {
+#pragma unroll
+            for (int k = 0; k < kColumns; ++k)
+              *reinterpret_cast<float4*>(sum + piece_at<kTile, D, kColumnsInside>(row, d + 4 * k)) = o[k];
+            if (d == 0) {
+              sum[kTile * D + row] = m;
+              sum[kTile * D + kTile + row] = l;
+            }
+          });
+    }
+    if (!last_of(p.arrived + kMaxCtas + first, groups, flag, sync)) return;
+  }
+  const int step = groups > 1 ? size : 1;
+  combine<kTile, D, kColumnsInside, kThreads, kColumns, kAtOnce>(
+      groups > 1 ? groups : n, rows, state, [&](int x) { return piece(x * step); }, sync, f);
 }
 
 }  // namespace pw_attn

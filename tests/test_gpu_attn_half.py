@@ -423,6 +423,27 @@ def test_attention_workspace_is_left_ready():
                 assert torch.equal(out, first[i][0]) and torch.equal(lse, first[i][1])
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("ql,kl,h,hk,d", [
+    ([1], [9000], 4, 1, 64),           # many pieces of few rows
+    ([4], [9000], 8, 2, 128),          # and of sixteen
+    ([3, 1], [7000, 2500], 15, 3, 64), # heads that do not divide the CTAs
+    ([70], [9000], 4, 1, 128),         # full tiles, joined in two steps
+    ([100], [9000], 9, 3, 64),
+    ([300, 5], [1500, 4000], 10, 5, 128),
+    ([260], [700], 2, 2, 64)])
+def test_attention_pieces_of_a_unit(ql, kl, h, hk, d, dtype):
+    """A unit that many CTAs share, joined in one step and in two; the same bits every time."""
+    b = Batch(ql, kl, h, hk, d, 16, dtype, 7)
+    ws = torch.zeros(pw.pw_paged_attention_workspace(b.T, len(kl), h, hk, d), dtype=torch.uint8, device=DEV)
+    out, lse, st = attend(b, ws)
+    assert st == 0
+    check_attention(b, out, lse)
+    for _ in range(3):
+        again, lse2, st = attend(b, ws)
+        assert st == 0 and torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_attention_strided_rows():
     """q and out inside wider rows; nothing beside out is written."""
     for ql in ([1, 1], [40, 3]):
