@@ -40,49 +40,64 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K, bool v
 }
 
 // Few tokens: the weights stream from memory into registers.  A CTA owns 16
-// weight rows and 8 tokens; its warps take every eighth group of 128 columns.
+// weight rows and kGroups x 8 tokens; its warps take every eighth group of 128
+// columns.
 // A lane loads 16 contiguous bytes of a row and feeds them to two MMAs as if
 // they were the four columns each of those wants: the same reordering of k on
 // both operands leaves the sum as it is.  Memory bounds it; 32 warps an SM keep
 // enough loads in flight (two or four groups a warp at once came out slower).
-// 1 x 6144 x 4096: 7.8 us, 3.2 TB/s of weights with the launch included.
-template <typename T>
+// 1 x 6144 x 4096: 7.7 us, 3.3 TB/s of weights with the launch included.
+template <typename T, int kGroups>
 __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid_constant__ LinearParams p) {
-  __shared__ float red[kWarps][kRows][9];
+  constexpr int kTokens = 8 * kGroups;
+  __shared__ float red[kWarps][kRows][kTokens + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRows;
   const uint8_t* b_lo = p.b + static_cast<int64_t>(n0 + g) * p.ldb;
   const uint8_t* b_hi = b_lo + 8 * p.ldb;
-  const uint8_t* a = p.a + static_cast<int64_t>(g) * p.lda;
-  const bool v_lo = n0 + g < p.N, v_hi = n0 + g + 8 < p.N, v_a = g < p.M;
+  const bool v_lo = n0 + g < p.N, v_hi = n0 + g + 8 < p.N;
   const float* sb = p.sb + (n0 / pw::kGroup) * p.sb_stride;
-  const int c = 2 * t;   // the lane's two tokens of the result
-  const float* sa0 = p.sa + static_cast<int64_t>(c < p.M ? c : 0) * p.sa_stride;
-  const float* sa1 = p.sa + static_cast<int64_t>(c + 1 < p.M ? c + 1 : 0) * p.sa_stride;
-  float sum[4] = {};
+  const uint8_t* a[kGroups];
+  const float* sa[kGroups][2];   // of the lane's two tokens of the result
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const int c = 8 * i + 2 * t;
+    a[i] = p.a + static_cast<int64_t>(8 * i + g) * p.lda;
+    sa[i][0] = p.sa + static_cast<int64_t>(c < p.M ? c : 0) * p.sa_stride;
+    sa[i][1] = p.sa + static_cast<int64_t>(c + 1 < p.M ? c + 1 : 0) * p.sa_stride;
+  }
+  float sum[kGroups][4] = {};
   for (int kb = warp; kb < p.KB; kb += kWarps) {
     const int k = kb * pw::kGroup + 16 * t;
     const uint4 w0 = load16(b_lo, k, p.K, v_lo), w1 = load16(b_hi, k, p.K, v_hi);
     const uint4 w2 = load16(b_lo, k + 64, p.K, v_lo), w3 = load16(b_hi, k + 64, p.K, v_hi);
-    const uint4 x0 = load16(a, k, p.K, v_a), x1 = load16(a, k + 64, p.K, v_a);
-    const float s = __ldg(sb + kb), s0 = s * __ldg(sa0 + kb), s1 = s * __ldg(sa1 + kb);
-    float acc[4] = {};
-    pw::mma_16832_e4m3(acc, w0.x, w1.x, w0.y, w1.y, x0.x, x0.y);
-    pw::mma_16832_e4m3(acc, w0.z, w1.z, w0.w, w1.w, x0.z, x0.w);
-    pw::mma_16832_e4m3(acc, w2.x, w3.x, w2.y, w3.y, x1.x, x1.y);
-    pw::mma_16832_e4m3(acc, w2.z, w3.z, w2.w, w3.w, x1.z, x1.w);
-    sum[0] += s0 * acc[0];
-    sum[1] += s1 * acc[1];
-    sum[2] += s0 * acc[2];
-    sum[3] += s1 * acc[3];
+    const float s = __ldg(sb + kb);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const bool v = 8 * i + g < p.M;
+      const uint4 x0 = load16(a[i], k, p.K, v), x1 = load16(a[i], k + 64, p.K, v);
+      const float s0 = s * __ldg(sa[i][0] + kb), s1 = s * __ldg(sa[i][1] + kb);
+      float acc[4] = {};
+      pw::mma_16832_e4m3(acc, w0.x, w1.x, w0.y, w1.y, x0.x, x0.y);
+      pw::mma_16832_e4m3(acc, w0.z, w1.z, w0.w, w1.w, x0.z, x0.w);
+      pw::mma_16832_e4m3(acc, w2.x, w3.x, w2.y, w3.y, x1.x, x1.y);
+      pw::mma_16832_e4m3(acc, w2.z, w3.z, w2.w, w3.w, x1.z, x1.w);
+      sum[i][0] += s0 * acc[0];
+      sum[i][1] += s1 * acc[1];
+      sum[i][2] += s0 * acc[2];
+      sum[i][3] += s1 * acc[3];
+    }
   }
-  red[warp][g][2 * t] = sum[0];
-  red[warp][g][2 * t + 1] = sum[1];
-  red[warp][g + 8][2 * t] = sum[2];
-  red[warp][g + 8][2 * t + 1] = sum[3];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    red[warp][g][8 * i + 2 * t] = sum[i][0];
+    red[warp][g][8 * i + 2 * t + 1] = sum[i][1];
+    red[warp][g + 8][8 * i + 2 * t] = sum[i][2];
+    red[warp][g + 8][8 * i + 2 * t + 1] = sum[i][3];
+  }
   __syncthreads();
-  if (threadIdx.x < kRows * 8) {
-    const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;
+  for (int e = threadIdx.x; e < kRows * kTokens; e += 32 * kWarps) {
+    const int row = e % kRows, col = e / kRows;
     float v = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) v += red[i][row][col];
@@ -91,9 +106,9 @@ __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid
   }
 }
 
-template <typename T>
+template <typename T, int kGroups>
 int launch_stream(const LinearParams& p, cudaStream_t s) {
-  linear_stream_kernel<T><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), 32 * kWarps, 0, s>>>(p);
+  linear_stream_kernel<T, kGroups><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), 32 * kWarps, 0, s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -560,14 +575,15 @@ int launch_tile(LinearParams p, int sms, cudaStream_t s) {
     ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   } else {
     // Few tiles: 2 or 4 CTAs share one's groups, as long as all clusters run at
-    // once (4 do not fit everywhere) and each CTA has two groups.  A step less
-    // of the loop takes 0.2 us, a cluster's addition about 1: 32 x 4096 x 4096
-    // takes 14.2, 10.3 and 9.2 us with 1, 2 and 4.
+    // once (4 do not fit everywhere).  A group less of the loop takes 0.28 us, a
+    // cluster and its addition 1.5 with 64 tokens and 3 with 128: 32 x 2048 x
+    // 4096 takes 13.0, 10.2 and 8.0 us with 1, 2 and 4, 32 x 2048 x 1024 5.7, 6.0
+    // and 5.4, 100 x 4096 x 1024 6.1, 7.3 and 7.4.
     p.splits = 1;
     for (int n = 2; n <= 4; n *= 2) {
       int fit = 0;
       if (int e = clusters_at_once<T, kTokens, kWide>(dev, n, fit)) return e;
-      if (tiles <= fit && p.KB >= 2 * n) p.splits = n;
+      if (tiles <= fit && p.KB - p.KB / n >= (kTokens == 64 ? 6 : 12)) p.splits = n;
     }
     cluster = p.splits;
     ctas = p.splits > 1 ? tiles * p.splits : (tiles < sms ? tiles : sms);
@@ -592,13 +608,19 @@ int launch(const LinearParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   // Up to 8 tokens, the weights stream through the warps' registers (8 x 6144 x
-  // 4096: 8.2 us, 11 by tiles); with 16 the tiles are ahead (10.9, 11.9 us).
-  if (p.M <= 8) return launch_stream<T>(p, s);
+  // 4096: 8.3 us, 10.4 by tiles; 8 x 1536 x 2048: 2.9 and 5.5).  Up to 32 they do
+  // where a warp has at most two groups of columns and two CTAs an SM suffice:
+  // there the tiles' 4 us of set-up weigh more (16 x 2048 x 2048: 4.0 us, 5.9 by
+  // tiles; 32 x 4096 x 2048: 7.1 and 7.2; beyond, 16 x 4096 x 4096: 10.0 and 8.9,
+  // 16 x 16384 x 2048: 14.2 and 10.2).
+  if (p.M <= 8) return launch_stream<T, 1>(p, s);
+  if (p.M <= 32 && p.KB <= 2 * kWarps && p.N <= 2 * sms * kRows)
+    return p.M <= 16 ? launch_stream<T, 2>(p, s) : launch_stream<T, 4>(p, s);
   if (p.M <= 64) return launch_tile<T, 64, 128>(p, sms, s);
   // Above, whichever needs less time in whole rounds over the SMs: a round of
   // pairs takes 1.5 times one of single CTAs (14.0 and 9.7 us at K = 4096) and
-  // does twice the work.  1024 x 6144 x 4096: 33 and 35 us; 509 x 4096 x 4096:
-  // 18 and 14.2 us.
+  // does twice the work.  1024 x 6144 x 4096: 32.0 and 34.1 us, 300 x 8192 x 6144:
+  // 24.7 and 33.5; 509 x 4096 x 4096: 17.7 and 13.7.
   const long long pairs = static_cast<long long>((p.M + 255) / 256) * ((p.N + 255) / 256);
   const long long singles = static_cast<long long>((p.M + 127) / 128) * ((p.N + 127) / 128);
   const long long pair_rounds = (pairs + sms / 2 - 1) / (sms / 2), single_rounds = (singles + sms - 1) / sms;

@@ -195,6 +195,15 @@ def test_fp8_linear(m, n, k, dtype):
     assert (y[:, n:] == 7).all() and int(st.item()) == 0
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("m,n,k", [(9, 33, 100), (15, 1000, 2048), (24, 130, 2000), (32, 4000, 300), (10, 520, 2064),
+                                   (31, 100, 4000), (12, 6000, 512), (48, 1000, 1600), (50, 300, 800), (100, 300, 2100),
+                                   (128, 200, 5000)])
+def test_fp8_linear_between_kernels(m, n, k, dtype):
+    """Sizes on both sides of the choices of a kernel and of its split."""
+    test_fp8_linear(m, n, k, dtype)
+
+
 def test_fp8_linear_same_result_twice():
     g = gen(5)
     for m in (5, 70, 300):
