@@ -25,7 +25,6 @@ struct LinearParams {
 };
 
 constexpr int kRows = 16;    // weight rows of a CTA: the m16 side of the warp MMA
-constexpr int kWarps = 8;
 
 // 16 bytes at column k of a row; columns from K on are 0.
 __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K, bool valid) {
@@ -40,14 +39,15 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K, bool v
 }
 
 // Few tokens: the weights stream from memory into registers.  A CTA owns 16
-// weight rows and kGroups x 8 tokens; its warps take every eighth group of 128
-// columns.
-// A lane loads 16 contiguous bytes of a row and feeds them to two MMAs as if
-// they were the four columns each of those wants: the same reordering of k on
-// both operands leaves the sum as it is.  Memory bounds it; 32 warps an SM keep
-// enough loads in flight (two or four groups a warp at once came out slower).
-// 1 x 6144 x 4096: 7.7 us, 3.3 TB/s of weights with the launch included.
-template <typename T, int kGroups>
+// weight rows and kGroups x 8 tokens; its warps take every kWarps-th group of
+// 128 columns.  A lane loads 16 contiguous bytes of a row and feeds them to two
+// MMAs as if they were the four columns each of those wants: the same
+// reordering of k on both operands leaves the sum as it is.  Memory bounds it;
+// what counts is how many warps have a group's loads under way (two groups a
+// warp at once, or L2 prefetches of the rows, came out slower).  1 x 6144 x 4096:
+// 7.7 us, 3.3 TB/s of weights with the launch included; 2 x 28672 x 8192: 39 us,
+// 6.0 TB/s.
+template <typename T, int kGroups, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kTokens = 8 * kGroups;
   __shared__ float red[kWarps][kRows][kTokens + 1];
@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid
   }
 }
 
-template <typename T, int kGroups>
+template <typename T, int kGroups, int kWarps>
 int launch_stream(const LinearParams& p, cudaStream_t s) {
-  linear_stream_kernel<T, kGroups><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), 32 * kWarps, 0, s>>>(p);
+  linear_stream_kernel<T, kGroups, kWarps><<<static_cast<unsigned>((p.N + kRows - 1) / kRows), 32 * kWarps, 0, s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -608,14 +608,20 @@ int launch(const LinearParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   // Up to 8 tokens, the weights stream through the warps' registers (8 x 6144 x
-  // 4096: 8.3 us, 10.4 by tiles; 8 x 1536 x 2048: 2.9 and 5.5).  Up to 32 they do
-  // where a warp has at most two groups of columns and two CTAs an SM suffice:
-  // there the tiles' 4 us of set-up weigh more (16 x 2048 x 2048: 4.0 us, 5.9 by
-  // tiles; 32 x 4096 x 2048: 7.1 and 7.2; beyond, 16 x 4096 x 4096: 10.0 and 8.9,
-  // 16 x 16384 x 2048: 14.2 and 10.2).
-  if (p.M <= 8) return launch_stream<T, 1>(p, s);
-  if (p.M <= 32 && p.KB <= 2 * kWarps && p.N <= 2 * sms * kRows)
-    return p.M <= 16 ? launch_stream<T, 2>(p, s) : launch_stream<T, 4>(p, s);
+  // 4096: 8.3 us, 10.4 by tiles); with 16 warps a CTA where all of them are on
+  // the SMs at once (8 x 4096 x 4096: 5.8 us, 7.6 with 8 warps; 8 x 8192 x 6144,
+  // in more than one wave: 13.1 and 12.9).
+  const int ctas = (p.N + kRows - 1) / kRows;
+  if (p.M <= 8) return ctas <= 2 * sms && p.KB > 8 ? launch_stream<T, 1, 16>(p, s) : launch_stream<T, 1, 8>(p, s);
+  // Up to 32 they do where a warp has one or two groups of columns: there the
+  // tiles' 4 us of set-up weigh more.  One CTA of 16 warps an SM: 16 x 2048 x
+  // 4096 takes 6.1 us, 7.7 by tiles, 32 x 2048 x 2048 4.9 (6.1; 5.2 with 8
+  // warps), but 32 x 2048 x 4096 8.5 (7.9 by tiles).  Two of 8 warps: 16 x 4096 x
+  // 2048 5.4 us, 6.7 by tiles, but 16 x 4096 x 4096 10.0 (8.9 by tiles).
+  if (p.M <= 32 && ctas <= sms && p.KB > 8 && p.KB <= (p.M <= 16 ? 32 : 16))
+    return p.M <= 16 ? launch_stream<T, 2, 16>(p, s) : launch_stream<T, 4, 16>(p, s);
+  if (p.M <= 32 && ctas <= 2 * sms && p.KB <= 16)
+    return p.M <= 16 ? launch_stream<T, 2, 8>(p, s) : launch_stream<T, 4, 8>(p, s);
   if (p.M <= 64) return launch_tile<T, 64, 128>(p, sms, s);
   // Above, whichever needs less time in whole rounds over the SMs: a round of
   // pairs takes 1.5 times one of single CTAs (14.0 and 9.7 us at K = 4096) and
