@@ -20,6 +20,7 @@ struct LinearParams {
   int M, N, K, KB;
   int splits;       // CTAs of a cluster that share a tile's groups
   int32_t* status;
+  bool wide_b;      // rows of b start at 32-byte addresses
   bool wide_y;      // rows of y start at 16-byte addresses
   bool wide_scales; // scales through tensor maps
 };
@@ -38,15 +39,29 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K, bool v
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 32 bytes at column k, by one load where `wide`.
+__device__ __forceinline__ void load32(const uint8_t* row, int k, int K, bool valid, bool wide, uint32_t (&v)[8]) {
+  if (wide && valid && k + 32 <= K) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(row + k));
+    return;
+  }
+  const uint4 lo = load16(row, k, K, valid), hi = load16(row, k + 16, K, valid);
+  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+  v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+}
+
 // Few tokens: the weights stream from memory into registers.  A CTA owns 16
 // weight rows and kGroups x 8 tokens; its warps take every kWarps-th group of
-// 128 columns.  A lane loads 16 contiguous bytes of a row and feeds them to two
-// MMAs as if they were the four columns each of those wants: the same
-// reordering of k on both operands leaves the sum as it is.  Memory bounds it;
-// what counts is how many warps have a group's loads under way (two groups a
-// warp at once, or L2 prefetches of the rows, came out slower).  1 x 6144 x 4096:
-// 7.7 us, 3.3 TB/s of weights with the launch included; 2 x 28672 x 8192: 39 us,
-// 6.0 TB/s.
+// 128 columns.  A lane loads 32 contiguous bytes of a row and feeds them to four
+// MMAs as if they were the columns that each of those wants: the same reordering
+// of k on both operands leaves the sum as it is.  Memory bounds it, and what
+// counts is that it sees whole 128-byte lines (halves of a line, in two loads of
+// 16 bytes, take a tenth longer) and many warps with one group under way (two
+// groups a warp at once, or L2 prefetches of the rows, scatter the accesses and
+// take a tenth to a third longer).  8 x 6144 x 4096: 7.5 us, 3.4 TB/s of weights
+// with the launch included; 2 x 28672 x 8192: 38 us, 6.2 TB/s.
 template <typename T, int kGroups, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid_constant__ LinearParams p) {
   constexpr int kTokens = 8 * kGroups;
@@ -68,20 +83,19 @@ __global__ void __launch_bounds__(32 * kWarps) linear_stream_kernel(const __grid
   }
   float sum[kGroups][4] = {};
   for (int kb = warp; kb < p.KB; kb += kWarps) {
-    const int k = kb * pw::kGroup + 16 * t;
-    const uint4 w0 = load16(b_lo, k, p.K, v_lo), w1 = load16(b_hi, k, p.K, v_hi);
-    const uint4 w2 = load16(b_lo, k + 64, p.K, v_lo), w3 = load16(b_hi, k + 64, p.K, v_hi);
+    const int k = kb * pw::kGroup + 32 * t;
+    uint32_t lo[8], hi[8];
+    load32(b_lo, k, p.K, v_lo, p.wide_b, lo);
+    load32(b_hi, k, p.K, v_hi, p.wide_b, hi);
     const float s = __ldg(sb + kb);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      const bool v = 8 * i + g < p.M;
-      const uint4 x0 = load16(a[i], k, p.K, v), x1 = load16(a[i], k + 64, p.K, v);
+      uint32_t x[8];
+      load32(a[i], k, p.K, 8 * i + g < p.M, false, x);
       const float s0 = s * __ldg(sa[i][0] + kb), s1 = s * __ldg(sa[i][1] + kb);
       float acc[4] = {};
-      pw::mma_16832_e4m3(acc, w0.x, w1.x, w0.y, w1.y, x0.x, x0.y);
-      pw::mma_16832_e4m3(acc, w0.z, w1.z, w0.w, w1.w, x0.z, x0.w);
-      pw::mma_16832_e4m3(acc, w2.x, w3.x, w2.y, w3.y, x1.x, x1.y);
-      pw::mma_16832_e4m3(acc, w2.z, w3.z, w2.w, w3.w, x1.z, x1.w);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) pw::mma_16832_e4m3(acc, lo[j], hi[j], lo[j + 1], hi[j + 1], x[j], x[j + 1]);
       sum[i][0] += s0 * acc[0];
       sum[i][1] += s1 * acc[1];
       sum[i][2] += s0 * acc[2];
@@ -608,20 +622,22 @@ int launch(const LinearParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   // Up to 8 tokens, the weights stream through the warps' registers (8 x 6144 x
-  // 4096: 8.3 us, 10.4 by tiles); with 16 warps a CTA where all of them are on
-  // the SMs at once (8 x 4096 x 4096: 5.8 us, 7.6 with 8 warps; 8 x 8192 x 6144,
-  // in more than one wave: 13.1 and 12.9).
+  // 4096: 7.5 us, 10.4 by tiles); with 16 warps a CTA where all of them are on
+  // the SMs at once (8 x 4096 x 4096: 5.7 us, 7.0 with 8 warps; 8 x 16384 x 4096,
+  // in more than one wave: 15.1 and 14.7).
   const int ctas = (p.N + kRows - 1) / kRows;
   if (p.M <= 8) return ctas <= 2 * sms && p.KB > 8 ? launch_stream<T, 1, 16>(p, s) : launch_stream<T, 1, 8>(p, s);
-  // Up to 32 they do where a warp has one or two groups of columns: there the
-  // tiles' 4 us of set-up weigh more.  One CTA of 16 warps an SM: 16 x 2048 x
-  // 4096 takes 6.1 us, 7.7 by tiles, 32 x 2048 x 2048 4.9 (6.1; 5.2 with 8
-  // warps), but 32 x 2048 x 4096 8.5 (7.9 by tiles).  Two of 8 warps: 16 x 4096 x
-  // 2048 5.4 us, 6.7 by tiles, but 16 x 4096 x 4096 10.0 (8.9 by tiles).
-  if (p.M <= 32 && ctas <= sms && p.KB > 8 && p.KB <= (p.M <= 16 ? 32 : 16))
-    return p.M <= 16 ? launch_stream<T, 2, 16>(p, s) : launch_stream<T, 4, 16>(p, s);
-  if (p.M <= 32 && ctas <= 2 * sms && p.KB <= 16)
-    return p.M <= 16 ? launch_stream<T, 2, 8>(p, s) : launch_stream<T, 4, 8>(p, s);
+  // Up to 32 they do where a warp has one or two groups of columns and the CTAs
+  // are on the SMs at once: there the tiles' 4 us of set-up weigh more.  One CTA
+  // of 16 warps an SM: 16 x 2048 x 4096 takes 6.0 us, 7.7 by tiles, 32 x 2048 x
+  // 2048 4.5 (6.1), but 32 x 2048 x 4096 9.1 (8.0 by tiles).  Two or three of 8
+  // warps: 16 x 4096 x 2048 5.0 us, 6.7 by tiles, 16 x 6144 x 2048 6.9 (8.5), 32 x
+  // 4096 x 2048 7.0 (7.2), but 16 x 4096 x 4096 9.4 (9.0 by tiles).
+  const bool few = p.M <= 16;
+  if (p.M <= 32 && ctas <= sms && p.KB > 8 && p.KB <= (few ? 32 : 16))
+    return few ? launch_stream<T, 2, 16>(p, s) : launch_stream<T, 4, 16>(p, s);
+  if (p.M <= 32 && ctas <= (few ? 3 : 2) * sms && p.KB <= 16)
+    return few ? launch_stream<T, 2, 8>(p, s) : launch_stream<T, 4, 8>(p, s);
   if (p.M <= 64) return launch_tile<T, 64, 128>(p, sms, s);
   // Above, whichever needs less time in whole rounds over the SMs: a round of
   // pairs takes 1.5 times one of single CTAs (14.0 and 9.7 us at K = 4096) and
@@ -674,6 +690,7 @@ extern "C" int pw_fp8_linear(const pw_linear_args* args, void* stream) {
   p.KB = kb;
   p.splits = 1;
   p.status = a.status;
+  p.wide_b = pw::aligned(a.b, 32) && a.ldb % 32 == 0;
   p.wide_y = pw::aligned(a.y, 16) && a.ldy % 8 == 0;
   // with one group a tile the slots of the scales would be reused too early
   p.wide_scales = kb >= 2 && pw::aligned(a.a_scale, 16) && pw::aligned(a.b_scale, 16) && a.a_scale_stride % 4 == 0 &&

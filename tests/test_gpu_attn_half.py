@@ -204,6 +204,24 @@ def test_fp8_linear_between_kernels(m, n, k, dtype):
     test_fp8_linear(m, n, k, dtype)
 
 
+@pytest.mark.parametrize("offset,pitch", [(0, 272), (16, 272), (16, 288), (32, 288)])
+@pytest.mark.parametrize("m", [3, 13, 29, 60])
+def test_fp8_linear_row_alignment(m, offset, pitch):
+    """Rows at 16-byte addresses, whichever of them are at 32-byte ones too."""
+    g, n, k = gen(m), 50, 240
+    def codes(rows):
+        t = (torch.randn(rows * pitch + 64, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn).to(DEV)
+        return t[offset:offset + rows * pitch].view(rows, pitch)[:, :k]
+    a, b = codes(m), codes(n)
+    sa, sb = torch.rand(m, 2, generator=g).to(DEV), torch.rand(1, 2, generator=g).to(DEV) / 64
+    y, st = torch.empty(m, n, dtype=torch.bfloat16, device=DEV), status()
+    pw.pw_fp8_linear(a, sa, b, sb, y, st)
+    want, mag = ref.fp8_linear(a.contiguous().view(torch.uint8).cpu().numpy(), f64(sa),
+                               b.contiguous().view(torch.uint8).cpu().numpy(), f64(sb))
+    within(f64(y), want, U[torch.bfloat16] * np.abs(want) * 1.01 + 2.0 ** -13 * mag + TINY[torch.bfloat16])
+    assert int(st.item()) == 0
+
+
 def test_fp8_linear_same_result_twice():
     g = gen(5)
     for m in (5, 70, 300):
