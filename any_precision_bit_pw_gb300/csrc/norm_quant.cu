@@ -5,8 +5,8 @@
 //   s = max(max|y over the group| / 448, 2^-100),  q = e4m3(y / s)
 //
 // Both read and write every value once; memory bandwidth bounds them (8192 x
-// 6144 with residual to e4m3: 55 us, 6.4 TB/s; weights of 8192 x 6144: 26 us,
-// 5.9 TB/s), and for a few rows the latency of one load, one reduction and one
+// 6144 with residual to e4m3: 55 us, 6.4 TB/s; weights of 8192 x 6144: 24 us,
+// 6.2 TB/s), and for a few rows the latency of one load, one reduction and one
 // store (one row of 4096: 2.0 us with the launch).
 #include "ops_common.cuh"
 
@@ -165,29 +165,44 @@ __global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024) row_kernel(const __g
   }
 }
 
-// One CTA per 128 x 128 block: 256 threads hold 8 rows x 8 columns each, packed.
-template <typename T, bool kAligned>
+// One CTA per 128 x 128 block: 256 threads hold 64 values each, packed: of 8
+// rows, or of 4 rows by accesses of 32 bytes (kWide), where they can be (8192 x
+// 6144: 24.2 us, 25.6 by 16 bytes).
+template <typename T, bool kAligned, bool kWide>
 __global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowParams p) {
+  constexpr int kParts = kWide ? 2 : 1, kTurns = 8 / kParts, kLanes = 16 / kParts, kStep = 256 / kLanes;
   __shared__ float tops[8];
   const int tid = threadIdx.x;
   const int kb = blockIdx.x;
-  const int col = kb * pw::kGroup + (tid & 15) * kVec;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * pw::kGroup + (tid >> 4);
-  uint4 x[8];
+  const int col = kb * pw::kGroup + (tid % kLanes) * kParts * kVec;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * pw::kGroup + tid / kLanes;
+  uint4 x[kTurns][kParts];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = row0 + 16 * i;
-    x[i] = load8<T, kAligned>(static_cast<const T*>(p.x) + (row < p.rows ? row : 0) * p.x_stride,
-                              row < p.rows ? col : p.cols, p.cols);
+  for (int i = 0; i < kTurns; ++i) {
+    const int64_t row = row0 + kStep * i;
+    const bool valid = row < p.rows && col < p.cols;
+    const T* src = static_cast<const T*>(p.x) + (row < p.rows ? row : 0) * p.x_stride;
+    if constexpr (kWide) {
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      if (valid)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x[i][0].x), "=r"(x[i][0].y), "=r"(x[i][0].z), "=r"(x[i][0].w), "=r"(x[i][1].x), "=r"(x[i][1].y),
+                       "=r"(x[i][1].z), "=r"(x[i][1].w)
+                     : "l"(src + col));
+    } else {
+      x[i][0] = load8<T, kAligned>(src, valid ? col : p.cols, p.cols);
+    }
   }
   float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v[kVec];
-    unpack8<T>(x[i], v);
+  for (int i = 0; i < kTurns; ++i)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) top = pw::max_nan(top, fabsf(v[j]));
-  }
+    for (int h = 0; h < kParts; ++h) {
+      float v[kVec];
+      unpack8<T>(x[i][h], v);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) top = pw::max_nan(top, fabsf(v[j]));
+    }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   if ((tid & 31) == 0) tops[tid >> 5] = top;
@@ -199,11 +214,25 @@ __global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowP
   if (tid == 0) p.scale[blockIdx.y * p.scale_stride + kb] = s;
   const float inv = 1.0f / s;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = row0 + 16 * i;
-    float v[kVec];
-    unpack8<T>(x[i], v);
-    if (row < p.rows) store8_e4m3<kAligned>(p.q + row * p.q_stride, col, p.cols, v, inv);
+  for (int i = 0; i < kTurns; ++i) {
+    const int64_t row = row0 + kStep * i;
+    if (row >= p.rows) break;
+    uint8_t* dst = p.q + row * p.q_stride;
+    if constexpr (kWide) {
+      uint32_t c[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[kVec];
+        unpack8<T>(x[i][h], v);
+        c[2 * h] = pw::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        c[2 * h + 1] = pw::e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+      }
+      if (col < p.cols) *reinterpret_cast<uint4*>(dst + col) = make_uint4(c[0], c[1], c[2], c[3]);
+    } else {
+      float v[kVec];
+      unpack8<T>(x[i][0], v);
+      store8_e4m3<kAligned>(dst, col, p.cols, v, inv);
+    }
   }
 }
 
@@ -248,7 +277,14 @@ template <typename T, bool kAligned>
 int launch_blocks(const RowParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.cols + pw::kGroup - 1) / pw::kGroup),
                   static_cast<unsigned>((p.rows + pw::kGroup - 1) / pw::kGroup));
-  block_kernel<T, kAligned><<<grid, 256, 0, s>>>(p);
+  if constexpr (kAligned) {
+    if (pw::aligned(p.x, 32) && pw::aligned(p.q, 16) && p.x_stride % 16 == 0 && p.q_stride % 16 == 0 && p.cols % 16 == 0) {
+      block_kernel<T, true, true><<<grid, 256, 0, s>>>(p);
+      PW_CUDA_TRY(cudaGetLastError());
+      return PW_OK;
+    }
+  }
+  block_kernel<T, kAligned, false><<<grid, 256, 0, s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
