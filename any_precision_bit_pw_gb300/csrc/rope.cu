@@ -9,15 +9,18 @@
 // lose a digit with every factor of ten in p).
 //
 // Reads q, k and v once and writes as much: bound by memory bandwidth for
-// prompts (7.3k tokens of 48 + 8 + 8 heads: 51 us, 4.7 TB/s; five CTAs an SM
-// with two units a thread under way, four with four units took 77 us), by the
-// chain offsets -> page -> store for single tokens (128 tokens: 3.7 us).
+// prompts (7.3k tokens of 48 + 8 + 8 heads: 40 us, 6.0 TB/s), by the chain
+// offsets -> page -> store for single tokens (128 tokens: 3.6 us).  What it takes
+// is little arithmetic on places per byte, and many CTAs, so that some wait for
+// their tokens' places while others copy: 32 bytes an access and six CTAs an SM
+// (with 16 bytes, two units a thread and five CTAs 52 us).
 #include "ops_common.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;    // units of a thread under way together
+template <int kVec>
+constexpr int kAhead = kVec == 16 ? 1 : 2;   // units of a thread under way together: 32 bytes
 constexpr int kPerCta = 2;
 constexpr int kMost = 8;     // tokens of a CTA
 
@@ -37,6 +40,13 @@ struct RopeParams {
 
 template <int kVec>
 struct Vec;
+struct alignas(32) Words {
+  uint32_t r[8];
+};
+template <>
+struct Vec<16> {
+  using type = Words;
+};
 template <>
 struct Vec<8> {
   using type = uint4;
@@ -56,6 +66,30 @@ union Values {
   T v[kVec];
   __device__ Values() {}
 };
+
+template <typename V>
+__device__ __forceinline__ V load(const void* src) {
+  return *static_cast<const V*>(src);
+}
+template <>
+__device__ __forceinline__ Words load<Words>(const void* src) {
+  Words w;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w.r[0]), "=r"(w.r[1]), "=r"(w.r[2]), "=r"(w.r[3]), "=r"(w.r[4]), "=r"(w.r[5]), "=r"(w.r[6]), "=r"(w.r[7])
+               : "l"(src)
+               : "memory");
+  return w;
+}
+template <typename V>
+__device__ __forceinline__ void store(void* dst, const V& v) {
+  *static_cast<V*>(dst) = v;
+}
+template <>
+__device__ __forceinline__ void store<Words>(void* dst, const Words& w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w.r[0]), "r"(w.r[1]), "r"(w.r[2]),
+               "r"(w.r[3]), "r"(w.r[4]), "r"(w.r[5]), "r"(w.r[6]), "r"(w.r[7])
+               : "memory");
+}
 
 __device__ __forceinline__ int quotient(int n, int d, uint32_t inv) {
   return inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), inv)) : n / d;
@@ -95,7 +129,7 @@ __device__ __forceinline__ void load_unit(const RopeParams& p, int t0, int w, in
       const bool near = a.interleaved && kVec > 1;
       u.first = a.interleaved && kVec == 1 ? 2 * at : at * kVec;
       u.second = near ? kNear : a.interleaved ? u.first + 1 : a.rotary_dim / 2 + u.first;
-      if (!near) u.y.raw = *reinterpret_cast<const V*>(src + u.second);
+      if (!near) u.y.raw = load<V>(src + u.second);
     } else {
       u.first = a.rotary_dim + (at - p.pair_units) * kVec;
       u.second = kCopied;
@@ -108,7 +142,7 @@ __device__ __forceinline__ void load_unit(const RopeParams& p, int t0, int w, in
     u.first = (w - u.head * p.value_units) * kVec;
     u.second = kCopied;
   }
-  u.x.raw = *reinterpret_cast<const V*>(src + u.first);
+  u.x.raw = load<V>(src + u.first);
 }
 
 template <typename T, int kVec>
@@ -130,16 +164,16 @@ __device__ __forceinline__ void finish_unit(Unit<T, kVec>& u, T* dst, bool inter
       u.x.v[i] = pw::from_float<T>(a * c[i].x - b * c[i].y);
       u.y.v[i] = pw::from_float<T>(a * c[i].y + b * c[i].x);
     }
-    *reinterpret_cast<V*>(dst + u.second) = u.y.raw;
+    store<V>(dst + u.second, u.y.raw);
   }
-  *reinterpret_cast<V*>(dst + u.first) = u.x.raw;
+  store<V>(dst + u.first, u.x.raw);
 }
 
 // A CTA takes p.per_cta tokens.  Their first values are loaded at once: they
 // depend on nothing, and the way to their place (sequence, length, page) takes
 // two trips to memory.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kVec == 16 ? 6 : 5) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ float2 cs[];
   __shared__ int found[kMost], slots[kMost];
   __shared__ int64_t k_at[kMost], v_at[kMost];   // offsets in the caches; -1: no place
@@ -147,10 +181,11 @@ __global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant
   const int tid = threadIdx.x, half = a.rotary_dim / 2;
   const int t0 = blockIdx.x * p.per_cta, tokens = min(p.per_cta, a.tokens - t0), total = tokens * p.units;
   if (tid < kMost) found[tid] = -1;
-  Unit<T, kVec> u[kAhead];
-  int kind[kAhead];
+  constexpr int kUnits = kAhead<kVec>;
+  Unit<T, kVec> u[kUnits];
+  int kind[kUnits];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load_unit<T, kVec>(p, t0, tid + i * kThreads, total, u[i], kind[i]);
+  for (int i = 0; i < kUnits; ++i) load_unit<T, kVec>(p, t0, tid + i * kThreads, total, u[i], kind[i]);
   __syncthreads();
   // the tokens' sequences
   for (int b = tid; b < a.batch; b += kThreads) {
@@ -191,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant
   __syncthreads();
   for (int w0 = 0;;) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kUnits; ++i) {
       const int token = u[i].token;
       if (token < 0 || found[token] < 0 || (kind[i] && k_at[token] < 0)) continue;
       T* dst = kind[i] == 0   ? static_cast<T*>(a.q_out) + static_cast<int64_t>(t0 + token) * a.q_out_stride_token +
@@ -200,15 +235,15 @@ __global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant
                               : static_cast<T*>(a.v_cache) + v_at[token] + u[i].head * a.v_cache_stride_head;
       finish_unit<T, kVec>(u[i], dst, a.interleaved, cs + token * half);
     }
-    w0 += kAhead * kThreads;
+    w0 += kUnits * kThreads;
     if (w0 >= total) break;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_unit<T, kVec>(p, t0, w0 + tid + i * kThreads, total, u[i], kind[i]);
+    for (int i = 0; i < kUnits; ++i) load_unit<T, kVec>(p, t0, w0 + tid + i * kThreads, total, u[i], kind[i]);
   }
 }
 
-// Values in one access: 8 where every address and length is a multiple of 8
-// values, else 4, else 1.
+// Values in one access: 16 where every address and length is a multiple of 16
+// values, else 8, 4 or 1.
 int vector_width(const pw_rope_args& a) {
   int64_t m = a.head_dim | (a.rotary_dim / 2);
   uintptr_t addr = 0;
@@ -226,7 +261,7 @@ int vector_width(const pw_rope_args& a) {
     add(a.k_cache, a.k_cache_stride_page, a.k_cache_stride_token, a.k_cache_stride_head);
     add(a.v_cache, a.v_cache_stride_page, a.v_cache_stride_token, a.v_cache_stride_head);
   }
-  for (int v : {8, 4})
+  for (int v : {16, 8, 4})
     if (m % v == 0 && addr % (2 * v) == 0) return v;
   return 1;
 }
@@ -243,7 +278,7 @@ int launch(const pw_rope_args& a, cudaStream_t s) {
   p.units = p.units_q + p.units_k + (a.k ? a.kv_heads * p.value_units : 0);
   if (p.units == 0) return PW_OK;   // no heads
   // one token a CTA while they do not fill the SMs, then kPerCta: the search for
-  // the place is shared (59 us with one, 56 with two)
+  // the place is shared (with halves: 47 us with one, 43 with two, 44 with four)
   const int sms = pw::sm_count();
   p.per_cta = a.tokens > 8 * sms ? kPerCta : 1;
   const bool few = static_cast<int64_t>(p.units) * p.per_cta < (1 << 16);
@@ -260,6 +295,7 @@ int launch(const pw_rope_args& a, cudaStream_t s) {
 template <typename T>
 int launch_width(const pw_rope_args& a, cudaStream_t s) {
   switch (vector_width(a)) {
+    case 16: return launch<T, 16>(a, s);
     case 8: return launch<T, 8>(a, s);
     case 4: return launch<T, 4>(a, s);
     default: return launch<T, 1>(a, s);

@@ -160,6 +160,23 @@ def test_quantize_extremes():
         assert bad[2, 130] and bad[3, 5] and not bad[2, :128].any() and not bad[2, 256:].any() and not bad[3, 128:].any()
 
 
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_same_result_at_any_alignment(block_rows):
+    rows, cols = 200, 336
+    x0 = draw(gen(6), rows, cols, dtype=torch.bfloat16)
+    want = None
+    for offset, pitch in ((0, 336), (16, 352), (8, 336), (0, 344), (1, 337)):
+        x = torch.empty(rows * pitch + 64, dtype=torch.bfloat16, device=DEV)[offset:offset + rows * pitch].view(rows, pitch)[:, :cols]
+        x.copy_(x0)
+        q = torch.zeros(rows * pitch + 64, dtype=torch.uint8, device=DEV)[offset:offset + rows * pitch].view(rows, pitch)[:, :cols]
+        sc = torch.empty(-(-rows // block_rows), -(-cols // 128), device=DEV)
+        pw.pw_quantize_fp8(x, q, sc, block_rows=block_rows)
+        if want is None:
+            want = (q.clone(), sc)
+            check_codes(q, sc, f64(x), block_rows)
+        assert torch.equal(q, want[0]) and torch.equal(sc, want[1])
+
+
 # ---------------------------------------------------------------- the 8-bit product
 LINEAR = [(1, 1, 16), (1, 128, 128), (3, 17, 130), (7, 200, 100), (8, 1000, 512), (9, 128, 1000), (16, 64, 2048),
           (17, 130, 256), (33, 129, 384), (64, 384, 144), (65, 1, 640), (100, 300, 1024), (128, 256, 128), (129, 513, 257),
@@ -342,6 +359,29 @@ def test_rope_far_positions():
     want = np.concatenate((a * c - b * s, a * s + b * c), -1)
     mag = np.concatenate((np.hypot(a, b),) * 2, -1)
     within(out, want, U[torch.float16] * np.abs(want) * 1.001 + 2.0 ** -20 * mag + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rotary", [128, 64, 16, 8])
+def test_rope_same_result_at_any_alignment(rotary, interleaved):
+    """Accesses of 16, 8, 4 and 1 values give the same bits."""
+    b = Batch([5, 1, 20], [30, 7, 20], 3, 2, 128, 16, torch.float16, 4)
+    turns, _ = pw.pw_rope_turns(rotary)
+    rows = 3 + 2 * 2
+    want = None
+    for offset, pitch in ((0, rows * 128), (8, rows * 128 + 8), (4, rows * 128 + 4), (3, rows * 128 + 1)):
+        room = torch.empty(b.T * pitch + 64, dtype=torch.float16, device=DEV)
+        qkv = room[offset:offset + b.T * pitch].view(b.T, pitch)[:, :rows * 128].unflatten(1, (rows, 128))
+        qkv.copy_(b.qkv)
+        kc, vc, st = b.k.clone(), b.v.clone(), status()
+        qo = torch.empty(b.T, 3, 128, dtype=torch.float16, device=DEV)
+        pw.pw_rope_append(qkv[:, :3], qkv[:, 3:5], qkv[:, 5:], turns.to(DEV), kc, vc, b.table, b.offsets, b.lens, qo, st,
+                          interleaved=interleaved)
+        assert int(st.item()) == 0
+        got = [t.view(torch.int16) for t in (qo, kc, vc)]
+        if want is None:
+            want = got
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_rope_reports_missing_pages():
