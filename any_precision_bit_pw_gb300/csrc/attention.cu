@@ -403,6 +403,11 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
   if (strides % 8 || !pw::aligned(a.q, 16) || !pw::aligned(a.out, 16) || !pw::aligned(a.k_cache, 16) ||
       !pw::aligned(a.v_cache, 16))
     return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: every head's row must be 16-byte aligned");
+  for (const void* ptr : {static_cast<const void*>(a.page_table), static_cast<const void*>(a.q_offsets),
+                          static_cast<const void*>(a.kv_lens), static_cast<const void*>(a.lse),
+                          static_cast<const void*>(a.status)})
+    if (!pw::aligned(ptr, 4))
+      return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: misaligned table, lengths, lse or status");
   const size_t need = pw_paged_attention_workspace(a.tokens, a.batch, a.heads, a.kv_heads, a.head_dim);
   if (ws_bytes < need || !pw::aligned(d_ws, 256))
     return pw::set_error(PW_ERR_WORKSPACE, "paged_attention: workspace needs %zu bytes, 256-byte aligned (got %zu)", need,

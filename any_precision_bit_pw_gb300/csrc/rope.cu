@@ -378,6 +378,11 @@ int pw_rope_append(const pw_rope_args* args, void* stream) {
   for (const void* ptr : {a.q, static_cast<const void*>(a.q_out), a.k, a.v, static_cast<const void*>(a.k_cache),
                           static_cast<const void*>(a.v_cache)})
     if (!pw::aligned(ptr, 2)) return pw::set_error(PW_ERR_INVALID_ARG, "rope_append: misaligned pointer");
+  for (const void* ptr : {static_cast<const void*>(a.page_table), static_cast<const void*>(a.q_offsets),
+                          static_cast<const void*>(a.kv_lens), static_cast<const void*>(a.positions),
+                          static_cast<const void*>(a.status)})
+    if (!pw::aligned(ptr, 4)) return pw::set_error(PW_ERR_INVALID_ARG, "rope_append: misaligned table, lengths or status");
+  if (!pw::aligned(a.turns, 8)) return pw::set_error(PW_ERR_INVALID_ARG, "rope_append: misaligned turns");
   cudaStream_t s = pw::as_stream(stream);
   return a.dtype == PW_DTYPE_F16 ? launch_width<__half>(a, s) : launch_width<__nv_bfloat16>(a, s);
 }

@@ -202,6 +202,16 @@ def test_attention_refusals(L, kw, code):
     assert rc == code and "paged_attention" in pw.pw_last_error()
 
 
+@pytest.mark.parametrize("name,offset", [("page_table", 2), ("q_offsets", 1), ("kv_lens", 2), ("status", 3)])
+def test_misaligned_words_are_refused(L, name, offset):
+    kw = {name: FAKE + offset}
+    assert L.pw_rope_append(ctypes.byref(_rope_args(**kw)), None) == pw.PW_ERR_INVALID_ARG
+    assert L.pw_paged_attention(ctypes.byref(_attn_args(**kw)), FAKE, 1 << 30, None) == pw.PW_ERR_INVALID_ARG
+    assert L.pw_paged_attention(ctypes.byref(_attn_args(lse=FAKE + offset)), FAKE, 1 << 30, None) == pw.PW_ERR_INVALID_ARG
+    for word in (dict(positions=FAKE + offset), dict(turns=FAKE + 4)):
+        assert L.pw_rope_append(ctypes.byref(_rope_args(**word)), None) == pw.PW_ERR_INVALID_ARG
+
+
 def test_attention_workspace(L):
     need = pw.pw_paged_attention_workspace(4, 2, 4, 2, 128)
     assert need > 0
