@@ -13,6 +13,7 @@ CUDA graph once the batch's tensors are in place.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
 
@@ -20,6 +21,17 @@ import torch
 
 from . import pw
 from .layer import APLMoEStack, MoECall
+
+
+def _on(stream):
+    """Makes ``stream`` (a torch stream or a raw handle; None: as it is) torch's
+    current one, so that libpw's calls and torch's own work are in one order."""
+    if stream is None:
+        return nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)   # 0 and 1: CUDA's names of the default stream
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 @dataclass
@@ -145,27 +157,32 @@ class DecoderLayer:
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor], batch: Batch, stream=None):
         """x fp16 [T][H] (the previous layer's output) and the residual before
         it (None at the first layer) -> this layer's (output, residual).  The
-        results are the layer's buffers, valid until its next call."""
+        results are the layer's buffers, valid until its next call.  All of it
+        runs on ``stream`` (None: torch's current stream)."""
+        with _on(stream):
+            return self._run(x, residual, batch)
+
+    def _run(self, x: torch.Tensor, residual: Optional[torch.Tensor], batch: Batch):
         T, w, c = batch.tokens, self.w, self.cache
         if x.shape[0] != T or T > self.tokens:
             raise ValueError(f"decoder layer: {x.shape[0]} rows for a batch of {T} tokens, at most {self.tokens}")
         x8, x8s, qkv, q, attn = self.x8[:T], self.x8_scale[:T], self.qkv[:T], self.q[:T], self.attn[:T]
         hq, hk = self.heads, self.kv_heads
         r1, r2 = self.residual[0][:T], self.residual[1][:T]
-        pw.pw_add_rmsnorm(x, w.attn_norm, self.eps, residual=residual, residual_out=r1, q=x8, scale=x8s, stream=stream)
-        pw.pw_fp8_linear(x8, x8s, w.qkv.codes, w.qkv.scale, qkv.view(T, -1), self.status, stream=stream)
+        pw.pw_add_rmsnorm(x, w.attn_norm, self.eps, residual=residual, residual_out=r1, q=x8, scale=x8s)
+        pw.pw_fp8_linear(x8, x8s, w.qkv.codes, w.qkv.scale, qkv.view(T, -1), self.status)
         pw.pw_rope_append(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], self.turns, c.k, c.v, batch.page_table,
                           batch.q_offsets, batch.kv_lens, q, self.status, interleaved=self.interleaved,
-                          factor=self.rope_factor, stream=stream)
+                          factor=self.rope_factor)
         pw.pw_paged_attention(q, c.k, c.v, batch.page_table, batch.q_offsets, batch.kv_lens, attn, self.ws, self.status,
                               scale=self.head_dim ** -0.5, window=self.window, max_q_len=batch.max_q_len,
-                              max_kv_len=batch.max_kv_len, stream=stream)
+                              max_kv_len=batch.max_kv_len)
         a8, a8s = self.attn8[:T], self.attn8_scale[:T]
-        pw.pw_quantize_fp8(attn.view(T, -1), a8, a8s, stream=stream)
-        pw.pw_fp8_linear(a8, a8s, w.out.codes, w.out.scale, self.o[:T], self.status, stream=stream)
+        pw.pw_quantize_fp8(attn.view(T, -1), a8, a8s)
+        pw.pw_fp8_linear(a8, a8s, w.out.codes, w.out.scale, self.o[:T], self.status)
         h = self.h[:T]
-        pw.pw_add_rmsnorm(self.o[:T], w.ffn_norm, self.eps, residual=r1, residual_out=r2, y=h, stream=stream)
+        pw.pw_add_rmsnorm(self.o[:T], w.ffn_norm, self.eps, residual=r1, residual_out=r2, y=h)
         logits = self.logits[:T]
         torch.mm(h.float(), w.router.t(), out=logits)   # the router: a few columns in 32 bits
-        y = self.moe(T)(self.index, h, logits, stream=stream)
+        y = self.moe(T)(self.index, h, logits)
         return y, r2

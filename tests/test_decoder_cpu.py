@@ -1,0 +1,87 @@
+"""The decoder layer without a GPU: what it calls, in which order and on which
+stream.  libpw's launches and torch's streams are recorded, not run."""
+from contextlib import contextmanager
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+pw = pytest.importorskip("any_precision_bit_pw_gb300.pw")
+from any_precision_bit_pw_gb300 import decoder  # noqa: E402
+from any_precision_bit_pw_gb300.decoder import DecoderLayer, DecoderWeights, Fp8Weight, PagedCache  # noqa: E402
+
+HEADS, KV, D, H, EXPERTS = 4, 2, 64, 256, 8
+LAUNCHES = ("pw_add_rmsnorm", "pw_quantize_fp8", "pw_fp8_linear", "pw_rope_append", "pw_paged_attention")
+
+
+class FakeMoE:
+    def __init__(self, stack, tokens, **kw):
+        self.T, self.status = tokens, torch.zeros(1, dtype=torch.int32)
+        self.y = torch.zeros(max(tokens, 1), H, dtype=torch.float16)
+        self.log = stack.log
+        self.log.append(("MoECall", stack.current()))
+
+    def __call__(self, layer, x, logits, stream=None, **kw):
+        self.log.append(("experts", self.log.stream if stream is None else stream))
+        return self.y[: self.T]
+
+
+class Log(list):
+    stream = None      # torch's current stream; None: the default one
+
+
+@pytest.fixture
+def log(monkeypatch):
+    log = Log()
+
+    def record(name):
+        def call(*args, stream=None, **kw):
+            log.append((name, log.stream if stream is None else stream))
+        return call
+    for name in LAUNCHES:
+        monkeypatch.setattr(pw, name, record(name))
+    monkeypatch.setattr(decoder, "MoECall", FakeMoE)
+
+    @contextmanager
+    def on(stream):
+        before, log.stream = log.stream, stream
+        yield
+        log.stream = before
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    mm = torch.mm
+
+    def product(*args, **kw):
+        log.append(("router", log.stream))
+        return mm(*args, **kw)
+    monkeypatch.setattr(torch, "mm", product)
+    return log
+
+
+def weight(n, k):
+    return Fp8Weight(torch.zeros(n, k, dtype=torch.float8_e4m3fn), torch.ones(-(-n // 128), -(-k // 128)))
+
+
+def layer(log, tokens=8, **kw):
+    stack = SimpleNamespace(device=torch.device("cpu"), H=H, routed=EXPERTS, log=log, current=lambda: log.stream)
+    w = DecoderWeights(torch.ones(H).half(), torch.ones(H).half(), weight((HEADS + 2 * KV) * D, H), weight(H, HEADS * D),
+                       torch.zeros(EXPERTS, H))
+    return DecoderLayer(stack, 0, w, HEADS, PagedCache(8, 16, KV, D, device="cpu"), tokens, **kw)
+
+
+ORDER = ["pw_add_rmsnorm", "pw_fp8_linear", "pw_rope_append", "pw_paged_attention", "pw_quantize_fp8", "pw_fp8_linear",
+         "pw_add_rmsnorm", "router", "experts"]
+
+
+@pytest.mark.parametrize("given,want", [(None, None), (0x5000, ("external", 0x5000)), (0, "default"), (1, "default")])
+def test_one_stream_for_the_whole_layer(log, given, want):
+    """The router's product is torch's: it has to follow the norm and precede
+    the experts on the stream that they run on."""
+    L = layer(log)
+    log.clear()
+    L(torch.zeros(3, H).half(), None, L.cache.batch([0, 1], [2, 1]), stream=given)
+    calls = [c for c in log if c[0] != "MoECall"]
+    assert [n for n, _ in calls] == ORDER
+    where = {s for _, s in calls}
+    assert where == {want}

@@ -1,0 +1,31 @@
+"""GPU: the decoder layer as a server uses it: on a stream of its own, with
+changing token counts, several layers in a row."""
+import pytest
+import torch
+
+from test_gpu_attn_half import _gpu, draw, gen  # noqa: F401
+from test_gpu_decoder import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_given_stream(raw):
+    """The whole layer runs on the stream that it is given, torch's part too:
+    that stream starts late, the current one has nothing to wait for."""
+    L, _ = build()
+    g, H = gen(31), L.stack.H
+    x, res = draw(g, 40, H), draw(g, 40, H)
+    out, r2 = L(x, res, L.cache.batch([0, 1], [33, 7]))
+    want, want_r = out.clone(), r2.clone()
+    other, other_res = draw(g, 40, H), draw(g, 40, H)
+    L(other, other_res, L.cache.batch([4, 5], [33, 7]))      # leaves the buffers with other values
+    batch = L.cache.batch([2, 3], [33, 7])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    out, r2 = L(x, res, batch, stream=side.cuda_stream if raw else side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(r2, want_r) and torch.equal(out, want)
+    assert int(L.status.item()) == 0 and int(L.moe(40).status.item()) == 0
