@@ -101,9 +101,10 @@ class Fp8Weight:
     def quantize(w: torch.Tensor, stream=None) -> "Fp8Weight":
         n, k = w.shape
         pad = -k % 16                              # rows of the product are 16-byte aligned
-        codes = torch.empty((n, k + pad), dtype=torch.float8_e4m3fn, device=w.device)[:, :k]
-        scale = torch.empty((-(-n // 128), -(-k // 128)), dtype=torch.float32, device=w.device)
-        pw.pw_quantize_fp8(w, codes, scale, block_rows=128, stream=stream)
+        with _on(stream):   # memory that another stream has just freed may still be in use there
+            codes = torch.empty((n, k + pad), dtype=torch.float8_e4m3fn, device=w.device)[:, :k]
+            scale = torch.empty((-(-n // 128), -(-k // 128)), dtype=torch.float32, device=w.device)
+            pw.pw_quantize_fp8(w, codes, scale, block_rows=128)
         return Fp8Weight(codes, scale)
 
 

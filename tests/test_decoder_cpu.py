@@ -85,3 +85,17 @@ def test_one_stream_for_the_whole_layer(log, given, want):
     assert [n for n, _ in calls] == ORDER
     where = {s for _, s in calls}
     assert where == {want}
+
+
+def test_a_weight_is_allocated_on_its_stream(log, monkeypatch):
+    """What one stream has freed another may not write: the codes come from the
+    memory of the stream that fills them."""
+    empty = torch.empty
+
+    def allocate(*args, **kw):
+        log.append(("empty", log.stream))
+        return empty(*args, **kw)
+    monkeypatch.setattr(torch, "empty", allocate)
+    w = Fp8Weight.quantize(torch.zeros(130, 200).half(), stream=0x5000)
+    assert w.codes.shape == (130, 200) and w.scale.shape == (2, 2) and w.codes.stride(0) % 16 == 0
+    assert log == [(n, ("external", 0x5000)) for n in ("empty", "empty", "pw_quantize_fp8")]
