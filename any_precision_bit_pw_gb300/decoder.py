@@ -7,9 +7,11 @@ expert layer of ``layer.py``, one stream, buffers allocated once.
     batch = cache.batch([3, 7], [1, 1])      # one new token of sequences 3 and 7
     x, residual = layer(x, residual, batch)  # both fp16 [T][H]
 
-Every computation but the router's small product is a libpw kernel (``pw.py``);
-nothing is allocated or synchronised in a call, so a step can be captured in a
-CUDA graph once the batch's tensors are in place.
+Every computation but the router's small product (a widening copy and cuBLAS) is
+a libpw kernel (``pw.py``); the layer allocates and synchronises nothing in a
+call, so a step can be captured in a CUDA graph once the batch's tensors are in
+place.  ``layer.status`` holds the first failure of any of its kernels, the
+experts' included; ``layer.experts.mass`` the experts' routing mass.
 """
 from __future__ import annotations
 
@@ -142,18 +144,22 @@ class DecoderLayer:
         self.attn8_scale = empty(tokens, -(-heads * D // 128), dtype=torch.float32)
         self.o, self.h = empty(tokens, H), empty(tokens, H)
         self.residual = [empty(tokens, H), empty(tokens, H)]
-        self.logits = empty(tokens, stack.routed, dtype=torch.float32)
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.h32, self.logits = empty(tokens, H, dtype=torch.float32), empty(tokens, stack.routed, dtype=torch.float32)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)   # of every call, the experts' too
         n = pw.pw_paged_attention_workspace(tokens, max_batch, heads, self.kv_heads, D)
         self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
-        self.calls: Dict[int, MoECall] = {}
+        # the experts' workspace grows with the tokens: one, for the most, serves every count
+        self.experts = MoECall(stack, tokens)
+        self.experts.status = self.status
+        if dev.type == "cuda":   # the layer may be called on any stream: its buffers are free and zeroed by then
+            torch.cuda.current_stream(dev).synchronize()
         assert tuple(weights.qkv.codes.shape) == (wide, H) and tuple(weights.out.codes.shape) == (H, heads * D)
 
     def moe(self, tokens: int) -> MoECall:
-        """The expert layer's buffers for a token count (kept)."""
-        if tokens not in self.calls:
-            self.calls[tokens] = MoECall(self.stack, tokens)
-        return self.calls[tokens]
+        """The expert layer's buffers; a call of ``tokens`` tokens uses their first rows."""
+        if tokens > self.tokens:
+            raise ValueError(f"decoder layer: {tokens} tokens, at most {self.tokens}")
+        return self.experts
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor], batch: Batch, stream=None):
         """x fp16 [T][H] (the previous layer's output) and the residual before
@@ -184,6 +190,6 @@ class DecoderLayer:
         h = self.h[:T]
         pw.pw_add_rmsnorm(self.o[:T], w.ffn_norm, self.eps, residual=r1, residual_out=r2, y=h)
         logits = self.logits[:T]
-        torch.mm(h.float(), w.router.t(), out=logits)   # the router: a few columns in 32 bits
-        y = self.moe(T)(self.index, h, logits)
+        torch.mm(self.h32[:T].copy_(h), w.router.t(), out=logits)   # the router: a few columns in 32 bits
+        y = self.moe(T)(self.index, h, logits)[:T]
         return y, r2

@@ -87,6 +87,25 @@ def test_one_stream_for_the_whole_layer(log, given, want):
     assert where == {want}
 
 
+def test_one_expert_workspace_for_every_token_count(log, monkeypatch):
+    """Ragged chunks: the buffers are the constructor's, whatever the counts,
+    and one status word takes the experts' failures too."""
+    L = layer(log)
+    assert [n for n, _ in log] == ["MoECall"] and L.experts.T == 8 and L.experts.status is L.status
+    batches = [L.cache.batch([i], [n]) for i, n in enumerate((5, 8, 1, 3))]
+
+    def allocate(*args, **kw):
+        raise AssertionError("an allocation in a call")
+    for name in ("empty", "zeros", "empty_like", "zeros_like"):
+        monkeypatch.setattr(torch, name, allocate)
+    monkeypatch.setattr(torch.Tensor, "float", allocate)
+    x = torch.ones(8, H).half()
+    for b in batches:
+        y, r = L(x[: b.tokens], None, b)
+        assert y.shape == r.shape == (b.tokens, H) and y.data_ptr() == L.experts.y.data_ptr()
+    assert [n for n, _ in log].count("MoECall") == 1
+
+
 def test_a_weight_is_allocated_on_its_stream(log, monkeypatch):
     """What one stream has freed another may not write: the codes come from the
     memory of the stream that fills them."""

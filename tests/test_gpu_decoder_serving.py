@@ -29,3 +29,22 @@ def test_given_stream(raw):
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(r2, want_r) and torch.equal(out, want)
     assert int(L.status.item()) == 0 and int(L.moe(40).status.item()) == 0
+
+
+def test_ragged_chunks_take_no_more_memory():
+    """Many token counts, one set of buffers; a count's result is that of a
+    layer made for it."""
+    L, _ = build(tokens=96)
+    g, H = gen(32), L.stack.H
+    x = draw(g, 96, H)
+    batches = [L.cache.batch([i], [n]) for i, n in enumerate((96, 1, 17, 64, 5))]
+    L(x[:96], None, batches[0])
+    held = torch.cuda.memory_allocated()
+    for i, b in enumerate(batches[1:], 1):
+        out, r = L(x[: b.tokens], None, b)
+        assert out.shape == r.shape == (b.tokens, H) and torch.cuda.memory_allocated() == held
+        own, _ = build(tokens=b.tokens)
+        want, want_r = own(x[: b.tokens], None, own.cache.batch([i], [b.tokens]))
+        assert torch.equal(out, want) and torch.equal(r, want_r)
+        del own, want, want_r
+    assert int(L.status.item()) == 0 and L.moe(1).status is L.status
