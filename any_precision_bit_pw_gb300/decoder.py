@@ -50,7 +50,9 @@ class Batch:
 class PagedCache:
     """Key/value pages of one layer and, on the host, which sequence holds
     which.  Page states are plain Python; the device sees them through the
-    tables that ``batch`` builds."""
+    tables that ``batch`` builds.  A table names pages and nothing of a layer: with
+    one cache per layer, all of one shape, the first one's ``batch`` serves all
+    layers of a step and the other caches are storage only."""
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.float16, device="cuda"):
         shape = (pages, page_size, kv_heads, head_dim)
@@ -120,12 +122,20 @@ class DecoderWeights:
 
 
 class DecoderLayer:
-    """One layer's calls and buffers for up to ``tokens`` tokens."""
+    """One layer's calls, and buffers for up to ``tokens`` tokens.  Layers that
+    run one after another on one stream can use the buffers of the first of them
+    (``share``): each reads its inputs before it writes its results, so the
+    results of one may be the inputs of the next.  ``max_batch`` goes to the
+    attention's workspace query, whose answer holds for any number of sequences.
+    """
+
+    BUFFERS = ("x8", "x8_scale", "qkv", "q", "attn", "attn8", "attn8_scale", "o", "h", "residual", "h32", "logits", "status",
+               "ws", "experts")
 
     def __init__(self, stack: APLMoEStack, index: int, weights: DecoderWeights, heads: int, cache: PagedCache,
                  tokens: int, rotary_dim: Optional[int] = None, rope_base: float = 1e6,
                  rope_scaling: Optional[pw.pw_rope_scaling] = None, interleaved: bool = False, window: int = 0,
-                 eps: float = 1e-5, max_batch: int = 256):
+                 eps: float = 1e-5, max_batch: int = 256, share: Optional["DecoderLayer"] = None):
         dev, H = stack.device, stack.H
         self.stack, self.index, self.w, self.cache = stack, index, weights, cache
         self.heads, self.kv_heads, self.head_dim = heads, cache.k.shape[2], cache.k.shape[3]
@@ -133,6 +143,13 @@ class DecoderLayer:
         turns, self.rope_factor = pw.pw_rope_turns(self.head_dim if rotary_dim is None else rotary_dim, rope_base, rope_scaling)
         self.turns = turns.to(dev)
         D, wide = self.head_dim, (heads + 2 * self.kv_heads) * self.head_dim
+        assert tuple(weights.qkv.codes.shape) == (wide, H) and tuple(weights.out.codes.shape) == (H, heads * D)
+        if share is not None:
+            if (share.stack, share.heads, share.kv_heads, D, tokens) != (stack, heads, self.kv_heads, share.head_dim, share.tokens):
+                raise ValueError("decoder layer: buffers are shared between layers of one stack with equal heads and tokens")
+            for name in self.BUFFERS:
+                setattr(self, name, getattr(share, name))
+            return
 
         def empty(*shape, dtype=torch.float16):
             return torch.empty(shape, dtype=dtype, device=dev)
@@ -153,7 +170,6 @@ class DecoderLayer:
         self.experts.status = self.status
         if dev.type == "cuda":   # the layer may be called on any stream: its buffers are free and zeroed by then
             torch.cuda.current_stream(dev).synchronize()
-        assert tuple(weights.qkv.codes.shape) == (wide, H) and tuple(weights.out.codes.shape) == (H, heads * D)
 
     def moe(self, tokens: int) -> MoECall:
         """The expert layer's buffers; a call of ``tokens`` tokens uses their first rows."""
@@ -164,8 +180,8 @@ class DecoderLayer:
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor], batch: Batch, stream=None):
         """x fp16 [T][H] (the previous layer's output) and the residual before
         it (None at the first layer) -> this layer's (output, residual).  The
-        results are the layer's buffers, valid until its next call.  All of it
-        runs on ``stream`` (None: torch's current stream)."""
+        results are the layer's buffers, valid until the next call of a layer that
+        has them.  All of it runs on ``stream`` (None: torch's current stream)."""
         with _on(stream):
             return self._run(x, residual, batch)
 

@@ -106,6 +106,20 @@ def test_one_expert_workspace_for_every_token_count(log, monkeypatch):
     assert [n for n, _ in log].count("MoECall") == 1
 
 
+def test_layers_share_buffers(log):
+    first = layer(log)
+    stack, w = first.stack, first.w
+    log.clear()
+    second = DecoderLayer(stack, 1, w, HEADS, PagedCache(8, 16, KV, D, device="cpu"), 8, share=first)
+    assert not log and all(getattr(second, n) is getattr(first, n) for n in DecoderLayer.BUFFERS)
+    mine = {n for n, v in vars(first).items() if isinstance(v, (torch.Tensor, list, FakeMoE)) and n != "turns"}
+    assert mine == set(DecoderLayer.BUFFERS)          # no buffer is left out
+    for kw in (dict(tokens=4), dict(stack=SimpleNamespace(**vars(stack), name="another"))):
+        args = {**dict(stack=stack, tokens=8), **kw}
+        with pytest.raises(ValueError):
+            DecoderLayer(args["stack"], 1, w, HEADS, PagedCache(8, 16, KV, D, device="cpu"), args["tokens"], share=first)
+
+
 def test_a_weight_is_allocated_on_its_stream(log, monkeypatch):
     """What one stream has freed another may not write: the codes come from the
     memory of the stream that fills them."""

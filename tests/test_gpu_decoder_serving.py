@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from test_gpu_attn_half import _gpu, draw, gen  # noqa: F401
+from any_precision_bit_pw_gb300.decoder import DecoderLayer, PagedCache
 from test_gpu_decoder import build
 
 pytestmark = pytest.mark.gpu
@@ -39,8 +40,8 @@ def test_ragged_chunks_take_no_more_memory():
     x = draw(g, 96, H)
     batches = [L.cache.batch([i], [n]) for i, n in enumerate((96, 1, 17, 64, 5))]
     L(x[:96], None, batches[0])
-    held = torch.cuda.memory_allocated()
     for i, b in enumerate(batches[1:], 1):
+        held = torch.cuda.memory_allocated()
         out, r = L(x[: b.tokens], None, b)
         assert out.shape == r.shape == (b.tokens, H) and torch.cuda.memory_allocated() == held
         own, _ = build(tokens=b.tokens)
@@ -48,3 +49,28 @@ def test_ragged_chunks_take_no_more_memory():
         assert torch.equal(out, want) and torch.equal(r, want_r)
         del own, want, want_r
     assert int(L.status.item()) == 0 and L.moe(1).status is L.status
+
+
+def test_layers_share_buffers_and_tables():
+    """Three layers in a row, each with its own cache: with the first one's
+    buffers and batches, the results are those of layers with their own."""
+    g = gen(33)
+    stacks = [build(tokens=48)[0] for _ in range(2)]
+    x = draw(g, 48, stacks[0].stack.H)
+    results = []
+    for first, shared in zip(stacks, (False, True)):
+        def another():
+            c = PagedCache(64, 16, first.kv_heads, first.head_dim, device="cuda")
+            return DecoderLayer(first.stack, 0, first.w, first.heads, c, 48, share=first if shared else None)
+        layers = [first, another(), another()]
+        for n in (48, 5, 1):
+            batches = [L.cache.batch([1, 2], [n - n // 3, n // 3]) for L in (layers[:1] if shared else layers)] * (3 if shared else 1)
+            h, r = x[:n], None
+            for L, b in zip(layers, batches):
+                h, r = L(h, r, b)
+            results.append((h.clone(), r.clone()))
+        assert all(int(L.status.item()) == 0 for L in layers)
+    for (h, r), (h2, r2) in zip(results[:3], results[3:]):
+        assert torch.equal(h, h2) and torch.equal(r, r2)
+    with pytest.raises(ValueError):
+        DecoderLayer(first.stack, 0, first.w, first.heads, first.cache, 47, share=first)
