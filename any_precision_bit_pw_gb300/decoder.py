@@ -189,6 +189,8 @@ class DecoderLayer:
         T, w, c = batch.tokens, self.w, self.cache
         if x.shape[0] != T or T > self.tokens:
             raise ValueError(f"decoder layer: {x.shape[0]} rows for a batch of {T} tokens, at most {self.tokens}")
+        if T == 0:
+            return self.experts.y[:0], self.residual[1][:0]
         x8, x8s, qkv, q, attn = self.x8[:T], self.x8_scale[:T], self.qkv[:T], self.q[:T], self.attn[:T]
         hq, hk = self.heads, self.kv_heads
         r1, r2 = self.residual[0][:T], self.residual[1][:T]

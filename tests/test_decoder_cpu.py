@@ -120,6 +120,21 @@ def test_layers_share_buffers(log):
             DecoderLayer(args["stack"], 1, w, HEADS, PagedCache(8, 16, KV, D, device="cpu"), args["tokens"], share=first)
 
 
+@pytest.mark.parametrize("seqs", [[], [3], [3, 1]])
+def test_a_step_without_tokens(log, seqs):
+    """No sequences, or none with new tokens: empty results, no launch."""
+    L = layer(log)
+    L.cache.batch([3], [5])
+    log.clear()
+    batch = L.cache.batch(seqs, [0] * len(seqs))
+    assert batch.tokens == 0 and batch.q_offsets.tolist() == [0] * (len(seqs) + 1)
+    y, r = L(torch.zeros(0, H).half(), None, batch)
+    assert y.shape == r.shape == (0, H) and y.dtype == r.dtype == torch.float16
+    assert [n for n, _ in log if n != "MoECall"] == []
+    with pytest.raises(ValueError):
+        L(torch.zeros(1, H).half(), None, batch)
+
+
 def test_a_weight_is_allocated_on_its_stream(log, monkeypatch):
     """What one stream has freed another may not write: the codes come from the
     memory of the stream that fills them."""
