@@ -65,9 +65,9 @@ __device__ __forceinline__ void store8(T* row, int c, int cols, const float (&v)
   }
 }
 template <bool kAligned>
-__device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const float (&v)[kVec], float inv) {
-  const uint32_t lo = pw::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  const uint32_t hi = pw::e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+__device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const float (&v)[kVec], const pw::Divisor& by) {
+  const uint32_t lo = pw::e4m3x4(by(v[0]), by(v[1]), by(v[2]), by(v[3]));
+  const uint32_t hi = pw::e4m3x4(by(v[4]), by(v[5]), by(v[6]), by(v[7]));
   if (kAligned) {
     if (c < cols) *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
   } else {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024) row_kernel(const __g
         for (int o = 8; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
         if (col < p.cols && (tid & 15) == 0) p.scale[row * p.scale_stride + col / pw::kGroup] = s;
-        store8_e4m3<kAligned>(q, col, p.cols, v[c], 1.0f / s);
+        store8_e4m3<kAligned>(q, col, p.cols, v[c], pw::Divisor(s));
       }
     }
   }
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowP
   for (int i = 1; i < 8; ++i) top = pw::max_nan(top, tops[i]);
   const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
   if (tid == 0) p.scale[blockIdx.y * p.scale_stride + kb] = s;
-  const float inv = 1.0f / s;
+  const pw::Divisor by(s);
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
     const int64_t row = row0 + kStep * i;
@@ -224,14 +224,14 @@ __global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowP
       for (int h = 0; h < 2; ++h) {
         float v[kVec];
         unpack8<T>(x[i][h], v);
-        c[2 * h] = pw::e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        c[2 * h + 1] = pw::e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+        c[2 * h] = pw::e4m3x4(by(v[0]), by(v[1]), by(v[2]), by(v[3]));
+        c[2 * h + 1] = pw::e4m3x4(by(v[4]), by(v[5]), by(v[6]), by(v[7]));
       }
       if (col < p.cols) *reinterpret_cast<uint4*>(dst + col) = make_uint4(c[0], c[1], c[2], c[3]);
     } else {
       float v[kVec];
       unpack8<T>(x[i][0], v);
-      store8_e4m3<kAligned>(dst, col, p.cols, v, inv);
+      store8_e4m3<kAligned>(dst, col, p.cols, v, by);
     }
   }
 }

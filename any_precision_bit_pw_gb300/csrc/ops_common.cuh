@@ -67,6 +67,22 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
 
+// Division of many values by one scale: a product with the rounded reciprocal
+// is off by up to 1.5 units in the last place, enough to fall on the other side
+// of a tie of the 8-bit rounding (1 code in 2000 to 10000).  One correction with
+// the exact remainder q s - v (fused multiply-add; Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990) leaves
+// 2^-46 before its own rounding: the 32-bit quotient.  The signs are chosen so
+// that zeros keep theirs.  An infinite scale divides finite values to 0.
+struct Divisor {
+  float s, inv;
+  __device__ __forceinline__ explicit Divisor(float scale) : s(isfinite(scale) ? scale : 0.0f), inv(1.0f / scale) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * inv;
+    return fmaf(fmaf(q, s, -v), -inv, q);
+  }
+};
+
 // A maximum that keeps NaN (fmaxf drops it): a group that holds one gets the
 // scale NaN, so its values come back as NaN rather than as numbers.
 __device__ __forceinline__ float max_nan(float a, float b) {

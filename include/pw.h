@@ -468,7 +468,7 @@ int pw_add_rmsnorm(const pw_norm_args* args, void* stream);
 
 /* 16-bit values x [rows][cols] to e4m3 codes q and fp32 scales:
  *   scale = max(largest magnitude of the group / 448, 2^-100)
- *   code  = e4m3(value / scale)
+ *   code  = e4m3(value / scale), the quotient in fp32
  * The groups are 128 columns (the last one may be narrower) of one row
  * (block_rows 1: activations, cols <= 32768) or of 128 rows (block_rows 128:
  * weights).  scale: [ceil(rows/block_rows)][ceil(cols/128)].  A group that
