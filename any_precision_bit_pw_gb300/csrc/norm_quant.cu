@@ -81,9 +81,11 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const
 // chunks in registers, so a row is read once, and loads the next row before the
 // reduction of this one, so that copies are always under way.  16 neighbouring
 // threads hold a group of 128 columns: a group's largest value is four
-// shuffles away.
+// shuffles away.  (Conversion alone of 32 values a thread: two CTAs an SM, which
+// takes 64 registers a thread; left to itself the compiler took 120, and 4096 x
+// 9001 83 us instead of 45.)
 template <typename T, int kChunks, bool kAligned, bool kNorm>
-__global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024) row_kernel(const __grid_constant__ RowParams p) {
+__global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024, kChunks == 4 && !kNorm ? 2 : 1) row_kernel(const __grid_constant__ RowParams p) {
   __shared__ float sums[2][32];
   const int tid = threadIdx.x, nthr = blockDim.x;
   uint4 w[kChunks], x[kChunks], res[kChunks];
