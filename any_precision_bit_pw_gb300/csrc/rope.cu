@@ -204,12 +204,16 @@ __global__ void __launch_bounds__(kThreads, kVec == 16 ? 6 : 5) rope_kernel(cons
       pw::report_status(a.status, PW_ERR_INVALID_ARG);
     } else if (a.k) {
       const int index = slot >= 0 ? slot / a.page_size : -1, in_page = slot - index * a.page_size;
-      const int page = index >= 0 && index < a.pages_per_seq ? a.page_table[seq * a.page_table_stride + index] : -1;
-      if (page < 0 || page >= a.num_pages) {
-        pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+      if (index < 0 || index >= a.pages_per_seq) {   // a length that the table cannot hold, or below the new tokens
+        pw::report_status(a.status, PW_ERR_INVALID_ARG);
       } else {
-        k_off = page * a.k_cache_stride_page + in_page * a.k_cache_stride_token;
-        v_off = page * a.v_cache_stride_page + in_page * a.v_cache_stride_token;
+        const int page = a.page_table[seq * a.page_table_stride + index];
+        if (page < 0 || page >= a.num_pages) {
+          pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
+        } else {
+          k_off = page * a.k_cache_stride_page + in_page * a.k_cache_stride_token;
+          v_off = page * a.v_cache_stride_page + in_page * a.v_cache_stride_token;
+        }
       }
     }
     k_at[tid] = k_off;

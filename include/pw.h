@@ -552,7 +552,13 @@ int pw_rope_turns(int rotary_dim, double base, const pw_rope_scaling* scaling, i
  *  The first rotary_dim values of a head turn by pairs: (2i, 2i+1) when
  *  interleaved, (i, i + rotary_dim/2) otherwise; the others are copied.
  *  turns: DEVICE array of pw_rope_turns; positions: int32 [tokens] or NULL
- *  (the position in the cache). */
+ *  (the position in the cache).
+ * A token that has no place is not stored and sets status: PW_ERR_INVALID_ARG
+ * for one that belongs to no sequence, or whose position in the cache is
+ * negative (kv_lens below the new tokens) or past its table;
+ * PW_ERR_NOT_RESIDENT for a page id outside 0 .. num_pages-1.  Its query is
+ * rotated all the same where the token has a sequence; a negative position, which
+ * queries alone may have, turns the other way. */
 typedef struct pw_rope_args {
   const void* q;
   void* q_out;
