@@ -414,6 +414,9 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
                          ws_bytes);
   Params p{};
   p.a = a;
+  // no sequence is longer than its table; a bound of 2^31 - 1 ("any") would wrap where it is rounded up to blocks
+  const int holds = a.page_size * a.pages_per_seq;
+  if (p.a.max_kv_len > holds) p.a.max_kv_len = holds;
   p.group = a.heads / a.kv_heads;
   // n * group_inv / 2^32 is exact while n times the excess of group_inv stays below 2^32 / group
   p.group_inv = static_cast<uint32_t>(((1ull << 32) + p.group - 1) / p.group);
