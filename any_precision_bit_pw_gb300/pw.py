@@ -649,7 +649,7 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     lp = 0
     if lse is not None:
         lp, ls = _matrix(lse, T, heads, _F32, "lse")
-        if ls != heads:
+        if ls != heads and T > 1:   # the stride of a single row says nothing
             raise ValueError("lse: need a contiguous tensor")
     if not ws.is_cuda:
         raise ValueError("ws: need a CUDA tensor")

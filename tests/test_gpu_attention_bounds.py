@@ -38,3 +38,19 @@ def call(b, ws, bound):
     pw.pw_paged_attention(b.q, b.k, b.v, b.table, b.offsets, b.lens, out, ws, st, scale=b.d ** -0.5, lse=lse,
                           max_q_len=b.T, max_kv_len=bound)
     return out, lse, st
+
+
+def test_one_row_of_a_wider_lse():
+    """A single token's log-sums may be a row of anything; several tokens' rows
+    have to follow each other."""
+    b = Batch([1], [30], 4, 2, 64, 16, torch.float16, 3)
+    ws = torch.zeros(pw.pw_paged_attention_workspace(1, 1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    _, want, _ = call(b, ws, 30)
+    wide = torch.full((5, 9), 7.0, device="cuda")
+    out, st = torch.empty_like(b.q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pw.pw_paged_attention(b.q, b.k, b.v, b.table, b.offsets, b.lens, out, ws, st, scale=0.125, lse=wide[2:3, 3:7])
+    assert torch.equal(wide[2:3, 3:7], want) and int((wide == 7).sum()) == 41 and int(st.item()) == 0
+    two = Batch([2], [30], 4, 2, 64, 16, torch.float16, 3)
+    with pytest.raises(ValueError):
+        pw.pw_paged_attention(two.q, two.k, two.v, two.table, two.offsets, two.lens, torch.empty_like(two.q), ws, st,
+                              scale=0.125, lse=wide[2:4, 3:7])
