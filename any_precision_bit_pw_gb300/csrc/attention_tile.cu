@@ -231,10 +231,9 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
         pw::tc_mma_ts(tmem + 2 * kBlock + h * D, tmem + h * kBlock + 8 * i, v + i * (2048 >> 4), kValues,
                       !first || part > 0 || j > 0);
       }
+      // o_done last: the CTA leaves after it, and no arrival may find it gone
+      if (part && free_after) pw::tc_commit(bar(sh.v_empty[vals.at]));
       pw::tc_commit(bar(part ? sh.o_done[h] : sh.o_half[h]));
-      if (part) {
-        if (free_after) pw::tc_commit(bar(sh.v_empty[vals.at]));
-      }
     }
     __syncwarp();
   };
