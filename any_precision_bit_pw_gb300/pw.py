@@ -461,30 +461,38 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
 
 
 def _refuse(t: torch.Tensor, shape, dtypes, name: str, rows: str):
-    raise ValueError(f"{name}: need a CUDA tensor {tuple(shape)} of {dtypes[0]} with {rows}, got {tuple(t.shape)} of "
-                     f"{t.dtype} with strides {t.stride()} on {t.device}")
+    raise ValueError(f"{name}: need a tensor {tuple(shape)} of {dtypes[0]} with {rows}, on the GPU of the call's first one, "
+                     f"got {tuple(t.shape)} of {t.dtype} with strides {t.stride()} on {t.device}")
 
 
-def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, dtypes, name: str):
+def _launch(f, dev: int, stream, *args) -> None:
+    """One of the calls below, whose tensors are on GPU `dev`; the kernel runs on
+    the current one."""
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"{f.__name__}: tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    _check(f(*args, _stream(stream)))
+
+
+def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, dtypes, name: str, dev: int):
     """(pointer, row stride) of a CUDA matrix whose rows are contiguous; (0, 0)
     for None."""
     if t is None:
         return 0, 0
     st = t.stride()
-    if t.dtype not in dtypes or not t.is_cuda or t.shape != (rows, cols) or (st[1] != 1 and cols > 1):
+    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != (rows, cols) or (st[1] != 1 and cols > 1):
         _refuse(t, (rows, cols), dtypes, name, "contiguous rows")
     # the stride of a single row says nothing
     return t.data_ptr(), st[0] if rows > 1 or st[0] > cols else cols
 
 
-def _vector(t: torch.Tensor, n: int, dtypes, name: str) -> int:
-    if t.dtype not in dtypes or not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+def _vector(t: torch.Tensor, n: int, dtypes, name: str, dev: int) -> int:
+    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         _refuse(t, (n,), dtypes, name, "contiguous values")
     return t.data_ptr()
 
 
-def _status(t: torch.Tensor) -> int:
-    if t.dtype is not torch.int32 or not t.is_cuda or t.numel() < 1:
+def _status(t: torch.Tensor, dev: int) -> int:
+    if t.dtype is not torch.int32 or t.get_device() != dev or dev < 0 or t.numel() < 1:
         _refuse(t, (1,), _I32, "status", "one value")
     return t.data_ptr()
 
@@ -506,54 +514,54 @@ def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: 
     """y = r * rsqrt(mean(r^2) + eps) * weight with r = x + residual; `y` in
     x's type and/or `q` (e4m3) with `scale` (fp32, a scale per 128 columns);
     `residual_out` receives r."""
-    dt = _dtype16(x, "x")
+    dt, dev = _dtype16(x, "x"), x.get_device()
     rows, cols = x.shape
     same = (x.dtype,)
-    xp, xs = _matrix(x, rows, cols, same, "x")
-    wp = _vector(weight, cols, same, "weight")
-    rp, rs = _matrix(residual, rows, cols, same, "residual")
-    rop, ros = _matrix(residual_out, rows, cols, same, "residual_out")
-    yp, ys = _matrix(y, rows, cols, same, "y")
-    qp, qs = _matrix(q, rows, cols, _CODES, "q")
-    sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale")
+    xp, xs = _matrix(x, rows, cols, same, "x", dev)
+    wp = _vector(weight, cols, same, "weight", dev)
+    rp, rs = _matrix(residual, rows, cols, same, "residual", dev)
+    rop, ros = _matrix(residual_out, rows, cols, same, "residual_out", dev)
+    yp, ys = _matrix(y, rows, cols, same, "y", dev)
+    qp, qs = _matrix(q, rows, cols, _CODES, "q", dev)
+    sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale", dev)
     args = _NORM_ARGS.pack(xp, rp, wp, rop, yp, qp, sp, xs, rs, ros, ys, qs, ss, rows, cols, dt, eps, 0)
-    _check(lib().pw_add_rmsnorm(args, _stream(stream)))
+    _launch(lib().pw_add_rmsnorm, dev, stream, args)
 
 
 def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
     """x (fp16 or bf16 matrix) to e4m3 codes `q` and fp32 `scale`: groups of
     128 columns of one row (block_rows 1) or of 128 rows (block_rows 128)."""
-    dt = _dtype16(x, "x")
+    dt, dev = _dtype16(x, "x"), x.get_device()
     rows, cols = x.shape
     if block_rows < 1:
         raise ValueError(f"block_rows: {block_rows}")
-    xp, xs = _matrix(x, rows, cols, (x.dtype,), "x")
-    qp, qs = _matrix(q, rows, cols, _CODES, "q")
-    sp, ss = _matrix(scale, -(-rows // block_rows), -(-cols // 128), _F32, "scale")
+    xp, xs = _matrix(x, rows, cols, (x.dtype,), "x", dev)
+    qp, qs = _matrix(q, rows, cols, _CODES, "q", dev)
+    sp, ss = _matrix(scale, -(-rows // block_rows), -(-cols // 128), _F32, "scale", dev)
     args = _QUANT_ARGS.pack(xp, qp, sp, xs, qs, ss, rows, cols, dt, block_rows, 0)
-    _check(lib().pw_quantize_fp8(args, _stream(stream)))
+    _launch(lib().pw_quantize_fp8, dev, stream, args)
 
 
 def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, y: torch.Tensor,
                   status: torch.Tensor, stream=None) -> None:
     """y [M][N] = a [M][K] b [N][K]^T of e4m3 codes with their scales:
     a_scale [M][ceil(K/128)], b_scale [ceil(N/128)][ceil(K/128)]."""
-    dt = _dtype16(y, "y")
+    dt, dev = _dtype16(y, "y"), y.get_device()
     M, K = a.shape
     N = b.shape[0]
     kb = -(-K // 128)
-    ap, lda = _matrix(a, M, K, _CODES, "a")
-    bp, ldb = _matrix(b, N, K, _CODES, "b")
-    yp, ldy = _matrix(y, M, N, (y.dtype,), "y")
-    sap, sa = _matrix(a_scale, M, kb, _F32, "a_scale")
-    sbp, sb = _matrix(b_scale, -(-N // 128), kb, _F32, "b_scale")
+    ap, lda = _matrix(a, M, K, _CODES, "a", dev)
+    bp, ldb = _matrix(b, N, K, _CODES, "b", dev)
+    yp, ldy = _matrix(y, M, N, (y.dtype,), "y", dev)
+    sap, sa = _matrix(a_scale, M, kb, _F32, "a_scale", dev)
+    sbp, sb = _matrix(b_scale, -(-N // 128), kb, _F32, "b_scale", dev)
     # a single row may have any stride: the row's own alignment is what counts
     if M == 1:
         lda = (lda + 15) // 16 * 16
     if N == 1:
         ldb = (ldb + 15) // 16 * 16
-    args = _LINEAR_ARGS.pack(ap, sap, bp, sbp, yp, _status(status), lda, sa, ldb, sb, ldy, M, N, K, dt)
-    _check(lib().pw_fp8_linear(args, _stream(stream)))
+    args = _LINEAR_ARGS.pack(ap, sap, bp, sbp, yp, _status(status, dev), lda, sa, ldb, sb, ldy, M, N, K, dt)
+    _launch(lib().pw_fp8_linear, dev, stream, args)
 
 
 def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_rope_scaling] = None):
@@ -565,18 +573,18 @@ def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_r
     return turns, float(factor.value)
 
 
-def _heads(t: torch.Tensor, shape, dtypes, name: str):
+def _heads(t: torch.Tensor, shape, dtypes, name: str, dev: int):
     """(pointer, outer strides) of a CUDA tensor whose last dimension is contiguous."""
     st = t.stride()
-    if t.dtype not in dtypes or not t.is_cuda or t.shape != shape or (st[-1] != 1 and shape[-1] > 1):
+    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != shape or (st[-1] != 1 and shape[-1] > 1):
         _refuse(t, shape, dtypes, name, "a contiguous last dimension")
     return t.data_ptr(), st
 
 
-def _sequences(q_offsets: torch.Tensor, kv_lens: torch.Tensor):
+def _sequences(q_offsets: torch.Tensor, kv_lens: torch.Tensor, dev: int):
     """(q_offsets, kv_lens, batch)"""
     batch = kv_lens.shape[0]
-    return _vector(q_offsets, batch + 1, _I32, "q_offsets"), _vector(kv_lens, batch, _I32, "kv_lens"), batch
+    return (_vector(q_offsets, batch + 1, _I32, "q_offsets", dev), _vector(kv_lens, batch, _I32, "kv_lens", dev), batch)
 
 
 def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -590,9 +598,9 @@ def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
     x = q if q is not None else k
     if x is None:
         raise ValueError("rope_append: neither q nor k")
-    dt, same = _dtype16(x, "q"), (x.dtype,)
+    dt, dev, same = _dtype16(x, "q"), x.get_device(), (x.dtype,)
     T, _, D = x.shape
-    offsets, lens, batch = _sequences(q_offsets, kv_lens)
+    offsets, lens, batch = _sequences(q_offsets, kv_lens, dev)
     qp = qop = kp = vp = kcp = vcp = table = pos = 0
     qs = qos = ks = vs = kcs = vcs = (0, 0, 0)
     heads = kv_heads = ts = pages = page_size = width = 0
@@ -600,28 +608,28 @@ def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
         if q_out is None:
             raise ValueError("rope_append: q needs q_out")
         heads = q.shape[1]
-        qp, qs = _heads(q, (T, heads, D), same, "q")
-        qop, qos = _heads(q_out, (T, heads, D), same, "q_out")
+        qp, qs = _heads(q, (T, heads, D), same, "q", dev)
+        qop, qos = _heads(q_out, (T, heads, D), same, "q_out", dev)
     if k is not None:
         if v is None or k_cache is None or v_cache is None or page_table is None:
             raise ValueError("rope_append: k, v, the caches and the page table come together")
         kv_heads, (pages, page_size) = k.shape[1], k_cache.shape[:2]
-        kp, ks = _heads(k, (T, kv_heads, D), same, "k")
-        vp, vs = _heads(v, (T, kv_heads, D), same, "v")
-        kcp, kcs = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache")
-        vcp, vcs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache")
+        kp, ks = _heads(k, (T, kv_heads, D), same, "k", dev)
+        vp, vs = _heads(v, (T, kv_heads, D), same, "v", dev)
+        kcp, kcs = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache", dev)
+        vcp, vcs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache", dev)
         width = page_table.shape[1]
-        table, ts = _matrix(page_table, batch, width, _I32, "page_table")
+        table, ts = _matrix(page_table, batch, width, _I32, "page_table", dev)
     elif v is not None or k_cache is not None or v_cache is not None:
         raise ValueError("rope_append: k, v, the caches and the page table come together")
     half = turns.shape[0]
-    tp = _vector(turns, half, (torch.int64,), "turns")
+    tp = _vector(turns, half, (torch.int64,), "turns", dev)
     if positions is not None:
-        pos = _vector(positions, T, _I32, "positions")
-    args = _ROPE_ARGS.pack(qp, qop, kp, vp, kcp, vcp, tp, pos, table, offsets, lens, _status(status), qs[0], qs[1],
+        pos = _vector(positions, T, _I32, "positions", dev)
+    args = _ROPE_ARGS.pack(qp, qop, kp, vp, kcp, vcp, tp, pos, table, offsets, lens, _status(status, dev), qs[0], qs[1],
                            qos[0], qos[1], ks[0], ks[1], vs[0], vs[1], kcs[0], kcs[1], kcs[2], vcs[0], vcs[1], vcs[2],
                            ts, T, batch, heads, kv_heads, D, 2 * half, page_size, pages, width, dt, interleaved, factor)
-    _check(lib().pw_rope_append(args, _stream(stream)))
+    _launch(lib().pw_rope_append, dev, stream, args)
 
 
 def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -636,24 +644,24 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     keys in the paged cache [pages][page_size][kv_heads][D].  `ws` must be
     zeroed before its first use.  max_q_len / max_kv_len: bounds of the lengths
     (0: the batch's tokens, and what the page table holds)."""
-    dt, same = _dtype16(q, "q"), (q.dtype,)
+    dt, dev, same = _dtype16(q, "q"), q.get_device(), (q.dtype,)
     T, heads, D = q.shape
     pages, page_size, kv_heads, _ = k_cache.shape
-    offsets, lens, batch = _sequences(q_offsets, kv_lens)
-    qp, qs = _heads(q, (T, heads, D), same, "q")
-    op, os_ = _heads(out, (T, heads, D), same, "out")
-    kp, ks = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache")
-    vp, vs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache")
+    offsets, lens, batch = _sequences(q_offsets, kv_lens, dev)
+    qp, qs = _heads(q, (T, heads, D), same, "q", dev)
+    op, os_ = _heads(out, (T, heads, D), same, "out", dev)
+    kp, ks = _heads(k_cache, (pages, page_size, kv_heads, D), same, "k_cache", dev)
+    vp, vs = _heads(v_cache, (pages, page_size, kv_heads, D), same, "v_cache", dev)
     width = page_table.shape[1]
-    table, ts = _matrix(page_table, batch, width, _I32, "page_table")
+    table, ts = _matrix(page_table, batch, width, _I32, "page_table", dev)
     lp = 0
     if lse is not None:
-        lp, ls = _matrix(lse, T, heads, _F32, "lse")
+        lp, ls = _matrix(lse, T, heads, _F32, "lse", dev)
         if ls != heads and T > 1:   # the stride of a single row says nothing
             raise ValueError("lse: need a contiguous tensor")
-    if not ws.is_cuda:
-        raise ValueError("ws: need a CUDA tensor")
-    args = _ATTN_ARGS.pack(qp, op, lp, kp, vp, table, offsets, lens, _status(status), qs[0], qs[1], os_[0], os_[1],
+    if ws.get_device() != dev:
+        raise ValueError("ws: need a tensor on q's GPU")
+    args = _ATTN_ARGS.pack(qp, op, lp, kp, vp, table, offsets, lens, _status(status, dev), qs[0], qs[1], os_[0], os_[1],
                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts, T, batch, heads, kv_heads, D, page_size, pages,
                            width, max_q_len or T, max_kv_len or page_size * width, dt, causal, window, scale)
-    _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _stream(stream)))
+    _launch(lib().pw_paged_attention, dev, stream, args, ws.data_ptr(), ws.nbytes)
