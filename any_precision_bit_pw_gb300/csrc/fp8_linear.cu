@@ -439,10 +439,13 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
         }
         break;   // one tile per cluster
       }
-      if (p.wide_y) {
-        // 16-bit rows through shared memory, 32 rows x 64 columns at a time
+      // 16-bit rows through shared memory, 32 rows x 64 columns at a time.  A
+      // tiled store drops what lies past the matrix in whole units of 16 bytes
+      // only: where N ends inside one, the last box goes value by value.
 #pragma unroll
-        for (int box = 0; box < C::kCols / 64; ++box) {
+      for (int box = 0; box < C::kCols / 64; ++box) {
+        const int n = n0 + 64 * box;
+        if (p.wide_y && (p.N % 8 == 0 || n + 64 <= p.N)) {
           pw::bulk_wait_read();   // the box before has left
           __syncwarp();
 #pragma unroll
@@ -458,19 +461,19 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide>::kThreads, 1)
           }
           pw::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && m0 < p.M && n0 + 64 * box < p.N) {
-            pw::tma_store_2d(&map_y, n0 + 64 * box, m0, pw::smem_u32(out));
+          if (lane == 0 && m0 < p.M && n < p.N) {
+            pw::tma_store_2d(&map_y, n, m0, pw::smem_u32(out));
             pw::bulk_commit();
           }
-        }
-      } else if (m < p.M) {
-        T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
+        } else if (m < p.M) {
+          T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n;
 #pragma unroll
-        for (int i = 0; i < C::kCols / 2; ++i) {
-          float lo, hi;
-          pw::unpack_f32x2(sum[i], lo, hi);
-          if (n0 + 2 * i < p.N) y[2 * i] = pw::from_float<T>(lo);
-          if (n0 + 2 * i + 1 < p.N) y[2 * i + 1] = pw::from_float<T>(hi);
+          for (int i = 0; i < 32; ++i) {
+            float lo, hi;
+            pw::unpack_f32x2(sum[32 * box + i], lo, hi);
+            if (n + 2 * i < p.N) y[2 * i] = pw::from_float<T>(lo);
+            if (n + 2 * i + 1 < p.N) y[2 * i + 1] = pw::from_float<T>(hi);
+          }
         }
       }
     }
