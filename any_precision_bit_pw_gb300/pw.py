@@ -465,12 +465,13 @@ def _refuse(t: torch.Tensor, shape, dtypes, name: str, rows: str):
                      f"got {tuple(t.shape)} of {t.dtype} with strides {t.stride()} on {t.device}")
 
 
-def _launch(f, dev: int, stream, *args) -> None:
-    """One of the calls below, whose tensors are on GPU `dev`; the kernel runs on
-    the current one."""
-    if torch._C._cuda_getDevice() != dev:
-        raise ValueError(f"{f.__name__}: tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
-    _check(f(*args, _stream(stream)))
+def _queue(stream, dev: int) -> int:
+    """The stream of a call whose tensors are on GPU `dev`: its kernel runs on the
+    current GPU, which has to be that one."""
+    if dev < 0 or torch._C._cuda_getDevice() != dev:
+        raise ValueError("need tensors on a GPU" if dev < 0 else
+                         f"tensors on cuda:{dev}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, dtypes, name: str, dev: int):
@@ -479,20 +480,20 @@ def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, dtypes, name: str, 
     if t is None:
         return 0, 0
     st = t.stride()
-    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != (rows, cols) or (st[1] != 1 and cols > 1):
+    if t.dtype not in dtypes or t.get_device() != dev or t.shape != (rows, cols) or (st[1] != 1 and cols > 1):
         _refuse(t, (rows, cols), dtypes, name, "contiguous rows")
     # the stride of a single row says nothing
     return t.data_ptr(), st[0] if rows > 1 or st[0] > cols else cols
 
 
 def _vector(t: torch.Tensor, n: int, dtypes, name: str, dev: int) -> int:
-    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+    if t.dtype not in dtypes or t.get_device() != dev or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         _refuse(t, (n,), dtypes, name, "contiguous values")
     return t.data_ptr()
 
 
 def _status(t: torch.Tensor, dev: int) -> int:
-    if t.dtype is not torch.int32 or t.get_device() != dev or dev < 0 or t.numel() < 1:
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.numel() < 1:
         _refuse(t, (1,), _I32, "status", "one value")
     return t.data_ptr()
 
@@ -525,7 +526,7 @@ def pw_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: 
     qp, qs = _matrix(q, rows, cols, _CODES, "q", dev)
     sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale", dev)
     args = _NORM_ARGS.pack(xp, rp, wp, rop, yp, qp, sp, xs, rs, ros, ys, qs, ss, rows, cols, dt, eps, 0)
-    _launch(lib().pw_add_rmsnorm, dev, stream, args)
+    _check(lib().pw_add_rmsnorm(args, _queue(stream, dev)))
 
 
 def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block_rows: int = 1, stream=None) -> None:
@@ -539,7 +540,7 @@ def pw_quantize_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, block
     qp, qs = _matrix(q, rows, cols, _CODES, "q", dev)
     sp, ss = _matrix(scale, -(-rows // block_rows), -(-cols // 128), _F32, "scale", dev)
     args = _QUANT_ARGS.pack(xp, qp, sp, xs, qs, ss, rows, cols, dt, block_rows, 0)
-    _launch(lib().pw_quantize_fp8, dev, stream, args)
+    _check(lib().pw_quantize_fp8(args, _queue(stream, dev)))
 
 
 def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, y: torch.Tensor,
@@ -561,7 +562,7 @@ def pw_fp8_linear(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
     if N == 1:
         ldb = (ldb + 15) // 16 * 16
     args = _LINEAR_ARGS.pack(ap, sap, bp, sbp, yp, _status(status, dev), lda, sa, ldb, sb, ldy, M, N, K, dt)
-    _launch(lib().pw_fp8_linear, dev, stream, args)
+    _check(lib().pw_fp8_linear(args, _queue(stream, dev)))
 
 
 def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_rope_scaling] = None):
@@ -576,7 +577,7 @@ def pw_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: Optional[pw_r
 def _heads(t: torch.Tensor, shape, dtypes, name: str, dev: int):
     """(pointer, outer strides) of a CUDA tensor whose last dimension is contiguous."""
     st = t.stride()
-    if t.dtype not in dtypes or t.get_device() != dev or dev < 0 or t.shape != shape or (st[-1] != 1 and shape[-1] > 1):
+    if t.dtype not in dtypes or t.get_device() != dev or t.shape != shape or (st[-1] != 1 and shape[-1] > 1):
         _refuse(t, shape, dtypes, name, "a contiguous last dimension")
     return t.data_ptr(), st
 
@@ -629,7 +630,7 @@ def pw_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
     args = _ROPE_ARGS.pack(qp, qop, kp, vp, kcp, vcp, tp, pos, table, offsets, lens, _status(status, dev), qs[0], qs[1],
                            qos[0], qos[1], ks[0], ks[1], vs[0], vs[1], kcs[0], kcs[1], kcs[2], vcs[0], vcs[1], vcs[2],
                            ts, T, batch, heads, kv_heads, D, 2 * half, page_size, pages, width, dt, interleaved, factor)
-    _launch(lib().pw_rope_append, dev, stream, args)
+    _check(lib().pw_rope_append(args, _queue(stream, dev)))
 
 
 def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -664,4 +665,4 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     args = _ATTN_ARGS.pack(qp, op, lp, kp, vp, table, offsets, lens, _status(status, dev), qs[0], qs[1], os_[0], os_[1],
                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts, T, batch, heads, kv_heads, D, page_size, pages,
                            width, max_q_len or T, max_kv_len or page_size * width, dt, causal, window, scale)
-    _launch(lib().pw_paged_attention, dev, stream, args, ws.data_ptr(), ws.nbytes)
+    _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _queue(stream, dev)))
