@@ -433,7 +433,9 @@ int pw_moe_route_apl_ffn_layers(const void* d_desc, int layer0, int L, const uin
  * Strides count elements; the innermost dimension is contiguous.  16-bit
  * types are fp16 and bf16 (`dtype`); 8-bit codes are e4m3 (finite, largest
  * magnitude 448).  Sums, statistics and scales are fp32; a 16-bit or 8-bit
- * output is rounded once, to nearest even. */
+ * output is rounded once, to nearest even.  One intermediate has fewer bits: the
+ * softmax weights are rounded to `dtype` before they meet the values (their sum
+ * takes them unrounded). */
 #define PW_DTYPE_F16 0
 #define PW_DTYPE_BF16 1
 
@@ -488,14 +490,17 @@ int pw_quantize_fp8(const pw_quant_args* args, void* stream);
 
 /* y[m][n] = sum_kb a_scale[m][kb] * b_scale[n/128][kb] * sum_{k in kb} a[m][k] b[n][k]
  * with kb the groups of 128 columns: a projection of quantised activations by
- * a quantised weight.
+ * a quantised weight.  a_scale * b_scale is formed first, in fp32: the product of
+ * a group's two scales has to be finite.
  *  a [m][k], b [n][k] e4m3; rows 16-byte aligned (address and stride)
  *  a_scale fp32 [m][ceil(k/128)], b_scale fp32 [ceil(n/128)][ceil(k/128)]
  *  y [m][n] in `dtype`
  *  status as in the fused layer (PW_ERR_TIMEOUT: a wait ran out).
  * m up to 2^20, n and k up to 2^24, no multiples needed.  Scales whose rows
  * start at 16-byte addresses (ceil(k/128) a multiple of 4, or padded strides)
- * and a y whose rows do take the wide paths. */
+ * and a y whose rows do take the wide paths; from 65 tokens on the others cost up
+ * to a third (scales) and two thirds (y) of the speed.  Nothing beside the n
+ * columns of y is written. */
 typedef struct pw_linear_args {
   const uint8_t* a;
   const float* a_scale;
@@ -512,10 +517,11 @@ int pw_fp8_linear(const pw_linear_args* args, void* stream);
 /* A batch of sequences in a paged cache, shared by the two calls below.
  * Sequence b has kv_lens[b] keys and values in the cache; its last
  * q_offsets[b+1] - q_offsets[b] are the call's new tokens, rows q_offsets[b]
- * .. q_offsets[b+1]-1 of q, k, v and out.  So new token i of n sits at position
- * kv_lens[b] - n + i.  Key j of a sequence is row j % page_size of the page
- * page_table[b][j / page_size].  Lengths, offsets and page ids are read on the
- * device; an offset, length or page id that the arrays cannot hold is not
+ * .. q_offsets[b+1]-1 of q, k, v and out.  A row that no sequence holds has no
+ * results (attention leaves its out and lse as they are, the append reports it).
+ * New token i of n sits at position kv_lens[b] - n + i.  Key j of a sequence is
+ * row j % page_size of the page page_table[b][j / page_size].  Lengths, offsets
+ * and page ids are read on the device; an offset, length or page id that the arrays cannot hold is not
  * followed and sets d_status (PW_ERR_INVALID_ARG; PW_ERR_NOT_RESIDENT for a
  * page id outside 0 .. num_pages-1). */
 
