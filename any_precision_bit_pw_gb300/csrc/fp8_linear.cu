@@ -694,6 +694,8 @@ extern "C" int pw_fp8_linear(const pw_linear_args* args, void* stream) {
   p.splits = 1;
   p.status = a.status;
   p.wide_b = pw::aligned(a.b, 32) && a.ldb % 32 == 0;
+  // (8192 x 8192 x 6144 at the shape's own strides 281 us; with rows of y at odd
+  // addresses 842, with rows of scales at 4-byte ones 379)
   p.wide_y = pw::aligned(a.y, 16) && a.ldy % 8 == 0;
   // with one group a tile the slots of the scales would be reused too early
   p.wide_scales = kb >= 2 && pw::aligned(a.a_scale, 16) && pw::aligned(a.b_scale, 16) && a.a_scale_stride % 4 == 0 &&

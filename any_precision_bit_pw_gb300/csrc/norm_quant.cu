@@ -5,8 +5,8 @@
 //   s = max(max|y over the group| / 448, 2^-100),  q = e4m3(y / s)
 //
 // Both read and write every value once; memory bandwidth bounds them (8192 x
-// 6144 with residual to e4m3: 55 us, 6.4 TB/s; weights of 8192 x 6144: 24 us,
-// 6.2 TB/s), and for a few rows the latency of one load, one reduction and one
+// 6144 with residual to e4m3: 55 us, 6.4 TB/s; weights of 8192 x 6144: 26 us,
+// 5.9 TB/s), and for a few rows the latency of one load, one reduction and one
 // store (one row of 4096: 2.0 us with the launch).
 #include "ops_common.cuh"
 
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024, kChunks == 4 && !kNo
 
 // One CTA per 128 x 128 block: 256 threads hold 64 values each, packed: of 8
 // rows, or of 4 rows by accesses of 32 bytes (kWide), where they can be (8192 x
-// 6144: 24.2 us, 25.6 by 16 bytes).
+// 6144: 25.7 us, 27.0 by 16 bytes).
 template <typename T, bool kAligned, bool kWide>
 __global__ void __launch_bounds__(256) block_kernel(const __grid_constant__ RowParams p) {
   constexpr int kParts = kWide ? 2 : 1, kTurns = 8 / kParts, kLanes = 16 / kParts, kStep = 256 / kLanes;
@@ -292,7 +292,9 @@ int launch_blocks(const RowParams& p, cudaStream_t s) {
 }
 
 // 16-byte accesses of 16-bit rows need the address, the stride and the width
-// in multiples of 8 values.
+// in multiples of 8 values.  Otherwise a thread's 8 values are accesses of 2
+// bytes (8192 x 6143: norm to e4m3 256 us, rows to e4m3 53 us, blocks 100 us, where
+// 6144 columns take 55, 29 and 26).
 bool rows_aligned(const void* ptr, int64_t stride, int cols) {
   return !ptr || (pw::aligned(ptr, 16) && stride % kVec == 0 && cols % kVec == 0);
 }

@@ -521,9 +521,9 @@ int pw_fp8_linear(const pw_linear_args* args, void* stream);
  * results (attention leaves its out and lse as they are, the append reports it).
  * New token i of n sits at position kv_lens[b] - n + i.  Key j of a sequence is
  * row j % page_size of the page page_table[b][j / page_size].  Lengths, offsets
- * and page ids are read on the device; an offset, length or page id that the arrays cannot hold is not
- * followed and sets d_status (PW_ERR_INVALID_ARG; PW_ERR_NOT_RESIDENT for a
- * page id outside 0 .. num_pages-1). */
+ * and page ids are read on the device; an offset, length or page id that the
+ * arrays cannot hold is not followed and sets d_status (PW_ERR_INVALID_ARG;
+ * PW_ERR_NOT_RESIDENT for a page id outside 0 .. num_pages-1). */
 
 /* Frequencies of rotary positions: h_turns[i] is the part of a full turn, in
  * units of 2^-64, that pair i turns per position, for i < rotary_dim/2;
