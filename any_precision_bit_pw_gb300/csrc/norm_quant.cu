@@ -8,11 +8,19 @@
 // 6144 with residual to e4m3: 55 us, 6.4 TB/s; weights of 8192 x 6144: 26 us,
 // 5.9 TB/s), and for a few rows the latency of one load, one reduction and one
 // store (one row of 4096: 2.0 us with the launch).
-#include "ops_common.cuh"
+#include "rows.cuh"
 
 namespace {
 
-constexpr int kVec = 8;               // values a thread holds of one chunk: 16 bytes
+using pw::check_matrix;
+using pw::codes_aligned;
+using pw::kVec;
+using pw::load8;
+using pw::rows_aligned;
+using pw::store8;
+using pw::store8_e4m3;
+using pw::unpack8;
+
 constexpr int kMaxCols = 32768;       // 512 threads x 8 chunks
 
 struct RowParams {
@@ -28,54 +36,6 @@ struct RowParams {
   int cols;
   float eps;
 };
-
-// Eight values at columns c .. c+7 of a row, packed; columns past the end are 0.
-template <typename T, bool kAligned>
-__device__ __forceinline__ uint4 load8(const T* row, int c, int cols) {
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (kAligned) {
-    if (c < cols) u = *reinterpret_cast<const uint4*>(row + c);
-  } else {
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(row) + c;
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = (c + 2 * i < cols ? v[2 * i] : 0u) | (c + 2 * i + 1 < cols ? static_cast<uint32_t>(v[2 * i + 1]) << 16 : 0u);
-    u = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  return u;
-}
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[kVec]) {
-  pw::unpack2<T>(u.x, v[0], v[1]);
-  pw::unpack2<T>(u.y, v[2], v[3]);
-  pw::unpack2<T>(u.z, v[4], v[5]);
-  pw::unpack2<T>(u.w, v[6], v[7]);
-}
-template <typename T, bool kAligned>
-__device__ __forceinline__ void store8(T* row, int c, int cols, const float (&v)[kVec]) {
-  if (kAligned) {
-    if (c < cols)
-      *reinterpret_cast<uint4*>(row + c) = make_uint4(pw::pack2<T>(v[0], v[1]), pw::pack2<T>(v[2], v[3]),
-                                                      pw::pack2<T>(v[4], v[5]), pw::pack2<T>(v[6], v[7]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (c + i < cols) row[c + i] = pw::from_float<T>(v[i]);
-  }
-}
-template <bool kAligned>
-__device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const float (&v)[kVec], const pw::Divisor& by) {
-  const uint32_t lo = pw::e4m3x4(by(v[0]), by(v[1]), by(v[2]), by(v[3]));
-  const uint32_t hi = pw::e4m3x4(by(v[4]), by(v[5]), by(v[6]), by(v[7]));
-  if (kAligned) {
-    if (c < cols) *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (c + i < cols) row[c + i] = static_cast<uint8_t>((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xFFu);
-  }
-}
 
 // A CTA takes every gridDim-th row.  A thread holds 8 values of each of kChunks
 // chunks in registers, so a row is read once, and loads the next row before the
@@ -154,12 +114,7 @@ __global__ void __launch_bounds__(kChunks > 2 ? 512 : 1024, kChunks == 4 && !kNo
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const int col = (c * nthr + tid) * kVec;
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) top = pw::max_nan(top, fabsf(v[c][i]));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
+        const float s = pw::group_scale(v[c]);
         if (col < p.cols && (tid & 15) == 0) p.scale[row * p.scale_stride + col / pw::kGroup] = s;
         store8_e4m3<kAligned>(q, col, p.cols, v[c], pw::Divisor(s));
       }
@@ -291,21 +246,9 @@ int launch_blocks(const RowParams& p, cudaStream_t s) {
   return PW_OK;
 }
 
-// 16-byte accesses of 16-bit rows need the address, the stride and the width
-// in multiples of 8 values.  Otherwise a thread's 8 values are accesses of 2
-// bytes (8192 x 6143: norm to e4m3 256 us, rows to e4m3 53 us, blocks 100 us, where
-// 6144 columns take 55, 29 and 26).
-bool rows_aligned(const void* ptr, int64_t stride, int cols) {
-  return !ptr || (pw::aligned(ptr, 16) && stride % kVec == 0 && cols % kVec == 0);
-}
-bool codes_aligned(const void* ptr, int64_t stride) { return !ptr || (pw::aligned(ptr, 8) && stride % 8 == 0); }
-
-int check_matrix(const char* op, const char* name, int64_t stride, int cols) {
-  if (stride < cols)
-    return pw::set_error(PW_ERR_INVALID_ARG, "%s: row stride %lld of %s is below the %d columns", op,
-                         static_cast<long long>(stride), name, cols);
-  return PW_OK;
-}
+// Where rows_aligned does not hold, a thread's 8 values are accesses of 2 bytes
+// (8192 x 6143: norm to e4m3 256 us, rows to e4m3 53 us, blocks 100 us, where 6144
+// columns take 55, 29 and 26).
 
 }  // namespace
 

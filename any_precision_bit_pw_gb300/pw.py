@@ -37,7 +37,8 @@ PW_PATH_AUTO, PW_PATH_DECODE, PW_PATH_PREFILL = 0, 1, 2
 PW_KERNEL_AUTO, PW_KERNEL_TENSOR, PW_KERNEL_CUDA_CORES = 0, 1, 2
 PW_FFN_FLAG_TEST_DROP_ONE_ARRIVAL = 1
 PW_FFN_FLAG_STRIP_COMBINE = 2
-PW_DTYPE_F16, PW_DTYPE_BF16 = 0, 1
+PW_DTYPE_F16, PW_DTYPE_BF16, PW_DTYPE_F32 = 0, 1, 2
+PW_ACT_SILU, PW_ACT_GELU_TANH = 0, 1
 PW_ROPE_PLAIN, PW_ROPE_LINEAR, PW_ROPE_NTK, PW_ROPE_YARN, PW_ROPE_BANDS = 0, 1, 2, 3, 4
 
 ERR_NAMES = {0: "PW_OK", -1: "PW_ERR_INVALID_ARG", -2: "PW_ERR_UNSUPPORTED", -3: "PW_ERR_NOT_RESIDENT",
@@ -54,6 +55,7 @@ EXPORTS = (
     "pw_moe_route_apl_ffn", "pw_moe_route_apl_ffn_ex", "pw_moe_route_apl_ffn_layers",
     "pw_add_rmsnorm", "pw_quantize_fp8", "pw_fp8_linear", "pw_rope_turns", "pw_rope_append",
     "pw_paged_attention_workspace", "pw_paged_attention",
+    "pw_norm_add_norm", "pw_token_logprobs",
     "pw_unpack_indices",
     "pw_apl_linear",
 )
@@ -126,6 +128,24 @@ class pw_attn_args(ctypes.Structure):
                 + [("scale", ctypes.c_float)])
 
 
+class pw_norms_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "post_weight", "gate", "weight", "residual_out", "y", "q",
+                                                "scale")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "gate_stride", "residual_out_stride",
+                                                 "y_stride", "q_stride", "scale_stride", "rows")]
+                + [(n, ctypes.c_int32) for n in ("cols", "dtype")]
+                + [(n, ctypes.c_float) for n in ("eps", "residual_scale", "block_scale")] + [("reserved", ctypes.c_int32)])
+
+
+class pw_logprob_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "targets", "logprobs", "lse", "entropy", "top_ids",
+                                                "top_logprobs")]
+                + [(n, ctypes.c_int64) for n in ("stride", "targets_stride", "logprobs_stride", "top_ids_stride",
+                                                 "top_logprobs_stride", "rows")]
+                + [(n, ctypes.c_int32) for n in ("vocab", "given", "top", "dtype")]
+                + [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)])
+
+
 _lib: Optional[ctypes.CDLL] = None
 P, I32, I64, U64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
 F32, F64 = ctypes.c_float, ctypes.c_double
@@ -179,6 +199,8 @@ def lib() -> ctypes.CDLL:
             "pw_rope_append": (I32, [P, P]),
             "pw_paged_attention_workspace": (SZ, [I32, I32, I32, I32, I32]),
             "pw_paged_attention": (I32, [P, P, SZ, P]),
+            "pw_norm_add_norm": (I32, [P, P]),
+            "pw_token_logprobs": (I32, [P, P]),
             "pw_unpack_indices": (I32, [P, I32, I32, P, P]),
             "pw_apl_linear": (I32, [P, I32, P, I32, P, P]),
         }
@@ -504,8 +526,11 @@ _QUANT_ARGS = struct.Struct("@3P4q4i")
 _LINEAR_ARGS = struct.Struct("@6P5q4i")
 _ROPE_ARGS = struct.Struct("@12P15q11if")
 _ATTN_ARGS = struct.Struct("@9P11q13if")
+_NORMS_ARGS = struct.Struct("@9P8q2i3fi")
+_LOGPROB_ARGS = struct.Struct("@7P6q4ifi")
 for _packed, _struct in ((_NORM_ARGS, pw_norm_args), (_QUANT_ARGS, pw_quant_args), (_LINEAR_ARGS, pw_linear_args),
-                         (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args)):
+                         (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args), (_NORMS_ARGS, pw_norms_args),
+                         (_LOGPROB_ARGS, pw_logprob_args)):
     assert _packed.size == ctypes.sizeof(_struct)
 
 
@@ -666,3 +691,62 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts, T, batch, heads, kv_heads, D, page_size, pages,
                            width, max_q_len or T, max_kv_len or page_size * width, dt, causal, window, scale)
     _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _queue(stream, dev)))
+
+
+# ---------------------------------------------------------------------------
+# Around the attention half: norms on both sides of a block, the model's end.
+# ---------------------------------------------------------------------------
+def pw_norm_add_norm(x: torch.Tensor, residual: torch.Tensor, eps: float, post_weight: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                     residual_scale: float = 1.0, block_scale: float = 1.0,
+                     residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """r = residual_scale * residual + block_scale * gate * u with u the
+    RMS norm of x by `post_weight` (x itself without it); `residual_out` receives
+    r, `y` and/or `q` (e4m3) with `scale` its RMS norm by `weight`.  `gate`:
+    a row for all rows [cols], or [rows][cols]."""
+    dt, dev = _dtype16(x, "x"), x.get_device()
+    rows, cols = x.shape
+    same = (x.dtype,)
+    xp, xs = _matrix(x, rows, cols, same, "x", dev)
+    rp, rs = _matrix(residual, rows, cols, same, "residual", dev)
+    pp = 0 if post_weight is None else _vector(post_weight, cols, same, "post_weight", dev)
+    wp = 0 if weight is None else _vector(weight, cols, same, "weight", dev)
+    gp = gs = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _vector(gate, cols, same, "gate", dev)
+        else:
+            gp, gs = _matrix(gate, rows, cols, same, "gate", dev)
+    rop, ros = _matrix(residual_out, rows, cols, same, "residual_out", dev)
+    yp, ys = _matrix(y, rows, cols, same, "y", dev)
+    qp, qs = _matrix(q, rows, cols, _CODES, "q", dev)
+    sp, ss = _matrix(scale, rows, -(-cols // 128), _F32, "scale", dev)
+    args = _NORMS_ARGS.pack(xp, rp, pp, gp, wp, rop, yp, qp, sp, xs, rs, gs, ros, ys, qs, ss, rows, cols, dt, eps,
+                            residual_scale, block_scale, 0)
+    _check(lib().pw_norm_add_norm(args, _queue(stream, dev)))
+
+
+def pw_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,
+                      logprobs: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      entropy: Optional[torch.Tensor] = None, top_ids: Optional[torch.Tensor] = None,
+                      top_logprobs: Optional[torch.Tensor] = None, scale: float = 1.0, stream=None) -> None:
+    """Of softmax(scale * logits) by rows [T][V] (fp16, bf16 or fp32): the log
+    probabilities of int32 `targets` [T][n] into `logprobs`, the logarithm of its
+    sum into `lse` [T], its `entropy` [T], and the most probable tokens with
+    their log probabilities into `top_ids`, `top_logprobs` [T][k]."""
+    dt, dev = PW_DTYPE_F32 if logits.dtype is torch.float32 else _dtype16(logits, "logits"), logits.get_device()
+    rows, vocab = logits.shape
+    zp, zs = _matrix(logits, rows, vocab, (logits.dtype,), "logits", dev)
+    if (targets is None) != (logprobs is None) or (top_ids is None) != (top_logprobs is None):
+        raise ValueError("token_logprobs: targets and logprobs, top_ids and top_logprobs come together")
+    given = 0 if targets is None else targets.shape[1]
+    top = 0 if top_ids is None else top_ids.shape[1]
+    tp, ts = _matrix(targets, rows, given, _I32, "targets", dev)
+    lp, ls = _matrix(logprobs, rows, given, _F32, "logprobs", dev)
+    ip, is_ = _matrix(top_ids, rows, top, _I32, "top_ids", dev)
+    op, os_ = _matrix(top_logprobs, rows, top, _F32, "top_logprobs", dev)
+    sp = 0 if lse is None else _vector(lse, rows, _F32, "lse", dev)
+    ep = 0 if entropy is None else _vector(entropy, rows, _F32, "entropy", dev)
+    args = _LOGPROB_ARGS.pack(zp, tp, lp, sp, ep, ip, op, zs, ts, ls, is_, os_, rows, vocab, given, top, dt, scale, 0)
+    _check(lib().pw_token_logprobs(args, _queue(stream, dev)))

@@ -633,6 +633,82 @@ size_t pw_paged_attention_workspace(int tokens, int batch, int heads, int kv_hea
 int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Around it: norms on both sides of a block, dense feed-forward, the end       */
+/* ------------------------------------------------------------------------ */
+/* Conventions of the attention half.  */
+
+/* By rows, the norms on both sides of a block (x is the block's output) with
+ * what is between them:
+ *   u = x * rsqrt(mean(x^2) + eps) * post_weight        (x itself without post_weight)
+ *   r = residual_scale * residual + block_scale * gate * u
+ *   y = r * rsqrt(mean(r^2) + eps) * weight
+ *  x, residual   [rows][cols]
+ *  post_weight   [cols] or NULL: no norm of the block's output
+ *  gate          [rows][cols], or [cols] (gate_stride 0), or NULL: 1
+ *  residual_out  [rows][cols] or NULL: r, rounded (the second norm uses the
+ *                unrounded sum); may be residual or x
+ *  weight        [cols], with y or q; NULL without both
+ *  y             [rows][cols] or NULL: y in `dtype`; may be x
+ *  q, scale      [rows][cols] e4m3 and fp32 [rows][ceil(cols/128)], or both
+ *                NULL: y in 8 bits (the unrounded y), as pw_quantize_fp8 with
+ *                block_rows 1
+ * At least one output.  Any alignment of the values' own size and any stride >=
+ * cols; cols <= 32768. */
+typedef struct pw_norms_args {
+  const void* x;
+  const void* residual;
+  const void* post_weight;
+  const void* gate;
+  const void* weight;
+  void* residual_out;
+  void* y;
+  uint8_t* q;
+  float* scale;
+  int64_t x_stride, residual_stride, gate_stride, residual_out_stride, y_stride, q_stride, scale_stride;
+  int64_t rows;
+  int32_t cols;
+  int32_t dtype;
+  float eps;
+  float residual_scale, block_scale;   /* finite */
+  int32_t reserved;
+} pw_norms_args;
+int pw_norm_add_norm(const pw_norms_args* args, void* stream);
+
+/* From the logits of next tokens, by rows, with z = scale * logit (scale: the
+ * reciprocal of a temperature) and p = softmax(z):
+ *   lse = ln sum e^z,   log p(t) = z_t - lse,   entropy = -sum p ln p
+ *  logits        [rows][vocab] in `dtype`: fp16, bf16 or fp32, rows `stride`
+ *                apart; scale times every finite one has to be finite
+ *  targets       int32 [rows][given] -> logprobs fp32 [rows][given].  An id
+ *                below 0 stands for no token and gets 0; one from vocab on gets
+ *                NaN (both are not followed)
+ *  lse, entropy  fp32 [rows] or NULL
+ *  top_ids, top_logprobs  int32 and fp32 [rows][top]: the tokens of the largest
+ *                logits in falling order, the lowest id first among equals
+ * A logit of -inf is a token of probability 0: it adds nothing to the entropy, and
+ * ranks behind every other.  A row with nothing else has lse and all log
+ * probabilities -inf and entropy 0.  A row that holds NaN or +inf has NaN for all of
+ * them; its top_ids are those of the logits' order, NaN ranking as -inf.  NULL and 0
+ * for given or top: not wanted; at least one output.  top <= 32. */
+#define PW_DTYPE_F32 2
+typedef struct pw_logprob_args {
+  const void* logits;
+  const int32_t* targets;
+  float* logprobs;
+  float* lse;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int64_t stride, targets_stride, logprobs_stride, top_ids_stride, top_logprobs_stride;
+  int64_t rows;
+  int32_t vocab, given, top;
+  int32_t dtype;
+  float scale;
+  int32_t reserved;
+} pw_logprob_args;
+int pw_token_logprobs(const pw_logprob_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test exports: they run the same device dequant code as the fused layer.     */
 /* ------------------------------------------------------------------------ */
 
