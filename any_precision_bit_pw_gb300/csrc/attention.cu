@@ -39,14 +39,14 @@ template <int D>
 constexpr size_t part_floats() { return static_cast<size_t>(kTile) * (D + 2); }
 
 // Starts the copies of one chunk (keys key0 .. key0+15 of the cursor's
-// sequence): rows outside [lo, hi) are zeros and their pages are not looked up.
-template <typename T, int D>
-__device__ __forceinline__ void load_chunk(const Params& p, const Cursor& c, int key0, uint32_t dst) {
+// sequence): rows that the tile does not see are zeros and their pages are not looked up.
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void load_chunk(const Params& p, const Cursor<kSinks>& c, int key0, uint32_t dst) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31;
   const int key = key0 + (lane & 15);
   long long off_k = -1, off_v = -1;
-  if (key >= c.r.lo && key < c.r.hi) {
+  if (pw_attn::in_sight<kSinks>(p, key, c.r.lo) && key < c.r.hi) {
     const int index = key / a.page_size;
     const int page = a.page_table[c.seq * a.page_table_stride + index];
     if (page >= 0 && page < a.num_pages) {
@@ -78,8 +78,8 @@ struct Rows {
   float m[2], l[2];        // of rows g and g + 8; l is this lane's share
 };
 
-template <typename T, int D>
-__device__ __forceinline__ void start_unit(const Params& p, const Cursor& c, Rows<T, D>& w) {
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void start_unit(const Params& p, const Cursor<kSinks>& c, Rows<T, D>& w) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rows = c.s.q_len * p.group;
@@ -107,8 +107,8 @@ __device__ __forceinline__ void start_unit(const Params& p, const Cursor& c, Row
   w.l[0] = w.l[1] = 0.0f;
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void compute_chunk(const Params& p, const Cursor& c, int key0, uint32_t src,
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void compute_chunk(const Params& p, const Cursor<kSinks>& c, int key0, uint32_t src,
                                               Rows<T, D>& w) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, mat = lane >> 3, r8 = lane & 7;
@@ -128,7 +128,7 @@ __device__ __forceinline__ void compute_chunk(const Params& p, const Cursor& c, 
   float keep[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // the row's visible keys are [lo, hi)
+    // the row's visible keys are [lo, hi), and the first ones below hi
     const int r = c.tile * kTile + g + 8 * i;
     const int pos = base + pw_attn::token_of(p, r);
     int hi = a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
@@ -139,7 +139,7 @@ __device__ __forceinline__ void compute_chunk(const Params& p, const Cursor& c, 
     for (int j = 0; j < 4; ++j) {
       const int key = key0 + (j >> 1) * 8 + 2 * t + (j & 1);
       float& v = s[j >> 1][2 * i + (j & 1)];
-      v = key >= lo && key < hi ? v * p.scale_log2 : -INFINITY;
+      v = pw_attn::in_sight<kSinks>(p, key, lo) && key < hi ? v * p.scale_log2 : -INFINITY;
       top = fmaxf(top, v);
     }
     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -183,8 +183,8 @@ struct Shared {
 
 // End of a CTA's work on a unit: the warps' states are joined, and the rows
 // are written, or left as a partial result whose last piece joins them all.
-template <typename T, int D>
-__device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, long long begin, long long seg_begin,
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void finish_unit(const Params& p, const Cursor<kSinks>& c, long long begin, long long seg_begin,
                                             long long seg_end, const pw_attn::Cut& cut, Rows<T, D>& w, Shared& sh,
                                             float* buf) {
   const pw_attn_args& a = p.a;
@@ -280,21 +280,21 @@ __device__ __forceinline__ void finish_unit(const Params& p, const Cursor& c, lo
       });
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kSinks>
 __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5;
   const uint32_t ring = pw::smem_u32(smem) + static_cast<uint32_t>(warp * kStages * stage_bytes<D>());
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * stage_bytes<D>());
-  Cursor c;
+  Cursor<kSinks> c;
   pw_attn::Cut cut;
   if (!pw_attn::find_start<kTile, kBlock, kThreads, 1>(p, c, cut)) return;
-  Cursor ahead = c;   // the copies run kStages - 1 blocks ahead of the arithmetic
+  Cursor<kSinks> ahead = c;   // the copies run kStages - 1 blocks ahead of the arithmetic
   int fill = 0;
   auto load_next = [&]() {
     if (!ahead.done()) {
-      load_chunk<T, D>(p, ahead, (ahead.r.b0 + ahead.block) * kBlock + warp * kChunk,
+      load_chunk<T, D>(p, ahead, ahead.r.block_at(ahead.block) * kBlock + warp * kChunk,
                        ring + static_cast<uint32_t>(fill * stage_bytes<D>()));
       ++ahead.pos;
       if (++ahead.block >= pw_attn::blocks_of(ahead.r) && !ahead.done()) pw_attn::next_unit<kTile, kBlock>(p, ahead);
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_cons
     pw::cp_async_wait<kStages - 2>();
     __syncwarp();
     load_next();   // into the stage that the last step has left
-    compute_chunk<T, D>(p, c, (c.r.b0 + c.block) * kBlock + warp * kChunk,
+    compute_chunk<T, D>(p, c, c.r.block_at(c.block) * kBlock + warp * kChunk,
                         ring + static_cast<uint32_t>(use * stage_bytes<D>()), w);
     __syncwarp();
     use = use + 1 == kStages ? 0 : use + 1;
@@ -331,14 +331,14 @@ __global__ void __launch_bounds__(kThreads) attn_stream_kernel(const __grid_cons
   pw::cp_async_wait<0>();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kSinks>
 int launch_stream(const Params& p, cudaStream_t s) {
   constexpr int kDevs = 64;
   static bool attr_done[kDevs] = {};
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= kDevs || !attr_done[dev]) {
-    PW_CUDA_TRY(cudaFuncSetAttribute(attn_stream_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>()));
+    PW_CUDA_TRY(cudaFuncSetAttribute(attn_stream_kernel<T, D, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>()));
     if (dev < kDevs) attr_done[dev] = true;
   }
   const int sms = pw::sm_count();
@@ -347,7 +347,7 @@ int launch_stream(const Params& p, cudaStream_t s) {
   const long long tiles = (static_cast<long long>(p.a.tokens) * p.group + kTile - 1) / kTile + p.a.batch;
   const long long blocks = tiles * ((p.a.max_kv_len + kBlock - 1) / kBlock + 1);
   const dim3 grid = pw_attn::grid_of(2ll * sms < pw_attn::kMaxCtas ? 2ll * sms : pw_attn::kMaxCtas, blocks, p.a.kv_heads);
-  attn_stream_kernel<T, D><<<grid, kThreads, smem_bytes<D>(), s>>>(p);
+  attn_stream_kernel<T, D, kSinks><<<grid, kThreads, smem_bytes<D>(), s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -355,7 +355,8 @@ int launch_stream(const Params& p, cudaStream_t s) {
 template <typename T>
 int launch(const Params& p, cudaStream_t s) {
   if (pw_attn::tile_kernel_takes(p)) return pw_attn::launch_tile_kernel(p, s);
-  return p.a.head_dim == 64 ? launch_stream<T, 64>(p, s) : launch_stream<T, 128>(p, s);
+  if (p.sinks) return p.a.head_dim == 64 ? launch_stream<T, 64, true>(p, s) : launch_stream<T, 128, true>(p, s);
+  return p.a.head_dim == 64 ? launch_stream<T, 64, false>(p, s) : launch_stream<T, 128, false>(p, s);
 }
 
 constexpr size_t kCounterBytes = 4096;   // the counters, rounded up
@@ -375,6 +376,10 @@ size_t pw_paged_attention_workspace(int tokens, int batch, int heads, int kv_hea
 }
 
 int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, void* stream) {
+  return pw_paged_attention_ex(args, nullptr, d_ws, ws_bytes, stream);
+}
+
+int pw_paged_attention_ex(const pw_attn_args* args, const pw_attn_options* options, void* d_ws, size_t ws_bytes, void* stream) {
   if (!args) return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: NULL argument");
   const pw_attn_args& a = *args;
   if (!pw::is_16bit(a.dtype)) return pw::set_error(PW_ERR_UNSUPPORTED, "paged_attention: dtype %d", a.dtype);
@@ -389,6 +394,11 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
     return pw::set_error(PW_ERR_UNSUPPORTED, "paged_attention: problem too large");
   if (a.window < 0 || a.window > (1 << 30) || (a.window && !a.causal))
     return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: window %d (needs causal)", a.window);
+  const int sinks = options ? options->sinks : 0;
+  if (sinks < 0 || sinks > (1 << 30)) return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: %d first keys", sinks);
+  if (options)
+    for (int32_t r : options->reserved)
+      if (r) return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: a reserved option is set");
   if (!std::isfinite(a.scale)) return pw::set_error(PW_ERR_INVALID_ARG, "paged_attention: scale is not finite");
   if (a.tokens == 0 || a.batch == 0) return PW_OK;
   if (a.page_size < 1 || a.num_pages < 1 || a.pages_per_seq < 1 || a.page_table_stride < a.pages_per_seq)
@@ -422,6 +432,7 @@ int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, vo
   p.group_inv = static_cast<uint32_t>(((1ull << 32) + p.group - 1) / p.group);
   p.group_max = p.group > 1 ? static_cast<int>(((1ull << 31) - 1) / p.group) : -1;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.sinks = a.window ? sinks : 0;   // without a window every token sees them anyway
   p.arrived = static_cast<uint32_t*>(d_ws);
   p.part = reinterpret_cast<float*>(static_cast<char*>(d_ws) + kCounterBytes);
   cudaStream_t s = pw::as_stream(stream);

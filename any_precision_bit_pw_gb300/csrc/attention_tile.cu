@@ -76,14 +76,15 @@ __device__ __forceinline__ bool wait(const uint64_t& bar, uint32_t parity, Share
 __device__ __forceinline__ uint32_t bar(const uint64_t& b) { return pw::smem_u32(&b); }
 
 // Number of 128-row halves with rows.
-__device__ __forceinline__ int halves_of(const Params& p, const Cursor& c) {
+template <bool kSinks>
+__device__ __forceinline__ int halves_of(const Params& p, const Cursor<kSinks>& c) {
   return pw::uniform(c.s.q_len * p.group - c.tile * kTile > kHalf ? 2 : 1);
 }
 
 // Walks the units of the CTA's stretch: f(cursor, first block, end block) with
 // block numbers of the unit.
-template <typename F>
-__device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
+template <bool kSinks, typename F>
+__device__ __forceinline__ void for_units(const Params& p, Cursor<kSinks> c, F f) {
   while (pw::uniform(!c.done())) {
     const int b0 = pw::uniform(c.block), n = pw_attn::blocks_of(c.r);
     const long long room = c.end - c.pos;
@@ -97,11 +98,11 @@ __device__ __forceinline__ void for_units(const Params& p, Cursor c, F f) {
 
 // ---------------------------------------------------------------- copies (a warp for keys, a warp for values)
 // Rows of values that no token of the call sees have to be zero: past the
-// sequence's end, and before every window.  They occur in the blocks at those
-// two places only: there the boxes that hold such rows are copied row by row,
-// with zeros for the others.
-template <int D>
-__device__ __forceinline__ void copy_rows(const Params& p, const Cursor& c, int key0, int first, int rows, int page,
+// sequence's end, and before every window, after the first keys.  They occur in the
+// blocks at those places only: there the boxes that hold such rows are copied row by
+// row, with zeros for the others.
+template <int D, bool kSinks>
+__device__ __forceinline__ void copy_rows(const Params& p, const Cursor<kSinks>& c, int key0, int first, int rows, int page,
                                           int begin, unsigned char* dst) {
   const pw_attn_args& a = p.a;
   constexpr int kUnits = D / 8;
@@ -109,15 +110,15 @@ __device__ __forceinline__ void copy_rows(const Params& p, const Cursor& c, int 
   for (int i = lane; i < rows * kUnits; i += 32) {
     const int row = first + i / kUnits, unit = i % kUnits, key = key0 + row;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (page >= 0 && key >= begin && key < c.s.kv_len)
+    if (page >= 0 && pw_attn::in_sight<kSinks>(p, key, begin) && key < c.s.kv_len)
       v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_cache) + page * a.v_stride_page +
                                           (key % a.page_size) * a.v_stride_token + c.head * a.v_stride_head + unit * 8);
     *reinterpret_cast<uint4*>(dst + (unit >> 3) * kHalfRow + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) = v;
   }
 }
 
-template <int D, bool kValues>
-__device__ __forceinline__ void load_role(const Params& p, const Cursor& start, const Maps& maps, Shared& sh,
+template <int D, bool kValues, bool kSinks>
+__device__ __forceinline__ void load_role(const Params& p, const Cursor<kSinks>& start, const Maps& maps, Shared& sh,
                                           unsigned char* ring) {
   const pw_attn_args& a = p.a;
   const int lane = threadIdx.x & 31;
@@ -129,13 +130,13 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
   constexpr uint32_t kSlots = kValues ? kValueSlots : kKeySlots;
   pw::Ring<kSlots> slot;
   uint32_t x = 0;                                   // blocks started
-  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+  for_units(p, start, [&](const Cursor<kSinks>& c, int b0, int b1) {
     const int32_t* table = a.page_table + c.seq * a.page_table_stride;
     // this lane's box: its first key, and where that is in the page table
-    int key0 = (c.r.b0 + b0) * kBlock, key = key0 + lane * box;
+    int key0 = c.r.block_at(b0) * kBlock, key = key0 + lane * box;
     int index = key / a.page_size, in_page = key - index * a.page_size;
     const int begin = pw_attn::first_key(a, c.s), end = c.s.kv_len;
-    auto wanted = [&]() { return lane < boxes && key < end && key + box > begin; };
+    auto wanted = [&]() { return lane < boxes && key < end && (key + box > begin || (kSinks && key < p.sinks)); };
     int page = wanted() ? table[index] : -1;
     for (int b = b0; b < b1; ++b, ++x) {
       const bool want = wanted();
@@ -143,7 +144,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
       bool take = want && this_page >= 0 && this_page < a.num_pages;
       if (want && !take && !kValues) pw::report_status(a.status, PW_ERR_NOT_RESIDENT);
       const uint32_t live = __ballot_sync(0xFFFFFFFFu, take);
-      if (kValues) take = take && key >= begin && key + box <= end;   // every row is visible to some token
+      // every row is visible to some token
+      if (kValues) take = take && (key >= begin || (kSinks && key + box <= p.sinks)) && key + box <= end;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
       // the next block's page: its latency passes during this block's waits
       key += kBlock;
@@ -152,6 +154,11 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
       if (in_page >= a.page_size) {
         in_page -= a.page_size;
         ++index;
+      }
+      if (kSinks && b + 1 == c.r.before()) {   // from the first keys to the window
+        key = c.r.b0 * kBlock + lane * box;
+        index = key / a.page_size;
+        in_page = key - index * a.page_size;
       }
       page = b + 1 < b1 && wanted() ? table[index] : -1;
       if (x >= kSlots && !wait(empties[slot.at], slot.parity ^ 1u, sh, p)) return false;
@@ -178,7 +185,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
         }
         __syncwarp();
       }
-      key0 += kBlock;
+      key0 = kSinks && b + 1 == c.r.before() ? c.r.b0 * kBlock : key0 + kBlock;
     }
     return true;
   });
@@ -196,8 +203,8 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor& start, 
 // descriptors are made beforehand, the halves are written out.  (One issuing
 // warp a half instead lets the halves' products alternate, and both finish
 // late: 1330 us against 1257 on 7.2k tokens over 16k keys.)
-template <int D, bool kBf16>
-__device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, Shared& sh, uint32_t tmem,
+template <int D, bool kBf16, bool kSinks>
+__device__ __forceinline__ void mma_role(const Params& p, const Cursor<kSinks>& start, Shared& sh, uint32_t tmem,
                                          uint32_t q_smem, uint32_t k_ring, uint32_t v_ring) {
   constexpr uint32_t kScores = pw::idesc_f32(kHalf, kBlock, kBf16, false);
   constexpr uint32_t kValues = pw::idesc_f32(kHalf, D, kBf16, true);
@@ -242,7 +249,7 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
     pw::tc_fence_after();
     return ok;
   };
-  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+  for_units(p, start, [&](const Cursor<kSinks>& c, int b0, int b1) {
     const bool two = halves_of(p, c) == 2;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -280,8 +287,8 @@ __device__ __forceinline__ void mma_role(const Params& p, const Cursor& start, S
 }
 
 // ---------------------------------------------------------------- softmax (four warps a half)
-template <typename T, int D>
-__device__ __forceinline__ void write_queries(const Params& p, const Cursor& c, int h, int tid, unsigned char* q_smem) {
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void write_queries(const Params& p, const Cursor<kSinks>& c, int h, int tid, unsigned char* q_smem) {
   constexpr int kUnits = D / 8;             // 16-byte units of a row
   constexpr int kStep = kHalf / kUnits;     // rows at once
   const pw_attn_args& a = p.a;
@@ -312,8 +319,8 @@ __device__ __forceinline__ void write_queries(const Params& p, const Cursor& c, 
   }
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void softmax_role(const Params& p, const Cursor& start, const pw_attn::Cut& cut, Shared& sh,
+template <typename T, int D, bool kSinks>
+__device__ __forceinline__ void softmax_role(const Params& p, const Cursor<kSinks>& start, const pw_attn::Cut& cut, Shared& sh,
                                              uint32_t tmem, unsigned char* q_smem) {
   const pw_attn_args& a = p.a;
   const int h = threadIdx.x / kHalf, tid = threadIdx.x % kHalf, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
@@ -321,7 +328,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
   const uint32_t s_tmem = tmem + lanes + h * kBlock, o_tmem = tmem + lanes + 2 * kBlock + h * D;
   const size_t part_floats = static_cast<size_t>(kTile) * (D + 2);
   uint32_t blocks = 0;   // of this half so far
-  for_units(p, start, [&](const Cursor& c, int b0, int b1) {
+  for_units(p, start, [&](const Cursor<kSinks>& c, int b0, int b1) {
     const int rows = c.s.q_len * p.group, r = c.tile * kTile + tid + h * kHalf;
     const bool live = r < rows;
     float m = -INFINITY, l = 0.0f;
@@ -337,10 +344,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
       const int hi = !live ? 0x7FFFFFFF : a.causal ? min(pos + 1, c.r.hi) : c.r.hi;
       const int lo = live && a.causal && a.window ? pos - a.window + 1 : 0;
       for (int b = b0; b < b1; ++b, ++blocks) {
-        const int key0 = (c.r.b0 + b) * kBlock;
+        const int key0 = c.r.block_at(b) * kBlock;
         wait(sh.s_full[h], blocks & 1u, sh, p);
         pw::tc_fence_after();
-        const bool all = __all_sync(0xFFFFFFFFu, lo <= key0 && hi >= key0 + kBlock);   // no mask in this block
+        // no mask in this block
+        const bool all = __all_sync(0xFFFFFFFFu, (lo <= key0 || (kSinks && p.sinks >= key0 + kBlock)) && hi >= key0 + kBlock);
         // 64 scores at a time: their maximum, then their weights, so that the
         // second product can start on the first 64 keys (with the maximum of all
         // 128 first it starts 350 cycles later, and the period is longer by as
@@ -353,10 +361,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
           pw::tmem_ld_x32(s_tmem + 64 * i + 32, s[1]);
           pw::tmem_ld_wait();
           if (!all) {
-            const int from = lo - key0 - 64 * i, to = hi - key0 - 64 * i;
+            const int from = lo - key0 - 64 * i, to = hi - key0 - 64 * i, first = kSinks ? p.sinks - key0 - 64 * i : 0;
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              if (j < from || j >= to) s[j >> 5][j & 31] = 0xFF800000u;   // -inf
+              if ((j < from && (!kSinks || j >= first)) || j >= to) s[j >> 5][j & 31] = 0xFF800000u;   // -inf
           }
           float most[4];
 #pragma unroll
@@ -504,14 +512,14 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor& star
   });
 }
 
-template <typename T, int D, bool kBf16>
+template <typename T, int D, bool kBf16, bool kSinks>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ Shared sh;
   unsigned char* smem = smem_raw + ((1024u - (pw::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = pw::uniform(static_cast<int>(threadIdx.x >> 5));
-  Cursor c;
+  Cursor<kSinks> c;
   pw_attn::Cut cut;
   if (!pw_attn::find_start<kTile, kBlock, kThreads, kLeast>(p, c, cut)) return;
   if (threadIdx.x == 0) {
@@ -573,14 +581,14 @@ int encode_cache(CUtensorMap* m, const pw_attn_args& a, const void* base, int64_
                                strides, bx);
 }
 
-template <typename T, int D, bool kBf16>
+template <typename T, int D, bool kBf16, bool kSinks>
 int launch(const Params& p, cudaStream_t s) {
   constexpr int kDevs = 64;
   static bool attr_done[kDevs] = {};
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
   if (dev >= kDevs || !attr_done[dev]) {
-    PW_CUDA_TRY(cudaFuncSetAttribute(attn_tile_kernel<T, D, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    PW_CUDA_TRY(cudaFuncSetAttribute(attn_tile_kernel<T, D, kBf16, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      smem_bytes<D>()));
     if (dev < kDevs) attr_done[dev] = true;
   }
@@ -596,7 +604,7 @@ int launch(const Params& p, cudaStream_t s) {
   const long long tiles = (static_cast<long long>(a.tokens) * p.group + kTile - 1) / kTile + a.batch;
   const long long blocks = tiles * ((a.max_kv_len + kBlock - 1) / kBlock + 1);
   const dim3 grid = pw_attn::grid_of(sms < pw_attn::kMaxCtas / 2 ? sms : pw_attn::kMaxCtas / 2, blocks, a.kv_heads);
-  attn_tile_kernel<T, D, kBf16><<<grid, kThreads, smem_bytes<D>(), s>>>(p, maps);
+  attn_tile_kernel<T, D, kBf16, kSinks><<<grid, kThreads, smem_bytes<D>(), s>>>(p, maps);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
@@ -622,10 +630,14 @@ bool tile_kernel_takes(const Params& p) {
   return true;
 }
 
-int launch_tile_kernel(const Params& p, cudaStream_t s) {
+template <bool kSinks>
+int launch_tile(const Params& p, cudaStream_t s) {
   if (p.a.dtype == PW_DTYPE_F16)
-    return p.a.head_dim == 64 ? launch<__half, 64, false>(p, s) : launch<__half, 128, false>(p, s);
-  return p.a.head_dim == 64 ? launch<__nv_bfloat16, 64, true>(p, s) : launch<__nv_bfloat16, 128, true>(p, s);
+    return p.a.head_dim == 64 ? launch<__half, 64, false, kSinks>(p, s) : launch<__half, 128, false, kSinks>(p, s);
+  return p.a.head_dim == 64 ? launch<__nv_bfloat16, 64, true, kSinks>(p, s) : launch<__nv_bfloat16, 128, true, kSinks>(p, s);
+}
+int launch_tile_kernel(const Params& p, cudaStream_t s) {
+  return p.sinks ? launch_tile<true>(p, s) : launch_tile<false>(p, s);
 }
 
 }  // namespace pw_attn

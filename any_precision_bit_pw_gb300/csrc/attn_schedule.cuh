@@ -15,6 +15,11 @@
 // longer for it: fewer CTAs then have two units to finish (24 sequences of 17 to
 // 65536 keys, one token each: 152 us, 164 cut as one line).  Otherwise it is
 // (CTAs, 1).
+//
+// kSinks: calls whose tokens see the first keys of their sequence beside the
+// window's.  A unit's blocks are then those of the first keys, as far as they
+// end before the window's first block, and the window's; the kernels are
+// compiled apart, so that the other calls do not pay for the second range.
 #pragma once
 
 #include "ops_common.cuh"
@@ -27,6 +32,7 @@ struct Params {
   uint32_t group_inv; // ceil(2^32 / group): rows up to group_max divide by a product
   int group_max;
   float scale_log2;   // scale * log2(e): the softmax runs in powers of two
+  int sinks;          // first keys that every token of a sequence sees; 0 without a window
   uint32_t* arrived;  // two counters per CTA, all 0 between calls
   float* part;        // 2 partial results per CTA
 };
@@ -77,44 +83,65 @@ __device__ __forceinline__ Sequence sequence(const pw_attn_args& a, int b, bool 
   return s;
 }
 
-// Key range [lo, hi) that the rows of a tile see, and its blocks.
+// Whether a key, not past the call's last token, is one that a row whose window starts at `lo` sees.
+template <bool kSinks>
+__device__ __forceinline__ bool in_sight(const Params& p, int key, int lo) {
+  return key >= lo || (kSinks && key < p.sinks);
+}
+
+// Key range [lo, hi) that the rows of a tile see, and its blocks b0 .. b1-1;
+// with first keys, the blocks 0 .. first-1 come before them.
+template <bool kSinks>
 struct Range {
   int lo, hi, b0, b1;
+  __device__ __forceinline__ int before() const { return 0; }
+  __device__ __forceinline__ int block_at(int i) const { return b0 + i; }
 };
-template <int kTile, int kBlock>
-__device__ __forceinline__ Range tile_range(const Params& p, const Sequence& s, int tile) {
+template <>
+struct Range<true> {
+  int lo, hi, b0, b1, first;
+  __device__ __forceinline__ int before() const { return first; }
+  __device__ __forceinline__ int block_at(int i) const { return i < first ? i : b0 + i - first; }
+};
+template <int kTile, int kBlock, bool kSinks>
+__device__ __forceinline__ Range<kSinks> tile_range(const Params& p, const Sequence& s, int tile) {
   const int rows = s.q_len * p.group;
   const int first = tile * kTile, last = min(rows, first + kTile) - 1;
   const int base = s.kv_len - s.q_len;
-  Range r;
+  Range<kSinks> r;
   r.hi = p.a.causal ? max(0, base + token_of(p, last) + 1) : s.kv_len;
   r.lo = p.a.causal && p.a.window ? max(0, base + token_of(p, first) - p.a.window + 1) : 0;
   if (r.lo >= r.hi) r.lo = r.hi = 0;
   r.b0 = r.lo / kBlock;
   r.b1 = (r.hi + kBlock - 1) / kBlock;
+  if constexpr (kSinks) r.first = min(r.b0, (p.sinks + kBlock - 1) / kBlock);
   return r;
 }
 // A unit whose rows see nothing still takes one (empty) block: its zeros have
 // to be written.
-__device__ __forceinline__ int blocks_of(const Range& r) { return max(1, r.b1 - r.b0); }
+template <bool kSinks>
+__device__ __forceinline__ int blocks_of(const Range<kSinks>& r) {
+  return max(1, r.before() + r.b1 - r.b0);
+}
 
 template <int kTile>
 __device__ __forceinline__ int tiles_of(const Params& p, const Sequence& s) {
   return (s.q_len * p.group + kTile - 1) / kTile;
 }
 
-template <int kTile, int kBlock>
+template <int kTile, int kBlock, bool kSinks>
 __device__ __forceinline__ long long sequence_blocks(const Params& p, const Sequence& s) {
   const int tiles = tiles_of<kTile>(p, s);
   long long n = 0;
-  for (int i = 0; i < tiles; ++i) n += blocks_of(tile_range<kTile, kBlock>(p, s, i));
+  for (int i = 0; i < tiles; ++i) n += blocks_of(tile_range<kTile, kBlock, kSinks>(p, s, i));
   return n;
 }
 
 // Where a CTA is on the line.
+template <bool kSinks>
 struct Cursor {
   Sequence s;
-  Range r;
+  Range<kSinks> r;
   int head, seq, tile;
   int block;                // next block of the unit, 0 .. blocks_of(r) - 1
   long long pos, end;       // its position on the line, and the end of the CTA's stretch
@@ -125,8 +152,8 @@ struct Cursor {
 };
 
 // Moves to the first block of the next unit; pos is that block's already.
-template <int kTile, int kBlock>
-__device__ __forceinline__ void next_unit(const Params& p, Cursor& c) {
+template <int kTile, int kBlock, bool kSinks>
+__device__ __forceinline__ void next_unit(const Params& p, Cursor<kSinks>& c) {
   ++c.tile;
   while (c.tile >= tiles_of<kTile>(p, c.s)) {
     c.tile = 0;
@@ -139,7 +166,7 @@ __device__ __forceinline__ void next_unit(const Params& p, Cursor& c) {
     }
     c.s = sequence(p.a, c.seq, false);
   }
-  c.r = tile_range<kTile, kBlock>(p, c.s, c.tile);
+  c.r = tile_range<kTile, kBlock, kSinks>(p, c.s, c.tile);
   c.block = 0;
 }
 
@@ -164,8 +191,8 @@ inline dim3 grid_of(long long ctas, long long blocks, int kv_heads) {
 
 // The cursor of this CTA, found by all its kThreads threads.  Returns false
 // when it has no stretch.
-template <int kTile, int kBlock, int kThreads, int kLeast>
-__device__ __forceinline__ bool find_start(const Params& p, Cursor& c, Cut& cut) {
+template <int kTile, int kBlock, int kThreads, int kLeast, bool kSinks>
+__device__ __forceinline__ bool find_start(const Params& p, Cursor<kSinks>& c, Cut& cut) {
   constexpr int kWarps = kThreads / 32;
   __shared__ long long warp_sum[2][kWarps];
   __shared__ long long sh_rest;
@@ -174,7 +201,7 @@ __device__ __forceinline__ bool find_start(const Params& p, Cursor& c, Cut& cut)
   // blocks of one head, and (batch <= kThreads) the prefix of this thread's sequence
   long long mine = 0;
   for (int b = tid; b < p.a.batch; b += kThreads)
-    mine += sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, blockIdx.x + blockIdx.y == 0));
+    mine += sequence_blocks<kTile, kBlock, kSinks>(p, sequence(p.a, b, blockIdx.x + blockIdx.y == 0));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -208,7 +235,7 @@ __device__ __forceinline__ bool find_start(const Params& p, Cursor& c, Cut& cut)
     long long before = 0;
     for (int b0 = 0, turn = 1; b0 < p.a.batch; b0 += kThreads, turn ^= 1) {
       const int b = b0 + tid;
-      const long long n = b < p.a.batch ? sequence_blocks<kTile, kBlock>(p, sequence(p.a, b, false)) : 0;
+      const long long n = b < p.a.batch ? sequence_blocks<kTile, kBlock, kSinks>(p, sequence(p.a, b, false)) : 0;
       incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -233,10 +260,10 @@ __device__ __forceinline__ bool find_start(const Params& p, Cursor& c, Cut& cut)
   c.s = sequence(p.a, c.seq, false);
   long long rest = sh_rest;
   c.tile = 0;
-  c.r = tile_range<kTile, kBlock>(p, c.s, 0);
+  c.r = tile_range<kTile, kBlock, kSinks>(p, c.s, 0);
   while (rest >= blocks_of(c.r)) {
     rest -= blocks_of(c.r);
-    c.r = tile_range<kTile, kBlock>(p, c.s, ++c.tile);
+    c.r = tile_range<kTile, kBlock, kSinks>(p, c.s, ++c.tile);
   }
   c.block = static_cast<int>(rest);
   return true;

@@ -54,7 +54,7 @@ EXPORTS = (
     "pw_moe_apl_ffn_workspace", "pw_moe_apl_ffn", "pw_moe_apl_ffn_ex", "pw_moe_apl_ffn_noalloc",
     "pw_moe_route_apl_ffn", "pw_moe_route_apl_ffn_ex", "pw_moe_route_apl_ffn_layers",
     "pw_add_rmsnorm", "pw_quantize_fp8", "pw_fp8_linear", "pw_rope_turns", "pw_rope_append",
-    "pw_paged_attention_workspace", "pw_paged_attention",
+    "pw_paged_attention_workspace", "pw_paged_attention", "pw_paged_attention_ex",
     "pw_norm_add_norm", "pw_token_logprobs",
     "pw_unpack_indices",
     "pw_apl_linear",
@@ -128,6 +128,10 @@ class pw_attn_args(ctypes.Structure):
                 + [("scale", ctypes.c_float)])
 
 
+class pw_attn_options(ctypes.Structure):
+    _fields_ = [("sinks", ctypes.c_int32), ("reserved", ctypes.c_int32 * 7)]
+
+
 class pw_norms_args(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "post_weight", "gate", "weight", "residual_out", "y", "q",
                                                 "scale")]
@@ -199,6 +203,7 @@ def lib() -> ctypes.CDLL:
             "pw_rope_append": (I32, [P, P]),
             "pw_paged_attention_workspace": (SZ, [I32, I32, I32, I32, I32]),
             "pw_paged_attention": (I32, [P, P, SZ, P]),
+            "pw_paged_attention_ex": (I32, [P, P, P, SZ, P]),
             "pw_norm_add_norm": (I32, [P, P]),
             "pw_token_logprobs": (I32, [P, P]),
             "pw_unpack_indices": (I32, [P, I32, I32, P, P]),
@@ -526,11 +531,12 @@ _QUANT_ARGS = struct.Struct("@3P4q4i")
 _LINEAR_ARGS = struct.Struct("@6P5q4i")
 _ROPE_ARGS = struct.Struct("@12P15q11if")
 _ATTN_ARGS = struct.Struct("@9P11q13if")
+_ATTN_OPTIONS = struct.Struct("@8i")
 _NORMS_ARGS = struct.Struct("@9P8q2i3fi")
 _LOGPROB_ARGS = struct.Struct("@7P6q4ifi")
 for _packed, _struct in ((_NORM_ARGS, pw_norm_args), (_QUANT_ARGS, pw_quant_args), (_LINEAR_ARGS, pw_linear_args),
-                         (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args), (_NORMS_ARGS, pw_norms_args),
-                         (_LOGPROB_ARGS, pw_logprob_args)):
+                         (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args), (_ATTN_OPTIONS, pw_attn_options),
+                         (_NORMS_ARGS, pw_norms_args), (_LOGPROB_ARGS, pw_logprob_args)):
     assert _packed.size == ctypes.sizeof(_struct)
 
 
@@ -665,10 +671,11 @@ def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: 
 def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                        q_offsets: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
                        status: torch.Tensor, scale: float, causal: bool = True, window: int = 0, max_q_len: int = 0,
-                       max_kv_len: int = 0, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+                       max_kv_len: int = 0, lse: Optional[torch.Tensor] = None, sinks: int = 0, stream=None) -> None:
     """out [T][heads][D] = attention of the new tokens q over their sequences'
-    keys in the paged cache [pages][page_size][kv_heads][D].  `ws` must be
-    zeroed before its first use.  max_q_len / max_kv_len: bounds of the lengths
+    keys in the paged cache [pages][page_size][kv_heads][D]; with a `window` a
+    token sees that many keys up to its own, and the first `sinks` of its
+    sequence.  `ws` must be zeroed before its first use.  max_q_len / max_kv_len: bounds of the lengths
     (0: the batch's tokens, and what the page table holds)."""
     dt, dev, same = _dtype16(q, "q"), q.get_device(), (q.dtype,)
     T, heads, D = q.shape
@@ -690,7 +697,11 @@ def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     args = _ATTN_ARGS.pack(qp, op, lp, kp, vp, table, offsets, lens, _status(status, dev), qs[0], qs[1], os_[0], os_[1],
                            ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts, T, batch, heads, kv_heads, D, page_size, pages,
                            width, max_q_len or T, max_kv_len or page_size * width, dt, causal, window, scale)
-    _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _queue(stream, dev)))
+    if sinks:
+        _check(lib().pw_paged_attention_ex(args, _ATTN_OPTIONS.pack(sinks, 0, 0, 0, 0, 0, 0, 0), ws.data_ptr(), ws.nbytes,
+                                           _queue(stream, dev)))
+    else:
+        _check(lib().pw_paged_attention(args, ws.data_ptr(), ws.nbytes, _queue(stream, dev)))
 
 
 # ---------------------------------------------------------------------------

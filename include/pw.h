@@ -632,6 +632,14 @@ typedef struct pw_attn_args {
 size_t pw_paged_attention_workspace(int tokens, int batch, int heads, int kv_heads, int head_dim);
 int pw_paged_attention(const pw_attn_args* args, void* d_ws, size_t ws_bytes, void* stream);
 
+/* Options of pw_paged_attention_ex (zero-initialise, then set what you need). */
+typedef struct pw_attn_options {
+  int32_t sinks;        /* with a window: a token sees the first `sinks` keys of its sequence too, those up to its own
+                           position (pages between these and every window may be gone) */
+  int32_t reserved[7];
+} pw_attn_options;
+int pw_paged_attention_ex(const pw_attn_args* args, const pw_attn_options* options, void* d_ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Around it: norms on both sides of a block, dense feed-forward, the end       */
 /* ------------------------------------------------------------------------ */

@@ -109,7 +109,7 @@ def token_positions(q_offsets, kv_lens):
             for b in range(len(kv_lens)) for i in range(int(q_offsets[b + 1] - q_offsets[b]))]
 
 
-def attention(q, k_cache, v_cache, page_table, q_offsets, kv_lens, scale, causal=True, window=0):
+def attention(q, k_cache, v_cache, page_table, q_offsets, kv_lens, scale, causal=True, window=0, sinks=0):
     """(out, lse, sum p|v|, largest sum |q||k| scale of a row): the last two
     are what error bounds are made of."""
     T, H, D = q.shape
@@ -123,7 +123,7 @@ def attention(q, k_cache, v_cache, page_table, q_offsets, kv_lens, scale, causal
             pos = n - m + i
             hi = min(n, pos + 1) if causal else n
             lo = max(0, pos - window + 1) if causal and window else 0
-            keys = range(lo, hi)
+            keys = [*range(min(sinks, lo, max(hi, 0))), *range(lo, hi)]   # the first ones, and the window's
             if len(keys) == 0:
                 continue
             at = np.array([int(page_table[b][j // ps]) * ps + j % ps for j in keys])

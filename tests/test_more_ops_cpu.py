@@ -110,3 +110,42 @@ def test_binding_checks():
         pw.pw_token_logprobs(x.double(), lse=torch.zeros(4))
     with pytest.raises(ValueError):          # one without the other
         pw.pw_token_logprobs(x, targets=torch.zeros(4, 1, dtype=torch.int32))
+
+
+def test_oracle_attention_with_first_keys():
+    from oracle import attn_half
+    # equal scores: the mean of the visible values
+    rng = np.random.default_rng(0)
+    v = rng.standard_normal((4, 4, 1, 8))
+    q, k = np.zeros((2, 2, 8)), rng.standard_normal((4, 4, 1, 8))
+    table = np.array([[2, 0, 1, 3]])
+    flat = v[[2, 0, 1, 3]].reshape(-1, 8)
+    out, lse, _, _ = attn_half.attention(q, k, v, table, [0, 2], [15], 0.5, window=3, sinks=2)
+    assert np.allclose(out[0, 0], flat[[0, 1, 11, 12, 13]].mean(0)) and np.allclose(out[1, 1], flat[[0, 1, 12, 13, 14]].mean(0))
+    assert np.allclose(lse, math.log(5))
+    # the first keys end where the token is, and where the window begins
+    out, _, _, _ = attn_half.attention(q, k, v, table, [0, 2], [2], 0.5, window=1, sinks=5)
+    assert np.allclose(out[0, 0], flat[0]) and np.allclose(out[1, 0], flat[:2].mean(0))
+
+
+def _attention(L, **options):
+    a = pw.pw_attn_args()
+    for n in ("q", "out", "k_cache", "v_cache", "page_table", "q_offsets", "kv_lens", "status"):
+        setattr(a, n, FAKE)
+    a.tokens, a.batch, a.heads, a.kv_heads, a.head_dim = 0, 2, 4, 2, 128
+    a.page_size, a.num_pages, a.pages_per_seq, a.page_table_stride = 16, 8, 4, 4
+    a.max_q_len, a.max_kv_len, a.causal, a.scale, a.window = 2, 64, 1, 0.1, 8
+    o = pw.pw_attn_options()
+    reserved = options.pop("reserved", None)
+    if reserved is not None:
+        o.reserved[reserved] = 1
+    for k, v in options.items():
+        setattr(o, k, v)
+    return L.pw_paged_attention_ex(ctypes.byref(a), ctypes.byref(o), FAKE, 1 << 30, None)
+
+
+@pytest.mark.parametrize("kw", [dict(sinks=-1), dict(sinks=(1 << 30) + 1), dict(reserved=0), dict(reserved=6)])
+def test_attention_option_refusals(L, kw):
+    assert _attention(L, **kw) == pw.PW_ERR_INVALID_ARG and "paged_attention" in pw.pw_last_error()
+    assert _attention(L, sinks=4) == 0                                   # no tokens
+    assert L.pw_paged_attention_ex(None, None, FAKE, 1 << 30, None) == pw.PW_ERR_INVALID_ARG
