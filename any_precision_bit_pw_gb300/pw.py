@@ -55,7 +55,7 @@ EXPORTS = (
     "pw_moe_route_apl_ffn", "pw_moe_route_apl_ffn_ex", "pw_moe_route_apl_ffn_layers",
     "pw_add_rmsnorm", "pw_quantize_fp8", "pw_fp8_linear", "pw_rope_turns", "pw_rope_append",
     "pw_paged_attention_workspace", "pw_paged_attention", "pw_paged_attention_ex",
-    "pw_norm_add_norm", "pw_token_logprobs",
+    "pw_norm_add_norm", "pw_fp8_gated_linear", "pw_token_logprobs",
     "pw_unpack_indices",
     "pw_apl_linear",
 )
@@ -141,6 +141,14 @@ class pw_norms_args(ctypes.Structure):
                 + [(n, ctypes.c_float) for n in ("eps", "residual_scale", "block_scale")] + [("reserved", ctypes.c_int32)])
 
 
+class pw_gated_args(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("a", "a_scale", "gate", "gate_scale", "up", "up_scale", "y", "q", "scale",
+                                                "status")]
+                + [(n, ctypes.c_int64) for n in ("lda", "a_scale_stride", "ld_gate", "gate_scale_stride", "ld_up",
+                                                 "up_scale_stride", "ldy", "ldq", "scale_stride")]
+                + [(n, ctypes.c_int32) for n in ("m", "n", "k", "dtype", "activation", "reserved")])
+
+
 class pw_logprob_args(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "targets", "logprobs", "lse", "entropy", "top_ids",
                                                 "top_logprobs")]
@@ -205,6 +213,7 @@ def lib() -> ctypes.CDLL:
             "pw_paged_attention": (I32, [P, P, SZ, P]),
             "pw_paged_attention_ex": (I32, [P, P, P, SZ, P]),
             "pw_norm_add_norm": (I32, [P, P]),
+            "pw_fp8_gated_linear": (I32, [P, P]),
             "pw_token_logprobs": (I32, [P, P]),
             "pw_unpack_indices": (I32, [P, I32, I32, P, P]),
             "pw_apl_linear": (I32, [P, I32, P, I32, P, P]),
@@ -533,10 +542,11 @@ _ROPE_ARGS = struct.Struct("@12P15q11if")
 _ATTN_ARGS = struct.Struct("@9P11q13if")
 _ATTN_OPTIONS = struct.Struct("@8i")
 _NORMS_ARGS = struct.Struct("@9P8q2i3fi")
+_GATED_ARGS = struct.Struct("@10P9q6i")
 _LOGPROB_ARGS = struct.Struct("@7P6q4ifi")
 for _packed, _struct in ((_NORM_ARGS, pw_norm_args), (_QUANT_ARGS, pw_quant_args), (_LINEAR_ARGS, pw_linear_args),
                          (_ROPE_ARGS, pw_rope_args), (_ATTN_ARGS, pw_attn_args), (_ATTN_OPTIONS, pw_attn_options),
-                         (_NORMS_ARGS, pw_norms_args), (_LOGPROB_ARGS, pw_logprob_args)):
+                         (_NORMS_ARGS, pw_norms_args), (_GATED_ARGS, pw_gated_args), (_LOGPROB_ARGS, pw_logprob_args)):
     assert _packed.size == ctypes.sizeof(_struct)
 
 
@@ -736,6 +746,36 @@ def pw_norm_add_norm(x: torch.Tensor, residual: torch.Tensor, eps: float, post_w
     args = _NORMS_ARGS.pack(xp, rp, pp, gp, wp, rop, yp, qp, sp, xs, rs, gs, ros, ys, qs, ss, rows, cols, dt, eps,
                             residual_scale, block_scale, 0)
     _check(lib().pw_norm_add_norm(args, _queue(stream, dev)))
+
+
+def pw_fp8_gated_linear(a: torch.Tensor, a_scale: torch.Tensor, gate: torch.Tensor, gate_scale: torch.Tensor,
+                        up: torch.Tensor, up_scale: torch.Tensor, status: torch.Tensor, y: Optional[torch.Tensor] = None,
+                        q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                        activation: int = PW_ACT_SILU, stream=None) -> None:
+    """h [M][N] = act(a gate^T) * (a up^T) of e4m3 codes a [M][K], gate and up
+    [N][K] with scales as in pw_fp8_linear; `y` receives h (fp16 or bf16),
+    and/or `q` its e4m3 codes with `scale` [M][ceil(N/128)]."""
+    dt, dev = PW_DTYPE_F16 if y is None else _dtype16(y, "y"), a.get_device()
+    M, K = a.shape
+    N = gate.shape[0]
+    kb, nb = -(-K // 128), -(-N // 128)
+    ap, lda = _matrix(a, M, K, _CODES, "a", dev)
+    gp, ldg = _matrix(gate, N, K, _CODES, "gate", dev)
+    up_, ldu = _matrix(up, N, K, _CODES, "up", dev)
+    sap, sa = _matrix(a_scale, M, kb, _F32, "a_scale", dev)
+    sgp, sg = _matrix(gate_scale, nb, kb, _F32, "gate_scale", dev)
+    sup, su = _matrix(up_scale, nb, kb, _F32, "up_scale", dev)
+    yp, ldy = (0, 0) if y is None else _matrix(y, M, N, (y.dtype,), "y", dev)
+    qp, ldq = _matrix(q, M, N, _CODES, "q", dev)
+    sp, ss = _matrix(scale, M, nb, _F32, "scale", dev)
+    # a single row may have any stride: the row's own alignment is what counts
+    if M == 1:
+        lda, ldq = (lda + 15) // 16 * 16, (ldq + 15) // 16 * 16
+    if N == 1:
+        ldg, ldu = (ldg + 15) // 16 * 16, (ldu + 15) // 16 * 16
+    args = _GATED_ARGS.pack(ap, sap, gp, sgp, up_, sup, yp, qp, sp, _status(status, dev), lda, sa, ldg, sg, ldu, su, ldy, ldq,
+                            ss, M, N, K, dt, activation, 0)
+    _check(lib().pw_fp8_gated_linear(args, _queue(stream, dev)))
 
 
 def pw_token_logprobs(logits: torch.Tensor, targets: Optional[torch.Tensor] = None,

@@ -682,6 +682,41 @@ typedef struct pw_norms_args {
 } pw_norms_args;
 int pw_norm_add_norm(const pw_norms_args* args, void* stream);
 
+/* A gated feed-forward block up to its down projection:
+ *   h[m][n] = act(sum_k a[m][k] gate[n][k]) * sum_k a[m][k] up[n][k]
+ * with the groups and scales of pw_fp8_linear (its requirements hold for a and both
+ * weights; rows and scales at 16-byte addresses take the wide paths).  The
+ * weights may be the two halves of one matrix, where n % 128 == 0 puts each in
+ * blocks of its own.
+ *  act           PW_ACT_SILU      g / (1 + e^-g)
+ *                PW_ACT_GELU_TANH g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
+ *  y             [m][n] in `dtype`, or NULL
+ *  q, scale      [m][n] e4m3 and fp32 [m][ceil(n/128)], or both NULL: h in 8
+ *                bits (the unrounded h), as pw_quantize_fp8 with block_rows 1: a
+ *                and a_scale of the down projection.  Rows of q at 16-byte
+ *                addresses are written in wide accesses.
+ * At least one of y and q.  m up to 2^20, n up to 2^23, k up to 2^24. */
+#define PW_ACT_SILU 0
+#define PW_ACT_GELU_TANH 1
+typedef struct pw_gated_args {
+  const uint8_t* a;
+  const float* a_scale;
+  const uint8_t* gate;
+  const float* gate_scale;
+  const uint8_t* up;
+  const float* up_scale;
+  void* y;
+  uint8_t* q;
+  float* scale;
+  int32_t* status;
+  int64_t lda, a_scale_stride, ld_gate, gate_scale_stride, ld_up, up_scale_stride, ldy, ldq, scale_stride;
+  int32_t m, n, k;
+  int32_t dtype;
+  int32_t activation;
+  int32_t reserved;
+} pw_gated_args;
+int pw_fp8_gated_linear(const pw_gated_args* args, void* stream);
+
 /* From the logits of next tokens, by rows, with z = scale * logit (scale: the
  * reciprocal of a temperature) and p = softmax(z):
  *   lse = ln sum e^z,   log p(t) = z_t - lse,   entropy = -sum p ln p

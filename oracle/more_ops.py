@@ -39,3 +39,10 @@ def token_logprobs(logits, targets, top, scale):
             out[i, j] = 0.0 if t < 0 else lp[i, t] if t < vocab else np.nan
     ids = np.argsort(-logits, axis=1, kind="stable")[:, :top]
     return out, lse[:, 0], entropy, ids, np.take_along_axis(lp, ids, axis=1)
+
+
+def activation(g, kind):
+    """(act(g), the magnitude of its exponent's argument)"""
+    t = g if kind == "silu" else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+    e = np.exp(-np.abs(t))
+    return g * np.where(t >= 0, 1, e) / (1 + e), np.abs(t)

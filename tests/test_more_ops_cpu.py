@@ -149,3 +149,35 @@ def test_attention_option_refusals(L, kw):
     assert _attention(L, **kw) == pw.PW_ERR_INVALID_ARG and "paged_attention" in pw.pw_last_error()
     assert _attention(L, sinks=4) == 0                                   # no tokens
     assert L.pw_paged_attention_ex(None, None, FAKE, 1 << 30, None) == pw.PW_ERR_INVALID_ARG
+
+
+def test_oracle_activations():
+    g = np.linspace(-30, 30, 101)
+    t = torch.from_numpy(g)
+    v, _ = ref.activation(g, "silu")
+    assert np.allclose(v, torch.nn.functional.silu(t).numpy(), rtol=1e-12)
+    v, _ = ref.activation(g, "gelu_tanh")
+    # (1 + tanh x cancels where x is far below 0: 2^-52 of g)
+    assert np.allclose(v, torch.nn.functional.gelu(t, approximate="tanh").numpy(), rtol=1e-12, atol=1e-14)
+
+
+def _gated(L, **kw):
+    return _call(L.pw_fp8_gated_linear, pw.pw_gated_args, dict(
+        a=FAKE, lda=256, a_scale=FAKE, a_scale_stride=2, gate=FAKE, ld_gate=256, gate_scale=FAKE, gate_scale_stride=2, up=FAKE,
+        ld_up=256, up_scale=FAKE, up_scale_stride=2, m=4, n=128, k=256, dtype=0, y=FAKE, ldy=128, q=FAKE, ldq=128, scale=FAKE,
+        scale_stride=1, status=FAKE), kw)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), -2), (dict(activation=2), -2), (dict(activation=-1), -2), (dict(m=-1), -1), (dict(n=0), -1), (dict(k=0), -1),
+    (dict(m=(1 << 20) + 1), -2), (dict(lda=240), -1), (dict(ld_gate=240), -1), (dict(ld_up=240), -1), (dict(ldy=127), -1),
+    (dict(ldq=127), -1), (dict(scale_stride=0), -1), (dict(a_scale_stride=1), -1), (dict(gate_scale_stride=1), -1),
+    (dict(up_scale_stride=1), -1), (dict(a=None), -1), (dict(a_scale=None), -1), (dict(gate=None), -1), (dict(gate_scale=None), -1),
+    (dict(up=None), -1), (dict(up_scale=None), -1), (dict(status=None), -1), (dict(q=None), -1), (dict(scale=None), -1),
+    (dict(y=None, q=None, scale=None), -1), (dict(a=FAKE + 8), -1), (dict(gate=FAKE + 8), -1), (dict(up=FAKE + 4), -1),
+    (dict(lda=264), -1), (dict(ld_gate=257), -1), (dict(ld_up=264), -1), (dict(a_scale=FAKE + 1), -1), (dict(scale=FAKE + 2), -1),
+    (dict(y=FAKE + 1), -1), (dict(status=FAKE + 2), -1), (dict(ld_up=1 << 39), -2), (dict(ldy=1 << 40), -2)])
+def test_gated_refusals(L, kw, code):
+    assert _gated(L, **kw) == code and "fp8_gated_linear" in pw.pw_last_error()
+    assert L.pw_fp8_gated_linear(None, None) == -1
+    assert _gated(L, m=0, a=None, y=None, q=None, scale=None, status=None) == 0
