@@ -10,9 +10,9 @@
 
 namespace {
 
-using pw::kVec;
+using pw::Access;
 
-constexpr int kMaxCols = 32768;       // 512 threads x 8 chunks
+constexpr int kMaxCols = 32768;       // 512 threads x 64 columns
 
 struct NormsParams {
   const void* x;
@@ -28,192 +28,336 @@ struct NormsParams {
   int64_t rows;
   int cols;
   float eps, res_scale, block_scale;
-  bool wide_q;      // rows of q start at 8-byte addresses
+  int q_align;      // 16 or 8: rows of q start at such addresses; 1 otherwise
 };
 
-// The sum over a CTA's threads, for all of them; `part` is not written again
-// before another barrier of the CTA.
-__device__ __forceinline__ float block_sum(float sum, float* part) {
-  const int lane = threadIdx.x & 31;
+constexpr int kMaxWarps = 16;
+
+// The sum over a CTA's threads, for all of them.  `part` (of the warps, zeros
+// behind them) is not written again before another barrier of the CTA.
+__device__ __forceinline__ float block_sum(uint64_t two, float* part) {
+  float lo, hi;
+  pw::unpack_f32x2(two, lo, hi);
+  float sum = lo + hi;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) part[threadIdx.x >> 5] = sum;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
   __syncthreads();
-  sum = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : 0.0f;
+  sum = 0.0f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  for (int i = 0; i < kMaxWarps / 4; ++i) {
+    if (128 * i >= static_cast<int>(blockDim.x)) break;
+    const float4 v = reinterpret_cast<const float4*>(part)[i];
+    sum += (v.x + v.y) + (v.z + v.w);
+  }
   return sum;
 }
+__device__ __forceinline__ uint64_t both(float v) { return pw::pack_f32x2(__float_as_uint(v), __float_as_uint(v)); }
 
-// A CTA takes every gridDim-th row.  A thread holds a unit of 8 values of each
-// of kChunks chunks in registers, so a row is read once, and loads the next row
-// before the reductions of this one, so that copies are always under way.  The
-// row vectors (weights, gate) stay in registers where a row has few chunks, and
-// come from the L1 cache again for every row otherwise.  Rows of 8 chunks (more
-// than 16384 columns) fill the registers: their loads are not ahead.
-constexpr int most_threads(int chunks) { return chunks == 1 ? 1024 : chunks == 2 ? 384 : 512; }
-template <typename T, int kChunks, bool kAligned, bool kMatrix>
-__global__ void __launch_bounds__(most_threads(kChunks), kChunks == 2 ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
-  constexpr bool kKeep = kChunks <= 2, kAhead = kChunks < 8;
-  __shared__ float sums[2][2][32];   // two rows in turn, two sums: one barrier a sum
+// A CTA takes every gridDim-th row.  A thread holds 16 neighbouring columns of each
+// of kParts parts of the row in registers, so a row is read once, and starts the
+// loads of the next row as soon as a register is free, so that copies are always
+// under way.  The vectors of a row's columns (block_scale * post_weight * gate,
+// and weight) wait as 32-bit numbers in shared memory, where each thread finds its
+// own (kSame, whose columns move with the row: [column % 16][column / 16], so that
+// neighbouring threads find neighbouring words).  Rows of more than 16384 columns fill the registers and more: they read the
+// vectors from the L1 cache and load nothing ahead.
+// Arithmetic in packed pairs: with single instructions the kernel was bound by
+// their number (39 a value; 8192 x 6144 to e4m3 102 us).
+template <typename T, int kParts, Access kAccess, bool kMatrix>
+__global__ void __launch_bounds__(512, kParts == 1 && !kMatrix ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
+  constexpr bool kKeep = kParts <= 2, kAhead = kParts <= 2, kSame = kAccess == Access::kSame;
+  static_assert(!kSame || kKeep, "moving columns find the vectors in shared memory");
+  __shared__ __align__(16) float sums[2][2][kMaxWarps];   // two rows in turn, two sums: one barrier a sum
+  extern __shared__ __align__(16) uint64_t vectors[];     // [kParts][2][4][threads] of two pairs
+  __shared__ uint32_t tops[kSame ? 2 : 1][kSame ? kParts * 32 * kMaxWarps * 16 / pw::kGroup + 1 : 1];   // of the groups, two rows in turn
   const int tid = threadIdx.x, nthr = blockDim.x;
-  uint4 x[kChunks], res[kChunks], gate[kChunks], post[kChunks], w[kChunks];
-  auto col = [&](int c) { return (c * nthr + tid) * kVec; };
+  const int cells = kParts * nthr + 1;   // kSame: of a line of the vectors
+  if constexpr (kSame) {
+    for (int i = tid; i < static_cast<int>(sizeof(tops) / 4); i += nthr) (&tops[0][0])[i] = 0u;
+    for (int i = tid; i < 2 * 16 * cells; i += nthr) reinterpret_cast<float*>(vectors)[i] = 0.0f;
+    __syncthreads();
+  }
+  if (tid < 4 * kMaxWarps) (&sums[0][0][0])[tid] = 0.0f;
+  int shift = 0;   // kSame: of the row
+  auto shift_of = [&](int64_t row) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + row * p.x_stride) >> 1 & 15);
+  };
+  auto col = [&](int c) { return (c * nthr + tid) * 16 - (kSame ? shift : 0); };
+  auto at = [&](const void* base, int64_t row, int64_t stride) { return static_cast<const T*>(base) + row * stride; };
   auto load = [&](const void* base, int64_t row, int64_t stride, int c) {
-    const T* at = static_cast<const T*>(base) + row * stride;
-    return kAligned ? pw::load8<T, true>(at, col(c), p.cols) : pw::load_granule(at, col(c) - pw::row_shift(at), p.cols);
+    const int first = kSame ? (c * nthr + tid) * 16 - shift_of(row) : col(c);   // (of a row ahead: its own shift)
+    return pw::load16<T, kAccess>(at(base, row, stride), first, p.cols);
   };
-  auto unit = [&](const uint4& v, const void* base, int64_t row, int64_t stride, int c, float (&t)[kVec]) {
-    const T* at = static_cast<const T*>(base) + row * stride;
-    pw::unpack8<T>(kAligned ? v : pw::unit_of(v, at, col(c), p.cols), t);
+  auto values = [&](const pw::Sixteen& v, const void* base, int64_t row, int64_t stride, int c, uint64_t (&t)[8]) {
+    pw::unpack16<T>(pw::columns16<T, kAccess>(v, at(base, row, stride), col(c), p.cols), t);
   };
-  auto store = [&](void* base, int64_t row, int64_t stride, int c, const float (&t)[kVec]) {
-    T* at = static_cast<T*>(base) + row * stride;
-    if (kAligned)
-      pw::store8<T, true>(at, col(c), p.cols, t);
-    else
-      pw::store_unit(at, col(c), p.cols, t);
+  auto store = [&](void* base, int64_t row, int64_t stride, int c, const uint64_t (&t)[8]) {
+    pw::store16<T, kAccess>(static_cast<T*>(base) + row * stride, col(c), p.cols, pw::pack16<T>(t));
   };
-  auto load_row = [&](int64_t row) {
+  // block_scale * post * gate (which = 0) or the weight (1) at the thread's columns, from memory
+  auto vector = [&](int which, int c, uint64_t (&t)[8]) {
+    const uint64_t scale = both(which ? 1.0f : p.block_scale);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      x[c] = load(p.x, row, p.x_stride, c);
-      res[c] = load(p.res, row, p.res_stride, c);
-      if (kMatrix) gate[c] = load(p.gate, row, p.gate_stride, c);
+    for (int i = 0; i < 8; ++i) t[i] = scale;
+    const void* of[2] = {which ? p.w : p.post, which || kMatrix ? nullptr : p.gate};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!of[k]) continue;
+      const T* v = static_cast<const T*>(of[k]);
+      pw::Sixteen u;
+      if (kAccess == Access::kWide || kAccess == Access::kHalves) {
+        u = pw::load16<T, Access::kHalves>(v, col(c), p.cols);
+      } else {
+        u.lo = pw::load8<T, false>(v, col(c), p.cols);
+        u.hi = pw::load8<T, false>(v, col(c) + pw::kVec, p.cols);
+      }
+      uint64_t f[8];
+      pw::unpack16<T>(u, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = pw::mul_f32x2(t[i], f[i]);
     }
   };
-  auto vector = [&](const void* base, int c) {
-    const T* v = static_cast<const T*>(base);
-    if (kAligned || ((reinterpret_cast<uintptr_t>(v) & 15) == 0 && col(c) + kVec <= p.cols)) return pw::load8<T, true>(v, col(c), p.cols);
-    return pw::load8<T, false>(v, col(c), p.cols);
+  auto kept = [&](int which, int c, uint64_t (&t)[8]) {
+    if constexpr (!kKeep) {
+      vector(which, c, t);
+    } else if constexpr (kSame) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        float two[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int k = i + j - shift;   // the cell before has the columns below 0
+          two[j] = reinterpret_cast<const float*>(vectors)[(which * 16 + (k & 15)) * cells + c * nthr + tid + (k >= 0)];
+        }
+        t[i / 2] = pw::pack_f32x2(__float_as_uint(two[0]), __float_as_uint(two[1]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const ulonglong2 v = reinterpret_cast<const ulonglong2*>(vectors)[((c * 2 + which) * 4 + i) * nthr + tid];
+        t[2 * i] = v.x;
+        t[2 * i + 1] = v.y;
+      }
+    }
   };
-  if (kAhead) load_row(blockIdx.x);
+  pw::Sixteen x[kParts], res[kParts], gate[kParts];
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int c = 0; c < kParts; ++c) {
+    if (!kAhead) break;
+    x[c] = load(p.x, row, p.x_stride, c);
+    res[c] = load(p.res, row, p.res_stride, c);
+    if (kMatrix) gate[c] = load(p.gate, row, p.gate_stride, c);
+  }
   if (kKeep) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      if (p.post) post[c] = vector(p.post, c);
-      if (!kMatrix && p.gate) gate[c] = vector(p.gate, c);
-      if (p.w) w[c] = vector(p.w, c);
-    }
+    for (int c = 0; c < kParts; ++c)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        uint64_t t[8];
+        vector(which, c, t);
+        if constexpr (kSame) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float two[2];
+            pw::unpack_f32x2(t[i], two[0], two[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (col(c) + 2 * i + j < p.cols)
+                reinterpret_cast<float*>(vectors)[(which * 16 + 2 * i + j) * cells + c * nthr + tid + 1] = two[j];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<ulonglong2*>(vectors)[((c * 2 + which) * 4 + i) * nthr + tid] = make_ulonglong2(t[2 * i], t[2 * i + 1]);
+        }
+      }
   }
+  __syncthreads();
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    if (!kAhead) load_row(row);
-    float v[kChunks][kVec];
-    uint4 r_in[kChunks], g_in[kChunks];
+  const uint64_t res_scale = both(p.res_scale);
+  for (int turn = 0; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const bool more = kAhead && row + gridDim.x < p.rows;
+    if (kSame) shift = shift_of(row);
+    uint64_t v[kParts][8];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      unit(x[c], p.x, row, p.x_stride, c, v[c]);
-      r_in[c] = res[c];
-      if (kMatrix) g_in[c] = gate[c];
+    for (int c = 0; c < kParts; ++c) {
+      if (!kAhead) x[c] = load(p.x, row, p.x_stride, c);
+      values(x[c], p.x, row, p.x_stride, c, v[c]);
+      if (more) x[c] = load(p.x, row + gridDim.x, p.x_stride, c);
     }
-    if (kAhead && row + gridDim.x < p.rows) load_row(row + gridDim.x);
-    float factor = p.block_scale;
+    uint64_t factor = both(1.0f);
     if (p.post) {
-      // the sums of squares in 32 bits: 8 x kChunks terms a thread, then a tree
-      float sum = 0.0f;
+      // the sums of squares in 32 bits: 8 x kParts terms in two sums a thread, then a tree
+      uint64_t sum = 0;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
+      for (int c = 0; c < kParts; ++c)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum += v[c][i] * v[c][i];
-      factor *= rsqrtf(block_sum(sum, sums[turn][0]) * inv_cols + p.eps);
+        for (int i = 0; i < 8; ++i) sum = pw::fma_f32x2(v[c][i], v[c][i], sum);
+      factor = both(rsqrtf(block_sum(sum, sums[turn][0]) * inv_cols + p.eps));
     }
-    float sum = 0.0f;
+    uint64_t sum = 0;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float t[kVec];
+    for (int c = 0; c < kParts; ++c) {
+      uint64_t t[8];
+      kept(0, c, t);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[c][i] *= factor;
-      if (p.post) {
-        pw::unpack8<T>(kKeep ? post[c] : vector(p.post, c), t);
+      for (int i = 0; i < 8; ++i) v[c][i] = pw::mul_f32x2(pw::mul_f32x2(v[c][i], factor), t[i]);
+      if (kMatrix) {
+        if (!kAhead) gate[c] = load(p.gate, row, p.gate_stride, c);
+        values(gate[c], p.gate, row, p.gate_stride, c, t);
+        if (more) gate[c] = load(p.gate, row + gridDim.x, p.gate_stride, c);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[c][i] *= t[i];
+        for (int i = 0; i < 8; ++i) v[c][i] = pw::mul_f32x2(v[c][i], t[i]);
       }
-      if (p.gate) {
-        if (kMatrix)
-          unit(g_in[c], p.gate, row, p.gate_stride, c, t);
-        else
-          pw::unpack8<T>(kKeep ? gate[c] : vector(p.gate, c), t);
+      if (!kAhead) res[c] = load(p.res, row, p.res_stride, c);
+      values(res[c], p.res, row, p.res_stride, c, t);
+      if (more) res[c] = load(p.res, row + gridDim.x, p.res_stride, c);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[c][i] *= t[i];
-      }
-      unit(r_in[c], p.res, row, p.res_stride, c, t);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        v[c][i] = fmaf(p.res_scale, t[i], v[c][i]);
-        sum += v[c][i] * v[c][i];
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = pw::fma_f32x2(res_scale, t[i], v[c][i]);
+        sum = pw::fma_f32x2(v[c][i], v[c][i], sum);
       }
     }
-    // (after every read of this row: residual_out may be the residual)
     if (p.res_out) {
-      if (!kAligned) __syncthreads();
+      // the results may lie over x or the residual, whose granules neighbouring warps share
+      if (kAccess == Access::kShifted) __syncthreads();
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) store(p.res_out, row, p.res_out_stride, c, v[c]);
+      for (int c = 0; c < kParts; ++c) store(p.res_out, row, p.res_out_stride, c, v[c]);
     }
     if (!p.y && !p.q) continue;
-    const float rs = rsqrtf(block_sum(sum, sums[turn][1]) * inv_cols + p.eps);
+    factor = both(rsqrtf(block_sum(sum, sums[turn][1]) * inv_cols + p.eps));
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float t[kVec];
-      pw::unpack8<T>(kKeep ? w[c] : vector(p.w, c), t);
+    for (int c = 0; c < kParts; ++c) {
+      uint64_t t[8];
+      kept(1, c, t);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[c][i] = v[c][i] * rs * t[i];
+      for (int i = 0; i < 8; ++i) v[c][i] = pw::mul_f32x2(pw::mul_f32x2(v[c][i], factor), t[i]);
       if (p.y) store(p.y, row, p.y_stride, c, v[c]);
+      if (kSame && p.q) continue;   // below
       if (p.q) {
-        const float s = pw::group_scale(v[c]);
-        if (col(c) < p.cols && (tid & 15) == 0) p.scale[row * p.scale_stride + col(c) / pw::kGroup] = s;
-        uint8_t* q = p.q + row * p.q_stride;
-        if (kAligned || (p.wide_q && col(c) + kVec <= p.cols))
-          pw::store8_e4m3<true>(q, col(c), p.cols, v[c], pw::Divisor(s));
-        else
-          pw::store8_e4m3<false>(q, col(c), p.cols, v[c], pw::Divisor(s));
+        // 8 neighbouring threads hold a group
+        float f[16], top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          pw::unpack_f32x2(v[c][i], f[2 * i], f[2 * i + 1]);
+          top = pw::max3_nan(top, fabsf(f[2 * i]), fabsf(f[2 * i + 1]));
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
+        if (col(c) < p.cols && (tid & 7) == 0) p.scale[row * p.scale_stride + col(c) / pw::kGroup] = s;
+        const pw::Divisor by(s);
+        uint32_t code[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = pw::e4m3x4(by(f[4 * i]), by(f[4 * i + 1]), by(f[4 * i + 2]), by(f[4 * i + 3]));
+        pw::store_codes16(p.q + row * p.q_stride, col(c), p.cols, code, p.q_align);
+      }
+    }
+    if constexpr (kSame) {
+      if (!p.q) continue;
+      // A thread's columns belong to one group or two; each group's largest
+      // magnitude by way of shared memory (as whole numbers, which rank the same
+      // way, NaN above infinity).
+      auto split_of = [&](int c) { return (col(c) + 15) / pw::kGroup * pw::kGroup - col(c); };   // columns before the second one
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        if (col(c) >= p.cols) continue;
+        const int split = split_of(c), group = (col(c) + 15) / pw::kGroup;
+        float before = 0.0f, top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float two[2];
+          pw::unpack_f32x2(v[c][i / 2], two[0], two[1]);
+          const float f = fabsf(two[i & 1]);
+          before = pw::max_nan(before, i < split ? f : 0.0f);
+          top = pw::max_nan(top, i < split ? 0.0f : f);
+        }
+        if (col(c) + max(split, 0) < p.cols) atomicMax(&tops[turn][group], __float_as_uint(top));
+        if (split > 0 && col(c) >= 0) atomicMax(&tops[turn][group - 1], __float_as_uint(before));
+      }
+      __syncthreads();
+      for (int i = tid; i < static_cast<int>(sizeof(tops[0]) / 4); i += nthr) tops[turn ^ 1][i] = 0u;   // read to the end a row ago
+#pragma unroll
+      for (int c = 0; c < kParts; ++c) {
+        if (col(c) >= p.cols) continue;
+        const int split = split_of(c), group = (col(c) + 15) / pw::kGroup;
+        auto scale_of = [&](int g) { return pw::max_nan(__uint_as_float(tops[turn][g]) / pw::kE4m3Max, pw::kMinScale); };
+        const float s = scale_of(group);
+        const pw::Divisor by(s), by_before(split > 0 && group > 0 ? scale_of(group - 1) : s);
+        if (split >= 0 && split < 16 && col(c) + split < p.cols) p.scale[row * p.scale_stride + group] = s;   // it begins here
+        uint32_t code[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[4];
+          pw::unpack_f32x2(v[c][2 * i], f[0], f[1]);
+          pw::unpack_f32x2(v[c][2 * i + 1], f[2], f[3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = 4 * i + j < split ? by_before(f[j]) : by(f[j]);
+          code[i] = pw::e4m3x4(f[0], f[1], f[2], f[3]);
+        }
+        pw::store_codes16(p.q + row * p.q_stride, col(c), p.cols, code, 16);
       }
     }
   }
 }
 
-template <typename T, int kChunks, bool kAligned, bool kMatrix>
-int launch_chunks(const NormsParams& p, int threads, int sms, cudaStream_t s) {
-  // as many CTAs as run at once
-  static int regs = 0;
-  if (!regs) {
-    cudaFuncAttributes at{};
-    PW_CUDA_TRY(cudaFuncGetAttributes(&at, norms_kernel<T, kChunks, kAligned, kMatrix>));
-    regs = (at.numRegs + 7) & ~7;
+template <typename T, int kParts, Access kAccess, bool kMatrix>
+int launch_parts(const NormsParams& p, int threads, int sms, cudaStream_t s) {
+  const size_t smem = kParts <= 2 ? 2 * 64 * (static_cast<size_t>(kParts) * threads + 1) : 0;
+  constexpr int kDevs = 64;
+  static int known[kDevs][kMaxWarps + 1] = {};   // CTAs that an SM runs at once, by the number of warps
+  int dev = 0;
+  PW_CUDA_TRY(cudaGetDevice(&dev));
+  int at_once = dev < kDevs ? known[dev][threads / 32] : 0;
+  if (!at_once) {
+    if (kParts <= 2)
+      PW_CUDA_TRY(cudaFuncSetAttribute(norms_kernel<T, kParts, kAccess, kMatrix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       2 * 64 * (kParts * 32 * kMaxWarps + 1)));
+    PW_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&at_once, norms_kernel<T, kParts, kAccess, kMatrix>, threads, smem));
+    if (at_once < 1) return pw::set_error(PW_ERR_CUDA, "norm_add_norm: the kernel does not fit an SM");
+    if (dev < kDevs) known[dev][threads / 32] = at_once;
   }
-  const int by_regs = 65536 / (regs * threads), by_threads = 2048 / threads;
-  const int at_once = by_regs < by_threads ? (by_regs < 1 ? 1 : by_regs) : by_threads;
   const int64_t most = static_cast<int64_t>(sms) * at_once;
-  norms_kernel<T, kChunks, kAligned, kMatrix><<<static_cast<unsigned>(p.rows < most ? p.rows : most), threads, 0, s>>>(p);
+  norms_kernel<T, kParts, kAccess, kMatrix><<<static_cast<unsigned>(p.rows < most ? p.rows : most), threads, smem, s>>>(p);
   PW_CUDA_TRY(cudaGetLastError());
   return PW_OK;
 }
 
-template <typename T, bool kAligned, bool kMatrix>
+template <typename T, Access kAccess, bool kMatrix>
 int launch_rows(const NormsParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
-  // Few rows: one chunk a thread where 1024 threads suffice, for the shortest
-  // way through a row.  Many: up to 512 threads, so that several CTAs an SM are
-  // at different stages.
-  const int units = (p.cols + kVec - 1) / kVec, most = p.rows <= sms ? 1024 : 512;
-  int chunks = 1;
-  while ((units + chunks - 1) / chunks > (chunks > 1 ? most_threads(chunks) : most)) chunks *= 2;
-  const int threads = ((units + chunks - 1) / chunks + 31) & ~31;
-  switch (chunks) {
-    case 1: return launch_chunks<T, 1, kAligned, kMatrix>(p, threads, sms, s);
-    case 2: return launch_chunks<T, 2, kAligned, kMatrix>(p, threads, sms, s);
-    case 4: return launch_chunks<T, 4, kAligned, kMatrix>(p, threads, sms, s);
-    default: return launch_chunks<T, 8, kAligned, kMatrix>(p, threads, sms, s);
+  const int units = (p.cols + (kAccess == Access::kSame ? 30 : 15)) / 16;   // 16 columns each, or up to 15 before them
+  int parts = 1;
+  while ((units + parts - 1) / parts > 32 * kMaxWarps) parts *= 2;
+  const int threads = ((units + parts - 1) / parts + 31) & ~31;
+  switch (parts) {
+    case 1: return launch_parts<T, 1, kAccess, kMatrix>(p, threads, sms, s);
+    case 2: return launch_parts<T, 2, kAccess, kMatrix>(p, threads, sms, s);
+    default:
+      if constexpr (kAccess == Access::kSame)
+        return pw::set_error(PW_ERR_UNSUPPORTED, "norm_add_norm: moving columns in four parts");   // not chosen
+      else
+        return launch_parts<T, 4, kAccess, kMatrix>(p, threads, sms, s);
   }
 }
 
-template <typename T>
-int launch(const NormsParams& p, bool aligned, cudaStream_t s) {
+template <typename T, Access kAccess>
+int launch_access(const NormsParams& p, cudaStream_t s) {
   const bool matrix = p.gate && p.gate_stride != 0 && p.rows > 1;
-  if (aligned) return matrix ? launch_rows<T, true, true>(p, s) : launch_rows<T, true, false>(p, s);
-  return matrix ? launch_rows<T, false, true>(p, s) : launch_rows<T, false, false>(p, s);
+  return matrix ? launch_rows<T, kAccess, true>(p, s) : launch_rows<T, kAccess, false>(p, s);
+}
+
+template <typename T>
+int launch(const NormsParams& p, Access access, cudaStream_t s) {
+  switch (access) {
+    case Access::kWide: return launch_access<T, Access::kWide>(p, s);
+    case Access::kHalves: return launch_access<T, Access::kHalves>(p, s);
+    case Access::kSame: return launch_access<T, Access::kSame>(p, s);
+    default: return launch_access<T, Access::kShifted>(p, s);
+  }
 }
 
 }  // namespace
@@ -273,11 +417,31 @@ extern "C" int pw_norm_add_norm(const pw_norms_args* args, void* stream) {
   p.eps = a.eps;
   p.res_scale = a.residual_scale;
   p.block_scale = a.block_scale;
-  p.wide_q = pw::codes_aligned(a.q, a.q_stride);
-  const bool aligned = pw::rows_aligned(a.x, a.x_stride, a.cols) && pw::rows_aligned(a.residual, a.residual_stride, a.cols) &&
-                       pw::rows_aligned(a.post_weight, 0, a.cols) && pw::rows_aligned(a.gate, a.gate_stride, a.cols) &&
-                       pw::rows_aligned(a.weight, 0, a.cols) && pw::rows_aligned(a.residual_out, a.residual_out_stride, a.cols) &&
-                       pw::rows_aligned(a.y, a.y_stride, a.cols) && p.wide_q;
+  const struct { const void* ptr; int64_t stride; } matrices[] = {
+      {a.x, a.x_stride}, {a.residual, a.residual_stride}, {a.gate, a.gate_stride}, {a.residual_out, a.residual_out_stride},
+      {a.y, a.y_stride}};
+  const auto whole = [&](size_t bytes) {   // every row of every matrix in pieces of `bytes`, the vectors in halves
+    const int64_t values = static_cast<int64_t>(bytes) / 2;
+    if (a.cols % values) return false;
+    for (const auto& m : matrices)
+      if (m.ptr && (!pw::aligned(m.ptr, bytes) || m.stride % values)) return false;
+    return pw::aligned(a.post_weight, 16) && pw::aligned(a.weight, 16);
+  };
+  // Widths or strides of odd numbers of values, as in matrices of an odd width one
+  // beside the other in memory: every row starts at its own place of a 32-byte cell, the same in all
+  // matrices.  (A gate of one row is a vector.  Where a row takes four parts, the
+  // vectors do not wait in shared memory.)
+  const auto same = [&] {
+    const auto place = [](const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) / 2 % 16; };
+    for (const auto& m : matrices)
+      if (m.ptr && !(m.ptr == a.gate && (a.gate_stride == 0 || a.rows == 1)) &&
+          (place(m.ptr) != place(a.x) || (a.rows > 1 && (m.stride - a.x_stride) % 16)))
+        return false;
+    if (a.q && (reinterpret_cast<uintptr_t>(a.q) % 16 != place(a.x) || (a.rows > 1 && (a.q_stride - a.x_stride) % 16))) return false;
+    return (a.cols + 30) / 16 <= 2 * 32 * kMaxWarps;
+  };
+  const Access access = whole(32) ? Access::kWide : whole(16) ? Access::kHalves : same() ? Access::kSame : Access::kShifted;
+  p.q_align = pw::aligned(a.q, 16) && a.q_stride % 16 == 0 ? 16 : pw::aligned(a.q, 8) && a.q_stride % 8 == 0 ? 8 : 1;
   cudaStream_t s = pw::as_stream(stream);
-  return a.dtype == PW_DTYPE_F16 ? launch<__half>(p, aligned, s) : launch<__nv_bfloat16>(p, aligned, s);
+  return a.dtype == PW_DTYPE_F16 ? launch<__half>(p, access, s) : launch<__nv_bfloat16>(p, access, s);
 }

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import more_ops as ref
-from test_gpu_attn_half import DEV, DTYPES, IDS, TINY, U, _gpu, check_codes, draw, f64, gen, pw, within  # noqa: F401
+from test_gpu_attn_half import DEV, DTYPES, IDS, TINY, U, _gpu, draw, f64, gen, pw, within  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-5
@@ -19,6 +19,18 @@ EPS = 1e-5
 def bound_y(u, tiny, r, y, mag, w):
     rms = np.sqrt(np.mean(r * r, axis=1, keepdims=True) + EPS)
     return u * np.abs(y) * 1.01 + 2.0 ** -17 * (np.abs(y) + mag / rms * np.abs(w)) + tiny
+
+
+def check_q(q, sc, r, want, mag, w):
+    """The scales and codes of the 32-bit y: what it may be off by, in scales and then in codes."""
+    cols = want.shape[1]
+    off = bound_y(0.0, 0.0, r, want, mag, w)
+    top = np.stack([np.abs(want[:, c:c + 128]).max(1) for c in range(0, cols, 128)], 1)
+    slack = np.stack([off[:, c:c + 128].max(1) for c in range(0, cols, 128)], 1)
+    within(sc, np.maximum(top / 448, 2.0 ** -100), slack / 448 + top * 2.0 ** -30)
+    s = np.repeat(f64(sc), 128, 1)[:, :cols]
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want / s), 2.0 ** -6))) - 3)
+    within(q.view(torch.float8_e4m3fn).double(), want / s, 0.5 * step * 1.0001 + 2 * off / s)
 
 
 def inputs(rows, cols, dtype, seed=0):
@@ -50,14 +62,7 @@ def test_norm_add_norm(rows, cols, dtype):
                                          None if gate is None else f64(gate), a, b)
         within(ro, r, u * np.abs(r) * 1.01 + 2.0 ** -17 * mag + tiny)
         within(y, want, bound_y(u, tiny, r, want, mag, f64(w)))
-        # the scales and codes of the 32-bit y: what it may be off by, in scales and then in codes
-        off = bound_y(0.0, 0.0, r, want, mag, f64(w))
-        top = np.stack([np.abs(want[:, c:c + 128]).max(1) for c in range(0, cols, 128)], 1)
-        slack = np.stack([off[:, c:c + 128].max(1) for c in range(0, cols, 128)], 1)
-        within(sc, np.maximum(top / 448, 2.0 ** -100), slack / 448 + top * 2.0 ** -30)
-        s = np.repeat(f64(sc), 128, 1)[:, :cols]
-        step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want / s), 2.0 ** -6))) - 3)
-        within(q.double(), want / s, 0.5 * step * 1.0001 + 2 * off / s)
+        check_q(q, sc, r, want, mag, f64(w))
         # one output each, in place
         res2, x2, q2 = res.clone(), x.clone(), torch.empty(rows, cols, dtype=torch.uint8, device=DEV)
         pw.pw_norm_add_norm(x2, res2, EPS, post_weight=p, gate=gate, residual_scale=a, block_scale=b, residual_out=res2)
@@ -105,7 +110,45 @@ def test_strides_and_alignment(rows, cols, pads, shifts, dtype):
         room = torch.full((rows, pitch), 9, dtype=torch.uint8, device=DEV)
         sc2 = torch.empty_like(sc)
         pw.pw_norm_add_norm(xv, rv, EPS, post_weight=pv, weight=wv, gate=gv, residual_scale=0.5, q=room[:, :cols], scale=sc2)
-        assert torch.equal(room[:, :cols], q) and torch.equal(sc, sc2) and (room[:, cols:] == 9).all()
+        # (rows of codes that start elsewhere may change the accesses, and with them the order of the sums)
+        check_q(room[:, :cols], sc2, r, want, mag, f64(w))
+        assert (room[:, cols:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("cols,pitch", [(130, 131), (5, 16), (300, 304), (1000, 1001), (5121, 5121), (9000, 9016), (16383, 16383)])
+@pytest.mark.parametrize("shift", [0, 1, 9, 15])
+def test_rows_that_all_start_alike(cols, pitch, shift, dtype):
+    """Every matrix at the same place of its 32-byte cells, the codes too: groups of a scale that begin inside a cell."""
+    rows = 7
+    g, x, res, post, w = inputs(rows, cols, dtype, shift)
+    gate = draw(g, rows, cols, dtype=dtype)
+
+    def wide(t, fill=7):
+        buf = torch.full((rows * pitch + shift + 40,), fill, dtype=t.dtype, device=DEV)
+        v = buf[shift:shift + rows * pitch].view(rows, pitch)[:, :cols]
+        v.copy_(t)
+        return buf, v
+    (_, xv), (_, rv), (_, gv), (rob, ro), (yb, y) = (wide(t) for t in (x, res, gate, x * 0, x * 0))
+    qb, q = wide(torch.zeros(rows, cols, dtype=torch.uint8, device=DEV))
+    sc = torch.empty(rows, -(-cols // 128), device=DEV)
+    r, want, mag = ref.norm_add_norm(f64(x), f64(res), EPS, f64(post), f64(w), f64(gate), 0.5, 2.0)
+    for g_, outs in ((gv, dict(residual_out=ro, y=y, q=q, scale=sc)), (gv, dict(y=y)), (gv, dict(q=q, scale=sc))):
+        pw.pw_norm_add_norm(xv, rv, EPS, post_weight=post, weight=w, gate=g_, residual_scale=0.5, block_scale=2.0, **outs)
+    u, tiny = U[dtype], TINY[dtype]
+    within(ro, r, u * np.abs(r) * 1.01 + 2.0 ** -17 * mag + tiny)
+    within(y, want, bound_y(u, tiny, r, want, mag, f64(w)))
+    check_q(q, sc, r, want, mag, f64(w))
+    for b in (rob, yb, qb):
+        side = b[shift:shift + rows * pitch].view(rows, pitch)[:, cols:]
+        assert (side == 7).all() and (b[:shift] == 7).all() and (b[shift + rows * pitch:] == 7).all()
+    # in place, and a gate that is a row at an address of its own
+    want_y = torch.empty_like(x)
+    pw.pw_norm_add_norm(xv, rv, EPS, post_weight=post, weight=w, gate=gate[0], residual_out=ro, y=y)
+    pw.pw_norm_add_norm(x, res, EPS, post_weight=post, weight=w, gate=gate[0].clone(), residual_out=res, y=want_y)
+    within(y, f64(want_y), 2 * (u * np.abs(f64(want_y)) + tiny))   # both are rounded, by half a step each
+    pw.pw_norm_add_norm(xv, rv, EPS, post_weight=post, weight=w, gate=gate[0], residual_out=rv, y=xv)
+    assert torch.equal(rv, ro) and torch.equal(xv, y)
 
 
 def test_extremes():
