@@ -32,6 +32,10 @@ struct NormsParams {
 };
 
 constexpr int kMaxWarps = 16;
+// Rows of one part: two CTAs an SM, whose 64 registers a thread (with a gate for
+// every row 80) set the threads.
+constexpr int most_threads(int parts, bool matrix) { return parts == 1 && matrix ? 384 : 32 * kMaxWarps; }
+constexpr int line_floats(int parts) { return parts * 32 * kMaxWarps + 1; }
 
 // The sum over a CTA's threads, for all of them.  `part` (of the warps, zeros
 // behind them) is not written again before another barrier of the CTA.
@@ -60,23 +64,24 @@ __device__ __forceinline__ uint64_t both(float v) { return pw::pack_f32x2(__floa
 // under way.  The vectors of a row's columns (block_scale * post_weight * gate,
 // and weight) wait as 32-bit numbers in shared memory, where each thread finds its
 // own (kSame, whose columns move with the row: [column % 16][column / 16], so that
-// neighbouring threads find neighbouring words).  Rows of more than 16384 columns fill the registers and more: they read the
-// vectors from the L1 cache and load nothing ahead.
+// neighbouring threads find neighbouring words).  Rows of more than 16384 columns
+// fill the registers and more: they read the vectors from the L1 cache and load
+// nothing ahead.
 // Arithmetic in packed pairs: with single instructions the kernel was bound by
 // their number (39 a value; 8192 x 6144 to e4m3 102 us).
 template <typename T, int kParts, Access kAccess, bool kMatrix>
-__global__ void __launch_bounds__(512, kParts == 1 && !kMatrix ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
+__global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
   constexpr bool kKeep = kParts <= 2, kAhead = kParts <= 2, kSame = kAccess == Access::kSame;
   static_assert(!kSame || kKeep, "moving columns find the vectors in shared memory");
   __shared__ __align__(16) float sums[2][2][kMaxWarps];   // two rows in turn, two sums: one barrier a sum
   extern __shared__ __align__(16) uint64_t vectors[];     // [kParts][2][4][threads] of two pairs
   __shared__ uint32_t tops[kSame ? 2 : 1][kSame ? kParts * 32 * kMaxWarps * 16 / pw::kGroup + 1 : 1];   // of the groups, two rows in turn
   const int tid = threadIdx.x, nthr = blockDim.x;
-  const int cells = kParts * nthr + 1;   // kSame: of a line of the vectors
+  constexpr int kPitch = line_floats(kParts);   // kSame: of a line of the vectors, [which][16 lines][cells, from -1]
+  float* const lines = reinterpret_cast<float*>(vectors);
   if constexpr (kSame) {
     for (int i = tid; i < static_cast<int>(sizeof(tops) / 4); i += nthr) (&tops[0][0])[i] = 0u;
-    for (int i = tid; i < 2 * 16 * cells; i += nthr) reinterpret_cast<float*>(vectors)[i] = 0.0f;
-    __syncthreads();
+    if (tid < 32) lines[tid * kPitch] = 0.0f;
   }
   if (tid < 4 * kMaxWarps) (&sums[0][0][0])[tid] = 0.0f;
   int shift = 0;   // kSame: of the row
@@ -122,16 +127,13 @@ __global__ void __launch_bounds__(512, kParts == 1 && !kMatrix ? 2 : 1) norms_ke
     if constexpr (!kKeep) {
       vector(which, c, t);
     } else if constexpr (kSame) {
+      // columns below 16 cell belong to the cell before
+      const float* const here = lines + which * 16 * kPitch + c * nthr + tid + 1 - shift * kPitch;
+      const float* const before = here + 16 * kPitch - 1;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        float two[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int k = i + j - shift;   // the cell before has the columns below 0
-          two[j] = reinterpret_cast<const float*>(vectors)[(which * 16 + (k & 15)) * cells + c * nthr + tid + (k >= 0)];
-        }
-        t[i / 2] = pw::pack_f32x2(__float_as_uint(two[0]), __float_as_uint(two[1]));
-      }
+      for (int i = 0; i < 8; ++i)
+        t[i] = pw::pack_f32x2(__float_as_uint((2 * i < shift ? before : here)[2 * i * kPitch]),
+                              __float_as_uint((2 * i + 1 < shift ? before : here)[(2 * i + 1) * kPitch]));
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -163,9 +165,7 @@ __global__ void __launch_bounds__(512, kParts == 1 && !kMatrix ? 2 : 1) norms_ke
             float two[2];
             pw::unpack_f32x2(t[i], two[0], two[1]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (col(c) + 2 * i + j < p.cols)
-                reinterpret_cast<float*>(vectors)[(which * 16 + 2 * i + j) * cells + c * nthr + tid + 1] = two[j];
+            for (int j = 0; j < 2; ++j) lines[(which * 16 + 2 * i + j) * kPitch + c * nthr + tid + 1] = two[j];
           }
         } else {
 #pragma unroll
@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(512, kParts == 1 && !kMatrix ? 2 : 1) norms_ke
 
 template <typename T, int kParts, Access kAccess, bool kMatrix>
 int launch_parts(const NormsParams& p, int threads, int sms, cudaStream_t s) {
-  const size_t smem = kParts <= 2 ? 2 * 64 * (static_cast<size_t>(kParts) * threads + 1) : 0;
+  constexpr size_t kMost = kParts <= 2 ? 2 * 64 * static_cast<size_t>(line_floats(kParts)) : 0;
+  const size_t smem = kAccess == Access::kSame ? kMost : kParts <= 2 ? 2 * 64 * static_cast<size_t>(kParts) * threads : 0;
   constexpr int kDevs = 64;
   static int known[kDevs][kMaxWarps + 1] = {};   // CTAs that an SM runs at once, by the number of warps
   int dev = 0;
@@ -314,7 +315,7 @@ int launch_parts(const NormsParams& p, int threads, int sms, cudaStream_t s) {
   if (!at_once) {
     if (kParts <= 2)
       PW_CUDA_TRY(cudaFuncSetAttribute(norms_kernel<T, kParts, kAccess, kMatrix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       2 * 64 * (kParts * 32 * kMaxWarps + 1)));
+                                       static_cast<int>(kMost)));
     PW_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&at_once, norms_kernel<T, kParts, kAccess, kMatrix>, threads, smem));
     if (at_once < 1) return pw::set_error(PW_ERR_CUDA, "norm_add_norm: the kernel does not fit an SM");
     if (dev < kDevs) known[dev][threads / 32] = at_once;
@@ -331,7 +332,7 @@ int launch_rows(const NormsParams& p, cudaStream_t s) {
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   const int units = (p.cols + (kAccess == Access::kSame ? 30 : 15)) / 16;   // 16 columns each, or up to 15 before them
   int parts = 1;
-  while ((units + parts - 1) / parts > 32 * kMaxWarps) parts *= 2;
+  while ((units + parts - 1) / parts > most_threads(parts, kMatrix)) parts *= 2;
   const int threads = ((units + parts - 1) / parts + 31) & ~31;
   switch (parts) {
     case 1: return launch_parts<T, 1, kAccess, kMatrix>(p, threads, sms, s);
