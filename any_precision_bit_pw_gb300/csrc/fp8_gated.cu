@@ -17,29 +17,24 @@ using pw_fp8::launch_tile;
 using pw_fp8::load32;
 
 // Few tokens: the weights stream from memory into registers, as in the product of
-// one weight.  A CTA owns 16 columns of h: two MMA tiles of 8 rows of the gate's
-// weight and the same 8 of the other's, so that a thread's results hold g and u of
-// the same column.  A scale of the 8-bit result belongs to 128 columns: a cluster of
-// 8 CTAs, which tell each other their largest magnitudes.
-constexpr int kCols = 16, kSets = 2, kCluster = 8;
-
-template <typename T, int kGroups, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) gated_stream_kernel(const __grid_constant__ GatedParams p) {
-  constexpr int kTokens = 8 * kGroups;
-  __shared__ float red[kWarps][kSets][16][kTokens + 1];
-  __shared__ float h[kTokens][kCols];
+// one weight.  A warp takes 8 columns of h and every kSplits-th group of 128 columns
+// of K: one MMA tile is 8 rows of the gate's weight and the same 8 of the other's,
+// so that a thread's results hold g and u of the same column.  A CTA has kWide such
+// strips of 8 columns.  A scale of the 8-bit result belongs to 128 columns: a
+// cluster of CTAs, which tell each other their largest magnitudes.
+template <typename T, int kGroups, int kWide, int kSplits>
+__global__ void __launch_bounds__(32 * kWide * kSplits) gated_stream_kernel(const __grid_constant__ GatedParams p) {
+  constexpr int kTokens = 8 * kGroups, kCols = 8 * kWide, kThreads = 32 * kWide * kSplits;
+  constexpr int kCluster = pw::kGroup / kCols;
+  __shared__ float red[kSplits][2][kCols][kTokens + 1];   // of g and of u
+  __shared__ float h[kTokens][kCols + 1];
   __shared__ float top[kTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kCols;
-  const uint8_t* gate[kSets];
-  const uint8_t* up[kSets];
-  bool valid[kSets];
-#pragma unroll
-  for (int j = 0; j < kSets; ++j) {
-    valid[j] = n0 + 8 * j + g < p.N;
-    gate[j] = p.b + static_cast<int64_t>(n0 + 8 * j + g) * p.ldb;
-    up[j] = p.u + static_cast<int64_t>(n0 + 8 * j + g) * p.ldu;
-  }
+  const int strip = warp % kWide, split = warp / kWide;
+  const int n0 = blockIdx.x * kCols, n = n0 + 8 * strip + g;
+  const bool valid = n < p.N;
+  const uint8_t* gate = p.b + static_cast<int64_t>(n) * p.ldb;
+  const uint8_t* up = p.u + static_cast<int64_t>(n) * p.ldu;
   const int block = min(n0, p.N - 1) / pw::kGroup;   // (a cluster's last CTAs may have no columns)
   const float* sg = p.sb + block * p.sb_stride;
   const float* su = p.su + block * p.su_stride;
@@ -52,51 +47,39 @@ __global__ void __launch_bounds__(32 * kWarps) gated_stream_kernel(const __grid_
     sa[i][0] = p.sa + static_cast<int64_t>(c < p.M ? c : 0) * p.sa_stride;
     sa[i][1] = p.sa + static_cast<int64_t>(c + 1 < p.M ? c + 1 : 0) * p.sa_stride;
   }
-  float sum[kSets][kGroups][4] = {};
-  for (int kb = warp; kb < p.KB; kb += kWarps) {
+  float sum[kGroups][4] = {};
+  for (int kb = split; kb < p.KB; kb += kSplits) {
     const int k = kb * pw::kGroup + 32 * t;
-    uint32_t wg[kSets][8], wu[kSets][8];
-#pragma unroll
-    for (int j = 0; j < kSets; ++j) {
-      load32(gate[j], k, p.K, valid[j], p.wide_b, wg[j]);
-      load32(up[j], k, p.K, valid[j], p.wide_b, wu[j]);
-    }
+    uint32_t wg[8], wu[8];
+    load32(gate, k, p.K, valid, p.wide_b, wg);
+    load32(up, k, p.K, valid, p.wide_b, wu);
     const float scale_g = __ldg(sg + kb), scale_u = __ldg(su + kb);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       uint32_t x[8];
       load32(a[i], k, p.K, 8 * i + g < p.M, false, x);
       const float s0 = __ldg(sa[i][0] + kb), s1 = __ldg(sa[i][1] + kb);
+      float acc[4] = {};
 #pragma unroll
-      for (int j = 0; j < kSets; ++j) {
-        float acc[4] = {};
-#pragma unroll
-        for (int e = 0; e < 8; e += 2)
-          pw::mma_16832_e4m3(acc, wg[j][e], wu[j][e], wg[j][e + 1], wu[j][e + 1], x[e], x[e + 1]);
-        sum[j][i][0] += scale_g * s0 * acc[0];
-        sum[j][i][1] += scale_g * s1 * acc[1];
-        sum[j][i][2] += scale_u * s0 * acc[2];
-        sum[j][i][3] += scale_u * s1 * acc[3];
-      }
+      for (int e = 0; e < 8; e += 2) pw::mma_16832_e4m3(acc, wg[e], wu[e], wg[e + 1], wu[e + 1], x[e], x[e + 1]);
+      sum[i][0] += scale_g * s0 * acc[0];
+      sum[i][1] += scale_g * s1 * acc[1];
+      sum[i][2] += scale_u * s0 * acc[2];
+      sum[i][3] += scale_u * s1 * acc[3];
     }
   }
 #pragma unroll
-  for (int j = 0; j < kSets; ++j)
+  for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      red[warp][j][g][8 * i + 2 * t] = sum[j][i][0];
-      red[warp][j][g][8 * i + 2 * t + 1] = sum[j][i][1];
-      red[warp][j][g + 8][8 * i + 2 * t] = sum[j][i][2];
-      red[warp][j][g + 8][8 * i + 2 * t + 1] = sum[j][i][3];
-    }
+    for (int j = 0; j < 4; ++j) red[split][j >> 1][8 * strip + g][8 * i + 2 * t + (j & 1)] = sum[i][j];
   __syncthreads();
-  for (int e = threadIdx.x; e < kCols * kTokens; e += 32 * kWarps) {
+  for (int e = threadIdx.x; e < kCols * kTokens; e += kThreads) {
     const int col = e % kCols, token = e / kCols;
     float vg = 0.0f, vu = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      vg += red[i][col >> 3][col & 7][token];
-      vu += red[i][col >> 3][8 + (col & 7)][token];
+    for (int i = 0; i < kSplits; ++i) {
+      vg += red[i][0][col][token];
+      vu += red[i][1][col][token];
     }
     const float v = gated(vg, vu, p.act);   // 0 for columns past the end
     if (p.q) h[token][col] = v;
@@ -105,32 +88,35 @@ __global__ void __launch_bounds__(32 * kWarps) gated_stream_kernel(const __grid_
   }
   if (!p.q) return;
   __syncthreads();
-  if (threadIdx.x < kTokens) {
+  for (int token = warp; token < kTokens; token += kWide * kSplits) {
     float most = 0.0f;
+    for (int i = lane; i < kCols; i += 32) most = pw::max_nan(most, fabsf(h[token][i]));
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) most = pw::max_nan(most, fabsf(h[threadIdx.x][i]));
-    top[threadIdx.x] = most;
+    for (int o = 16; o; o >>= 1) most = pw::max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    if (lane == 0) top[token] = most;
   }
   pw::cluster_sync();
   const uint32_t rank = pw::cluster_rank();
-  for (int token = warp; token < min(kTokens, p.M); token += kWarps) {
-    float most = pw::ld_cluster_f32(pw::map_shared(pw::smem_u32(&top[token]), lane % kCluster));
+  for (int token = warp; token < min(kTokens, p.M); token += kWide * kSplits) {
+    float most = 0.0f;
 #pragma unroll
-    for (int o = kCluster / 2; o; o >>= 1) most = pw::max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    for (int i = 0; i < kCluster; ++i) most = pw::max_nan(most, pw::ld_cluster_f32(pw::map_shared(pw::smem_u32(&top[token]), i)));
     const float s = pw::max_nan(most / pw::kE4m3Max, pw::kMinScale);
+    const pw::Divisor by(s);
     if (rank == 0 && lane == 0) p.scale[static_cast<int64_t>(token) * p.scale_stride + block] = s;
-    if (lane < kCols && n0 + lane < p.N)
-      p.q[static_cast<int64_t>(token) * p.ldq + n0 + lane] = static_cast<uint8_t>(pw::e4m3x2(pw::Divisor(s)(h[token][lane]), 0.0f));
+    for (int i = lane; i < kCols; i += 32)
+      if (n0 + i < p.N) p.q[static_cast<int64_t>(token) * p.ldq + n0 + i] = static_cast<uint8_t>(pw::e4m3x2(by(h[token][i]), 0.0f));
   }
   pw::cluster_sync();   // nobody leaves while its magnitudes are read
 }
 
-template <typename T, int kGroups, int kWarps>
+template <typename T, int kGroups, int kWide, int kSplits>
 int launch_stream(const GatedParams& p, cudaStream_t s) {
-  const unsigned ctas = static_cast<unsigned>((p.N + kCols - 1) / kCols);
+  constexpr unsigned kCols = 8 * kWide, kCluster = pw::kGroup / kCols;
+  const unsigned ctas = (static_cast<unsigned>(p.N) + kCols - 1) / kCols;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.q ? (ctas + kCluster - 1) / kCluster * kCluster : ctas);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(32 * kWide * kSplits);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -138,7 +124,7 @@ int launch_stream(const GatedParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.q ? 1 : 0;
-  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, gated_stream_kernel<T, kGroups, kWarps>, p));
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, gated_stream_kernel<T, kGroups, kWide, kSplits>, p));
   return PW_OK;
 }
 
@@ -146,7 +132,22 @@ template <typename T>
 int launch(const GatedParams& p, cudaStream_t s) {
   const int sms = pw::sm_count();
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
-  if (p.M <= 8) return launch_stream<T, 1, 8>(p, s);
+  // Up to 8 tokens, the weights stream through the warps' registers.  Where all
+  // CTAs of 16 columns and 8 splits of K are on the SMs at once (two an SM), they
+  // have most loads under way (4096 x 4096: 10.7 us, 17.8 with 32 columns and two
+  // splits, 11.9 by tiles); beyond, a cluster of 8 waits for 8 free places, and
+  // clusters of 4 larger CTAs are faster (14336 x 4096: 23.9 us, 33.6; 24.3 by
+  // tiles).  A 16-bit result needs no cluster (22.3 and 22.5 us).
+  const int ctas = (p.N + 15) / 16;
+  if (p.M <= 8) return ctas <= 2 * sms || !p.q ? launch_stream<T, 1, 2, 8>(p, s) : launch_stream<T, 1, 4, 2>(p, s);
+  // Up to 16, and up to 32 for a 16-bit result, where one CTA an SM and one or two
+  // groups of K a warp are all: 16 x 1408 x 2048 in 8 bits 5.7 us, 7.4 by tiles, in 16 bits 4.1
+  // and 7.2; 32 tokens in 16 bits 5.5 and 7.7, in 8 bits 8.0 and 8.0; but 16 x
+  // 4096 x 2048 18.8 and 9.7.
+  if (ctas <= sms && p.KB <= 16) {
+    if (p.M <= 16) return launch_stream<T, 2, 2, 8>(p, s);
+    if (p.M <= 32 && !p.q) return launch_stream<T, 4, 2, 8>(p, s);
+  }
   if (p.M <= 64) return launch_tile<T, 64, 256, true>(p, sms, s);
   const long long wide = (p.N + 127) / 128;
   const long long pairs = (p.M + 255) / 256 * wide, singles = (p.M + 127) / 128 * wide;

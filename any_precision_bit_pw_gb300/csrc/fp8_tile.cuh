@@ -38,13 +38,29 @@ struct GatedParams : LinearParams {
   bool wide_q;      // rows of q start at 16-byte addresses
 };
 
-// act(g) * u.  Both activations are g / (1 + 2^-t): t is g log2(e) for SiLU, and
-// for GELU by its tanh form 1/2 g (1 + tanh x) the same with 2 x for g, which does not
-// cancel for negative g.  (2^-t may be an infinity: the quotient is 0.)
+// act(g) * u, of two columns.  Both activations are g / (1 + 2^-t): t is g log2(e)
+// for SiLU, and for GELU by its tanh form 1/2 g (1 + tanh x) the same with 2 x for g,
+// which does not cancel for negative g.  (2^-t may be an infinity: the quotient is 0.)
+__device__ __forceinline__ uint64_t gated2(uint64_t g, uint64_t u, int act) {
+  constexpr float kLog2e = 1.4426950408889634f, kGelu = -2.0f * 0.7978845608028654f * kLog2e;
+  uint64_t t;   // -t
+  if (act == PW_ACT_SILU) {
+    t = pw::mul_f32x2(g, pw::twice(-kLog2e));
+  } else {
+    const uint64_t square = pw::mul_f32x2(g, g);
+    t = pw::mul_f32x2(g, pw::fma_f32x2(square, pw::twice(0.044715f * kGelu), pw::twice(kGelu)));
+  }
+  float lo, hi;
+  pw::unpack_f32x2(t, lo, hi);
+  const uint64_t e = pw::pack_f32x2(__float_as_uint(pw::exp2_fast(lo)), __float_as_uint(pw::exp2_fast(hi)));
+  pw::unpack_f32x2(pw::add_f32x2(e, pw::twice(1.0f)), lo, hi);
+  const uint64_t r = pw::pack_f32x2(__float_as_uint(pw::reciprocal_fast(lo)), __float_as_uint(pw::reciprocal_fast(hi)));
+  return pw::mul_f32x2(pw::mul_f32x2(g, r), u);
+}
 __device__ __forceinline__ float gated(float g, float u, int act) {
-  constexpr float kLog2e = 1.4426950408889634f, kGelu = 2.0f * 0.7978845608028654f * kLog2e;
-  const float t = act == PW_ACT_SILU ? g * kLog2e : kGelu * fmaf(0.044715f * g * g, g, g);
-  return __fdividef(g, 1.0f + pw::exp2_fast(-t)) * u;
+  float lo, hi;
+  pw::unpack_f32x2(gated2(pw::twice(g), pw::twice(u), act), lo, hi);
+  return lo;
 }
 
 // 16 bytes at column k of a row; columns from K on are 0.
@@ -431,13 +447,10 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float g0, g1, u0, u1;
-          pw::unpack_f32x2(sum[i], g0, g1);
-          pw::unpack_f32x2(sum[32 + i], u0, u1);
-          g0 = gated(g0, u0, p.act);
-          g1 = gated(g1, u1, p.act);
-          top = pw::max_nan(top, pw::max_nan(fabsf(g0), fabsf(g1)));
-          sum[i] = pw::pack_f32x2(__float_as_uint(g0), __float_as_uint(g1));
+          float h0, h1;
+          sum[i] = gated2(sum[i], sum[32 + i], p.act);
+          pw::unpack_f32x2(sum[i], h0, h1);
+          top = pw::max3_nan(top, fabsf(h0), fabsf(h1));
         }
         if (p.q) {
           gsh.top[turn][side][32 * quarter + lane] = top;
@@ -449,6 +462,11 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
           turn_parity ^= 1;
           const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
           const pw::Divisor by(s);
+          const uint64_t by_s = pw::twice(by.s), by_inv = pw::twice(by.inv), by_neg = pw::twice(-by.inv);
+          auto quotient = [&](uint64_t v) {   // Divisor's, of two
+            const uint64_t q = pw::mul_f32x2(v, by_inv);
+            return pw::fma_f32x2(pw::fma_f32x2(q, by_s, v ^ 0x8000000080000000ull), by_neg, q);
+          };
           if (m < p.M) {
             if (side == 0) p.scale[static_cast<int64_t>(m) * p.scale_stride + nt] = s;
             uint8_t* q = p.q + static_cast<int64_t>(m) * p.ldq + n0;
@@ -458,9 +476,9 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 float f[4];
-                pw::unpack_f32x2(sum[8 * i + 2 * j], f[0], f[1]);
-                pw::unpack_f32x2(sum[8 * i + 2 * j + 1], f[2], f[3]);
-                w[j] = pw::e4m3x4(by(f[0]), by(f[1]), by(f[2]), by(f[3]));
+                pw::unpack_f32x2(quotient(sum[8 * i + 2 * j]), f[0], f[1]);
+                pw::unpack_f32x2(quotient(sum[8 * i + 2 * j + 1]), f[2], f[3]);
+                w[j] = pw::e4m3x4(f[0], f[1], f[2], f[3]);
               }
               if (p.wide_q && n0 + 16 * i + 16 <= p.N) {
                 *reinterpret_cast<uint4*>(q + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);

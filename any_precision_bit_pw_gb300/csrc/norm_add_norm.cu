@@ -56,7 +56,6 @@ __device__ __forceinline__ float block_sum(uint64_t two, float* part) {
   }
   return sum;
 }
-__device__ __forceinline__ uint64_t both(float v) { return pw::pack_f32x2(__float_as_uint(v), __float_as_uint(v)); }
 
 // A CTA takes every gridDim-th row.  A thread holds 16 neighbouring columns of each
 // of kParts parts of the row in registers, so a row is read once, and starts the
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
   };
   // block_scale * post * gate (which = 0) or the weight (1) at the thread's columns, from memory
   auto vector = [&](int which, int c, uint64_t (&t)[8]) {
-    const uint64_t scale = both(which ? 1.0f : p.block_scale);
+    const uint64_t scale = pw::twice(which ? 1.0f : p.block_scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = scale;
     const void* of[2] = {which ? p.w : p.post, which || kMatrix ? nullptr : p.gate};
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
   }
   __syncthreads();
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  const uint64_t res_scale = both(p.res_scale);
+  const uint64_t res_scale = pw::twice(p.res_scale);
   for (int turn = 0; row < p.rows; row += gridDim.x, turn ^= 1) {
     const bool more = kAhead && row + gridDim.x < p.rows;
     if (kSame) shift = shift_of(row);
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
       values(x[c], p.x, row, p.x_stride, c, v[c]);
       if (more) x[c] = load(p.x, row + gridDim.x, p.x_stride, c);
     }
-    uint64_t factor = both(1.0f);
+    uint64_t factor = pw::twice(1.0f);
     if (p.post) {
       // the sums of squares in 32 bits: 8 x kParts terms in two sums a thread, then a tree
       uint64_t sum = 0;
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
       for (int c = 0; c < kParts; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = pw::fma_f32x2(v[c][i], v[c][i], sum);
-      factor = both(rsqrtf(block_sum(sum, sums[turn][0]) * inv_cols + p.eps));
+      factor = pw::twice(rsqrtf(block_sum(sum, sums[turn][0]) * inv_cols + p.eps));
     }
     uint64_t sum = 0;
 #pragma unroll
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
       for (int c = 0; c < kParts; ++c) store(p.res_out, row, p.res_out_stride, c, v[c]);
     }
     if (!p.y && !p.q) continue;
-    factor = both(rsqrtf(block_sum(sum, sums[turn][1]) * inv_cols + p.eps));
+    factor = pw::twice(rsqrtf(block_sum(sum, sums[turn][1]) * inv_cols + p.eps));
 #pragma unroll
     for (int c = 0; c < kParts; ++c) {
       uint64_t t[8];

@@ -109,6 +109,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // First failure wins; the kernels go on without the offending access.
 __device__ __forceinline__ void report_status(int32_t* status, int code) {
   if (status) atomicCAS(status, 0, code);
