@@ -8,10 +8,10 @@
 // not cancel where one token has nearly all of the probability.
 //
 // The most probable tokens come from the same pass.  Every thread remembers the
-// largest logit of each of its segments, 8 to 32 vectors of 32 bytes; the k largest values
-// lie in the k segments with the largest maxima (any other segment has k larger
-// values outside), so those are read again, from L2, and their values go through a
-// sorted list in the registers of each warp.
+// largest logit of each of its segments, 8 vectors of 32 bytes and more.  The k-th largest
+// of the threads' maxima is no larger than the k-th largest value, so the k largest
+// lie in the segments whose maxima are not below it, at most 4 k of them: those are read again,
+// from L2, and their values go through a sorted list in the registers of each warp.
 //
 // Memory bandwidth bounds it (a value costs five to six instructions, one of them
 // an exponential), and for few rows the chain of a load, reductions and the
@@ -95,9 +95,10 @@ struct Row {
     vectors = (lead + n + Vec<T>::kSize - 1) / Vec<T>::kSize;
   }
   __device__ __forceinline__ int first_of(int v) const { return v * Vec<T>::kSize - lead; }
-  __device__ __forceinline__ void load(int v, uint32_t (&w)[8]) const {
+  // Vector v, or nothing but -inf from vector `end` on.
+  __device__ __forceinline__ void load(int v, int end, uint32_t (&w)[8]) const {
     const int first = first_of(v);
-    if (first >= 0 && first + Vec<T>::kSize <= size) {
+    if (first >= 0 && first + Vec<T>::kSize <= size && v < end) {
       asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                    : "l"(data + first));
@@ -105,6 +106,7 @@ struct Row {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = Vec<T>::kLowest;
+    if (v >= end) return;
 #pragma unroll
     for (int i = 0; i < Vec<T>::kSize; ++i) {
       if (first + i < 0 || first + i >= size) continue;
@@ -179,20 +181,31 @@ __device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b_reversed) {
   }
   return key;
 }
-__device__ __forceinline__ uint64_t reversed(uint64_t key) {
-  return __shfl_sync(0xFFFFFFFFu, key, 31 - static_cast<int>(threadIdx.x & 31));
-}
-
 struct Shared {
   Sums sums[kWarps], total;
   uint64_t lists[kWarps][kMaxTop];
-  uint64_t chosen[kMaxTop];
+  uint64_t segments[kSegments][kThreads];   // their maxima; 0: no values
+  uint64_t bound, best[kWarps], result[kMaxTop];
+  int chosen[kSegments * kMaxTop], count;   // segments to look at, by the vector of their maximum
 };
 
-// The list of the first `warps` warps' lists together, in warp 0.  All threads of
-// the CTA come here.
-__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, Shared& sh) {
+__device__ __forceinline__ uint64_t largest_key(uint64_t key) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const uint64_t k = other(key, o);
+    key = k > key ? k : key;
+  }
+  return key;
+}
+// The list of the first `warps` warps' lists together, in warp 0 (for one value only
+// its first key).  All threads of the CTA come here.
+__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top, Shared& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (top == 1) {
+    if (lane == 0) sh.best[warp] = list;
+    __syncthreads();
+    return warp == 0 ? largest_key(lane < warps ? sh.best[lane] : 0) : 0;
+  }
 #pragma unroll
   for (int half = kWarps / 2; half; half /= 2) {
     if (half >= warps) continue;
@@ -220,12 +233,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const int begin = static_cast<int>(static_cast<int64_t>(row.vectors) * rank / cluster);
   const int end = static_cast<int>(static_cast<int64_t>(row.vectors) * (rank + 1) / cluster);
   const int steps = (end - begin + kThreads - 1) / kThreads;
-  const int length = max(kLeast, (steps + kSegments - 1) / kSegments);   // steps of a segment
+  const int length = max(kLeast, ((steps + kSegments - 1) / kSegments + kAhead - 1) / kAhead * kAhead);   // steps of a segment
 
   Sums sum{-INFINITY, 0.0f, 0.0f};
   uint64_t s2 = 0, t2 = 0;              // two parts of S and T
-  uint64_t list = 0;                    // the largest segments of the warp
-  const uint64_t scale2 = pw::pack_f32x2(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+  uint64_t best = 0;                    // the thread's largest value
+  const uint64_t scale2 = pw::twice(p.scale_log2);
   for (int seg = 0; seg < kSegments && seg * length < steps; ++seg) {
     const int v0 = begin + seg * length * kThreads + tid, v1 = min(end, begin + (seg + 1) * length * kThreads);
     float top = -INFINITY;              // of the segment, and the vector that has it
@@ -233,29 +246,30 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     for (int v = v0; v < v1; v += kAhead * kThreads) {
       uint32_t w[kAhead][8];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (v + i * kThreads < v1) row.load(v + i * kThreads, w[i]);
+      for (int i = 0; i < kAhead; ++i) row.load(v + i * kThreads, v1, w[i]);
+      float most = -INFINITY;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (v + i * kThreads >= v1) break;
-        const float most = Vec<T>::largest(w[i]);
-        if (most > top) {
-          top = most;
+        const float x = Vec<T>::largest(w[i]);
+        most = fmaxf(most, x);
+        if (x > top) {
+          top = x;
           at = v + i * kThreads;
         }
-        if (most > sum.m) {
-          float s0, s1, t0, t1;
-          pw::unpack_f32x2(s2, s0, s1);
-          pw::unpack_f32x2(t2, t0, t1);
-          Sums x{sum.m, s0, t0}, y{sum.m, s1, t1};
-          sum.m = most;
-          raise(x, most, p.scale_log2);
-          raise(y, most, p.scale_log2);
-          s2 = pw::pack_f32x2(__float_as_uint(x.s), __float_as_uint(y.s));
-          t2 = pw::pack_f32x2(__float_as_uint(x.t), __float_as_uint(y.t));
-        }
-        const float off = -base_of(sum.m);
-        const uint64_t off2 = pw::pack_f32x2(__float_as_uint(off), __float_as_uint(off));
+      }
+      if (most > sum.m) {   // once for all the vectors: it takes as long as six values of one
+        float lo, hi;
+        pw::unpack_f32x2(s2, lo, hi);
+        sum.s = lo + hi;
+        pw::unpack_f32x2(t2, lo, hi);
+        sum.t = lo + hi;
+        raise(sum, most, p.scale_log2);
+        s2 = pw::pack_f32x2(__float_as_uint(sum.s), 0u);
+        t2 = pw::pack_f32x2(__float_as_uint(sum.t), 0u);
+      }
+      const uint64_t off2 = pw::twice(-base_of(sum.m));
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
 #pragma unroll
         for (int j = 0; j < kSize / 2; ++j) {
           float lo, hi;
@@ -269,11 +283,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
           s2 = pw::add_f32x2(s2, e);
           t2 = pw::fma_f32x2(e, pw::pack_f32x2(__float_as_uint(d0), __float_as_uint(d1)), t2);
         }
-      }
     }
     if (a.top) {
-      const uint64_t key = sorted(v0 < v1 ? key_of(top, at) : 0);
-      list = seg ? merged(list, reversed(key)) : key;
+      const uint64_t key = v0 < v1 ? key_of(top, at) : 0;
+      sh.segments[seg][tid] = key;
+      best = key > best ? key : best;
     }
   }
   {
@@ -289,43 +303,41 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
                            __shfl_xor_sync(0xFFFFFFFFu, sum.t, o)}, p.scale_log2);
   if (lane == 0) sh.sums[warp] = sum;
 
+  uint64_t list = 0;
   if (a.top) {
-    list = join_lists(list, kWarps, sh);
-    if (warp == 0) sh.chosen[lane] = lane < a.top ? list : 0;
+    if (tid == 0) sh.count = 0;
+    list = join_lists(a.top == 1 ? largest_key(best) : sorted(best), kWarps, a.top, sh);
+    if (warp == 0 && lane == a.top - 1) sh.bound = list;
     __syncthreads();
-    // The k-th largest segment's maximum is no larger than the k-th largest value:
-    // what ranks behind that vector's last value is not wanted.
-    const uint64_t last = sh.chosen[a.top - 1];
+    const uint64_t last = sh.bound;     // 0: fewer threads than wanted values have any
+    for (int i = 0; i < kSegments && i * length < steps; ++i) {
+      const uint64_t key = sh.segments[i][tid];
+      if (key && key >= last) sh.chosen[atomicAdd(&sh.count, 1)] = index_of(key);
+    }
+    __syncthreads();
+    const int items = sh.count * length;
+    // What ranks behind the last value of the bound's vector is not wanted.
     const uint64_t least = last ? (last & 0xFFFFFFFF00000000ull) | ~static_cast<uint32_t>(row.first_of(index_of(last)) + kSize - 1) : 1;
     list = 0;
     uint64_t want = least;              // a key below this one changes nothing
-    for (int e0 = warp * 32; e0 < a.top * length; e0 += kThreads) {
+    for (int e0 = warp * 32; e0 < items; e0 += kThreads) {
       const int e = e0 + lane;
-      const uint64_t segment = e < a.top * length ? sh.chosen[e / length] : 0;
       uint32_t w[8];
       int first = 0;
       bool live = false;
-      if (segment) {
-        const int place = index_of(segment) - begin, step = place / kThreads / length * length + e % length;
+      if (e < items) {
+        const int place = sh.chosen[e / length] - begin, step = place / kThreads / length * length + e % length;
         const int v = begin + step * kThreads + place % kThreads;
-        live = v < end;
-        if (live) {
-          row.load(v, w);
-          first = row.first_of(v);
-          live = rank_of(Vec<T>::largest(w)) >= static_cast<uint32_t>(want >> 32);
-        }
+        row.load(v, end, w);
+        first = row.first_of(v);
+        live = v < end && rank_of(Vec<T>::largest(w)) >= static_cast<uint32_t>(want >> 32);
       }
       if (!__any_sync(0xFFFFFFFFu, live)) continue;
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < kSize; ++i) {
-        // (a loop over a vector in registers: its words move down)
-        float x;
-        if constexpr (kSize == 8) {
-          x = __uint_as_float(w[0]);
-        } else {
-          float hi;
-          pw::unpack2<T>(w[0], x, hi);
-        }
+        float two[2];
+        two_values<T>(w, i / 2, two[0], two[1]);
+        const float x = two[i & 1];
         const int index = first + i;
         const uint64_t key = live && index >= 0 && index < row.size ? key_of(x, index) : 0;
         uint32_t found = __ballot_sync(0xFFFFFFFFu, key >= want);
@@ -338,16 +350,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
           const uint64_t kth = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
           want = kth >= least ? kth + 1 : least;
         }
-        if constexpr (kSize == 8) {
-#pragma unroll
-          for (int j = 0; j < 7; ++j) w[j] = w[j + 1];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = w[j] >> 16 | (j < 7 ? w[j + 1] << 16 : 0u);
-        }
       }
     }
-    list = join_lists(list, kWarps, sh);
+    list = join_lists(list, kWarps, a.top, sh);
   } else {
     __syncthreads();
   }
@@ -358,17 +363,17 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   for (int i = 1; i < kWarps; ++i) sum = joined(sum, sh.sums[i], p.scale_log2);
   if (cluster > 1) {
     if (warp == 0) {
-      sh.chosen[lane] = list;
+      sh.result[lane] = list;
       if (lane == 0) sh.total = sum;
     }
     pw::cluster_sync();
     if (rank == 0) {
-      const uint64_t theirs = warp < cluster ? pw::ld_cluster_u64(pw::map_shared(pw::smem_u32(&sh.chosen[lane]), warp)) : 0;
+      const uint64_t theirs = warp < cluster ? pw::ld_cluster_u64(pw::map_shared(pw::smem_u32(&sh.result[lane]), warp)) : 0;
       for (int i = 0; i < cluster; ++i) {
         const float4 t = pw::ld_cluster_f4(pw::map_shared(pw::smem_u32(&sh.total), i));
         sum = i ? joined(sum, Sums{t.x, t.y, t.z}, p.scale_log2) : Sums{t.x, t.y, t.z};
       }
-      if (a.top) list = join_lists(theirs, cluster, sh);
+      if (a.top) list = join_lists(theirs, cluster, a.top, sh);
     }
     pw::cluster_sync();                 // nobody leaves while its results are read
     if (rank != 0) return;
