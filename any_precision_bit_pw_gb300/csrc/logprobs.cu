@@ -13,10 +13,12 @@
 // lie in the segments whose maxima are not below it, at most 4 k of them: those are read again,
 // from L2, and their values go through a sorted list in the registers of each warp.
 //
-// Memory bandwidth bounds it (a value costs five to six instructions, one of them
-// an exponential), and for few rows the chain of a load, reductions and the
-// second look at a few segments.  Few rows: a cluster of up to 8 CTAs shares one
-// and joins its results through distributed shared memory.
+// Memory bandwidth bounds it (4096 rows of 131072 bf16 logits: 178 us with one
+// alternative, 6.0 TB/s, and 161 without), with the instructions close behind: 9 a
+// value, one of them an exponential.  For few rows it is the chain of a load,
+// reductions and the second look at a few segments (one row of 32000: 8.2 us).  Few
+// rows: a cluster of up to 8 CTAs shares one and joins its results through
+// distributed shared memory.
 #include <type_traits>
 
 #include "ops_common.cuh"
@@ -24,13 +26,11 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kSegments = 4;          // of a thread
+constexpr int kAhead = 4;             // vectors that a thread has under way
 constexpr int kLeast = 8;             // vectors of a segment at the least, where there are several
 constexpr int kMaxTop = 32;           // a list is one value a lane
-constexpr int kMaxCluster = 8;        // CTAs of a row: one warp a CTA joins them
-static_assert(kMaxCluster <= kWarps, "lists");
+constexpr int kMaxCluster = 8;        // CTAs of a row
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNothing = -200.0f;   // 2^-200 is 0, and a finite factor leaves it 0 in T
 
@@ -142,6 +142,14 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b, float scale_log2) {
   return {m, a.s + b.s, a.t + b.t};
 }
 
+// The sums of `n` lanes (a power of two) together, in all of them.
+__device__ __forceinline__ Sums joined_lanes(Sums a, int n, float scale_log2) {
+  for (int o = n / 2; o; o >>= 1)
+    a = joined(a, Sums{__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                       __shfl_xor_sync(0xFFFFFFFFu, a.t, o)}, scale_log2);
+  return a;
+}
+
 // ---------------------------------------------------------------- ranked keys
 // A value and its index as one number: larger is more probable, equal values
 // rank by the lower index.  NaN ranks as -inf; 0 is no key.
@@ -181,7 +189,9 @@ __device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b_reversed) {
   }
   return key;
 }
+template <int kThreads>
 struct Shared {
+  static constexpr int kWarps = kThreads / 32;
   Sums sums[kWarps], total;
   uint64_t lists[kWarps][kMaxTop];
   uint64_t segments[kSegments][kThreads];   // their maxima; 0: no values
@@ -199,7 +209,9 @@ __device__ __forceinline__ uint64_t largest_key(uint64_t key) {
 }
 // The list of the first `warps` warps' lists together, in warp 0 (for one value only
 // its first key).  All threads of the CTA come here.
-__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top, Shared& sh) {
+template <int kThreads>
+__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top, Shared<kThreads>& sh) {
+  constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (top == 1) {
     if (lane == 0) sh.best[warp] = list;
@@ -220,11 +232,10 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top
 // ---------------------------------------------------------------- the kernel
 // CTA `rank` of the cluster takes its share of the row's vectors; a thread takes
 // every kThreads-th of them.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobParams p, int cluster) {
-  constexpr int kSize = Vec<T>::kSize;
-  constexpr int kAhead = 4;             // vectors that a thread has under way
-  __shared__ Shared sh;
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const __grid_constant__ LogprobParams p, int cluster) {
+  constexpr int kSize = Vec<T>::kSize, kWarps = kThreads / 32;
+  __shared__ Shared<kThreads> sh;
   const pw_logprob_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = cluster > 1 ? static_cast<int>(pw::cluster_rank()) : 0;
@@ -297,10 +308,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     sum.s = s0 + s1;
     sum.t = t0 + t1;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    sum = joined(sum, Sums{__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o),
-                           __shfl_xor_sync(0xFFFFFFFFu, sum.t, o)}, p.scale_log2);
+  sum = joined_lanes(sum, 32, p.scale_log2);
   if (lane == 0) sh.sums[warp] = sum;
 
   uint64_t list = 0;
@@ -358,9 +366,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   }
 
   // the CTA's sums, then the cluster's
-  sum = sh.sums[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) sum = joined(sum, sh.sums[i], p.scale_log2);
+  sum = joined_lanes(sh.sums[lane % kWarps], kWarps, p.scale_log2);
   if (cluster > 1) {
     if (warp == 0) {
       sh.result[lane] = list;
@@ -369,10 +375,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     pw::cluster_sync();
     if (rank == 0) {
       const uint64_t theirs = warp < cluster ? pw::ld_cluster_u64(pw::map_shared(pw::smem_u32(&sh.result[lane]), warp)) : 0;
-      for (int i = 0; i < cluster; ++i) {
-        const float4 t = pw::ld_cluster_f4(pw::map_shared(pw::smem_u32(&sh.total), i));
-        sum = i ? joined(sum, Sums{t.x, t.y, t.z}, p.scale_log2) : Sums{t.x, t.y, t.z};
-      }
+      const float4 t = pw::ld_cluster_f4(pw::map_shared(pw::smem_u32(&sh.total), lane % cluster));
+      sum = joined_lanes(Sums{t.x, t.y, t.z}, cluster, p.scale_log2);
       if (a.top) list = join_lists(theirs, cluster, a.top, sh);
     }
     pw::cluster_sync();                 // nobody leaves while its results are read
@@ -403,13 +407,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   }
 }
 
-template <typename T>
-int launch(const LogprobParams& p, cudaStream_t s) {
-  const int sms = pw::sm_count();
-  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
-  const int vectors = (p.a.vocab + Vec<T>::kSize - 1) / Vec<T>::kSize;
-  int cluster = 1;
-  while (cluster < kMaxCluster && p.a.rows * 2 * cluster <= 2 * sms && vectors >= 2 * cluster * kThreads / 2) cluster *= 2;
+template <typename T, int kThreads>
+int launch_threads(const LogprobParams& p, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.rows * cluster));
   cfg.blockDim = dim3(kThreads);
@@ -420,8 +419,27 @@ int launch(const LogprobParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p, cluster));
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads>, p, cluster));
   return PW_OK;
+}
+
+template <typename T>
+int launch(const LogprobParams& p, cudaStream_t s) {
+  const int sms = pw::sm_count();
+  if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
+  const int vectors = (p.a.vocab + Vec<T>::kSize - 1) / Vec<T>::kSize;
+  // Few rows: as many CTAs of a cluster as two an SM allow, with 4 vectors a thread
+  // and more each.  One row of 131072 16-bit logits, 20 alternatives: 14.3, 11.6, 9.7 and 9.1 us
+  // by 1, 2, 4 and 8 CTAs; of 32000: 8.2 and 8.7 by 1 and 2; 61 rows of 151937
+  // 32-bit ones 25.9, 19.1, 16.2 and 17.5; 128 rows of 131072 18.4, 16.7 and 18.0.
+  int cluster = 1;
+  while (cluster < kMaxCluster && p.a.rows * 2 * cluster <= 2 * sms && vectors >= 2 * cluster * 1024) cluster *= 2;
+  // Many short rows: CTAs of 128 threads, so that an SM has twice as many rows at
+  // different stages (4096 rows of 32000: 59 us, 72 with 256 threads; of 8000: 30
+  // and 53; but 4096 rows of 131072 with 20 alternatives 199 and 194; 512 rows of 32000
+  // 16.8 and 16.2).
+  if (p.a.rows > 4 * sms && vectors <= 4096) return launch_threads<T, 128>(p, cluster, s);
+  return launch_threads<T, 256>(p, cluster, s);
 }
 
 }  // namespace
