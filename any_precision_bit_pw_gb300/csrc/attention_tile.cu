@@ -105,15 +105,24 @@ template <int D, bool kSinks>
 __device__ __forceinline__ void copy_rows(const Params& p, const Cursor<kSinks>& c, int key0, int first, int rows, int page,
                                           int begin, unsigned char* dst) {
   const pw_attn_args& a = p.a;
-  constexpr int kUnits = D / 8;
+  constexpr int kUnits = D / 8, kAtOnce = 8;   // (the loads of a turn before its stores: one latency a turn)
   const int lane = threadIdx.x & 31;
-  for (int i = lane; i < rows * kUnits; i += 32) {
-    const int row = first + i / kUnits, unit = i % kUnits, key = key0 + row;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (page >= 0 && pw_attn::in_sight<kSinks>(p, key, begin) && key < c.s.kv_len)
-      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_cache) + page * a.v_stride_page +
-                                          (key % a.page_size) * a.v_stride_token + c.head * a.v_stride_head + unit * 8);
-    *reinterpret_cast<uint4*>(dst + (unit >> 3) * kHalfRow + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) = v;
+  for (int i0 = lane; i0 < rows * kUnits; i0 += 32 * kAtOnce) {
+    uint4 v[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int i = i0 + 32 * j, row = first + i / kUnits, unit = i % kUnits, key = key0 + row;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (i < rows * kUnits && page >= 0 && pw_attn::in_sight<kSinks>(p, key, begin) && key < c.s.kv_len)
+        v[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_cache) + page * a.v_stride_page +
+                                               (key % a.page_size) * a.v_stride_token + c.head * a.v_stride_head + unit * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int i = i0 + 32 * j, row = first + i / kUnits, unit = i % kUnits;
+      if (i < rows * kUnits)
+        *reinterpret_cast<uint4*>(dst + (unit >> 3) * kHalfRow + row * 128 + (((unit & 7) ^ (row & 7)) << 4)) = v[j];
+    }
   }
 }
 
@@ -155,8 +164,9 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor<kSinks>&
         in_page -= a.page_size;
         ++index;
       }
-      if (kSinks && b + 1 == c.r.before()) {   // from the first keys to the window
-        key = c.r.b0 * kBlock + lane * box;
+      const bool back = kSinks && b + 1 == c.r.b1 - c.r.b0;   // from the window to the first keys
+      if (back) {
+        key = lane * box;
         index = key / a.page_size;
         in_page = key - index * a.page_size;
       }
@@ -185,7 +195,7 @@ __device__ __forceinline__ void load_role(const Params& p, const Cursor<kSinks>&
         }
         __syncwarp();
       }
-      key0 = kSinks && b + 1 == c.r.before() ? c.r.b0 * kBlock : key0 + kBlock;
+      key0 = back ? 0 : key0 + kBlock;
     }
     return true;
   });
