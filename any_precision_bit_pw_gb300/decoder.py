@@ -1,11 +1,17 @@
 """A decoder layer around the mixed-precision experts: residual norm, 8-bit
 projections, rotary positions, attention over a paged cache, and the routed
-expert layer of ``layer.py``, one stream, buffers allocated once.
+expert layer of ``layer.py`` or a dense gated block, one stream, buffers allocated
+once; and the model's end, the head's projection with the probabilities.
 
     cache = PagedCache(pages=4096, page_size=16, kv_heads=8, head_dim=128)
     layer = DecoderLayer(stack, 0, weights, heads=32, cache=cache, tokens=64)
     batch = cache.batch([3, 7], [1, 1])      # one new token of sequences 3 and 7
     x, residual = layer(x, residual, batch)  # both fp16 [T][H]
+    head = Head(norm, Fp8Weight.quantize(w_head), tokens=64, top=5, after=layer)
+    scores = head(x, residual, targets)      # log probabilities, entropy, alternatives
+
+A layer's output is added to the residual by the layer (or the head) that comes
+``after`` it, where the norms on both sides of a block are one kernel.
 
 Every computation but the router's small product (a widening copy and cuBLAS) is
 a libpw kernel (``pw.py``); the layer allocates and synchronises nothing in a
@@ -91,8 +97,22 @@ class PagedCache:
 
     def release(self, seq: int) -> None:
         """Returns a sequence's pages (once the stream has passed the calls that read them)."""
-        self.free_pages.extend(reversed(self.pages.pop(seq, [])))
+        self.free_pages.extend(p for p in reversed(self.pages.pop(seq, [])) if p >= 0)
         self.lens.pop(seq, None)
+
+    def trim(self, seq: int, window: int, sinks: int = 0) -> int:
+        """Returns the pages of a sequence that no later token sees in attention
+        over the last ``window`` keys and the first ``sinks`` (once the stream has
+        passed the calls that read them), and how many they are."""
+        if window < 1 or sinks < 0:
+            raise ValueError(f"trim: window {window}, sinks {sinks}")
+        pages, n = self.pages.get(seq, []), self.page_size
+        seen_from = self.lens.get(seq, 0) - window + 1            # by the next token
+        gone = [j for j in range(-(-sinks // n), max(seen_from, 0) // n) if pages[j] >= 0]
+        for j in gone:
+            self.free_pages.append(pages[j])
+            pages[j] = -1
+        return len(gone)
 
 
 @dataclass
@@ -118,7 +138,24 @@ class DecoderWeights:
     ffn_norm: torch.Tensor     # [H]
     qkv: Fp8Weight             # [(heads + 2 kv_heads) * head_dim][H]
     out: Fp8Weight             # [H][heads * head_dim]
-    router: torch.Tensor       # [experts][H] fp32
+    router: Optional[torch.Tensor] = None      # [experts][H] fp32; None: a dense block instead of the experts
+    gate: Optional[Fp8Weight] = None           # the dense block: [I][H]
+    up: Optional[Fp8Weight] = None             # [I][H]
+    down: Optional[Fp8Weight] = None           # [H][I]
+    # where a block's output is added: r = residual_scale * residual + gate * norm(output)
+    post_attn_norm: Optional[torch.Tensor] = None   # [H]
+    post_ffn_norm: Optional[torch.Tensor] = None    # [H]
+    attn_gate: Optional[torch.Tensor] = None        # [H]
+    ffn_gate: Optional[torch.Tensor] = None         # [H]
+    residual_scale: float = 1.0
+
+
+def _add_norm(x, residual, eps, weight, post, gate, residual_scale, **out) -> None:
+    """The block's output x joins the residual, and the norm before the next block."""
+    if post is None and gate is None and residual_scale == 1.0:
+        pw.pw_add_rmsnorm(x, weight, eps, residual=residual, **out)
+    else:
+        pw.pw_norm_add_norm(x, residual, eps, post_weight=post, weight=weight, gate=gate, residual_scale=residual_scale, **out)
 
 
 class DecoderLayer:
@@ -127,16 +164,27 @@ class DecoderLayer:
     (``share``): each reads its inputs before it writes its results, so the
     results of one may be the inputs of the next.  ``max_batch`` goes to the
     attention's workspace query, whose answer holds for any number of sequences.
+    ``after``: the layer whose results come in (None for the first, whose ``x`` is
+    the embedding).  With a ``window``, the first ``sinks`` keys of a sequence stay
+    visible.  A layer with a dense block needs no ``stack``.
     """
 
     BUFFERS = ("x8", "x8_scale", "qkv", "q", "attn", "attn8", "attn8_scale", "o", "h", "residual", "h32", "logits", "status",
                "ws", "experts")
+    DENSE_BUFFERS = ("ff8", "ff8_scale", "y")   # None without a dense block
 
-    def __init__(self, stack: APLMoEStack, index: int, weights: DecoderWeights, heads: int, cache: PagedCache,
+    def __init__(self, stack: Optional[APLMoEStack], index: int, weights: DecoderWeights, heads: int, cache: PagedCache,
                  tokens: int, rotary_dim: Optional[int] = None, rope_base: float = 1e6,
                  rope_scaling: Optional[pw.pw_rope_scaling] = None, interleaved: bool = False, window: int = 0,
-                 eps: float = 1e-5, max_batch: int = 256, share: Optional["DecoderLayer"] = None):
-        dev, H = stack.device, stack.H
+                 eps: float = 1e-5, max_batch: int = 256, share: Optional["DecoderLayer"] = None, sinks: int = 0,
+                 after: Optional["DecoderLayer"] = None, activation: int = pw.PW_ACT_SILU):
+        self.dense = weights.down is not None
+        if self.dense == (weights.router is not None) or (stack is None and not self.dense):
+            raise ValueError("decoder layer: a router and a stack of experts, or the gate, up and down of a dense block")
+        H = weights.attn_norm.shape[0]
+        dev = weights.attn_norm.device if stack is None else stack.device
+        assert stack is None or stack.H == H
+        self.sinks, self.after, self.activation = sinks, after, activation
         self.stack, self.index, self.w, self.cache = stack, index, weights, cache
         self.heads, self.kv_heads, self.head_dim = heads, cache.k.shape[2], cache.k.shape[3]
         self.eps, self.window, self.interleaved, self.tokens = eps, window, interleaved, tokens
@@ -144,11 +192,17 @@ class DecoderLayer:
         self.turns = turns.to(dev)
         D, wide = self.head_dim, (heads + 2 * self.kv_heads) * self.head_dim
         assert tuple(weights.qkv.codes.shape) == (wide, H) and tuple(weights.out.codes.shape) == (H, heads * D)
+        width = 0
+        if self.dense:
+            width = weights.down.codes.shape[1]
+            assert tuple(weights.gate.codes.shape) == tuple(weights.up.codes.shape) == (width, H) == tuple(weights.down.codes.shape)[::-1]
         if share is not None:
             if (share.stack, share.heads, share.kv_heads, D, tokens) != (stack, heads, self.kv_heads, share.head_dim, share.tokens):
                 raise ValueError("decoder layer: buffers are shared between layers of one stack with equal heads and tokens")
-            for name in self.BUFFERS:
+            for name in self.BUFFERS + self.DENSE_BUFFERS:
                 setattr(self, name, getattr(share, name))
+            if self.dense and (self.ff8 is None or self.ff8.shape[1] != width):
+                self._dense_buffers(tokens, H, width, dev)
             return
 
         def empty(*shape, dtype=torch.float16):
@@ -161,15 +215,26 @@ class DecoderLayer:
         self.attn8_scale = empty(tokens, -(-heads * D // 128), dtype=torch.float32)
         self.o, self.h = empty(tokens, H), empty(tokens, H)
         self.residual = [empty(tokens, H), empty(tokens, H)]
-        self.h32, self.logits = empty(tokens, H, dtype=torch.float32), empty(tokens, stack.routed, dtype=torch.float32)
+        self.h32 = self.logits = self.experts = self.ff8 = self.ff8_scale = self.y = None
+        if stack is not None:
+            self.h32, self.logits = empty(tokens, H, dtype=torch.float32), empty(tokens, stack.routed, dtype=torch.float32)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)   # of every call, the experts' too
         n = pw.pw_paged_attention_workspace(tokens, max_batch, heads, self.kv_heads, D)
         self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
         # the experts' workspace grows with the tokens: one, for the most, serves every count
-        self.experts = MoECall(stack, tokens)
-        self.experts.status = self.status
+        if stack is not None:
+            self.experts = MoECall(stack, tokens)
+            self.experts.status = self.status
+        if self.dense:
+            self._dense_buffers(tokens, H, width, dev)
         if dev.type == "cuda":   # the layer may be called on any stream: its buffers are free and zeroed by then
             torch.cuda.current_stream(dev).synchronize()
+
+    def _dense_buffers(self, tokens: int, H: int, width: int, dev) -> None:
+        pad = -width % 16                          # rows of the product are 16-byte aligned
+        self.ff8 = torch.empty((tokens, width + pad), dtype=torch.float8_e4m3fn, device=dev)[:, :width]
+        self.ff8_scale = torch.empty((tokens, -(-width // 128)), dtype=torch.float32, device=dev)
+        self.y = torch.empty((tokens, H), dtype=torch.float16, device=dev)
 
     def moe(self, tokens: int) -> MoECall:
         """The expert layer's buffers; a call of ``tokens`` tokens uses their first rows."""
@@ -190,24 +255,100 @@ class DecoderLayer:
         if x.shape[0] != T or T > self.tokens:
             raise ValueError(f"decoder layer: {x.shape[0]} rows for a batch of {T} tokens, at most {self.tokens}")
         if T == 0:
-            return self.experts.y[:0], self.residual[1][:0]
+            return (self.y if self.dense else self.experts.y)[:0], self.residual[1][:0]
         x8, x8s, qkv, q, attn = self.x8[:T], self.x8_scale[:T], self.qkv[:T], self.q[:T], self.attn[:T]
         hq, hk = self.heads, self.kv_heads
         r1, r2 = self.residual[0][:T], self.residual[1][:T]
-        pw.pw_add_rmsnorm(x, w.attn_norm, self.eps, residual=residual, residual_out=r1, q=x8, scale=x8s)
+        if self.after is not None and residual is not None:
+            before = self.after.w
+            _add_norm(x, residual, self.eps, w.attn_norm, before.post_ffn_norm, before.ffn_gate, before.residual_scale,
+                      residual_out=r1, q=x8, scale=x8s)
+        else:
+            pw.pw_add_rmsnorm(x, w.attn_norm, self.eps, residual=residual, residual_out=r1, q=x8, scale=x8s)
         pw.pw_fp8_linear(x8, x8s, w.qkv.codes, w.qkv.scale, qkv.view(T, -1), self.status)
         pw.pw_rope_append(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], self.turns, c.k, c.v, batch.page_table,
                           batch.q_offsets, batch.kv_lens, q, self.status, interleaved=self.interleaved,
                           factor=self.rope_factor)
         pw.pw_paged_attention(q, c.k, c.v, batch.page_table, batch.q_offsets, batch.kv_lens, attn, self.ws, self.status,
                               scale=self.head_dim ** -0.5, window=self.window, max_q_len=batch.max_q_len,
-                              max_kv_len=batch.max_kv_len)
+                              max_kv_len=batch.max_kv_len, sinks=self.sinks)
         a8, a8s = self.attn8[:T], self.attn8_scale[:T]
         pw.pw_quantize_fp8(attn.view(T, -1), a8, a8s)
         pw.pw_fp8_linear(a8, a8s, w.out.codes, w.out.scale, self.o[:T], self.status)
+        if self.dense:
+            f8, f8s, y = self.ff8[:T], self.ff8_scale[:T], self.y[:T]
+            _add_norm(self.o[:T], r1, self.eps, w.ffn_norm, w.post_attn_norm, w.attn_gate, w.residual_scale, residual_out=r2,
+                      q=x8, scale=x8s)
+            pw.pw_fp8_gated_linear(x8, x8s, w.gate.codes, w.gate.scale, w.up.codes, w.up.scale, self.status, q=f8, scale=f8s,
+                                   activation=self.activation)
+            pw.pw_fp8_linear(f8, f8s, w.down.codes, w.down.scale, y, self.status)
+            return y, r2
         h = self.h[:T]
-        pw.pw_add_rmsnorm(self.o[:T], w.ffn_norm, self.eps, residual=r1, residual_out=r2, y=h)
+        _add_norm(self.o[:T], r1, self.eps, w.ffn_norm, w.post_attn_norm, w.attn_gate, w.residual_scale, residual_out=r2, y=h)
         logits = self.logits[:T]
         torch.mm(self.h32[:T].copy_(h), w.router.t(), out=logits)   # the router: a few columns in 32 bits
         y = self.moe(T)(self.index, h, logits)[:T]
         return y, r2
+
+
+@dataclass
+class Scores:
+    """What a model says of next tokens, by rows of the call (the head's buffers)."""
+    logits: torch.Tensor                    # fp16 [T][V]
+    lse: torch.Tensor                       # fp32 [T]
+    entropy: torch.Tensor                   # fp32 [T]
+    logprobs: Optional[torch.Tensor]        # fp32 [T][n], of the targets
+    top_ids: Optional[torch.Tensor]         # int32 [T][top]
+    top_logprobs: Optional[torch.Tensor]    # fp32 [T][top]
+
+
+class Head:
+    """The model's end: the last layer's output joins the residual, the last norm,
+    the projection to the vocabulary, and the probabilities of next tokens; buffers
+    for up to ``tokens`` rows with ``given`` targets each.  ``after``: the last
+    layer.  ``temperature`` divides the logits before the probabilities."""
+
+    def __init__(self, norm: torch.Tensor, weight: Fp8Weight, tokens: int, top: int = 0, given: int = 1,
+                 after: Optional[DecoderLayer] = None, eps: float = 1e-5, temperature: float = 1.0):
+        V, H = weight.codes.shape
+        dev = norm.device
+        assert norm.shape == (H,)
+        if not temperature > 0:
+            raise ValueError(f"head: temperature {temperature}")
+        self.norm, self.weight, self.after, self.eps, self.scale = norm, weight, after, eps, 1.0 / temperature
+        self.tokens, self.given, self.top = tokens, given, top
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+        self.x8, self.x8_scale = empty(tokens, H + -H % 16, dtype=torch.float8_e4m3fn)[:, :H], empty(tokens, -(-H // 128))
+        self.logits = empty(tokens, V + -V % 16, dtype=torch.float16)[:, :V]   # rows at 32-byte addresses
+        self.lse, self.entropy, self.logprobs = empty(tokens), empty(tokens), empty(tokens, given)
+        self.top_ids, self.top_logprobs = empty(tokens, top, dtype=torch.int32), empty(tokens, top)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        if dev.type == "cuda":   # the head may be called on any stream: its buffers are free and zeroed by then
+            torch.cuda.current_stream(dev).synchronize()
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor], targets: Optional[torch.Tensor] = None,
+                 stream=None) -> Scores:
+        """x, residual: the last layer's results, or some of their rows, fp16
+        [T][H]; targets int32 [T][n] or None.  The results are the head's buffers,
+        valid until its next call."""
+        T, n = x.shape[0], 0 if targets is None else targets.shape[1]
+        if T > self.tokens or n > self.given:
+            raise ValueError(f"head: {T} rows of {n} targets, at most {self.tokens} of {self.given}")
+        s = Scores(self.logits[:T], self.lse[:T], self.entropy[:T], self.logprobs[:T, :n] if n else None,
+                   self.top_ids[:T] if self.top else None, self.top_logprobs[:T] if self.top else None)
+        if T == 0:
+            return s
+        x8, x8s = self.x8[:T], self.x8_scale[:T]
+        with _on(stream):
+            if self.after is not None and residual is not None:
+                before = self.after.w
+                _add_norm(x, residual, self.eps, self.norm, before.post_ffn_norm, before.ffn_gate, before.residual_scale,
+                          q=x8, scale=x8s)
+            else:
+                pw.pw_add_rmsnorm(x, self.norm, self.eps, residual=residual, q=x8, scale=x8s)
+            pw.pw_fp8_linear(x8, x8s, self.weight.codes, self.weight.scale, s.logits, self.status)
+            pw.pw_token_logprobs(s.logits, targets=targets if n else None, logprobs=s.logprobs, lse=s.lse, entropy=s.entropy,
+                                 top_ids=s.top_ids, top_logprobs=s.top_logprobs, scale=self.scale)
+        return s
