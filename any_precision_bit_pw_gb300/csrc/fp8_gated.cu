@@ -149,10 +149,24 @@ int launch(const GatedParams& p, cudaStream_t s) {
     if (p.M <= 32 && !p.q) return launch_stream<T, 4, 2, 8>(p, s);
   }
   if (p.M <= 64) return launch_tile<T, 64, 256, true>(p, sms, s);
+  // Above, whichever tiles need least time, in groups of K (0.36 us each): those of
+  // a CTA times the rounds over the SMs, and the addition of a cluster that shares a
+  // tile's groups (4 with 64 tokens, 9 with 128).  In us by pairs of CTAs, 128 and 64 tokens:
+  // 128 x 1408 x 2048 12.7, 10.4 and 9.1; 256 x 1408 x 4096 19.8, 13.4 and 15.0;
+  // 300 x 2048 x 6144 26.1, 20.7 and 26.7; 1024 x 1408 x 2048 14.0, 13.6 and
+  // 22.6; 128 x 14336 x 4096 37.3, 26.2 and 37.6.
   const long long wide = (p.N + 127) / 128;
-  const long long pairs = (p.M + 255) / 256 * wide, singles = (p.M + 127) / 128 * wide;
-  const long long pair_rounds = (pairs + sms / 2 - 1) / (sms / 2), single_rounds = (singles + sms - 1) / sms;
-  return pair_rounds <= single_rounds ? launch_tile<T, 256, 256, true>(p, sms, s) : launch_tile<T, 128, 256, true>(p, sms, s);
+  auto groups = [&](long long tiles, int splits, int added) {
+    return splits > 1 ? p.KB / splits + added : (tiles + sms - 1) / sms * p.KB;
+  };
+  const long long pairs = (p.M + 255) / 256 * wide, singles = (p.M + 127) / 128 * wide, halves = (p.M + 63) / 64 * wide;
+  int split128 = 1, split64 = 1;
+  if (int e = pw_fp8::splits_of<T, 128, 256, true>(singles, p.KB, split128)) return e;
+  if (int e = pw_fp8::splits_of<T, 64, 256, true>(halves, p.KB, split64)) return e;
+  const long long by_pairs = (pairs + sms / 2 - 1) / (sms / 2) * p.KB;
+  const long long by_128 = groups(singles, split128, 9), by_64 = groups(halves, split64, 4);
+  if (by_pairs <= by_128 && by_pairs <= by_64) return launch_tile<T, 256, 256, true>(p, sms, s);
+  return by_128 <= by_64 ? launch_tile<T, 128, 256, true>(p, sms, s) : launch_tile<T, 64, 256, true>(p, sms, s);
 }
 
 }  // namespace

@@ -609,6 +609,18 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
   }
 }
 
+// The kernel's shared memory, set once per device.
+template <typename T, int kTokens, int kWide, bool kGated>
+int allow_smem(int dev) {
+  constexpr int kDevs = 64;
+  static bool done[kDevs] = {};
+  if (dev < kDevs && done[dev]) return PW_OK;
+  PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kTokens, kWide, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   Tile<kTokens, kWide, kGated>::kSmem));
+  if (dev < kDevs) done[dev] = true;
+  return PW_OK;
+}
+
 // How many clusters of n CTAs the device runs at once (asked once per device).
 template <typename T, int kTokens, int kWide, bool kGated>
 int clusters_at_once(int dev, int n, int& fit) {
@@ -619,6 +631,7 @@ int clusters_at_once(int dev, int n, int& fit) {
     fit = known[dev][n] - 1;
     return PW_OK;
   }
+  if (int e = allow_smem<T, kTokens, kWide, kGated>(dev)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(n));
   cfg.blockDim = dim3(C::kThreads);
@@ -634,18 +647,31 @@ int clusters_at_once(int dev, int n, int& fit) {
   return PW_OK;
 }
 
+// How many CTAs share the groups of each of `tiles` tiles of single CTAs.  Few
+// tiles: 2 or 4, as long as all clusters run at once (4 do not fit everywhere).  A
+// group less of the loop takes 0.28 us, a cluster and its addition 1.5 with 64 tokens
+// and 3 with 128: 32 x 2048 x 4096 takes 13.0, 10.2 and 8.0 us with 1, 2 and 4, 32 x
+// 2048 x 1024 5.7, 6.0 and 5.4, 100 x 4096 x 1024 6.1, 7.3 and 7.4.
+template <typename T, int kTokens, int kWide, bool kGated>
+int splits_of(long long tiles, int groups, int& splits) {
+  int dev = 0;
+  PW_CUDA_TRY(cudaGetDevice(&dev));
+  splits = 1;
+  for (int n = 2; n <= 4; n *= 2) {
+    int fit = 0;
+    if (int e = clusters_at_once<T, kTokens, kWide, kGated>(dev, n, fit)) return e;
+    if (tiles <= fit && groups - groups / n >= (kTokens == 64 ? 6 : 12)) splits = n;
+  }
+  return PW_OK;
+}
+
 template <typename T, int kTokens, int kWide, bool kGated>
 int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
   using C = Tile<kTokens, kWide, kGated>;
   constexpr bool kPair = C::kPair;
-  constexpr int kDevs = 64;
-  static bool attr_done[kDevs] = {};
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
-  if (dev >= kDevs || !attr_done[dev]) {
-    PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kTokens, kWide, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
-    if (dev < kDevs) attr_done[dev] = true;
-  }
+  if (int e = allow_smem<T, kTokens, kWide, kGated>(dev)) return e;
   Maps<kGated> maps;
   const uint64_t da[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M)};
   const uint64_t db[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N)};
@@ -681,17 +707,7 @@ int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
     cluster = 2;
     ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   } else {
-    // Few tiles: 2 or 4 CTAs share one's groups, as long as all clusters run at
-    // once (4 do not fit everywhere).  A group less of the loop takes 0.28 us, a
-    // cluster and its addition 1.5 with 64 tokens and 3 with 128: 32 x 2048 x
-    // 4096 takes 13.0, 10.2 and 8.0 us with 1, 2 and 4, 32 x 2048 x 1024 5.7, 6.0
-    // and 5.4, 100 x 4096 x 1024 6.1, 7.3 and 7.4.
-    p.splits = 1;
-    for (int n = 2; n <= 4; n *= 2) {
-      int fit = 0;
-      if (int e = clusters_at_once<T, kTokens, kWide, kGated>(dev, n, fit)) return e;
-      if (tiles <= fit && p.KB - p.KB / n >= (kTokens == 64 ? 6 : 12)) p.splits = n;
-    }
+    if (int e = splits_of<T, kTokens, kWide, kGated>(tiles, p.KB, p.splits)) return e;
     cluster = p.splits;
     ctas = p.splits > 1 ? tiles * p.splits : (tiles < sms ? tiles : sms);
   }
