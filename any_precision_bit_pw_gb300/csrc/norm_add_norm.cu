@@ -4,8 +4,11 @@
 //   r = residual_scale * residual + block_scale * gate * u
 //   y = r * rsqrt(mean(r^2) + eps) * weight           (in 16 bits and/or in e4m3)
 //
-// Every value is read and written once: memory bandwidth bounds it, and for a
-// few rows the latency of one load, two reductions and one store.
+// Every value is read and written once: memory bandwidth bounds it (8192 x 6144
+// bf16 to e4m3 60.5 us, 5.8 TB/s; 8192 x 5120 in 16 bits 52.5 us, 6.4 TB/s; with a gate for
+// every row 75 us at 6144 columns, 6.7 TB/s), for a few rows the latency of one load, two
+// reductions and one store (one row of 4096: 2.6 us), and for odd widths the
+// instructions that clip and shift (1531 x 5121 20 us, 13 at 5120).
 #include "rows.cuh"
 
 namespace {
@@ -32,9 +35,9 @@ struct NormsParams {
 };
 
 constexpr int kMaxWarps = 16;
-// Rows of one part: two CTAs an SM, whose 64 registers a thread (with a gate for
-// every row 80) set the threads.
-constexpr int most_threads(int parts, bool matrix) { return parts == 1 && matrix ? 384 : 32 * kMaxWarps; }
+// Rows of one part: two CTAs an SM, whose 64 registers a thread set the threads; 80
+// with a gate for every row, and where cells move (8192 x 5121: 73 us, 94 with 64).
+constexpr int most_threads(int parts, bool more) { return parts == 1 && more ? 384 : 32 * kMaxWarps; }
 constexpr int line_floats(int parts) { return parts * 32 * kMaxWarps + 1; }
 
 // The sum over a CTA's threads, for all of them.  `part` (of the warps, zeros
@@ -67,9 +70,9 @@ __device__ __forceinline__ float block_sum(uint64_t two, float* part) {
 // fill the registers and more: they read the vectors from the L1 cache and load
 // nothing ahead.
 // Arithmetic in packed pairs: with single instructions the kernel was bound by
-// their number (39 a value; 8192 x 6144 to e4m3 102 us).
+// their number (39 a value; 8192 x 6144 to e4m3 102 us, now 60.5).
 template <typename T, int kParts, Access kAccess, bool kMatrix>
-__global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
+__global__ void __launch_bounds__(most_threads(kParts, kMatrix || kAccess == Access::kSame), kParts == 1 ? 2 : 1) norms_kernel(const __grid_constant__ NormsParams p) {
   constexpr bool kKeep = kParts <= 2, kAhead = kParts <= 2, kSame = kAccess == Access::kSame;
   static_assert(!kSame || kKeep, "moving columns find the vectors in shared memory");
   __shared__ __align__(16) float sums[2][2][kMaxWarps];   // two rows in turn, two sums: one barrier a sum
@@ -90,11 +93,23 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix), kParts == 1 ? 2
   auto col = [&](int c) { return (c * nthr + tid) * 16 - (kSame ? shift : 0); };
   auto at = [&](const void* base, int64_t row, int64_t stride) { return static_cast<const T*>(base) + row * stride; };
   auto load = [&](const void* base, int64_t row, int64_t stride, int c) {
-    const int first = kSame ? (c * nthr + tid) * 16 - shift_of(row) : col(c);   // (of a row ahead: its own shift)
-    return pw::load16<T, kAccess>(at(base, row, stride), first, p.cols);
+    if constexpr (kSame) {
+      // (of a row ahead: its own shift.)  The matrix may end before the first row's first cell does, and with
+      // the last row.
+      const int first = (c * nthr + tid) * 16 - shift_of(row);
+      const bool inside = row > 0 && row + 1 < p.rows && stride >= 16;
+      return pw::load_cell(at(base, row, stride), first, p.cols, inside || (first >= 0 && first + 16 <= p.cols));
+    } else {
+      return pw::load16<T, kAccess>(at(base, row, stride), col(c), p.cols);
+    }
   };
-  auto values = [&](const pw::Sixteen& v, const void* base, int64_t row, int64_t stride, int c, uint64_t (&t)[8]) {
-    pw::unpack16<T>(pw::columns16<T, kAccess>(v, at(base, row, stride), col(c), p.cols), t);
+  auto values = [&](pw::Sixteen v, const void* base, int64_t row, int64_t stride, int c, uint64_t (&t)[8]) {
+    if constexpr (kSame) {
+      pw::clip_cell(v, col(c), p.cols);
+      pw::unpack16<T>(v, t);
+    } else {
+      pw::unpack16<T>(pw::columns16<T, kAccess>(v, at(base, row, stride), col(c), p.cols), t);
+    }
   };
   auto store = [&](void* base, int64_t row, int64_t stride, int c, const uint64_t (&t)[8]) {
     pw::store16<T, kAccess>(static_cast<T*>(base) + row * stride, col(c), p.cols, pw::pack16<T>(t));
@@ -331,7 +346,7 @@ int launch_rows(const NormsParams& p, cudaStream_t s) {
   if (sms < 1) return pw::set_error(PW_ERR_CUDA, "could not query the SM count");
   const int units = (p.cols + (kAccess == Access::kSame ? 30 : 15)) / 16;   // 16 columns each, or up to 15 before them
   int parts = 1;
-  while ((units + parts - 1) / parts > most_threads(parts, kMatrix)) parts *= 2;
+  while ((units + parts - 1) / parts > most_threads(parts, kMatrix || kAccess == Access::kSame)) parts *= 2;
   const int threads = ((units + parts - 1) / parts + 31) & ~31;
   switch (parts) {
     case 1: return launch_parts<T, 1, kAccess, kMatrix>(p, threads, sms, s);

@@ -62,7 +62,9 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int cols, const
 //  kHalves   of whole 16 bytes: two
 //  kSame     all rows with the same number s of values between a 32-byte address
 //            and their first column: a thread takes columns 16i - s .. 16i - s + 15,
-//            those of one 32-byte cell, and the row's first and last cell value by value
+//            those of one 32-byte cell.  What the first and the last cell of a row
+//            hold of its neighbours is loaded with them, unless the matrix may end
+//            there, and dropped; they are stored value by value
 //  kShifted  any.  The row's memory is cut into granules of 16 bytes at 16-byte
 //            addresses: with s values of the first one before the row, granule j
 //            holds columns 8j - s .. 8j - s + 7.  Granules inside the row move in one
@@ -126,19 +128,17 @@ __device__ __forceinline__ uint4 shift_up(const uint4& v) {
                     __shfl_up_sync(0xFFFFFFFFu, v.z, 1), __shfl_up_sync(0xFFFFFFFFu, v.w, 1));
 }
 
-// What the thread of columns c .. c+15 loads of the row: those columns (kSame: c may
-// be negative), or (kShifted) two granules.
+// What the thread of columns c .. c+15 loads of the row: those columns, or
+// (kShifted) two granules.
 template <typename T, Access kAccess>
 __device__ __forceinline__ Sixteen load16(const T* row, int c, int cols) {
   Sixteen v{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if constexpr (kAccess == Access::kWide || kAccess == Access::kSame) {
-    if (kAccess == Access::kWide ? c < cols : c >= 0 && c + 16 <= cols)
+  if constexpr (kAccess == Access::kWide) {
+    if (c < cols)
       asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z), "=r"(v.hi.w)
                    : "l"(row + c)
                    : "memory");
-    else if (kAccess == Access::kSame && c < cols)
-      v = Sixteen{by_value8(row, c, cols), by_value8(row, c + kVec, cols)};
   } else if constexpr (kAccess == Access::kHalves) {
     if (c < cols) v.lo = *reinterpret_cast<const uint4*>(row + c);
     if (c + kVec < cols) v.hi = *reinterpret_cast<const uint4*>(row + c + kVec);
@@ -191,6 +191,31 @@ __device__ __forceinline__ void store16(T* row, int c, int cols, const Sixteen& 
     granule(s ? eight_of(v.lo, v.hi, off) : v.hi, c + kVec - s, 0);
     if (lane == 31 && s) store_by_value8(row, c + kVec, c + 2 * kVec - s, cols, v.hi);   // and the last lane's end is nobody else's
   }
+}
+// kSame: the cell of columns c .. c+15 (c may be negative); `whole`: all of it lies in
+// the matrix.  (One load, whose values are dropped where they are used: loads of
+// single values are packed at once, which waits for each of them in the warps at
+// the row's ends, and the others wait for these at the barrier: a third of all
+// stalls.)
+template <typename T>
+__device__ __forceinline__ Sixteen load_cell(const T* row, int c, int cols, bool whole) {
+  Sixteen v{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (c >= cols) return v;
+  if (!whole) return Sixteen{by_value8(row, c, cols), by_value8(row, c + kVec, cols)};
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z), "=r"(v.hi.w)
+               : "l"(row + c)
+               : "memory");
+  return v;
+}
+// Values outside the row to 0.
+__device__ __forceinline__ void clip_cell(Sixteen& v, int c, int cols) {
+  if (c >= 0 && c + 16 <= cols) return;
+  uint32_t w[8] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w, v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i] &= (c + 2 * i >= 0 && c + 2 * i < cols ? 0xFFFFu : 0u) | (c + 2 * i + 1 >= 0 && c + 2 * i + 1 < cols ? 0xFFFF0000u : 0u);
+  v = Sixteen{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
 }
 template <typename T>
 __device__ __forceinline__ void unpack16(const Sixteen& u, uint64_t (&v)[8]) {
