@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix || kAccess == Acc
     for (int i = tid; i < static_cast<int>(sizeof(tops) / 4); i += nthr) (&tops[0][0])[i] = 0u;
     if (tid < 32) lines[tid * kPitch] = 0.0f;
   }
-  if (tid < 4 * kMaxWarps) (&sums[0][0][0])[tid] = 0.0f;
+  for (int i = tid; i < 4 * kMaxWarps; i += nthr) (&sums[0][0][0])[i] = 0.0f;
   int shift = 0;   // kSame: of the row
   auto shift_of = [&](int64_t row) {
     return static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + row * p.x_stride) >> 1 & 15);
