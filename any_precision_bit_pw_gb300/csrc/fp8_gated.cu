@@ -148,25 +148,35 @@ int launch(const GatedParams& p, cudaStream_t s) {
     if (p.M <= 16) return launch_stream<T, 2, 2, 8>(p, s);
     if (p.M <= 32 && !p.q) return launch_stream<T, 4, 2, 8>(p, s);
   }
-  if (p.M <= 64) return launch_tile<T, 64, 256, true>(p, sms, s);
-  // Above, whichever tiles need least time, in groups of K (0.36 us each): those of
+  // Above, whichever tiles need least time, in groups of K (0.42 us each): those of
   // a CTA times the rounds over the SMs, and the addition of a cluster that shares a
   // tile's groups (4 with 64 tokens, 9 with 128).  In us by pairs of CTAs, 128 and 64 tokens:
   // 128 x 1408 x 2048 12.7, 10.4 and 9.1; 256 x 1408 x 4096 19.8, 13.4 and 15.0;
   // 300 x 2048 x 6144 26.1, 20.7 and 26.7; 1024 x 1408 x 2048 14.0, 13.6 and
   // 22.6; 128 x 14336 x 4096 37.3, 26.2 and 37.6.
-  const long long wide = (p.N + 127) / 128;
-  auto groups = [&](long long tiles, int splits, int added) {
-    return splits > 1 ? p.KB / splits + added : (tiles + sms - 1) / sms * p.KB;
+  const long long wide = (p.N + 127) / 128, strips = (p.M + 127) / 128;
+  auto groups = [&](long long tiles, int splits, double added) {
+    return splits > 1 ? p.KB / splits + added : static_cast<double>((tiles + sms - 1) / sms) * p.KB;
   };
-  const long long pairs = (p.M + 255) / 256 * wide, singles = (p.M + 127) / 128 * wide, halves = (p.M + 63) / 64 * wide;
-  int split128 = 1, split64 = 1;
-  if (int e = pw_fp8::splits_of<T, 128, 256, true>(singles, p.KB, split128)) return e;
-  if (int e = pw_fp8::splits_of<T, 64, 256, true>(halves, p.KB, split64)) return e;
-  const long long by_pairs = (pairs + sms / 2 - 1) / (sms / 2) * p.KB;
-  const long long by_128 = groups(singles, split128, 9), by_64 = groups(halves, split64, 4);
-  if (by_pairs <= by_128 && by_pairs <= by_64) return launch_tile<T, 256, 256, true>(p, sms, s);
-  return by_128 <= by_64 ? launch_tile<T, 128, 256, true>(p, sms, s) : launch_tile<T, 64, 256, true>(p, sms, s);
+  int split = 1;
+  if (int e = pw_fp8::splits_of<T, 64, 256, true>((p.M + 63) / 64 * wide, p.KB, split)) return e;
+  const double by_64 = groups((p.M + 63) / 64 * wide, split, 4);
+  if (int e = pw_fp8::splits_of<T, 128, 256, true>(strips * wide, p.KB, split)) return e;
+  const double by_128 = p.M <= 64 ? INFINITY : groups(strips * wide, split, 9);
+  const long long pairs = (p.M + 255) / 256 * wide;
+  const double by_pairs = p.M <= 64 ? INFINITY : static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * p.KB;
+  const double least = fmin(fmin(by_64, by_128), by_pairs);
+  // For 16-bit results also 128 tokens by 64 columns: three quarters of a group's
+  // time for half of the work, but 4 groups less to begin and end with (509 x 1408 x
+  // 2048 9.3 us, 12.3 by pairs; 64 x 1408 x 2048 7.8 and 8.7; but 1024 x 1408 x
+  // 2048 15.5 and 12.9, 128 x 14336 x 4096 29.0 and 26.3).
+  if (!p.q) {
+    const long long tiles = strips * ((p.N + 63) / 64);
+    if (int e = pw_fp8::splits_of<T, 128, 128, true>(tiles, p.KB, split)) return e;
+    if (0.76 * groups(tiles, split, 7) - 4 < least) return launch_tile<T, 128, 128, true>(p, sms, s);
+  }
+  if (least == by_pairs) return launch_tile<T, 256, 256, true>(p, sms, s);
+  return least == by_128 ? launch_tile<T, 128, 256, true>(p, sms, s) : launch_tile<T, 64, 256, true>(p, sms, s);
 }
 
 }  // namespace

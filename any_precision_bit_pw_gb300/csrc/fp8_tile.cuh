@@ -135,7 +135,8 @@ struct Tile {
   static constexpr int kPartRow = kN + 4;   // floats of a row of sums in shared memory: 16-byte lanes on distinct banks
   static constexpr int kOutN = kGated ? kN / 2 : kN;   // columns of the result
   static_assert(kSmem <= 227 * 1024 && (kPair || kRowsA * kPartRow * 4 <= kStages * kStageBytes), "shared memory");
-  static_assert(!kGated || kN == 256, "128 rows of each weight: a group of the result's scales");
+  static constexpr bool kCodes = kGated && kOutN == 128;   // a tile has whole groups of the result's scales
+  static constexpr int kHalf = kGated ? kCols / 2 : kCols;  // of the result's columns a thread has
 };
 template <bool kGated>
 using Params = typename std::conditional<kGated, GatedParams, LinearParams>::type;
@@ -176,9 +177,9 @@ __device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int&
 }
 
 //
-// Gated: a tile's weight rows are 128 of the gate's and the same 128 of the other
-// weight (of a pair, a CTA loads one of them); a thread sums 64 columns of each,
-// so that the activation and the product are its own.
+// Gated: a tile's weight rows are 128 (or 64, for 16-bit results only) of the gate's and
+// the same of the other weight (of a pair, a CTA loads one of them); a thread sums 64
+// (32) columns of each, so that the activation and the product are its own.
 template <typename T, int kTokens, int kWide, bool kGated>
 __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ Params<kGated> p, const __grid_constant__ Maps<kGated> maps) {
@@ -211,10 +212,10 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
       // (seven fours of a tile of two groups or more).
       const uint32_t sbar = pw::smem_u32(&sh.scales[slot.at]), sdst = scale_smem + slot.at * C::kSlotBytes;
       if (pw::elect_one()) {
-        pw::mbar_arrive_expect_tx(sbar, 16 * (C::kRowsA + C::kN / 128));
+        pw::mbar_arrive_expect_tx(sbar, 16 * (C::kRowsA + (kGated ? 2 : C::kN / 128)));
         pw::tma_load_2d(sdst, &maps.sa, kb & ~3, row_a, sbar);
-        pw::tma_load_2d(sdst + kTokenScaleBytes, &maps.sb, kb & ~3, nt * (C::kOutN / 128), sbar);
-        if constexpr (kGated) pw::tma_load_2d(sdst + kTokenScaleBytes + 128, &maps.su, kb & ~3, nt, sbar);
+        pw::tma_load_2d(sdst + kTokenScaleBytes, &maps.sb, kb & ~3, nt * C::kOutN / 128, sbar);
+        if constexpr (kGated) pw::tma_load_2d(sdst + kTokenScaleBytes + 128, &maps.su, kb & ~3, nt * C::kOutN / 128, sbar);
       }
       ++fours;
       slot.next();
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         pw::mbar_arrive_expect_tx(bar, C::kStageBytes);
         pw::tma_load_2d(dst, &maps.a, kb * pw::kGroup, row_a, bar);
         pw::tma_load_2d(dst + C::kRowsA * kBoxBytes, &maps.b, kb * pw::kGroup, row_b, bar);
-        if constexpr (kGated) pw::tma_load_2d(dst + (C::kRowsA + 128) * kBoxBytes, &maps.u, kb * pw::kGroup, row_b, bar);
+        if constexpr (kGated) pw::tma_load_2d(dst + (C::kRowsA + C::kOutN) * kBoxBytes, &maps.u, kb * pw::kGroup, row_b, bar);
       }
     }
     stage.next();
@@ -406,18 +407,19 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         const uint64_t scale_u = kGated ? pw::pack_f32x2(__float_as_uint(sc_u), __float_as_uint(sc_u)) : 0;
         if (!(ok = wait(sh.done[buf], acc.parity, sh, p))) break;
         pw::tc_fence_after();
-        const uint32_t src = tmem + lanes + buf * C::kN + (kGated ? 64 : C::kCols) * side;
+        const uint32_t src = tmem + lanes + buf * C::kN + C::kHalf * side;
         uint32_t v[2][16];
 #pragma unroll
         for (int c = 0; c < C::kCols / 32; ++c) {
-          const int col = kGated && c >= 2 ? 64 + 32 * c : 32 * c;   // gated: 64 columns of each weight
+          const bool other = kGated && 32 * c >= C::kHalf;           // gated: kHalf columns of each weight
+          const int col = other ? C::kOutN - C::kHalf + 32 * c : 32 * c;
           pw::tmem_ld_x16(src + col, v[0]);
           pw::tmem_ld_x16(src + col + 16, v[1]);
           pw::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             sum[16 * c + i] = pw::fma_f32x2(pw::pack_f32x2(v[i / 8][2 * (i % 8)], v[i / 8][2 * (i % 8) + 1]),
-                                            kGated && c >= 2 ? scale_u : scale, sum[16 * c + i]);
+                                            other ? scale_u : scale, sum[16 * c + i]);
         }
         pw::tc_fence_before();
         __syncwarp();
@@ -433,26 +435,26 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
       if (!kPair && p.splits > 1) {
         // rows of sums for the cluster; the copies' memory is free (every MMA
         // of the CTA has completed)
-        float* part = reinterpret_cast<float*>(smem) + (32 * quarter + lane) * C::kPartRow + (kGated ? 64 : C::kCols) * side;
+        float* part = reinterpret_cast<float*>(smem) + (32 * quarter + lane) * C::kPartRow + C::kHalf * side;
 #pragma unroll
         for (int i = 0; i < C::kCols / 4; ++i) {
           float4 f;
           pw::unpack_f32x2(sum[2 * i], f.x, f.y);
           pw::unpack_f32x2(sum[2 * i + 1], f.z, f.w);
-          *reinterpret_cast<float4*>(part + 4 * i + (kGated && i >= 16 ? 64 : 0)) = f;
+          *reinterpret_cast<float4*>(part + 4 * i + (4 * i >= C::kHalf ? C::kOutN - C::kHalf : 0)) = f;
         }
         break;   // one tile per cluster
       }
       if constexpr (kGated) {
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < C::kHalf / 2; ++i) {
           float h0, h1;
-          sum[i] = gated2(sum[i], sum[32 + i], p.act);
+          sum[i] = gated2(sum[i], sum[C::kHalf / 2 + i], p.act);
           pw::unpack_f32x2(sum[i], h0, h1);
           top = pw::max3_nan(top, fabsf(h0), fabsf(h1));
         }
-        if (p.q) {
+        if (C::kCodes && p.q) {
           gsh.top[turn][side][32 * quarter + lane] = top;
           __syncwarp();
           if (lane == 0) pw::mbar_arrive(pw::smem_u32(&gsh.met[quarter]));
@@ -492,40 +494,60 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         }
         if (!p.y) continue;
       }
-      // 16-bit rows through shared memory, 32 rows x 64 columns at a time.  A
-      // tiled store drops what lies past the matrix in whole units of 16 bytes
-      // only: where N ends inside one, the last box goes value by value.
+      if constexpr (kGated && !C::kCodes) {   // 32 columns a row: 64 bytes
+        if (m < p.M) {
+          T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
 #pragma unroll
-      for (int box = 0; box < C::kOutN / 2 / 64; ++box) {
-        const int n = n0 + 64 * box;
-        if (p.wide_y && (p.N % 8 == 0 || n + 64 <= p.N)) {
-          pw::bulk_wait_read();   // the box before has left
-          __syncwarp();
+          for (int i = 0; i < C::kHalf / 8; ++i) {
+            float f[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t w[4];
+            for (int j = 0; j < 4; ++j) pw::unpack_f32x2(sum[4 * i + j], f[2 * j], f[2 * j + 1]);
+            if (p.wide_y && n0 + 8 * i + 8 <= p.N) {
+              *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pw::pack2<T>(f[0], f[1]), pw::pack2<T>(f[2], f[3]),
+                                                                pw::pack2<T>(f[4], f[5]), pw::pack2<T>(f[6], f[7]));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float lo, hi;
-              pw::unpack_f32x2(sum[32 * box + 4 * i + j], lo, hi);
-              w[j] = pw::pack2<T>(lo, hi);
+              for (int j = 0; j < 8; ++j)
+                if (n0 + 8 * i + j < p.N) y[8 * i + j] = pw::from_float<T>(f[j]);
             }
-            *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          pw::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 < p.M && n < p.N) {
-            pw::tma_store_2d(&maps.y, n, m0, pw::smem_u32(out));
-            pw::bulk_commit();
-          }
-        } else if (m < p.M) {
-          T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n;
+        }
+      } else {
+        // 16-bit rows through shared memory, 32 rows x 64 columns at a time.  A
+        // tiled store drops what lies past the matrix in whole units of 16 bytes
+        // only: where N ends inside one, the last box goes value by value.
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float lo, hi;
-            pw::unpack_f32x2(sum[32 * box + i], lo, hi);
-            if (n + 2 * i < p.N) y[2 * i] = pw::from_float<T>(lo);
-            if (n + 2 * i + 1 < p.N) y[2 * i + 1] = pw::from_float<T>(hi);
+        for (int box = 0; box < C::kOutN / 2 / 64; ++box) {
+          const int n = n0 + 64 * box;
+          if (p.wide_y && (p.N % 8 == 0 || n + 64 <= p.N)) {
+            pw::bulk_wait_read();   // the box before has left
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                pw::unpack_f32x2(sum[32 * box + 4 * i + j], lo, hi);
+                w[j] = pw::pack2<T>(lo, hi);
+              }
+              *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            pw::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && m0 < p.M && n < p.N) {
+              pw::tma_store_2d(&maps.y, n, m0, pw::smem_u32(out));
+              pw::bulk_commit();
+            }
+          } else if (m < p.M) {
+            T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float lo, hi;
+              pw::unpack_f32x2(sum[32 * box + i], lo, hi);
+              if (n + 2 * i < p.N) y[2 * i] = pw::from_float<T>(lo);
+              if (n + 2 * i + 1 < p.N) y[2 * i + 1] = pw::from_float<T>(hi);
+            }
           }
         }
       }
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
       // each CTA of the cluster finishes its share of the tile's rows
       int mt, nt;
       tile_at<C::kM>(first_tile, tiles_m, tiles_n, mt, nt);
-      const int rows = min(C::kM, p.M - mt * C::kM), col = 4 * lane, n = nt * 128 + col;
+      const int rows = min(C::kM, p.M - mt * C::kM), col = 4 * lane, n = nt * C::kOutN + col;
       auto sum_at = [&](uint32_t at) {   // all loads, then the sum in the order of the ranks
         float4 part[4];
 #pragma unroll
@@ -566,15 +588,16 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         return v;
       };
       for (int row = rank + p.splits * warp; row < rows; row += p.splits * (C::kThreads / 32)) {
+        if (col >= C::kOutN) continue;
         const uint32_t at = stages + 4u * static_cast<uint32_t>(row * C::kPartRow + col);
         float4 v = sum_at(at);
         if constexpr (kGated) {
-          const float4 u = sum_at(at + 4 * 128);
+          const float4 u = sum_at(at + 4 * C::kOutN);
           v = make_float4(gated(v.x, u.x, p.act), gated(v.y, u.y, p.act), gated(v.z, u.z, p.act), gated(v.w, u.w, p.act));
         }
         if (sh.dead) continue;
         if constexpr (kGated) {
-          if (p.q) {   // the warp has the 128 columns of a scale
+          if (C::kCodes && p.q) {   // the warp has the 128 columns of a scale
             float top = pw::max_nan(pw::max_nan(fabsf(v.x), fabsf(v.y)), pw::max_nan(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -678,12 +701,12 @@ int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
   const uint64_t dy[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)};
   const uint64_t sta[1] = {static_cast<uint64_t>(p.lda)}, stb[1] = {static_cast<uint64_t>(p.ldb)};
   const uint64_t sty[1] = {2 * static_cast<uint64_t>(p.ldy)};
-  const uint32_t box[2] = {kBoxBytes, C::kRowsA}, boxw[2] = {kBoxBytes, kGated ? 128 : C::kRowsB}, boxy[2] = {64, 32};
+  const uint32_t box[2] = {kBoxBytes, C::kRowsA}, boxw[2] = {kBoxBytes, static_cast<uint32_t>(kGated ? C::kOutN : C::kRowsB)}, boxy[2] = {64, 32};
   if (int e = pw::encode_tensor_map(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.a, da, sta, box)) return e;
   if (int e = pw::encode_tensor_map(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.b, db, stb, boxw)) return e;
   maps.y = maps.sa = maps.sb = maps.a;
   const uint64_t dsb[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>((p.N + pw::kGroup - 1) / pw::kGroup)};
-  const uint32_t boxb[2] = {4, C::kOutN / 128};
+  const uint32_t boxb[2] = {4, kGated ? 1u : C::kN / 128u};
   if (p.wide_scales) {
     const uint64_t dsa[2] = {static_cast<uint64_t>(p.KB), static_cast<uint64_t>(p.M)};
     const uint64_t stsa[1] = {4 * static_cast<uint64_t>(p.sa_stride)}, stsb[1] = {4 * static_cast<uint64_t>(p.sb_stride)};

@@ -72,12 +72,13 @@ def run(m, n, k, dtype, act, y_pad=3, q_pad=None, seed=0, strides=None):
     within(y[:, :n], h, u * np.abs(h) * 1.01 + off * 1.01 + TINY[dtype])
     check_codes(codes, sc[:, :nb], h, off)
     assert (y[:, n:] == 7).all() and (q[:, n:] == 9).all() and (sc[:, nb:] == 5).all()
-    # one output alone: the same bits
+    # one output alone (other tiles may add in another order)
     y2, q2, sc2 = torch.zeros_like(y), torch.zeros_like(q), torch.zeros_like(sc)
     pw.pw_fp8_gated_linear(*args, st, y=y2[:, :n], activation=ACTS[act])
     pw.pw_fp8_gated_linear(*args, st, q=q2[:, :n], scale=sc2[:, :nb], activation=ACTS[act])
-    assert torch.equal(y2[:, :n], y[:, :n]) and torch.equal(q2[:, :n], q[:, :n]) and torch.equal(sc2[:, :nb], sc[:, :nb])
-    assert int(st.item()) == 0
+    within(y2[:, :n], h, u * np.abs(h) * 1.01 + off * 1.01 + TINY[dtype])
+    check_codes(q2.view(torch.float8_e4m3fn)[:, :n], sc2[:, :nb], h, off)
+    assert int(st.item()) == 0 and (y2[:, n:] == 0).all() and (q2[:, n:] == 0).all()
 
 
 SIZES = [(1, 1, 16), (1, 128, 128), (3, 17, 130), (7, 200, 100), (8, 1000, 512), (8, 130, 2064), (9, 128, 1000), (16, 64, 2048),

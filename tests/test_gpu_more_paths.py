@@ -32,7 +32,10 @@ def gated(m, n, k, q=True):
     (40, 20000, 256, True, "linear_tile_kernel", (64, 256)),         # more tiles than SMs
     (128, 300, 2048, True, "linear_tile_kernel", (64, 256)),         # 4 CTAs a tile
     (240, 1408, 4096, True, "linear_tile_kernel", (128, 256)),       # and of 128 tokens
-    (1100, 4200, 256, True, "linear_tile_kernel", (128, 256)), (2500, 1100, 256, True, "linear_tile_kernel", (256, 256))])
+    (1100, 4200, 256, True, "linear_tile_kernel", (128, 256)),
+    (509, 1408, 700, False, "linear_tile_kernel", (128, 128)), (60, 700, 2048, False, "linear_tile_kernel", (128, 128)),
+    (2000, 1500, 256, False, "linear_tile_kernel", (128, 128)),
+    (2500, 1100, 256, True, "linear_tile_kernel", (256, 256))])
 def test_every_kernel_of_the_gated_block(m, n, k, q, kernel, numbers):
     if sms() != 152:
         pytest.skip("the rules count SMs")
