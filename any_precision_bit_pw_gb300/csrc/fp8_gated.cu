@@ -159,9 +159,9 @@ int launch(const GatedParams& p, cudaStream_t s) {
     return splits > 1 ? p.KB / splits + added : static_cast<double>((tiles + sms - 1) / sms) * p.KB;
   };
   int split = 1;
-  if (int e = pw_fp8::splits_of<T, 64, 256, true>((p.M + 63) / 64 * wide, p.KB, split)) return e;
+  if (int e = pw_fp8::splits_of<T, 64, 256, true, false>((p.M + 63) / 64 * wide, p.KB, split)) return e;
   const double by_64 = groups((p.M + 63) / 64 * wide, split, 4);
-  if (int e = pw_fp8::splits_of<T, 128, 256, true>(strips * wide, p.KB, split)) return e;
+  if (int e = pw_fp8::splits_of<T, 128, 256, true, false>(strips * wide, p.KB, split)) return e;
   const double by_128 = p.M <= 64 ? INFINITY : groups(strips * wide, split, 9);
   const long long pairs = (p.M + 255) / 256 * wide;
   const double by_pairs = p.M <= 64 ? INFINITY : static_cast<double>((pairs + sms / 2 - 1) / (sms / 2)) * p.KB;
@@ -172,7 +172,7 @@ int launch(const GatedParams& p, cudaStream_t s) {
   // 2048 15.5 and 12.9, 128 x 14336 x 4096 29.0 and 26.3).
   if (!p.q) {
     const long long tiles = strips * ((p.N + 63) / 64);
-    if (int e = pw_fp8::splits_of<T, 128, 128, true>(tiles, p.KB, split)) return e;
+    if (int e = pw_fp8::splits_of<T, 128, 128, true, false>(tiles, p.KB, split)) return e;
     if (0.76 * groups(tiles, split, 7) - 4 < least) return launch_tile<T, 128, 128, true>(p, sms, s);
   }
   if (least == by_pairs) return launch_tile<T, 256, 256, true>(p, sms, s);

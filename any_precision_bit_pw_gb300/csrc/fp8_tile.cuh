@@ -165,6 +165,47 @@ __device__ __forceinline__ bool wait(const uint64_t& bar, uint32_t parity, TileS
   return pw::warp_wait(&bar, parity, &sh.dead, p.status);
 }
 
+// A warp's 32 rows of kW 16-bit results (a thread has a row, in pairs) to rows of y at
+// any address: through shared memory, so that a store covers neighbouring columns of a
+// row (value by value from its owner, a store touches 32 rows: 8192 x 8191 x 6144 takes
+// 839 us, 324 so; gated 2000 x 1500 x 256 36 and 11).  Columns from
+// `left` and rows from `rows` on are not written.
+template <typename T, int kW>
+__device__ __forceinline__ void store_rows(const uint64_t* sum, T* y, int64_t ldy, int rows, int left, unsigned char* out) {
+  constexpr int kUnits = kW / 8, kRow = 2 * kW;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      pw::unpack_f32x2(sum[4 * i + j], lo, hi);
+      w[j] = pw::pack2<T>(lo, hi);
+    }
+    *reinterpret_cast<uint4*>(out + lane * kRow + ((i ^ (lane & (kUnits - 1))) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  // two columns a lane; 64 columns take a warp, 32 half of one
+  constexpr int kAtOnce = 64 / kW;
+  const int col = 2 * (lane % (kW / 2)), unit = col >> 3;
+  const bool pairs = (reinterpret_cast<uintptr_t>(y) & 3) == 0 && ldy % 2 == 0;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+    const int r = r0 + lane / (kW / 2);
+    if (r >= rows || col >= left) continue;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(out + r * kRow + ((unit ^ (r & (kUnits - 1))) << 4) + 2 * (col & 7));
+    uint16_t* to = reinterpret_cast<uint16_t*>(y + r * ldy + col);
+    if (pairs && col + 1 < left) {
+      *reinterpret_cast<uint32_t*>(to) = w;
+    } else {
+      to[0] = static_cast<uint16_t>(w);
+      if (col + 1 < left) to[1] = static_cast<uint16_t>(w >> 16);
+    }
+  }
+  __syncwarp();   // the memory is free again
+}
+
 // Tiles in strips of 2048 tokens, so that the CTAs that run at the same time
 // share both operands through L2.
 template <int kM>
@@ -180,7 +221,10 @@ __device__ __forceinline__ void tile_at(int tile, int tiles_m, int tiles_n, int&
 // Gated: a tile's weight rows are 128 (or 64, for 16-bit results only) of the gate's and
 // the same of the other weight (of a pair, a CTA loads one of them); a thread sums 64
 // (32) columns of each, so that the activation and the product are its own.
-template <typename T, int kTokens, int kWide, bool kGated>
+//
+// kRagged: rows of y do not start at 16-byte addresses.  (Apart, because the other
+// kernel is 4 % slower with those stores in it: 8192 x 8192 x 6144 281 and 294 us.)
+template <typename T, int kTokens, int kWide, bool kGated, bool kRagged>
 __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
     linear_tile_kernel(const __grid_constant__ Params<kGated> p, const __grid_constant__ Maps<kGated> maps) {
   using C = Tile<kTokens, kWide, kGated>;
@@ -494,7 +538,15 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         }
         if (!p.y) continue;
       }
-      if constexpr (kGated && !C::kCodes) {   // 32 columns a row: 64 bytes
+      if constexpr (kRagged) {
+        constexpr int kW = C::kHalf < 64 ? C::kHalf : 64;
+#pragma unroll
+        for (int box = 0; box < C::kHalf / kW; ++box) {
+          const int n = n0 + kW * box;
+          store_rows<T, kW>(sum + kW / 2 * box, static_cast<T*>(p.y) + static_cast<int64_t>(m0) * p.ldy + n, p.ldy, p.M - m0,
+                            p.N - n, out);
+        }
+      } else if constexpr (kGated && !C::kCodes) {   // 32 columns a row: 64 bytes
         if (m < p.M) {
           T* y = static_cast<T*>(p.y) + static_cast<int64_t>(m) * p.ldy + n0;
 #pragma unroll
@@ -502,7 +554,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
             float f[8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) pw::unpack_f32x2(sum[4 * i + j], f[2 * j], f[2 * j + 1]);
-            if (p.wide_y && n0 + 8 * i + 8 <= p.N) {
+            if (n0 + 8 * i + 8 <= p.N) {
               *reinterpret_cast<uint4*>(y + 8 * i) = make_uint4(pw::pack2<T>(f[0], f[1]), pw::pack2<T>(f[2], f[3]),
                                                                 pw::pack2<T>(f[4], f[5]), pw::pack2<T>(f[6], f[7]));
             } else {
@@ -517,9 +569,9 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
         // tiled store drops what lies past the matrix in whole units of 16 bytes
         // only: where N ends inside one, the last box goes value by value.
 #pragma unroll
-        for (int box = 0; box < C::kOutN / 2 / 64; ++box) {
+        for (int box = 0; box < C::kHalf / 64; ++box) {
           const int n = n0 + 64 * box;
-          if (p.wide_y && (p.N % 8 == 0 || n + 64 <= p.N)) {
+          if (p.N % 8 == 0 || n + 64 <= p.N) {
             pw::bulk_wait_read();   // the box before has left
             __syncwarp();
 #pragma unroll
@@ -633,19 +685,19 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
 }
 
 // The kernel's shared memory, set once per device.
-template <typename T, int kTokens, int kWide, bool kGated>
+template <typename T, int kTokens, int kWide, bool kGated, bool kRagged>
 int allow_smem(int dev) {
   constexpr int kDevs = 64;
   static bool done[kDevs] = {};
   if (dev < kDevs && done[dev]) return PW_OK;
-  PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kTokens, kWide, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  PW_CUDA_TRY(cudaFuncSetAttribute(linear_tile_kernel<T, kTokens, kWide, kGated, kRagged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    Tile<kTokens, kWide, kGated>::kSmem));
   if (dev < kDevs) done[dev] = true;
   return PW_OK;
 }
 
 // How many clusters of n CTAs the device runs at once (asked once per device).
-template <typename T, int kTokens, int kWide, bool kGated>
+template <typename T, int kTokens, int kWide, bool kGated, bool kRagged>
 int clusters_at_once(int dev, int n, int& fit) {
   using C = Tile<kTokens, kWide, kGated>;
   constexpr int kDevs = 64;
@@ -654,7 +706,7 @@ int clusters_at_once(int dev, int n, int& fit) {
     fit = known[dev][n] - 1;
     return PW_OK;
   }
-  if (int e = allow_smem<T, kTokens, kWide, kGated>(dev)) return e;
+  if (int e = allow_smem<T, kTokens, kWide, kGated, kRagged>(dev)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(n));
   cfg.blockDim = dim3(C::kThreads);
@@ -665,7 +717,7 @@ int clusters_at_once(int dev, int n, int& fit) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  PW_CUDA_TRY(cudaOccupancyMaxActiveClusters(&fit, linear_tile_kernel<T, kTokens, kWide, kGated>, &cfg));
+  PW_CUDA_TRY(cudaOccupancyMaxActiveClusters(&fit, linear_tile_kernel<T, kTokens, kWide, kGated, kRagged>, &cfg));
   if (dev < kDevs) known[dev][n] = fit + 1;
   return PW_OK;
 }
@@ -675,26 +727,26 @@ int clusters_at_once(int dev, int n, int& fit) {
 // group less of the loop takes 0.28 us, a cluster and its addition 1.5 with 64 tokens
 // and 3 with 128: 32 x 2048 x 4096 takes 13.0, 10.2 and 8.0 us with 1, 2 and 4, 32 x
 // 2048 x 1024 5.7, 6.0 and 5.4, 100 x 4096 x 1024 6.1, 7.3 and 7.4.
-template <typename T, int kTokens, int kWide, bool kGated>
+template <typename T, int kTokens, int kWide, bool kGated, bool kRagged>
 int splits_of(long long tiles, int groups, int& splits) {
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
   splits = 1;
   for (int n = 2; n <= 4; n *= 2) {
     int fit = 0;
-    if (int e = clusters_at_once<T, kTokens, kWide, kGated>(dev, n, fit)) return e;
+    if (int e = clusters_at_once<T, kTokens, kWide, kGated, kRagged>(dev, n, fit)) return e;
     if (tiles <= fit && groups - groups / n >= (kTokens == 64 ? 6 : 12)) splits = n;
   }
   return PW_OK;
 }
 
-template <typename T, int kTokens, int kWide, bool kGated>
-int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
+template <typename T, int kTokens, int kWide, bool kGated, bool kRagged>
+int launch_tile_as(Params<kGated> p, int sms, cudaStream_t s) {
   using C = Tile<kTokens, kWide, kGated>;
   constexpr bool kPair = C::kPair;
   int dev = 0;
   PW_CUDA_TRY(cudaGetDevice(&dev));
-  if (int e = allow_smem<T, kTokens, kWide, kGated>(dev)) return e;
+  if (int e = allow_smem<T, kTokens, kWide, kGated, kRagged>(dev)) return e;
   Maps<kGated> maps;
   const uint64_t da[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.M)};
   const uint64_t db[2] = {static_cast<uint64_t>(p.K), static_cast<uint64_t>(p.N)};
@@ -730,7 +782,7 @@ int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
     cluster = 2;
     ctas = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   } else {
-    if (int e = splits_of<T, kTokens, kWide, kGated>(tiles, p.KB, p.splits)) return e;
+    if (int e = splits_of<T, kTokens, kWide, kGated, kRagged>(tiles, p.KB, p.splits)) return e;
     cluster = p.splits;
     ctas = p.splits > 1 ? tiles * p.splits : (tiles < sms ? tiles : sms);
   }
@@ -745,8 +797,14 @@ int launch_tile(Params<kGated> p, int sms, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_tile_kernel<T, kTokens, kWide, kGated>, p, maps));
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, linear_tile_kernel<T, kTokens, kWide, kGated, kRagged>, p, maps));
   return PW_OK;
+}
+
+template <typename T, int kTokens, int kWide, bool kGated>
+int launch_tile(const Params<kGated>& p, int sms, cudaStream_t s) {
+  return p.y && !p.wide_y ? launch_tile_as<T, kTokens, kWide, kGated, true>(p, sms, s)
+                          : launch_tile_as<T, kTokens, kWide, kGated, false>(p, sms, s);
 }
 
 }  // namespace pw_fp8

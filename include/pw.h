@@ -499,7 +499,7 @@ int pw_quantize_fp8(const pw_quant_args* args, void* stream);
  * m up to 2^20, n and k up to 2^24, no multiples needed.  Scales whose rows
  * start at 16-byte addresses (ceil(k/128) a multiple of 4, or padded strides)
  * and a y whose rows do take the wide paths; from 65 tokens on the others cost up
- * to a third (scales) and two thirds (y) of the speed.  Nothing beside the n
+ * to a third (scales) and a fifth (y) of the speed.  Nothing beside the n
  * columns of y is written. */
 typedef struct pw_linear_args {
   const uint8_t* a;
