@@ -507,12 +507,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
           turn ^= 1;
           turn_parity ^= 1;
           const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
-          const pw::Divisor by(s);
-          const uint64_t by_s = pw::twice(by.s), by_inv = pw::twice(by.inv), by_neg = pw::twice(-by.inv);
-          auto quotient = [&](uint64_t v) {   // Divisor's, of two
-            const uint64_t q = pw::mul_f32x2(v, by_inv);
-            return pw::fma_f32x2(pw::fma_f32x2(q, by_s, v ^ 0x8000000080000000ull), by_neg, q);
-          };
+          const pw::PairDivisor by{pw::Divisor(s)};
           if (m < p.M) {
             if (side == 0) p.scale[static_cast<int64_t>(m) * p.scale_stride + nt] = s;
             uint8_t* q = p.q + static_cast<int64_t>(m) * p.ldq + n0;
@@ -520,12 +515,7 @@ __global__ void __launch_bounds__(Tile<kTokens, kWide, kGated>::kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float f[4];
-                pw::unpack_f32x2(quotient(sum[8 * i + 2 * j]), f[0], f[1]);
-                pw::unpack_f32x2(quotient(sum[8 * i + 2 * j + 1]), f[2], f[3]);
-                w[j] = pw::e4m3x4(f[0], f[1], f[2], f[3]);
-              }
+              for (int j = 0; j < 4; ++j) w[j] = pw::e4m3_pairs(by(sum[8 * i + 2 * j]), by(sum[8 * i + 2 * j + 1]));
               if (p.wide_q && n0 + 16 * i + 16 <= p.N) {
                 *reinterpret_cast<uint4*>(q + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
               } else {

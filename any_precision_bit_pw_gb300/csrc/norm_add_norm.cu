@@ -252,20 +252,21 @@ __global__ void __launch_bounds__(most_threads(kParts, kMatrix || kAccess == Acc
       if (kSame && p.q) continue;   // below
       if (p.q) {
         // 8 neighbouring threads hold a group
-        float f[16], top = 0.0f;
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          pw::unpack_f32x2(v[c][i], f[2 * i], f[2 * i + 1]);
-          top = pw::max3_nan(top, fabsf(f[2 * i]), fabsf(f[2 * i + 1]));
+          float lo, hi;
+          pw::unpack_f32x2(v[c][i], lo, hi);
+          top = pw::max3_nan(top, fabsf(lo), fabsf(hi));
         }
 #pragma unroll
         for (int o = 4; o; o >>= 1) top = pw::max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         const float s = pw::max_nan(top / pw::kE4m3Max, pw::kMinScale);
         if (col(c) < p.cols && (tid & 7) == 0) p.scale[row * p.scale_stride + col(c) / pw::kGroup] = s;
-        const pw::Divisor by(s);
+        const pw::PairDivisor by{pw::Divisor(s)};
         uint32_t code[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = pw::e4m3x4(by(f[4 * i]), by(f[4 * i + 1]), by(f[4 * i + 2]), by(f[4 * i + 3]));
+        for (int i = 0; i < 4; ++i) code[i] = pw::e4m3_pairs(by(v[c][2 * i]), by(v[c][2 * i + 1]));
         pw::store_codes16(p.q + row * p.q_stride, col(c), p.cols, code, p.q_align);
       }
     }

@@ -7,6 +7,7 @@
 
 #include <cstdint>
 
+#include "ops_common.cuh"
 #include "tc_ptx.cuh"
 #include "umma_host.h"
 
@@ -261,6 +262,22 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// Divisor's quotients, of two values.
+struct PairDivisor {
+  uint64_t s, inv, neg;
+  __device__ __forceinline__ explicit PairDivisor(const Divisor& by) : s(twice(by.s)), inv(twice(by.inv)), neg(twice(-by.inv)) {}
+  __device__ __forceinline__ uint64_t operator()(uint64_t v) const {
+    const uint64_t q = mul_f32x2(v, inv);
+    return fma_f32x2(fma_f32x2(q, s, v ^ 0x8000000080000000ull), neg, q);
+  }
+};
+// e4m3 codes of four values.
+__device__ __forceinline__ uint32_t e4m3_pairs(uint64_t a, uint64_t b) {
+  float f[4];
+  unpack_f32x2(a, f[0], f[1]);
+  unpack_f32x2(b, f[2], f[3]);
+  return e4m3x4(f[0], f[1], f[2], f[3]);
 }
 
 }  // namespace pw
