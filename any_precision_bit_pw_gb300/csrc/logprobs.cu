@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
 
   const float log_s = log2f(sum.s), base = base_of(sum.m);
   const bool empty = sum.m == -INFINITY && sum.s == 0.0f;   // nothing but -inf: no token has a probability
-  auto logprob = [&](float x) { return empty ? -INFINITY : ((x - base) * p.scale_log2 - log_s) * kLn2; };
+  // (not in powers of two: 1.44 times a masked logit, the lowest of its type, is infinite)
+  auto logprob = [&](float x) { return empty ? -INFINITY : fmaf(x - base, a.scale, -log_s * kLn2); };
   if (tid == 0) {
     if (a.lse) a.lse[row_index] = empty ? -INFINITY : fmaf(base, a.scale, log_s * kLn2);
     if (a.entropy) a.entropy[row_index] = empty ? 0.0f : (log_s - sum.t / sum.s) * kLn2;
@@ -455,7 +456,7 @@ extern "C" int pw_token_logprobs(const pw_logprob_args* args, void* stream) {
   if (a.rows > (1 << 24) || a.vocab > (1 << 28) || a.top > kMaxTop)
     return pw::set_error(PW_ERR_UNSUPPORTED, "%s: rows=%lld (at most 2^24), vocab=%d (2^28), top=%d (%d)", op,
                          static_cast<long long>(a.rows), a.vocab, a.top, kMaxTop);
-  if (!(a.scale > 0.0f) || !std::isfinite(a.scale))
+  if (!(a.scale > 0.0f) || !std::isfinite(a.scale * 1.4426950408889634f))   // in powers of two
     return pw::set_error(PW_ERR_INVALID_ARG, "%s: scale %g", op, static_cast<double>(a.scale));
   if (a.stride < a.vocab || (a.given && (a.targets_stride < a.given || a.logprobs_stride < a.given)) ||
       (a.top && (a.top_ids_stride < a.top || a.top_logprobs_stride < a.top)))

@@ -721,7 +721,9 @@ int pw_fp8_gated_linear(const pw_gated_args* args, void* stream);
  * reciprocal of a temperature) and p = softmax(z):
  *   lse = ln sum e^z,   log p(t) = z_t - lse,   entropy = -sum p ln p
  *  logits        [rows][vocab] in `dtype`: fp16, bf16 or fp32, rows `stride`
- *                apart; scale times every finite one has to be finite
+ *                apart; scale times every finite one, and their differences,
+ *                have to be finite (the type's lowest value is, as a mask);
+ *                scale up to 2^127
  *  targets       int32 [rows][given] -> logprobs fp32 [rows][given].  An id
  *                below 0 stands for no token and gets 0; one from vocab on gets
  *                NaN (both are not followed)

@@ -225,3 +225,35 @@ def test_refusals():
     with pytest.raises(ValueError):
         pw.pw_token_logprobs(z.t(), lse=torch.zeros(64, device=DEV))
     pw.pw_token_logprobs(z[:0], lse=lse[:0])
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+@pytest.mark.parametrize("rows,vocab", [(3, 40), (2, 5000), (1, 40000)])
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_masks_of_the_types_lowest_value(dtype, rows, vocab, scale):
+    """Masked tokens have finite log probabilities, of the mask's size; the others
+    do not notice them.  (A product and a sum round a masked token's: 2^-23.)"""
+    lowest = torch.finfo(dtype).min
+    z, _ = make(rows, vocab, dtype, 12)
+    z[:, 0::2] = lowest
+    z[-1, 33:] = lowest                       # fewer unmasked tokens than alternatives
+    targets = torch.tensor([[0, 1, 2, 31]], dtype=torch.int32, device=DEV).repeat(rows, 1)
+    out = call(z, targets, 32, scale)
+    lp, lse, h, ids, best = ref.token_logprobs(f64(z), targets.cpu().numpy(), 32, scale)
+    big = 2.0 ** -18 + 2.0 ** -21 * 2 * (np.abs(f64(z[:, 1::2][:, :16])).max() + 40)
+    within(out["lse"], lse, big)
+    within(out["entropy"], h, big + 2.0 ** -18 * h)
+    for got, want in ((out["logprobs"], lp), (out["top_logprobs"], best)):
+        assert np.isfinite(want).all()
+        within(got, want, np.where(np.abs(want) > 1e3, 2.0 ** -22 * np.abs(want), big))
+    assert np.array_equal(out["top_ids"].cpu().numpy(), ids)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+def test_rows_of_nothing_but_the_lowest_value(dtype):
+    z = torch.full((2, 1000), torch.finfo(dtype).min, dtype=dtype, device=DEV)
+    out = call(z, torch.tensor([[7], [999]], dtype=torch.int32, device=DEV), 3)
+    for name in ("logprobs", "top_logprobs"):
+        within(out[name], np.full(out[name].shape, -math.log(1000)), 2.0 ** -18)
+    within(out["entropy"], np.full(2, math.log(1000)), 2.0 ** -17)
+    assert out["top_ids"].tolist() == [[0, 1, 2]] * 2 and torch.isfinite(out["lse"]).all()

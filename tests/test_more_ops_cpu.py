@@ -181,3 +181,9 @@ def test_gated_refusals(L, kw, code):
     assert _gated(L, **kw) == code and "fp8_gated_linear" in pw.pw_last_error()
     assert L.pw_fp8_gated_linear(None, None) == -1
     assert _gated(L, m=0, a=None, y=None, q=None, scale=None, status=None) == 0
+
+
+def test_logprobs_scales(L):
+    """The sums run in powers of two: scale * log2(e) has to be finite."""
+    assert _logprobs(L, scale=3e38) == -1 and "scale" in pw.pw_last_error()
+    assert _logprobs(L, scale=2.0 ** 127, rows=0) == 0
