@@ -15,7 +15,9 @@
 // the second product wants its weights in, so the weights stay in registers.
 // 64 sequences of 4096 keys, one token, 32 heads on 8: 168 us, 6.4 TB/s; 24
 // sequences of 17 to 65536 keys, 48 heads on 8: 152 us, 6.3 TB/s; one of 131072
-// keys: 91 us, 5.9 TB/s; one of 1021 keys: 9.4 us.
+// keys: 91 us, 5.9 TB/s; one of 1021 keys: 9.4 us.  With a window of 4096 and the
+// first 67 keys: 64 sequences of 17 to 32768 keys, 48 heads on 8, 101 us, 5.3 TB/s, and
+// 168 us, 6.5 TB/s, where all have 8192 and more.
 #include "attn_schedule.cuh"
 #include "tc_ptx.cuh"
 
