@@ -194,7 +194,9 @@ def prepare(case, seed):
         likely = pick(rows, 3)
         if case["masked"]:
             wide.masked_fill_(torch.rand(wide.shape, generator=g, device="cuda") < 0.5, -math.inf)
-        logits[row, likely] = (8 + 4 * torch.rand((rows, 3), generator=g, device="cuda")).to(logits.dtype)
+        high = (8 + 4 * torch.rand((rows, 3), generator=g, device="cuda")).to(logits.dtype)
+        for i in range(3):  # a row may draw one position twice: the later value stays
+            logits[row[:, 0], likely[:, i]] = high[:, i]
         targets = pick(rows, given)
         if given:
             targets[:, 0] = torch.where(torch.rand(rows, generator=g, device="cuda") < 0.7, likely[:, 0], targets[:, 0])
