@@ -29,6 +29,7 @@ namespace {
 constexpr int kSegments = 4;          // of a thread
 constexpr int kAhead = 4;             // vectors that a thread has under way
 constexpr int kLeast = 8;             // vectors of a segment at the least, where there are several
+constexpr int kFold = 64;             // vectors of a thread whose terms one sum takes: 512 in each of two parts
 constexpr int kMaxTop = 32;           // a list is one value a lane
 constexpr int kMaxCluster = 8;        // CTAs of a row
 constexpr float kLn2 = 0.6931471805599453f;
@@ -189,10 +190,10 @@ __device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b_reversed) {
   }
   return key;
 }
-template <int kThreads>
+template <int kThreads, bool kLong>
 struct Shared {
   static constexpr int kWarps = kThreads / 32;
-  Sums sums[kWarps], total;
+  Sums sums[kWarps], total, folded[kLong ? kThreads : 1];
   uint64_t lists[kWarps][kMaxTop];
   uint64_t segments[kSegments][kThreads];   // their maxima; 0: no values
   uint64_t bound, best[kWarps], result[kMaxTop];
@@ -209,8 +210,8 @@ __device__ __forceinline__ uint64_t largest_key(uint64_t key) {
 }
 // The list of the first `warps` warps' lists together, in warp 0 (for one value only
 // its first key).  All threads of the CTA come here.
-template <int kThreads>
-__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top, Shared<kThreads>& sh) {
+template <int kThreads, bool kLong>
+__device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top, Shared<kThreads, kLong>& sh) {
   constexpr int kWarps = kThreads / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (top == 1) {
@@ -232,10 +233,15 @@ __device__ __forceinline__ uint64_t join_lists(uint64_t list, int warps, int top
 // ---------------------------------------------------------------- the kernel
 // CTA `rank` of the cluster takes its share of the row's vectors; a thread takes
 // every kThreads-th of them.
-template <typename T, int kThreads>
+//
+// kLong: more than kFold vectors a thread.  Of n equal terms, one running sum may lose 2^-25 n
+// of its size (2^28 tokens in a row: 9e-4), so these threads start afresh after kFold
+// vectors and add up their sums in shared memory (1e-5).  Apart, because it costs the
+// others 1 to 3 % (4096 x 131072 175.5 and 177.6 us).
+template <typename T, int kThreads, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(const __grid_constant__ LogprobParams p, int cluster) {
   constexpr int kSize = Vec<T>::kSize, kWarps = kThreads / 32;
-  __shared__ Shared<kThreads> sh;
+  __shared__ Shared<kThreads, kLong> sh;
   const pw_logprob_args& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = cluster > 1 ? static_cast<int>(pw::cluster_rank()) : 0;
@@ -246,15 +252,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
   const int steps = (end - begin + kThreads - 1) / kThreads;
   const int length = max(kLeast, ((steps + kSegments - 1) / kSegments + kAhead - 1) / kAhead * kAhead);   // steps of a segment
 
+  if (kLong) sh.folded[tid] = {-INFINITY, 0.0f, 0.0f};
   Sums sum{-INFINITY, 0.0f, 0.0f};
   uint64_t s2 = 0, t2 = 0;              // two parts of S and T
+  auto fold_sums = [&] {
+    float s0, s1, t0, t1;
+    pw::unpack_f32x2(s2, s0, s1);
+    pw::unpack_f32x2(t2, t0, t1);
+    sh.folded[tid] = joined(sh.folded[tid], Sums{sum.m, s0 + s1, t0 + t1}, p.scale_log2);
+    s2 = t2 = 0;
+  };
   uint64_t best = 0;                    // the thread's largest value
   const uint64_t scale2 = pw::twice(p.scale_log2);
   for (int seg = 0; seg < kSegments && seg * length < steps; ++seg) {
     const int v0 = begin + seg * length * kThreads + tid, v1 = min(end, begin + (seg + 1) * length * kThreads);
     float top = -INFINITY;              // of the segment, and the vector that has it
     int at = v0;
+    int until = v0;                     // the next fold
     for (int v = v0; v < v1; v += kAhead * kThreads) {
+      if (kLong && v >= until) {
+        fold_sums();                    // of what came before
+        until = v + kFold * kThreads;
+      }
       uint32_t w[kAhead][8];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) row.load(v + i * kThreads, v1, w[i]);
@@ -308,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
     sum.s = s0 + s1;
     sum.t = t0 + t1;
   }
+  if (kLong) sum = joined(sh.folded[tid], sum, p.scale_log2);
   sum = joined_lanes(sum, 32, p.scale_log2);
   if (lane == 0) sh.sums[warp] = sum;
 
@@ -408,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(con
   }
 }
 
-template <typename T, int kThreads>
+template <typename T, int kThreads, bool kLong>
 int launch_threads(const LogprobParams& p, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.rows * cluster));
@@ -420,7 +440,7 @@ int launch_threads(const LogprobParams& p, int cluster, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
-  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads>, p, cluster));
+  PW_CUDA_TRY(cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kThreads, kLong>, p, cluster));
   return PW_OK;
 }
 
@@ -439,8 +459,10 @@ int launch(const LogprobParams& p, cudaStream_t s) {
   // different stages (4096 rows of 32000: 59 us, 72 with 256 threads; of 8000: 30
   // and 53; but 4096 rows of 131072 with 20 alternatives 199 and 194; 512 rows of 32000
   // 16.8 and 16.2).
-  if (p.a.rows > 4 * sms && vectors <= 4096) return launch_threads<T, 128>(p, cluster, s);
-  return launch_threads<T, 256>(p, cluster, s);
+  if (p.a.rows > 4 * sms && vectors <= 4096) return launch_threads<T, 128, false>(p, cluster, s);
+  // (a row may begin inside its first vector)
+  if ((vectors + cluster) / cluster > kFold * 256) return launch_threads<T, 256, true>(p, cluster, s);
+  return launch_threads<T, 256, false>(p, cluster, s);
 }
 
 }  // namespace

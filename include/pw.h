@@ -733,8 +733,10 @@ int pw_fp8_gated_linear(const pw_gated_args* args, void* stream);
  * A logit of -inf is a token of probability 0: it adds nothing to the entropy, and
  * ranks behind every other.  A row with nothing else has lse and all log
  * probabilities -inf and entropy 0.  A row that holds NaN or +inf has NaN for all of
- * them; its top_ids are those of the logits' order, NaN ranking as -inf.  NULL and 0
- * for given or top: not wanted; at least one output.  top <= 32. */
+ * them; its top_ids are those of the logits' order, NaN ranking as -inf.  Sums are of
+ * 32 bits, of 512 terms in a row at most, and of such sums: off by up to 2^-13.4 of their size
+ * at 2^28 tokens if no rounding cancels another (2^-16 of equal terms).  NULL and 0
+ * for given or top: not wanted; at least one output.  top <= 32, rows <= 2^24, vocab <= 2^28. */
 #define PW_DTYPE_F32 2
 typedef struct pw_logprob_args {
   const void* logits;
