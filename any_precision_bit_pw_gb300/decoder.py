@@ -42,6 +42,12 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _settle(dev: torch.device) -> None:
+    """Memory that was taken on the current stream is free (and zeroed, where it has to be) for calls on any stream."""
+    if dev.type == "cuda":
+        torch.cuda.current_stream(dev).synchronize()
+
+
 @dataclass
 class Batch:
     """New tokens of some sequences, as the kernels read them (pw.h)."""
@@ -68,6 +74,7 @@ class PagedCache:
         self.free_pages: List[int] = list(range(pages - 1, -1, -1))
         self.pages: Dict[int, List[int]] = {}
         self.lens: Dict[int, int] = {}
+        _settle(self.device)
 
     def batch(self, seqs: Sequence[int], new_tokens: Sequence[int], width: Optional[int] = None) -> Batch:
         """Makes room for ``new_tokens`` more keys of each sequence and returns
@@ -189,7 +196,7 @@ class DecoderLayer:
         self.heads, self.kv_heads, self.head_dim = heads, cache.k.shape[2], cache.k.shape[3]
         self.eps, self.window, self.interleaved, self.tokens = eps, window, interleaved, tokens
         turns, self.rope_factor = pw.pw_rope_turns(self.head_dim if rotary_dim is None else rotary_dim, rope_base, rope_scaling)
-        self.turns = turns.to(dev)
+        self.turns = turns.to(dev)   # (a copy from pageable memory: it is done when this returns)
         D, wide = self.head_dim, (heads + 2 * self.kv_heads) * self.head_dim
         assert tuple(weights.qkv.codes.shape) == (wide, H) and tuple(weights.out.codes.shape) == (H, heads * D)
         width = 0
@@ -203,6 +210,7 @@ class DecoderLayer:
                 setattr(self, name, getattr(share, name))
             if self.dense and (self.ff8 is None or self.ff8.shape[1] != width):
                 self._dense_buffers(tokens, H, width, dev)
+                _settle(dev)
             return
 
         def empty(*shape, dtype=torch.float16):
@@ -227,8 +235,7 @@ class DecoderLayer:
             self.experts.status = self.status
         if self.dense:
             self._dense_buffers(tokens, H, width, dev)
-        if dev.type == "cuda":   # the layer may be called on any stream: its buffers are free and zeroed by then
-            torch.cuda.current_stream(dev).synchronize()
+        _settle(dev)
 
     def _dense_buffers(self, tokens: int, H: int, width: int, dev) -> None:
         pad = -width % 16                          # rows of the product are 16-byte aligned
@@ -325,8 +332,7 @@ class Head:
         self.lse, self.entropy, self.logprobs = empty(tokens), empty(tokens), empty(tokens, given)
         self.top_ids, self.top_logprobs = empty(tokens, top, dtype=torch.int32), empty(tokens, top)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        if dev.type == "cuda":   # the head may be called on any stream: its buffers are free and zeroed by then
-            torch.cuda.current_stream(dev).synchronize()
+        _settle(dev)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor], targets: Optional[torch.Tensor] = None,
                  stream=None) -> Scores:

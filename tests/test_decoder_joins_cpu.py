@@ -1,0 +1,39 @@
+"""Layers that follow one another, without a GPU: the buffers that they share, and how one
+layer's output joins the residual in the next."""
+import pytest
+import torch
+
+from test_decoder_dense_cpu import D, H, HEADS, KV, V, layer, log, weight, weights  # noqa: F401
+from any_precision_bit_pw_gb300 import decoder
+from any_precision_bit_pw_gb300.decoder import DecoderLayer, Head, PagedCache
+
+W = 200   # another width of the dense block
+
+
+def narrow():
+    w = weights()
+    w.gate, w.up, w.down = weight(W, H), weight(W, H), weight(H, W)
+    return w
+
+
+def test_memory_is_settled_where_it_is_taken(monkeypatch):
+    """A constructor that takes memory waits for what the current stream has under way, since
+    calls may run on another; one that takes none does not."""
+    settled = []
+    monkeypatch.setattr(decoder, "_settle", lambda dev: settled.append(dev))
+
+    def count(f):
+        settled.clear()
+        return f(), len(settled)
+    caches = [count(lambda: PagedCache(8, 16, KV, D, device="cpu")) for _ in range(4)]
+    assert [n for _, n in caches] == [1] * 4
+    make = lambda i, w, **kw: DecoderLayer(None, 0, w, HEADS, caches[i][0], 8, **kw)  # noqa: E731
+    first, n = count(lambda: make(0, weights()))
+    assert n == 1
+    same, n = count(lambda: make(1, weights(), share=first))
+    assert n == 0 and same.ff8 is first.ff8
+    other, n = count(lambda: make(2, narrow(), share=first))
+    assert n == 1 and other.ff8.shape == (8, W) and other.x8 is first.x8
+    again, n = count(lambda: make(3, narrow(), share=other))
+    assert n == 0 and again.ff8 is other.ff8 and again.y is other.y
+    assert count(lambda: Head(torch.ones(H).half(), weight(V, H), 8))[1] == 1
