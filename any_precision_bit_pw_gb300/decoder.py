@@ -204,8 +204,10 @@ class DecoderLayer:
             width = weights.down.codes.shape[1]
             assert tuple(weights.gate.codes.shape) == tuple(weights.up.codes.shape) == (width, H) == tuple(weights.down.codes.shape)[::-1]
         if share is not None:
-            if (share.stack, share.heads, share.kv_heads, D, tokens) != (stack, heads, self.kv_heads, share.head_dim, share.tokens):
-                raise ValueError("decoder layer: buffers are shared between layers of one stack with equal heads and tokens")
+            if ((share.stack, share.heads, share.kv_heads, share.head_dim, share.tokens, share.h.shape[1], share.h.device)
+                    != (stack, heads, self.kv_heads, D, tokens, H, self.turns.device)):
+                raise ValueError("decoder layer: buffers are shared between layers of one stack, on one device, with equal hidden "
+                                 "width, heads and tokens")
             for name in self.BUFFERS + self.DENSE_BUFFERS:
                 setattr(self, name, getattr(share, name))
             if self.dense and (self.ff8 is None or self.ff8.shape[1] != width):

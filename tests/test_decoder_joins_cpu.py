@@ -5,7 +5,7 @@ import torch
 
 from test_decoder_dense_cpu import D, H, HEADS, KV, V, layer, log, weight, weights  # noqa: F401
 from any_precision_bit_pw_gb300 import decoder
-from any_precision_bit_pw_gb300.decoder import DecoderLayer, Head, PagedCache
+from any_precision_bit_pw_gb300.decoder import DecoderLayer, DecoderWeights, Fp8Weight, Head, PagedCache
 
 W = 200   # another width of the dense block
 
@@ -37,3 +37,20 @@ def test_memory_is_settled_where_it_is_taken(monkeypatch):
     again, n = count(lambda: make(3, narrow(), share=other))
     assert n == 0 and again.ff8 is other.ff8 and again.y is other.y
     assert count(lambda: Head(torch.ones(H).half(), weight(V, H), 8))[1] == 1
+
+
+def test_buffers_are_not_shared_across_widths_and_devices():
+    """Dense layers have no stack that would tell: another hidden width, another device."""
+    first = layer()
+
+    def another(h, device="cpu"):
+        def matrix(n, k):
+            return Fp8Weight(torch.zeros(n, k, dtype=torch.float8_e4m3fn, device=device), torch.ones(-(-n // 128), -(-k // 128), device=device))
+        one = torch.ones(h, device=device).half()
+        w = DecoderWeights(one, one, matrix((HEADS + 2 * KV) * D, h), matrix(h, HEADS * D), gate=matrix(W, h), up=matrix(W, h),
+                           down=matrix(h, W))
+        return DecoderLayer(None, 0, w, HEADS, PagedCache(8, 16, KV, D, device=device), 8, share=first)
+    assert another(H).x8 is first.x8
+    for bad in ((2 * H, "cpu"), (H, "meta")):
+        with pytest.raises(ValueError, match="shared"):
+            another(*bad)
