@@ -157,6 +157,11 @@ class DecoderWeights:
     residual_scale: float = 1.0
 
 
+def _is_joined(w: DecoderWeights) -> bool:
+    """Whether the feed-forward output joins the residual by more than an addition."""
+    return w.post_ffn_norm is not None or w.ffn_gate is not None or w.residual_scale != 1.0
+
+
 def _add_norm(x, residual, eps, weight, post, gate, residual_scale, **out) -> None:
     """The block's output x joins the residual, and the norm before the next block."""
     if post is None and gate is None and residual_scale == 1.0:
@@ -172,7 +177,9 @@ class DecoderLayer:
     results of one may be the inputs of the next.  ``max_batch`` goes to the
     attention's workspace query, whose answer holds for any number of sequences.
     ``after``: the layer whose results come in (None for the first, whose ``x`` is
-    the embedding).  With a ``window``, the first ``sinks`` keys of a sequence stay
+    the embedding).  A layer whose weights have a norm, a gate or a scale for the
+    feed-forward output needs a layer or a head ``after`` it; ``joined`` says that the
+    caller adds its output to the residual instead.  With a ``window``, the first ``sinks`` keys of a sequence stay
     visible.  A layer with a dense block needs no ``stack``.
     """
 
@@ -184,14 +191,16 @@ class DecoderLayer:
                  tokens: int, rotary_dim: Optional[int] = None, rope_base: float = 1e6,
                  rope_scaling: Optional[pw.pw_rope_scaling] = None, interleaved: bool = False, window: int = 0,
                  eps: float = 1e-5, max_batch: int = 256, share: Optional["DecoderLayer"] = None, sinks: int = 0,
-                 after: Optional["DecoderLayer"] = None, activation: int = pw.PW_ACT_SILU):
+                 after: Optional["DecoderLayer"] = None, activation: int = pw.PW_ACT_SILU, joined: bool = False):
         self.dense = weights.down is not None
         if self.dense == (weights.router is not None) or (stack is None and not self.dense):
             raise ValueError("decoder layer: a router and a stack of experts, or the gate, up and down of a dense block")
         H = weights.attn_norm.shape[0]
         dev = weights.attn_norm.device if stack is None else stack.device
         assert stack is None or stack.H == H
-        self.sinks, self.after, self.activation = sinks, after, activation
+        self.sinks, self.after, self.activation, self.joined = sinks, after, activation, joined
+        if after is not None:
+            after.joined = True
         self.stack, self.index, self.w, self.cache = stack, index, weights, cache
         self.heads, self.kv_heads, self.head_dim = heads, cache.k.shape[2], cache.k.shape[3]
         self.eps, self.window, self.interleaved, self.tokens = eps, window, interleaved, tokens
@@ -263,6 +272,8 @@ class DecoderLayer:
         T, w, c = batch.tokens, self.w, self.cache
         if x.shape[0] != T or T > self.tokens:
             raise ValueError(f"decoder layer: {x.shape[0]} rows for a batch of {T} tokens, at most {self.tokens}")
+        if _is_joined(w) and not self.joined:
+            raise ValueError("decoder layer: nothing comes `after` it that would take the norm, gate or scale of its output")
         if T == 0:
             return (self.y if self.dense else self.experts.y)[:0], self.residual[1][:0]
         x8, x8s, qkv, q, attn = self.x8[:T], self.x8_scale[:T], self.qkv[:T], self.q[:T], self.attn[:T]
@@ -326,6 +337,8 @@ class Head:
             raise ValueError(f"head: temperature {temperature}")
         self.norm, self.weight, self.after, self.eps, self.scale = norm, weight, after, eps, 1.0 / temperature
         self.tokens, self.given, self.top = tokens, given, top
+        if after is not None:
+            after.joined = True
 
         def empty(*shape, dtype=torch.float32):
             return torch.empty(shape, dtype=dtype, device=dev)

@@ -54,3 +54,26 @@ def test_buffers_are_not_shared_across_widths_and_devices():
     for bad in ((2 * H, "cpu"), (H, "meta")):
         with pytest.raises(ValueError, match="shared"):
             another(*bad)
+
+
+@pytest.mark.parametrize("kw", [dict(post_ffn_norm=torch.ones(H).half()), dict(ffn_gate=torch.ones(H).half()), dict(residual_scale=0.5)])
+def test_an_output_that_nothing_joins_is_refused(log, kw):  # noqa: F811
+    """A norm, gate or scale of a layer's output is taken by what was made `after` it: without that,
+    the next layer would add the bare output."""
+    first = layer(weights(**kw))
+    second = layer(share=first)                     # (not told what comes in)
+    x, b = torch.zeros(2, H).half(), first.cache.batch([0], [2])
+    with pytest.raises(ValueError, match="after"):
+        second(*first(x, None, b), b)
+    assert not log
+    second = layer(share=first, after=first)
+    y, r = second(*first(x, None, b), b)
+    assert [n for n, _, _ in log].count("pw_norm_add_norm") == 1 + ("residual_scale" in kw)
+    # a head, or the caller
+    for L, end in ((layer(weights(**kw)), True), (layer(weights(**kw), joined=True), False)):
+        if end:
+            Head(torch.ones(H).half(), weight(V, H), 8, after=L)
+        assert L(x, None, L.cache.batch([0], [2]))[0].shape == (2, H)
+    # plain layers need nobody
+    plain = layer()
+    assert plain(x, None, plain.cache.batch([0], [2]))[0].shape == (2, H)
