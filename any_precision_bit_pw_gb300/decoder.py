@@ -162,6 +162,15 @@ def _is_joined(w: DecoderWeights) -> bool:
     return w.post_ffn_norm is not None or w.ffn_gate is not None or w.residual_scale != 1.0
 
 
+def _comes_after(after: Optional["DecoderLayer"], eps: float) -> None:
+    """A layer or head that takes another one's output: the norm of that output and its own are one kernel with one eps."""
+    if after is None:
+        return
+    if after.w.post_ffn_norm is not None and after.eps != eps:
+        raise ValueError(f"the norm of the layer's output has eps {after.eps}, what comes after it {eps}")
+    after.joined = True
+
+
 def _add_norm(x, residual, eps, weight, post, gate, residual_scale, **out) -> None:
     """The block's output x joins the residual, and the norm before the next block."""
     if post is None and gate is None and residual_scale == 1.0:
@@ -178,8 +187,9 @@ class DecoderLayer:
     attention's workspace query, whose answer holds for any number of sequences.
     ``after``: the layer whose results come in (None for the first, whose ``x`` is
     the embedding).  A layer whose weights have a norm, a gate or a scale for the
-    feed-forward output needs a layer or a head ``after`` it; ``joined`` says that the
-    caller adds its output to the residual instead.  With a ``window``, the first ``sinks`` keys of a sequence stay
+    feed-forward output needs a layer or a head ``after`` it (of the same ``eps``, if
+    it is a norm); ``joined`` says that the caller adds its output to the residual
+    instead.  With a ``window``, the first ``sinks`` keys of a sequence stay
     visible.  A layer with a dense block needs no ``stack``.
     """
 
@@ -199,8 +209,6 @@ class DecoderLayer:
         dev = weights.attn_norm.device if stack is None else stack.device
         assert stack is None or stack.H == H
         self.sinks, self.after, self.activation, self.joined = sinks, after, activation, joined
-        if after is not None:
-            after.joined = True
         self.stack, self.index, self.w, self.cache = stack, index, weights, cache
         self.heads, self.kv_heads, self.head_dim = heads, cache.k.shape[2], cache.k.shape[3]
         self.eps, self.window, self.interleaved, self.tokens = eps, window, interleaved, tokens
@@ -212,11 +220,13 @@ class DecoderLayer:
         if self.dense:
             width = weights.down.codes.shape[1]
             assert tuple(weights.gate.codes.shape) == tuple(weights.up.codes.shape) == (width, H) == tuple(weights.down.codes.shape)[::-1]
+        if share is not None and (
+                (share.stack, share.heads, share.kv_heads, share.head_dim, share.tokens, share.h.shape[1], share.h.device)
+                != (stack, heads, self.kv_heads, D, tokens, H, self.turns.device)):
+            raise ValueError("decoder layer: buffers are shared between layers of one stack, on one device, with equal hidden "
+                             "width, heads and tokens")
+        _comes_after(after, eps)
         if share is not None:
-            if ((share.stack, share.heads, share.kv_heads, share.head_dim, share.tokens, share.h.shape[1], share.h.device)
-                    != (stack, heads, self.kv_heads, D, tokens, H, self.turns.device)):
-                raise ValueError("decoder layer: buffers are shared between layers of one stack, on one device, with equal hidden "
-                                 "width, heads and tokens")
             for name in self.BUFFERS + self.DENSE_BUFFERS:
                 setattr(self, name, getattr(share, name))
             if self.dense and (self.ff8 is None or self.ff8.shape[1] != width):
@@ -337,8 +347,7 @@ class Head:
             raise ValueError(f"head: temperature {temperature}")
         self.norm, self.weight, self.after, self.eps, self.scale = norm, weight, after, eps, 1.0 / temperature
         self.tokens, self.given, self.top = tokens, given, top
-        if after is not None:
-            after.joined = True
+        _comes_after(after, eps)
 
         def empty(*shape, dtype=torch.float32):
             return torch.empty(shape, dtype=dtype, device=dev)

@@ -77,3 +77,15 @@ def test_an_output_that_nothing_joins_is_refused(log, kw):  # noqa: F811
     # plain layers need nobody
     plain = layer()
     assert plain(x, None, plain.cache.batch([0], [2]))[0].shape == (2, H)
+
+
+def test_norms_in_one_kernel_have_one_eps():
+    """The norm of a layer's output runs with that of what comes after it: another eps would be lost."""
+    first = layer(weights(post_ffn_norm=torch.ones(H).half()), eps=1e-6)
+    for make in (lambda **kw: layer(after=first, **kw), lambda **kw: Head(torch.ones(H).half(), weight(V, H), 8, after=first, **kw)):
+        with pytest.raises(ValueError, match="eps"):
+            make()
+        assert not first.joined
+    for make in (lambda **kw: layer(after=first, **kw), lambda **kw: Head(torch.ones(H).half(), weight(V, H), 8, after=first, **kw)):
+        assert make(eps=1e-6).after is first and first.joined
+    assert layer(after=layer(weights(ffn_gate=torch.ones(H).half()), eps=1e-6)).eps == 1e-5      # no norm of the output
