@@ -171,6 +171,16 @@ def _comes_after(after: Optional["DecoderLayer"], eps: float) -> None:
     after.joined = True
 
 
+def _take_output(after: Optional["DecoderLayer"], x, residual, eps, weight, **out) -> None:
+    """The results of the layer that came before join, and the norm of what comes now."""
+    if after is None or (residual is None and not _is_joined(after.w)):
+        pw.pw_add_rmsnorm(x, weight, eps, residual=residual, **out)
+    elif residual is None:
+        raise ValueError("the output of the layer that came before goes with its residual")
+    else:
+        _add_norm(x, residual, eps, weight, after.w.post_ffn_norm, after.w.ffn_gate, after.w.residual_scale, **out)
+
+
 def _add_norm(x, residual, eps, weight, post, gate, residual_scale, **out) -> None:
     """The block's output x joins the residual, and the norm before the next block."""
     if post is None and gate is None and residual_scale == 1.0:
@@ -289,12 +299,7 @@ class DecoderLayer:
         x8, x8s, qkv, q, attn = self.x8[:T], self.x8_scale[:T], self.qkv[:T], self.q[:T], self.attn[:T]
         hq, hk = self.heads, self.kv_heads
         r1, r2 = self.residual[0][:T], self.residual[1][:T]
-        if self.after is not None and residual is not None:
-            before = self.after.w
-            _add_norm(x, residual, self.eps, w.attn_norm, before.post_ffn_norm, before.ffn_gate, before.residual_scale,
-                      residual_out=r1, q=x8, scale=x8s)
-        else:
-            pw.pw_add_rmsnorm(x, w.attn_norm, self.eps, residual=residual, residual_out=r1, q=x8, scale=x8s)
+        _take_output(self.after, x, residual, self.eps, w.attn_norm, residual_out=r1, q=x8, scale=x8s)
         pw.pw_fp8_linear(x8, x8s, w.qkv.codes, w.qkv.scale, qkv.view(T, -1), self.status)
         pw.pw_rope_append(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], self.turns, c.k, c.v, batch.page_table,
                           batch.q_offsets, batch.kv_lens, q, self.status, interleaved=self.interleaved,
@@ -372,12 +377,7 @@ class Head:
             return s
         x8, x8s = self.x8[:T], self.x8_scale[:T]
         with _on(stream):
-            if self.after is not None and residual is not None:
-                before = self.after.w
-                _add_norm(x, residual, self.eps, self.norm, before.post_ffn_norm, before.ffn_gate, before.residual_scale,
-                          q=x8, scale=x8s)
-            else:
-                pw.pw_add_rmsnorm(x, self.norm, self.eps, residual=residual, q=x8, scale=x8s)
+            _take_output(self.after, x, residual, self.eps, self.norm, q=x8, scale=x8s)
             pw.pw_fp8_linear(x8, x8s, self.weight.codes, self.weight.scale, s.logits, self.status)
             pw.pw_token_logprobs(s.logits, targets=targets if n else None, logprobs=s.logprobs, lse=s.lse, entropy=s.entropy,
                                  top_ids=s.top_ids, top_logprobs=s.top_logprobs, scale=self.scale)

@@ -89,3 +89,19 @@ def test_norms_in_one_kernel_have_one_eps():
     for make in (lambda **kw: layer(after=first, **kw), lambda **kw: Head(torch.ones(H).half(), weight(V, H), 8, after=first, **kw)):
         assert make(eps=1e-6).after is first and first.joined
     assert layer(after=layer(weights(ffn_gate=torch.ones(H).half()), eps=1e-6)).eps == 1e-5      # no norm of the output
+
+
+def test_an_output_without_its_residual_is_refused(log):  # noqa: F811
+    """What comes after a layer with a norm, gate or scale of its output takes both results of it."""
+    first = layer(weights(ffn_gate=torch.ones(H).half()))
+    x, b = torch.zeros(2, H).half(), first.cache.batch([0], [2])
+    for then in (lambda x, r, L=layer(after=first): L(x, r, b), Head(torch.ones(H).half(), weight(V, H), 8, after=first)):
+        with pytest.raises(ValueError, match="residual"):
+            then(x, None)
+        assert not log
+        then(x, x)
+        assert log[0][0] == "pw_norm_add_norm"
+        log.clear()
+    plain = layer()
+    layer(after=plain)(x, None, b)
+    assert log[0][0] == "pw_add_rmsnorm"
