@@ -681,7 +681,7 @@ def pw_paged_attention_workspace(tokens: int, batch: int, heads: int, kv_heads: 
 def pw_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
                        q_offsets: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
                        status: torch.Tensor, scale: float, causal: bool = True, window: int = 0, max_q_len: int = 0,
-                       max_kv_len: int = 0, lse: Optional[torch.Tensor] = None, sinks: int = 0, stream=None) -> None:
+                       max_kv_len: int = 0, lse: Optional[torch.Tensor] = None, stream=None, sinks: int = 0) -> None:
     """out [T][heads][D] = attention of the new tokens q over their sequences'
     keys in the paged cache [pages][page_size][kv_heads][D]; with a `window` a
     token sees that many keys up to its own, and the first `sinks` of its
