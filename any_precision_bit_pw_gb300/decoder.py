@@ -110,7 +110,9 @@ class PagedCache:
     def trim(self, seq: int, window: int, sinks: int = 0) -> int:
         """Returns the pages of a sequence that no later token sees in attention
         over the last ``window`` keys and the first ``sinks`` (once the stream has
-        passed the calls that read them), and how many they are."""
+        passed the calls that read them), and how many they are.  Tables serve all
+        layers of a step: ``window`` and ``sinks`` are the largest of any layer that reads
+        them, and where one of them attends to every key there is nothing to return."""
         if window < 1 or sinks < 0:
             raise ValueError(f"trim: window {window}, sinks {sinks}")
         pages, n = self.pages.get(seq, []), self.page_size
