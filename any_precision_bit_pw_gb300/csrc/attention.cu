@@ -157,6 +157,8 @@ __device__ __forceinline__ void compute_chunk(const Params& p, const Cursor<kSin
       sum += v;
     }
     w.l[i] = w.l[i] * keep[i] + sum;
+    // The weights are rounded to the values' type, which both operands of the instruction have: half a step each,
+    // against one rounding of the result; their sum is not.
     pr[i] = pw::pack2<T>(s[0][2 * i], s[0][2 * i + 1]);
     pr[2 + i] = pw::pack2<T>(s[1][2 * i], s[1][2 * i + 1]);
   }

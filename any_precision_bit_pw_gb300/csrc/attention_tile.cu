@@ -434,7 +434,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, const Cursor<kSink
             e0 = pw::exp2_fast(e0);
             e1 = pw::exp2_fast(e1);
             sum[j & 1] = pw::add_f32x2(sum[j & 1], pw::pack_f32x2(__float_as_uint(e0), __float_as_uint(e1)));
-            w[j] = pw::pack2<T>(e0, e1);
+            w[j] = pw::pack2<T>(e0, e1);   // in the values' type, as the instruction wants it; the sum is of the unrounded
           }
           pw::tmem_st_x32(s_tmem + 32 * i, w);
           pw::tmem_st_wait();

@@ -21,8 +21,11 @@
 // first keys, as far as they lie before the window's first block.  (The few keys
 // of that last block seldom move the running maximum; in front, they set one that the
 // window's keys move again: chunks of 2048 tokens with a window of 4096 and 1, 4 and
-// 64 such keys take 387, 376 and 392 us, 425, 390 and 372 in front.)  The kernels are compiled apart, so that the other calls do not pay for
-// the second range.
+// 64 such keys take 387, 376 and 392 us, 425, 390 and 372 in front.  These are keys drawn
+// alike.  Where the first ones' scores stand 5 to 10 above all others, they hold nearly every
+// row's maximum and the last block moves it once more: 378, 382 and 375 us, against 376, 378 and 375
+// of keys drawn alike in that run; in front was not timed there.)  The kernels are compiled
+// apart, so that the other calls do not pay for the second range.
 #pragma once
 
 #include "ops_common.cuh"

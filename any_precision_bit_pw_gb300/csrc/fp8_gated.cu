@@ -8,7 +8,9 @@
 // in 16 bits, or in e4m3 with a scale per row and 128 columns: what the down
 // projection reads.  Neither g nor u is stored.
 //
-// Few tokens: the weights' bytes bound it (7 x 14336 x 4096 in 8 bits 24 us, 4.8 TB/s).
+// Few tokens: the weights' bytes bound it (7 x 14336 x 4096 in 8 bits 24 us, 4.8 TB/s; by
+// a line through K of 2048 to 8192, 4.9 us and then 6.0 TB/s, with a 16-bit result, whose
+// CTAs need no cluster, 5.4 us and 6.7 TB/s).
 // Many: the accumulators, which are read and scaled once a group of 128, and the power
 // limit (8192 x 16384 x 6144 in 8 bits 1257 to 1285 us, 2.6 PFLOP/s; cool, in 16 bits,
 // 1160, the product of one weight as large as both 1077).  Between them, the rounds of the

@@ -15,10 +15,11 @@
 //
 // Memory bandwidth bounds it (4096 rows of 131072 bf16 logits: 178 us with one
 // alternative, 6.0 TB/s, and 161 without), with the instructions close behind: 9 a
-// value, one of them an exponential.  For few rows it is the chain of a load,
-// reductions and the second look at a few segments (one row of 32000: 8.2 us).  Few
-// rows: a cluster of up to 8 CTAs shares one and joins its results through
-// distributed shared memory.
+// value, one of them an exponential (ex2.approx: within 2^-22 of its value).  For few
+// rows it is the chain of a load, reductions and the second look at a few segments
+// (one row of 32000: 8.2 us), and so it is for many short ones, a row a CTA: 4096 rows of 1000 bf16 logits 15.7 us without alternatives,
+// 25.4 with one, 42 with twenty, of 8000 20.3, 30 and 46.  Few rows: a cluster of up to 8
+// CTAs shares one and joins its results through distributed shared memory.
 #include <type_traits>
 
 #include "ops_common.cuh"

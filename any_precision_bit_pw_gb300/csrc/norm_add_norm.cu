@@ -7,8 +7,10 @@
 // Every value is read and written once: memory bandwidth bounds it (8192 x 6144
 // bf16 to e4m3 60.5 us, 5.8 TB/s; 8192 x 5120 in 16 bits 52.5 us, 6.4 TB/s; with a gate for
 // every row 75 us at 6144 columns, 6.7 TB/s), for a few rows the latency of one load, two
-// reductions and one store (one row of 4096: 2.6 us), and for odd widths the
-// instructions that clip and shift (1531 x 5121 20 us, 13 at 5120).
+// reductions and one store (one row of 4096: 2.6 us).  Odd widths: 2.5 us for a row of
+// every CTA, 1.8 at 5120 columns, and 2.7 us more to begin (1531 x 5121 20 us, 13.4 at
+// 5120); issue is at 49 % and 33 % of the warps are there, so it is neither memory nor the
+// 46 instructions a value alone.
 #include "rows.cuh"
 
 namespace {
@@ -68,7 +70,8 @@ __device__ __forceinline__ float block_sum(uint64_t two, float* part) {
 // own (kSame, whose columns move with the row: [column % 16][column / 16], so that
 // neighbouring threads find neighbouring words).  Rows of more than 16384 columns
 // fill the registers and more: they read the vectors from the L1 cache and load
-// nothing ahead.
+// nothing ahead (2048 rows of 16384: 47 us, of 20000 104, at 6.8 TB/s 40 and 48); shifted
+// ones of that length also spill up to 200 bytes a thread (2048 x 20001: 240 us).
 // Arithmetic in packed pairs: with single instructions the kernel was bound by
 // their number (39 a value; 8192 x 6144 to e4m3 102 us, now 60.5).
 template <typename T, int kParts, Access kAccess, bool kMatrix>
